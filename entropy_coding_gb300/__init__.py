@@ -4,6 +4,8 @@ ZipNN-style pipeline (nucleation NOTE-241: ZipNN, Method): exponent
 extraction and byte grouping, per-chunk order-0 12-bit frequency tables,
 32-lane interleaved rANS with raw passthrough (cuZipNN 0.1.0 API:
 passthrough_threshold), a chunk-offset prefix scan and per-chunk zlib CRC-32.
+An 8-bit key/value cache (kv.py) quantises the tokens of a model in service,
+reads them back and attends to them.
 Every step runs in the CUDA kernels of ``libzc.so`` (include/zc.h); this
 module only marshals arguments through ctypes and uses PyTorch for device
 memory and streams. There is no CPU fallback: without the library every call
@@ -18,13 +20,16 @@ import threading
 import torch
 
 from . import build as _build
+from . import kv as _kv
+from .kv import KVBatch, KVCache, kv_attend, kv_attend_into, kv_read, kv_read_into, kv_write
 from .workloads import BF16, FP16, FP32, U8, U16, U32
 
 __all__ = ["compress", "decompress", "crc32", "verify", "verify_into", "blob_info", "blob_size", "workspace_size",
            "compress_into", "decompress_into", "compress_delta", "decompress_delta", "compress_delta_into",
            "decompress_delta_into", "compress_batch", "compress_batch_into", "decompress_batch",
            "decompress_batch_into", "workspace_size_batch", "decompress_workspace_size_batch", "ZcError", "lib", "SHARED_TABLES", "LANE_WORDS", "OK", "EINVAL", "EFORMAT",
-           "ECRC", "ECORRUPT", "ETIMEOUT", "ECAPACITY", "ECUDA", "NO_VERIFY", "PACKED"]
+           "ECRC", "ECORRUPT", "ETIMEOUT", "ECAPACITY", "ECUDA", "NO_VERIFY", "PACKED",
+           "KVCache", "KVBatch", "kv_write", "kv_read", "kv_read_into", "kv_attend", "kv_attend_into"]
 
 OK, EINVAL, EFORMAT, ECRC, ECORRUPT, ETIMEOUT, ECAPACITY, ECUDA = 0, 1, 2, 4, 8, 16, 32, 64
 NO_VERIFY = 1
@@ -113,6 +118,7 @@ def lib() -> ctypes.CDLL:
                                             u64, vp, vp]
             L.zc_decompress_batch.restype = i32
             L.zc_decompress_batch.argtypes = [u32, vp, ctypes.POINTER(_Info), vp, vp, pu64, u32, vp, u64, vp, vp]
+            _kv.declare(L)
             _lib = L
     return _lib
 

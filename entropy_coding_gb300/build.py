@@ -1,4 +1,5 @@
-"""Build libzc.so (the C-ABI library) from csrc/*.cu with nvcc for sm_103a.
+"""Build libzc.so (the C-ABI library) from csrc/*.cu and csrc/kv/*.cu with nvcc
+for sm_103a.
 
 Each translation unit compiles in parallel; the objects are linked into
 entropy_coding_gb300/_lib/libzc.so. Rebuilds only when a source or header is
@@ -30,11 +31,11 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "kv", "*.cu")))
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return _sources() + glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def needs_build() -> bool:

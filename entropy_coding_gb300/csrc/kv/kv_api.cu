@@ -1,0 +1,120 @@
+// kv_api.cu — the C ABI of the 8-bit key/value cache operators: argument
+// checks and launches. As in zc_api.cu, no entry point allocates or
+// synchronises; what only the device can see is reported through *d_status.
+#include <cmath>
+
+#include "kv_common.cuh"
+
+namespace {
+
+using namespace zc::kv;
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+int elt_bytes(int dtype) {
+    switch (dtype) {
+    case ZC_BF16: case ZC_FP16: return 2;
+    case ZC_FP32: return 4;
+    default: return 0;
+    }
+}
+
+int make_cache(const zc_kv_cache *c, Cache &o) {
+    if (!c || !c->d_k || !c->d_v || !c->d_k_scale || !c->d_v_scale) return ZC_EINVAL;
+    if (c->head_dim == 0 || c->head_dim % 16 || c->head_dim > kMaxHeadDim) return ZC_EINVAL;
+    if (c->block_tokens == 0 || c->block_tokens % 16 || c->block_tokens > kMaxBlockTokens) return ZC_EINVAL;
+    if (c->kv_heads == 0 || c->kv_heads > 65535 || c->n_blocks == 0 || c->n_blocks > 0x7FFFFFFFu) return ZC_EINVAL;
+    const int64_t need = int64_t(c->kv_heads) * c->block_tokens * c->head_dim;
+    if (c->block_stride < need || c->block_stride % 16 || c->scale_stride < int64_t(c->kv_heads)) return ZC_EINVAL;
+    if (c->block_stride > INT64_MAX / int64_t(c->n_blocks) || c->scale_stride > INT64_MAX / 4 / int64_t(c->n_blocks)) return ZC_EINVAL;
+    if (!aligned(c->d_k, 16) || !aligned(c->d_v, 16) || !aligned(c->d_k_scale, 4) || !aligned(c->d_v_scale, 4)) return ZC_EINVAL;
+    o.code[0] = static_cast<uint8_t *>(c->d_k);
+    o.code[1] = static_cast<uint8_t *>(c->d_v);
+    o.scale[0] = c->d_k_scale;
+    o.scale[1] = c->d_v_scale;
+    o.block_stride = c->block_stride;
+    o.scale_stride = c->scale_stride;
+    o.n_blocks = c->n_blocks;
+    o.heads = c->kv_heads;
+    o.tokens = c->block_tokens;
+    o.dim = c->head_dim;
+    return ZC_OK;
+}
+
+int make_batch(const zc_kv_batch *b, Batch &o) {
+    if (!b) return ZC_EINVAL;
+    if (b->n_seqs > 0x00FFFFFFu || b->total_tokens > 0x7FFFFFFFu || b->table_width > 0x7FFFFFFFu) return ZC_EINVAL;
+    if (b->max_tokens > b->total_tokens || (b->total_tokens && (b->max_tokens == 0 || b->n_seqs == 0))) return ZC_EINVAL;
+    if (uint64_t(b->max_tokens) * b->n_seqs < b->total_tokens) return ZC_EINVAL;
+    if (b->n_seqs && (!b->d_table || !b->d_cu || !b->d_lens)) return ZC_EINVAL;
+    if (b->n_seqs && (b->table_width == 0 || b->table_stride < int64_t(b->table_width))) return ZC_EINVAL;
+    if (!aligned(b->d_table, 4) || !aligned(b->d_cu, 4) || !aligned(b->d_lens, 4)) return ZC_EINVAL;
+    o.table = b->d_table;
+    o.table_stride = b->table_stride;
+    o.cu = b->d_cu;
+    o.lens = b->d_lens;
+    o.n_seqs = b->n_seqs;
+    o.total = b->total_tokens;
+    o.most = b->max_tokens;
+    o.width = b->table_width;
+    return ZC_OK;
+}
+
+// Rows of `heads` heads are read and written 16 bytes at a time.
+int make_rows(const zc_kv_rows &r, int elt, Rows &o) {
+    if (!r.d_data || !aligned(r.d_data, 16)) return ZC_EINVAL;
+    if (r.token_stride % (16 / elt) || r.head_stride % (16 / elt)) return ZC_EINVAL;
+    o.p = r.d_data;
+    o.token = r.token_stride;
+    o.head = r.head_stride;
+    return ZC_OK;
+}
+
+int move(bool write, const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, const zc_kv_rows *k,
+         const zc_kv_rows *v, int32_t *d_status, void *stream) {
+    MoveArgs a{};
+    const int elt = elt_bytes(dtype);
+    if (!elt || !k || !v || !d_status || !aligned(d_status, 4)) return ZC_EINVAL;
+    int st = make_cache(cache, a.c);
+    if (st == ZC_OK) st = make_batch(batch, a.b);
+    if (st != ZC_OK) return st;
+    if (a.b.total == 0) return ZC_OK;
+    if ((st = make_rows(*k, elt, a.x[0])) != ZC_OK || (st = make_rows(*v, elt, a.x[1])) != ZC_OK) return st;
+    a.d_status = d_status;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return write ? launch_write(dtype, a, s) : launch_read(dtype, a, s);
+}
+
+} // namespace
+
+extern "C" int zc_kv_write(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, const zc_kv_rows *k,
+                           const zc_kv_rows *v, int32_t *d_status, void *stream) {
+    return move(true, cache, batch, dtype, k, v, d_status, stream);
+}
+
+extern "C" int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, const zc_kv_rows *k,
+                          const zc_kv_rows *v, int32_t *d_status, void *stream) {
+    return move(false, cache, batch, dtype, k, v, d_status, stream);
+}
+
+extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
+                            const zc_kv_rows *q, const zc_kv_rows *out, float *d_lse, double scale, uint32_t flags,
+                            uint32_t window, int32_t *d_status, void *stream) {
+    AttendArgs a{};
+    if ((dtype != ZC_BF16 && dtype != ZC_FP16) || !q || !out || !d_status || !aligned(d_status, 4)) return ZC_EINVAL;
+    if ((flags & ~ZC_KV_CAUSAL) || !std::isfinite(scale) || std::fabs(scale) > 1e18 || !aligned(d_lse, 4)) return ZC_EINVAL;
+    int st = make_cache(cache, a.c);
+    if (st == ZC_OK) st = make_batch(batch, a.b);
+    if (st != ZC_OK) return st;
+    if (heads == 0 || heads % a.c.heads || heads > 65535) return ZC_EINVAL;
+    if (a.b.total == 0) return ZC_OK;
+    if ((st = make_rows(*q, 2, a.q)) != ZC_OK || (st = make_rows(*out, 2, a.out)) != ZC_OK) return st;
+    a.lse = d_lse;
+    a.heads = heads;
+    a.group = heads / a.c.heads;
+    a.scale_log2 = float(scale * 1.4426950408889634);
+    a.causal = flags & ZC_KV_CAUSAL;
+    a.window = window;
+    a.d_status = d_status;
+    return launch_attend(dtype, a, static_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,176 @@
+// kv_common.cuh — argument blocks and device helpers of the 8-bit key/value
+// cache kernels (kv_write.cu, kv_read.cu, kv_rows.cu; the C ABI of the
+// operators is in kv_api.cu and include/zc.h).
+//
+// The cache. For block b, head h, row r (a token of the block) and column d,
+// the number is value(code) * scale[b][h], with E4M3 codes in
+// [block][head][row][column] order and one float32 scale for each block and
+// head, for K and for V apart.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "zc.h"  // from include/ (on the -I path)
+
+namespace zc {
+namespace kv {
+
+constexpr uint32_t kMaxHeadDim = 128, kMaxBlockTokens = 256;
+constexpr float kCodeMax = 448.0f;  // the largest E4M3 value
+
+// The cache and the batch as the kernels take them.
+struct Cache {
+    uint8_t *code[2];    // K, V
+    float *scale[2];
+    int64_t block_stride;  // bytes
+    int64_t scale_stride;  // floats
+    uint32_t n_blocks, heads, tokens, dim;
+};
+
+struct Batch {
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *cu;
+    const int32_t *lens;
+    uint32_t n_seqs, total, most, width;
+};
+
+// A [token][head][dim] tensor with its own strides (elements).
+struct Rows {
+    void *p;
+    int64_t token, head;
+};
+
+struct MoveArgs {  // write and read
+    Cache c;
+    Batch b;
+    Rows x[2];  // K, V
+    int32_t *d_status;
+};
+
+struct AttendArgs {
+    Cache c;
+    Batch b;
+    Rows q, out;
+    float *lse;            // [total][heads] or null
+    uint32_t heads, group;
+    float scale_log2;      // softmax scale * log2(e)
+    uint32_t causal, window;
+    int32_t *d_status;
+};
+
+int launch_write(int dtype, const MoveArgs &a, cudaStream_t s);
+int launch_read(int dtype, const MoveArgs &a, cudaStream_t s);
+int launch_attend(int dtype, const AttendArgs &a, cudaStream_t s);
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ void report(int32_t *d_status, int bits) { atomicOr(d_status, bits); }
+
+// One sequence of the batch: n new tokens, packed from `first` on, the last
+// of its `len` tokens.
+struct Seq {
+    uint32_t s, first, n;
+    int32_t len;
+    bool ok;
+};
+
+// Reads and checks sequence s; every thread that asks gets the same answer.
+// `need_table`: whether the tokens' blocks are looked up.
+__device__ __forceinline__ Seq read_seq(const Batch &b, uint32_t s, int32_t *d_status, uint32_t block_tokens, bool speak) {
+    const int32_t c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1);
+    Seq q;
+    q.s = s;
+    q.first = uint32_t(c0);
+    q.n = uint32_t(c1 - c0);
+    q.len = __ldg(b.lens + s);
+    q.ok = c0 >= 0 && c1 >= c0 && uint32_t(c1) <= b.total && uint32_t(c1 - c0) <= b.most && q.len >= 0;
+    if (!q.ok && speak) report(d_status, ZC_EFORMAT);
+    if (q.ok && uint64_t(q.len) > uint64_t(b.width) * block_tokens) {
+        if (speak) report(d_status, ZC_ECAPACITY);
+        q.ok = false;
+    }
+    return q;
+}
+
+// Work of a ragged batch without a host copy of its lengths. Sequence s takes
+// the slots from f(s) = floor(cu[s] * per / unit) + extra * s on; f(s + 1) -
+// f(s) >= ceil(n * per / unit) + extra - 1, so extra = 1 gives every run of n
+// tokens its ceil(n * per / unit) tiles, and extra = 2 the blocks of a run
+// that may start inside one. The launch covers f(n_seqs) slots. The CTA
+// counts the f(s) at or below its slot: one round of loads for any batch up
+// to the CTA's size, where a binary search would take one dependent load for
+// each halving.
+__device__ __forceinline__ uint64_t slot_of(uint64_t tokens, uint32_t s, uint32_t per, uint32_t unit, uint32_t extra) {
+    return tokens * per / unit + uint64_t(extra) * s;
+}
+__host__ __device__ inline uint64_t slots_of(uint64_t total, uint32_t n_seqs, uint32_t per, uint32_t unit, uint32_t extra) {
+    return total * per / unit + uint64_t(extra) * n_seqs;
+}
+
+// The sequence of slot u (the whole CTA calls this); `at`: the slot's index
+// within the sequence.
+__device__ __forceinline__ uint32_t find_seq(const Batch &b, uint64_t u, uint32_t per, uint32_t unit, uint32_t extra, uint64_t &at) {
+    uint32_t below = 0;
+    for (uint32_t s0 = 0; s0 < b.n_seqs; s0 += blockDim.x) {
+        const uint32_t s = s0 + threadIdx.x;
+        bool in = false;
+        if (s < b.n_seqs) in = slot_of(uint32_t(max(__ldg(b.cu + s), 0)), s, per, unit, extra) <= u;
+        const uint32_t n = __syncthreads_count(in);
+        below += n;
+        if (n < blockDim.x) break;  // f grows with s
+    }
+    const uint32_t s = below ? below - 1 : 0;
+    at = u - slot_of(uint32_t(max(__ldg(b.cu + s), 0)), s, per, unit, extra);
+    return s;
+}
+
+// Block of the table, or -1 (reported) where the entry names none.
+__device__ __forceinline__ int64_t read_block(const Batch &b, const Cache &c, uint32_t s, uint32_t i, int32_t *d_status) {
+    const int32_t e = __ldg(b.table + int64_t(s) * b.table_stride + i);
+    if (uint32_t(e) < c.n_blocks) return e;
+    report(d_status, ZC_EFORMAT);
+    return -1;
+}
+
+// ---------------------------------------------------------------------------
+// E4M3
+
+// Two E4M3 codes (low byte first) to two halves; exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t v) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+    return r;
+}
+// Two floats to two codes, to nearest even, saturating at +-448, NaN stays NaN.
+__device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {
+    const uint32_t h = e4m3x2_to_half2(v);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Two 16-bit elements of type DT to floats, and back (rounded once).
+template <int DT> __device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if (DT == ZC_FP16) return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if (DT == ZC_FP16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+#endif  // __CUDACC__
+
+} // namespace kv
+} // namespace zc

@@ -1,0 +1,75 @@
+// kv_read.cu — tokens of the 8-bit cache as numbers: value(code) * scale,
+// rounded once to the type asked for.
+//
+// One CTA does kTokens packed tokens of one head, K or V: the tokens' places
+// first, then 16 codes (16 bytes) a thread.
+#include "kv_common.cuh"
+
+namespace zc {
+namespace kv {
+namespace {
+
+constexpr int kThreads = 128, kTokens = 16;
+
+template <int DT> __device__ __forceinline__ void store16(void *p, const float (&x)[16]) {
+    if (DT == ZC_FP32) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            static_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            static_cast<uint4 *>(p)[i] = make_uint4(pack2<DT>(x[8 * i], x[8 * i + 1]), pack2<DT>(x[8 * i + 2], x[8 * i + 3]),
+                                                    pack2<DT>(x[8 * i + 4], x[8 * i + 5]), pack2<DT>(x[8 * i + 6], x[8 * i + 7]));
+    }
+}
+
+template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(MoveArgs a) {
+    uint64_t at;
+    const uint32_t s = find_seq(a.b, blockIdx.x, 1, kTokens, 1, at);
+    const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, threadIdx.x == 0 && at == 0);
+    if (!q.ok || q.n == 0) return;
+    if (uint32_t(q.len) < q.n) {
+        if (threadIdx.x == 0 && at == 0) report(a.d_status, ZC_EFORMAT);
+        return;
+    }
+    const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y, kvi = blockIdx.z;
+    const uint32_t per_row = D / 16;
+    for (uint32_t i = threadIdx.x; i < kTokens * per_row; i += kThreads) {
+        const uint64_t t = at * kTokens + i / per_row;
+        if (t >= q.n) break;
+        const uint32_t pos = uint32_t(q.len) - q.n + uint32_t(t), col = i % per_row * 16;
+        const int64_t id = read_block(a.b, a.c, s, pos / B, a.d_status);
+        if (id < 0) continue;
+        const uint4 c = __ldg(reinterpret_cast<const uint4 *>(a.c.code[kvi] + id * a.c.block_stride +
+                                                              (int64_t(h) * B + pos % B) * D + col));
+        const float scale = __ldg(a.c.scale[kvi] + id * a.c.scale_stride + h);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        float x[16];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const float2 f = e4m3x2_to_float2(uint16_t(w[k / 2] >> (16 * (k & 1))));
+            x[2 * k] = f.x * scale, x[2 * k + 1] = f.y * scale;
+        }
+        const int elt = DT == ZC_FP32 ? 4 : 2;
+        store16<DT>(static_cast<uint8_t *>(a.x[kvi].p) +
+                        ((int64_t(q.first) + int64_t(t)) * a.x[kvi].token + int64_t(h) * a.x[kvi].head + col) * elt, x);
+    }
+}
+
+} // namespace
+
+int launch_read(int dtype, const MoveArgs &a, cudaStream_t s) {
+    const uint64_t slots = slots_of(a.b.total, a.b.n_seqs, 1, kTokens, 1);
+    if (slots > 0x7FFFFFFFull) return ZC_EINVAL;
+    const dim3 grid(uint32_t(slots), a.c.heads, 2);
+    switch (dtype) {
+    case ZC_BF16: read_kernel<ZC_BF16><<<grid, kThreads, 0, s>>>(a); break;
+    case ZC_FP16: read_kernel<ZC_FP16><<<grid, kThreads, 0, s>>>(a); break;
+    default: read_kernel<ZC_FP32><<<grid, kThreads, 0, s>>>(a); break;
+    }
+    return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
+}
+
+} // namespace kv
+} // namespace zc

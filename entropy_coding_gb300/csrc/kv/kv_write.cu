@@ -1,0 +1,145 @@
+// kv_write.cu — new tokens quantised into the 8-bit cache.
+//
+// For each block that new tokens fall into, each head, and K and V apart:
+// with a = the largest finite |x| of the new rows, `need` is the least power
+// of two 2^e (e >= -126) with a <= 448 2^e. A block that held rows before
+// keeps the larger of its scale (rounded up to a power of two) and `need`;
+// when that grows, its old codes move to the new scale. New codes are
+// x / scale to the nearest E4M3 value. Scales are powers of two, so that
+// dividing by them is exact: the only rounding of a row is that to 4
+// significant bits, and moving old codes rounds again only those that leave
+// E4M3's normal range.
+//
+// One CTA does one block of one head: first the magnitudes, then the codes.
+#include "kv_common.cuh"
+
+namespace zc {
+namespace kv {
+namespace {
+
+constexpr int kThreads = 128;
+
+// Eight elements from 16-byte aligned memory.
+template <int DT> __device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
+    if (DT == ZC_FP32) {
+        const float4 a = __ldg(static_cast<const float4 *>(p)), b = __ldg(static_cast<const float4 *>(p) + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+        const uint4 v = __ldg(static_cast<const uint4 *>(p));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 f = unpack2<DT>(w[i]);
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// Exponent field of the least power of two s >= 2^-126 with a <= 448 s, for
+// the bits of a finite a >= 0: 448 = 1.75 2^8.
+__device__ __forceinline__ uint32_t need_exponent(uint32_t a) {
+    const int e = int(a >> 23) - 8 + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return uint32_t(max(e, 1));
+}
+// Exponent field of a scale rounded up to a power of two.
+__device__ __forceinline__ uint32_t ceil_exponent(float s) {
+    const uint32_t u = __float_as_uint(s) & 0x7FFFFFFFu;
+    return min(max((u >> 23) + ((u & 0x7FFFFFu) ? 1u : 0u), 1u), 254u);
+}
+__device__ __forceinline__ float two_to(int field) {  // 2^(field - 127), fields outside [1, 254] clamped
+    return __uint_as_float(uint32_t(min(max(field, 1), 254)) << 23);
+}
+
+template <int DT> __global__ void __launch_bounds__(kThreads) write_kernel(MoveArgs a) {
+    __shared__ uint32_t s_max;
+    uint64_t at;
+    const uint32_t s = find_seq(a.b, blockIdx.x, 1, a.c.tokens, 2, at);
+    const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, threadIdx.x == 0 && at == 0);
+    if (!q.ok || q.n == 0) return;
+    const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y, kvi = blockIdx.z;
+    if (uint32_t(q.len) < q.n) {  // more new tokens than the sequence has
+        if (threadIdx.x == 0 && at == 0) report(a.d_status, ZC_EFORMAT);
+        return;
+    }
+    const uint32_t start = uint32_t(q.len) - q.n;
+    const uint64_t blk = uint64_t(start / B) + at;
+    if (blk * B >= uint64_t(q.len)) return;
+    const uint32_t lo = max(start, uint32_t(blk) * B), hi = min(uint32_t(q.len), uint32_t(blk + 1) * B);
+    const uint32_t n0 = lo - uint32_t(blk) * B, rows = hi - lo;
+    const int64_t id = read_block(a.b, a.c, s, uint32_t(blk), a.d_status);
+    if (id < 0) return;
+
+    const int elt = DT == ZC_FP32 ? 4 : 2;
+    const uint8_t *x = static_cast<const uint8_t *>(a.x[kvi].p) +
+                       ((int64_t(q.first) + (lo - start)) * a.x[kvi].token + int64_t(h) * a.x[kvi].head) * elt;
+    uint8_t *codes = a.c.code[kvi] + id * a.c.block_stride + int64_t(h) * B * D;
+    float *scale = a.c.scale[kvi] + id * a.c.scale_stride + h;
+    const uint32_t per_row = D / 8, chunks = rows * per_row;
+
+    if (threadIdx.x == 0) s_max = 0;
+    __syncthreads();
+    uint32_t top = 0;  // bits of the largest finite magnitude
+    for (uint32_t i = threadIdx.x; i < chunks; i += kThreads) {
+        float v[8];
+        load8<DT>(x + (int64_t(i / per_row) * a.x[kvi].token + (i % per_row) * 8) * elt, v);
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const uint32_t u = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+            if (u < 0x7F800000u) top = max(top, u);
+        }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((threadIdx.x & 31) == 0) atomicMax(&s_max, top);
+    __syncthreads();
+
+    uint32_t field = need_exponent(s_max);
+    if (n0) {
+        const float old = *scale;
+        field = max(field, ceil_exponent(old));
+        const float now = two_to(int(field));
+        if (now != old) {
+            // 1 / now is exact: field <= 254 - 8 for a finite x, and a larger one only restates the old scale
+            const float ratio = old / now;
+            for (uint32_t i = threadIdx.x; i < n0 * per_row; i += kThreads) {
+                uint2 *p = reinterpret_cast<uint2 *>(codes) + i;
+                uint2 c = *p;
+                uint16_t w[4] = {uint16_t(c.x), uint16_t(c.x >> 16), uint16_t(c.y), uint16_t(c.y >> 16)};
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const float2 f = e4m3x2_to_float2(w[k]);
+                    w[k] = float2_to_e4m3x2(f.x * ratio, f.y * ratio);
+                }
+                *p = make_uint2(w[0] | uint32_t(w[1]) << 16, w[2] | uint32_t(w[3]) << 16);
+            }
+        }
+        __syncthreads();  // everyone has read the old scale
+    }
+    const float inv = 1.0f / two_to(int(field));
+    if (threadIdx.x == 0) *scale = two_to(int(field));
+    for (uint32_t i = threadIdx.x; i < chunks; i += kThreads) {
+        float v[8];
+        load8<DT>(x + (int64_t(i / per_row) * a.x[kvi].token + (i % per_row) * 8) * elt, v);
+        uint16_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[k] = float2_to_e4m3x2(v[2 * k] * inv, v[2 * k + 1] * inv);
+        reinterpret_cast<uint2 *>(codes + int64_t(n0) * D)[i] =
+            make_uint2(w[0] | uint32_t(w[1]) << 16, w[2] | uint32_t(w[3]) << 16);
+    }
+}
+
+} // namespace
+
+int launch_write(int dtype, const MoveArgs &a, cudaStream_t s) {
+    const uint64_t slots = slots_of(a.b.total, a.b.n_seqs, 1, a.c.tokens, 2);
+    if (slots > 0x7FFFFFFFull) return ZC_EINVAL;
+    const dim3 grid(uint32_t(slots), a.c.heads, 2);
+    switch (dtype) {
+    case ZC_BF16: write_kernel<ZC_BF16><<<grid, kThreads, 0, s>>>(a); break;
+    case ZC_FP16: write_kernel<ZC_FP16><<<grid, kThreads, 0, s>>>(a); break;
+    default: write_kernel<ZC_FP32><<<grid, kThreads, 0, s>>>(a); break;
+    }
+    return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
+}
+
+} // namespace kv
+} // namespace zc

@@ -1,0 +1,230 @@
+"""An 8-bit key/value cache: writing tokens, reading them back, and attention.
+
+The cache is a pool of blocks of tokens; each block and key/value head has
+E4M3 codes and one float32 scale, for K and for V. A batch names sequences of
+uneven length by a block table and their lengths, all on the device. The
+operators run in the CUDA kernels of ``libzc.so`` (include/zc.h, zc_kv_*),
+launch on the current stream (or ``stream``) and do not synchronise; errors
+that only the device can see are OR-ed into the cache's status, which
+``KVCache.check`` reads.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+__all__ = ["KVCache", "KVBatch", "kv_write", "kv_read", "kv_read_into", "kv_attend", "kv_attend_into"]
+
+_BF16, _FP16, _FP32 = 4, 5, 6
+_CODE = {torch.bfloat16: _BF16, torch.float16: _FP16, torch.float32: _FP32}
+_CAUSAL = 1
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p), ("d_k_scale", ctypes.c_void_p),
+                ("d_v_scale", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("n_blocks", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32), ("block_tokens", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("d_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("d_cu", ctypes.c_void_p),
+                ("d_lens", ctypes.c_void_p), ("n_seqs", ctypes.c_uint32), ("total_tokens", ctypes.c_uint32),
+                ("max_tokens", ctypes.c_uint32), ("table_width", ctypes.c_uint32)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("d_data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+def _fail(what: str):
+    from . import EINVAL, ZcError
+    raise ZcError(EINVAL, what)
+
+
+def _lib():
+    from . import lib
+    return lib()
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """Argument types of the zc_kv_* entry points."""
+    vp, u32, i32 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int
+    for f in (L.zc_kv_write, L.zc_kv_read):
+        f.restype = i32
+        f.argtypes = [vp, vp, i32, vp, vp, vp, vp]
+    L.zc_kv_attend.restype = i32
+    L.zc_kv_attend.argtypes = [vp, vp, i32, u32, vp, vp, vp, ctypes.c_double, u32, u32, vp, vp]
+
+
+class KVCache:
+    """A pool of cache blocks, over tensors that the caller owns.
+
+    ``k``, ``v``: float8_e4m3fn (or uint8) CUDA tensors [n_blocks, kv_heads,
+    block_tokens, head_dim], contiguous within a block; ``k_scale``,
+    ``v_scale``: float32 [n_blocks, kv_heads]. Slices of a larger pool along
+    the block dimension (one layer of several) are fine as long as K and V
+    have the same strides. ``KVCache.empty`` allocates one."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
+            _fail("KVCache: k and v are [n_blocks, kv_heads, block_tokens, head_dim] with the same strides")
+        n, h, b, d = k.shape
+        if any(t.dtype not in (torch.float8_e4m3fn, torch.uint8) for t in (k, v)):
+            _fail("KVCache: codes are float8_e4m3fn or uint8")
+        if k.stride()[1:] != (b * d, d, 1):
+            _fail("KVCache: a block's codes are contiguous")
+        for t in (k_scale, v_scale):
+            if t.shape != (n, h) or t.dtype != torch.float32 or t.stride(1) != 1:
+                _fail("KVCache: scales are float32 [n_blocks, kv_heads]")
+        if k_scale.stride() != v_scale.stride():
+            _fail("KVCache: k_scale and v_scale have the same strides")
+        if not all(t.is_cuda and t.device == k.device for t in (k, v, k_scale, v_scale)):
+            _fail("KVCache expects CUDA tensors of one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_blocks, self.kv_heads, self.block_tokens, self.head_dim = n, h, b, d
+        self.device = k.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                         max(k.stride(0), h * b * d), max(k_scale.stride(0), h), n, h, b, d)
+        self._ref = ctypes.addressof(self._c)
+        self._status = self.status.data_ptr()
+
+    @classmethod
+    def empty(cls, n_blocks: int, kv_heads: int, head_dim: int, block_tokens: int = 64, device="cuda") -> "KVCache":
+        """A cache of zeros."""
+        shape = (n_blocks, kv_heads, block_tokens, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+    def check(self) -> None:
+        """Raise ZcError if a call on this cache reported an error (and forget
+        it); synchronises."""
+        from . import ZcError
+        st = int(self.status.item())
+        if st:
+            self.status.zero_()
+            raise ZcError(st, "zc_kv (device)")
+
+
+class KVBatch:
+    """The sequences of a call: their block table, their new tokens and their
+    lengths with them, made once for all layers of a step.
+
+    ``block_table`` int32 [n_seqs, width]; ``cu_tokens`` int32 [n_seqs + 1]:
+    sequence s has the rows cu[s] .. cu[s + 1] of a call's tensors; ``lens``
+    int32 [n_seqs]: tokens of each sequence, those rows being its last.
+    ``total_tokens`` and ``max_tokens`` (of one sequence) are the host's
+    numbers. The tensors may change between calls (a captured graph is
+    replayed with new lengths) as long as the totals hold."""
+
+    def __init__(self, block_table: torch.Tensor, cu_tokens: torch.Tensor, lens: torch.Tensor, total_tokens: int,
+                 max_tokens: int):
+        n = lens.numel()
+        if any(t.dtype != torch.int32 or not t.is_cuda for t in (block_table, cu_tokens, lens)):
+            _fail("KVBatch expects int32 CUDA tensors")
+        if block_table.dim() != 2 or block_table.shape[0] != n or cu_tokens.shape != (n + 1,) or lens.dim() != 1:
+            _fail("KVBatch: block_table is [n_seqs, width], cu_tokens [n_seqs + 1], lens [n_seqs]")
+        if (n and block_table.stride(1) != 1) or not cu_tokens.is_contiguous() or not lens.is_contiguous():
+            _fail("KVBatch: rows of the table, cu_tokens and lens are contiguous")
+        if not (0 <= max_tokens <= total_tokens <= max_tokens * n) or total_tokens > 0x7FFFFFFF:
+            _fail("KVBatch: max_tokens <= total_tokens <= max_tokens * n_seqs")
+        self.block_table, self.cu_tokens, self.lens = block_table, cu_tokens, lens
+        self.n_seqs, self.total_tokens, self.max_tokens = n, total_tokens, max_tokens
+        self._c = _Batch(block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]) if n else 0,
+                         cu_tokens.data_ptr(), lens.data_ptr(), n, total_tokens, max_tokens, block_table.shape[1])
+        self._ref = ctypes.addressof(self._c)
+
+
+def _rows(t: torch.Tensor, shape, device, what: str) -> _Rows:
+    if t.shape != shape or t.stride(2) != 1 or t.device != device:
+        _fail(f"{what} is a tensor {tuple(shape)} on the cache's device, contiguous in its last dimension")
+    return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _stream(stream, device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream, device):
+    """Outputs of a call belong to the stream that it runs on."""
+    if stream is None:
+        return torch.cuda.device(device)
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(s)
+
+
+def _check(st: int, what: str) -> None:
+    if st:
+        from . import ZcError
+        raise ZcError(st, what)
+
+
+def _move(fn, what, cache, batch, k, v, stream):
+    if k.dtype not in _CODE or v.dtype != k.dtype:
+        _fail(f"{what}: k and v are bfloat16, float16 or float32")
+    shape = (batch.total_tokens, cache.kv_heads, cache.head_dim)
+    rk, rv = _rows(k, shape, cache.device, "k"), _rows(v, shape, cache.device, "v")
+    _check(fn(cache._ref, batch._ref, _CODE[k.dtype], ctypes.byref(rk), ctypes.byref(rv), cache._status,
+              _stream(stream, cache.device)), what)
+
+
+def kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """Quantise the batch's tokens into the cache (zc_kv_write). ``k``, ``v``:
+    [total_tokens, kv_heads, head_dim] in bfloat16, float16 or float32, any
+    strides that are multiples of 16 bytes (views of a fused projection)."""
+    _move(_lib().zc_kv_write, "zc_kv_write", cache, batch, k, v, stream)
+
+
+def kv_read_into(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """Read the batch's tokens back into ``k`` and ``v`` (zc_kv_read)."""
+    _move(_lib().zc_kv_read, "zc_kv_read", cache, batch, k, v, stream)
+
+
+def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16, stream=None):
+    """The batch's tokens as (k, v), [total_tokens, kv_heads, head_dim]."""
+    shape = (batch.total_tokens, cache.kv_heads, cache.head_dim)
+    with _on(stream, cache.device):
+        k, v = (torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    kv_read_into(cache, batch, k, v, stream)
+    return k, v
+
+
+def kv_attend_into(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None = None,
+                   scale: float | None = None, causal: bool = True, window: int = 0, stream=None) -> None:
+    """Attention of the batch's tokens over the cache (zc_kv_attend) into
+    ``out`` and, if given, ``lse`` (float32 [total_tokens, heads])."""
+    if q.dtype not in (torch.bfloat16, torch.float16) or out.dtype != q.dtype:
+        _fail("zc_kv_attend: q and out are bfloat16 or float16")
+    heads = q.shape[1] if q.dim() == 3 else 0
+    shape = (batch.total_tokens, heads, cache.head_dim)
+    rq, ro = _rows(q, shape, cache.device, "q"), _rows(out, shape, cache.device, "out")
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            lse.device != cache.device):
+        _fail("zc_kv_attend: lse is float32 [total_tokens, heads]")
+    if window < 0 or window > 0x7FFFFFFF:
+        _fail("zc_kv_attend: window >= 0")
+    _check(_lib().zc_kv_attend(cache._ref, batch._ref, _CODE[q.dtype], heads, ctypes.byref(rq), ctypes.byref(ro),
+                               lse.data_ptr() if lse is not None else None,
+                               cache.head_dim ** -0.5 if scale is None else scale, _CAUSAL if causal else 0, window,
+                               cache._status, _stream(stream, cache.device)), "zc_kv_attend")
+
+
+def kv_attend(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | None = None, causal: bool = True,
+              window: int = 0, stream=None):
+    """Attention of the batch's tokens over the cache: (out, lse).
+
+    ``q`` [total_tokens, heads, head_dim], bfloat16 or float16; heads is a
+    multiple of the cache's. A query at position p sees the positions j < lens
+    with j <= p (``causal``) and j > p - window (``window`` > 0). ``scale``
+    defaults to head_dim ** -0.5. The tokens' own keys and values are in the
+    cache already (kv_write first)."""
+    with _on(stream, cache.device):
+        out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device)
+    kv_attend_into(cache, batch, q, out, lse, scale, causal, window, stream)
+    return out, lse

@@ -360,6 +360,100 @@ ZC_API int zc_compress_noalloc(const void *d_src, uint64_t nbytes, int dtype, in
                                void *d_blob, uint64_t blob_capacity, uint64_t *d_blob_bytes,
                                int32_t *d_status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * An 8-bit key/value cache (none of the source pages has a counterpart): the
+ * other large tensor of a model in service next to its weights. It is
+ * quantised as tokens are written, read back as numbers, and attended to as
+ * it is. Its blocks are bytes (ZC_U8), so blocks that leave the device can go
+ * through zc_compress.
+ *
+ * The cache is a pool of blocks of block_tokens tokens. For each block and
+ * key/value head it has block_tokens x head_dim E4M3 codes and one float32
+ * scale, for K and for V apart; a number is value(code) * scale. Scales are
+ * positive and finite; zc_kv_write makes them powers of two.
+ *   d_k, d_v        codes [n_blocks][kv_heads][block_tokens][head_dim], blocks
+ *                   block_stride bytes apart (a multiple of 16, at least
+ *                   kv_heads * block_tokens * head_dim), 16-byte aligned
+ *   d_k_scale, ...  floats [n_blocks][kv_heads], blocks scale_stride floats
+ *                   apart
+ *   kv_heads        1 to 65535
+ *   block_tokens    a multiple of 16 up to 256
+ *   head_dim        a multiple of 16 up to 128 */
+typedef struct {
+    void *d_k, *d_v;
+    float *d_k_scale, *d_v_scale;
+    int64_t block_stride, scale_stride;
+    uint32_t n_blocks, kv_heads, block_tokens, head_dim;
+} zc_kv_cache;
+
+/* Sequences of uneven length, with lengths and tables on the device. Token i
+ * of sequence s, of n = cu[s + 1] - cu[s], is row cu[s] + i of the call's
+ * tensors, and its position in the sequence is lens[s] - n + i: a batch is the
+ * last n tokens of each sequence, with lens counting them.
+ *   d_table       int32 [n_seqs][table_width], rows table_stride apart: block
+ *                 p / block_tokens of sequence s holds its position p
+ *   d_cu          int32 [n_seqs + 1], from 0, not falling
+ *   d_lens        int32 [n_seqs], at most table_width * block_tokens
+ *   total_tokens  cu[n_seqs], as the host knows it
+ *   max_tokens    at least the largest n, at most total_tokens
+ * A call skips a sequence whose entries are out of these ranges (ZC_EFORMAT;
+ * a length beyond the table: ZC_ECAPACITY), and takes a table entry that
+ * names no block as a block that is not there (ZC_EFORMAT): it is not read or
+ * written, and outputs that need it are unspecified. */
+typedef struct {
+    const int32_t *d_table;
+    int64_t table_stride;
+    const int32_t *d_cu, *d_lens;
+    uint32_t n_seqs, total_tokens, max_tokens, table_width;
+} zc_kv_batch;
+
+/* A tensor [tokens][heads][head_dim] with strides in elements; head_dim is
+ * contiguous. The address and the strides are multiples of 16 bytes. */
+typedef struct {
+    void *d_data;
+    int64_t token_stride, head_stride;
+} zc_kv_rows;
+
+/* Quantise the batch's tokens into the cache.
+ *   dtype   ZC_BF16, ZC_FP16 or ZC_FP32: the type of k and v
+ *   k, v    [total_tokens][kv_heads][head_dim]
+ * For each block that new tokens fall into, each head, K and V apart: let a
+ * be the largest finite magnitude of its new rows and need the least power of
+ * two 2^e, e >= -126, with a <= 448 * 2^e. The block's scale becomes need or,
+ * where the block has rows of earlier positions, the larger of need and its
+ * scale (rounded up to a power of two); when that changes, those rows' codes
+ * move to the new scale (rounded to nearest even). New codes are x / scale,
+ * to nearest even; infinities become +-448, NaN stays NaN. Rows of the block
+ * past the sequence's end keep no meaning. No two sequences of a call may
+ * write to one block. Writing the same tokens again changes nothing. */
+ZC_API int zc_kv_write(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, const zc_kv_rows *k,
+                       const zc_kv_rows *v, int32_t *d_status, void *stream);
+
+/* Read the batch's tokens back into k and v ([total_tokens][kv_heads]
+ * [head_dim] of dtype ZC_BF16, ZC_FP16 or ZC_FP32): value(code) * scale,
+ * rounded once. */
+ZC_API int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, const zc_kv_rows *k,
+                      const zc_kv_rows *v, int32_t *d_status, void *stream);
+
+/* Attention of the batch's tokens over the cache:
+ *   s_ij = scale * q_i . k_j,  p_ij = exp(s_ij) / sum_j exp(s_ij),
+ *   out_i = sum_j p_ij v_j,  lse_i = log sum_j exp(s_ij)
+ * over the positions j < lens[s] that a query at position p sees: j <= p with
+ * ZC_KV_CAUSAL, and j > p - window with window > 0. Query head h reads
+ * key/value head h / (heads / kv_heads). A row that sees nothing (or only
+ * scores of -infinity) is 0 with lse = -infinity; keys that a row does not
+ * see have no influence on it, whatever they hold.
+ *   dtype   ZC_BF16 or ZC_FP16: the type of q and out
+ *   heads   query heads, a multiple of kv_heads
+ *   q, out  [total_tokens][heads][head_dim]
+ *   d_lse   NULL or float [total_tokens][heads]
+ * Scores, weights' sums and outputs are accumulated in float32; weights are
+ * rounded to half, in units of the row's largest contribution. */
+#define ZC_KV_CAUSAL 1u
+ZC_API int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
+                        const zc_kv_rows *q, const zc_kv_rows *out, float *d_lse, double scale, uint32_t flags,
+                        uint32_t window, int32_t *d_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
