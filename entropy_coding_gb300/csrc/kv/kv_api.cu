@@ -1,13 +1,33 @@
 // kv_api.cu — the C ABI of the 8-bit key/value cache operators: argument
 // checks and launches. As in zc_api.cu, no entry point allocates or
 // synchronises; what only the device can see is reported through *d_status.
+#include <atomic>
 #include <cmath>
 
 #include "kv_common.cuh"
 
+namespace zc {
+namespace kv {
+
+// Streaming multiprocessors of the current device (asked for once).
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 1;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
+
+} // namespace kv
+} // namespace zc
+
 namespace {
 
 using namespace zc::kv;
+
+uint64_t pad256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -97,9 +117,17 @@ extern "C" int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, in
     return move(false, cache, batch, dtype, k, v, d_status, stream);
 }
 
+extern "C" uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads) {
+    Cache c{};
+    Batch b{};
+    if (make_cache(cache, c) != ZC_OK || make_batch(batch, b) != ZC_OK) return 0;
+    if (heads == 0 || heads % c.heads || heads > 65535) return 0;
+    return pad256(4 * rows_counters(b, c, heads / c.heads)) + pad256(rows_part_bytes(c.dim));
+}
+
 extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
                             const zc_kv_rows *q, const zc_kv_rows *out, float *d_lse, double scale, uint32_t flags,
-                            uint32_t window, int32_t *d_status, void *stream) {
+                            uint32_t window, void *d_ws, uint64_t ws_bytes, int32_t *d_status, void *stream) {
     AttendArgs a{};
     if ((dtype != ZC_BF16 && dtype != ZC_FP16) || !q || !out || !d_status || !aligned(d_status, 4)) return ZC_EINVAL;
     if ((flags & ~ZC_KV_CAUSAL) || !std::isfinite(scale) || std::fabs(scale) > 1e18 || !aligned(d_lse, 4)) return ZC_EINVAL;
@@ -112,6 +140,11 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
     a.lse = d_lse;
     a.heads = heads;
     a.group = heads / a.c.heads;
+    const uint64_t counters = pad256(4 * rows_counters(a.b, a.c, a.group));
+    if (!d_ws || !aligned(d_ws, 16)) return ZC_EINVAL;
+    if (ws_bytes < counters + rows_part_bytes(a.c.dim)) return ZC_ECAPACITY;
+    a.counters = static_cast<uint32_t *>(d_ws);
+    a.parts = static_cast<uint8_t *>(d_ws) + counters;
     a.scale_log2 = float(scale * 1.4426950408889634);
     a.causal = flags & ZC_KV_CAUSAL;
     a.window = window;

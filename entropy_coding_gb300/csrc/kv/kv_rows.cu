@@ -6,7 +6,17 @@
 //   s_ij = scale * ks_b(j) * (q_i . kc_j)
 //   out_i = sum_j 2^(s_ij log2e - m) vs_b(j) vc_j / sum_j 2^(s_ij log2e - m)
 //
-// A CTA takes 16 rows, a warp 16 keys at a time, and both products run on
+// An item is 16 rows of one sequence and key/value head. Decoding has few
+// items and long key axes, so items are cut along the keys: the batch's work
+// is one line of 64-key units, items one after another, and each CTA of a
+// resident grid takes an equal piece of it (a few whole items and a part of
+// one at either end, whatever the sequences' lengths). An item that lies in
+// several CTAs leaves one partial result for each in the workspace, and the
+// CTA that comes last, by the item's counter, joins them in the order of the
+// keys: no second launch, and the same bits whichever CTA is last. The counter
+// is left at zero for the next call.
+//
+// A CTA has 4 warps; a warp takes 16 keys at a time, and both products run on
 // mma.m16n8k16 with half operands and float accumulators. E4M3 codes are
 // exact in half. A query row is exact in half too after it is multiplied by a
 // power of two that brings its largest element to [2^14, 2^15) (what falls
@@ -18,11 +28,13 @@
 // of s.
 //
 // Each warp streams its own keys and values through shared memory with
-// cp.async, kStages slices of 16 rows deep, and the warps meet only at the
-// end. Rows are padded by 16 bytes, which spreads a fragment's reads over the
+// cp.async, kStages slices of 16 rows deep, and the warps meet only at an
+// item's end. Rows are padded by 16 bytes, which spreads a fragment's reads over the
 // banks. Within a row the columns are dealt to the threads of a quad in runs
 // (the order of a product's inner index is free as long as both operands
 // share it), so that fragments are read 16 bytes at a time.
+#include <atomic>
+
 #include "kv_common.cuh"
 
 namespace zc {
@@ -30,7 +42,9 @@ namespace kv {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 4;
-constexpr int kRows = 16, kSlice = 16;  // rows of a CTA; keys of a warp's step
+constexpr int kRows = 16, kSlice = 16;  // rows of an item; keys of a warp's step
+constexpr int kUnit = kWarps * kSlice;  // keys of a unit of work
+constexpr int kResident = 3;            // CTAs of an SM
 constexpr float kNone = -INFINITY;
 
 template <int DP> struct Stage {
@@ -42,6 +56,12 @@ template <int DP> struct Stage {
 template <int DP> struct Merge {  // over the stages, once the loop is done
     float o[kWarps][kRows][DP + 4];
     float m[kWarps][kRows], mw[kWarps][kRows], l[kWarps][kRows];
+};
+
+// A part of an item: rows in units of 2^mw (o) and 2^m (l).
+template <int DP> struct Part {
+    float o[kRows][DP];
+    float m[kRows], mw[kRows], l[kRows];
 };
 
 template <int DP> constexpr size_t smem_bytes() {
@@ -78,21 +98,68 @@ __device__ __forceinline__ float ratio2(float a, float b) { return a == kNone ? 
 // Whether one of the four codes is NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool any_nan(uint32_t v) { return __vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0; }
 
-template <int DT, int DP> __global__ void __launch_bounds__(kThreads, 3) rows_kernel(AttendArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
+// Units of work of a sequence's items (the same for all of them).
+__device__ __forceinline__ uint32_t first_unit(const AttendArgs &a, const Seq &q) {
+    const int64_t lo = a.window ? int64_t(q.len) - int64_t(q.n) - int64_t(a.window) + 1 : 0;
+    return uint32_t(max(lo, int64_t(0)) / kUnit);
+}
+__device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &q) {
+    return max((uint32_t(q.len) + kUnit - 1) / kUnit, first_unit(a, q) + 1) - first_unit(a, q);
+}
+__device__ __forceinline__ uint64_t tiles_of(const AttendArgs &a, const Seq &q) {
+    return (uint64_t(q.n) * a.group + kRows - 1) / kRows;
+}
+__device__ __forceinline__ uint64_t work_of(const AttendArgs &a, const Seq &q) {
+    return q.ok ? tiles_of(a, q) * a.c.heads * units_of(a, q) : 0;
+}
+
+// Inclusive sum of the threads before and including this one; `total`: of all.
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t *s_warp, uint64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) v += s_warp[w];
+        total += s_warp[w];
+    }
+    return v;
+}
+
+// The finished row: 8 columns from `col` on, in units (M, W, L).
+template <int DT>
+__device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32_t h, uint64_t row, int col, const float *x,
+                                     int n, float M, float W, float L) {
+    // out = x / L in the units of M; a row that sees no key is 0. (L is NaN where a score was.)
+    const float by = L == 0.0f ? 0.0f : (W == kNone ? 0.0f : ex2(W - M)) / L;
+    const int64_t token = int64_t(seq.first) + int64_t(row / a.group), head = int64_t(h) * a.group + int64_t(row % a.group);
+    uint16_t *o = static_cast<uint16_t *>(a.out.p) + token * a.out.token + head * a.out.head + col;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < n / 2; k++) w[k] = L == 0.0f ? 0u : pack2<DT>(x[2 * k] * by, x[2 * k + 1] * by);
+    if (n == 8) *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    if (a.lse && col == 0) a.lse[token * a.heads + head] = L == 0.0f ? kNone : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// The piece [unit0, unit0 + units) of item (seq, tile, h); part: where its
+// partial result goes, or null if the piece is the whole item.
+template <int DT, int DP>
+__device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
+                                      uint32_t unit0, uint32_t units, Part<DP> *part) {
     constexpr int kSteps = DP / 16;      // inner steps of q k
     constexpr int kTiles = DP / 8;       // column tiles of the output
     constexpr int kRun = DP / 4;         // columns of q and k that a thread of a quad holds
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const uint32_t h = blockIdx.y, D = a.c.dim, B = a.c.tokens;
-
-    uint64_t tile;
-    const uint32_t s = find_seq(a.b, blockIdx.x, a.group, kRows, 1, tile);
-    const bool speak = threadIdx.x == 0 && tile == 0 && h == 0;
-    const Seq seq = read_seq(a.b, s, a.d_status, B, speak);
-    if (!seq.ok) return;
+    const uint32_t D = a.c.dim, B = a.c.tokens, s = seq.s;
     const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
-    if (row0 >= n_rows) return;
 
     // The keys that each of the thread's two rows sees: [lo, hi).
     const int64_t pos0 = int64_t(seq.len) - int64_t(seq.n);  // position of the sequence's first new token
@@ -155,7 +222,10 @@ template <int DT, int DP> __global__ void __launch_bounds__(kThreads, 3) rows_ke
     }
 
     Stage<DP> *stages = reinterpret_cast<Stage<DP> *>(smem) + warp * kStages;
-    const int first = all_lo / kSlice + warp, end = (all_hi + kSlice - 1) / kSlice;  // slices of this warp: first, + kWarps, ...
+    // Slices of this warp: first, first + kWarps, ... below end.
+    const int end = min((all_hi + kSlice - 1) / kSlice, int((unit0 + units) * kWarps));
+    int first = int(unit0) * kWarps + warp;
+    if (first < all_lo / kSlice) first += (all_lo / kSlice - first + kWarps - 1) / kWarps * kWarps;
 
     // Fetches slice i into stage st; rows outside the keys that someone sees, and
     // columns from D on, are zeros.
@@ -316,8 +386,7 @@ template <int DT, int DP> __global__ void __launch_bounds__(kThreads, 3) rows_ke
     __syncthreads();
     for (int i = threadIdx.x; i < kRows * DP / 8; i += kThreads) {
         const int r = i / (DP / 8), col = i % (DP / 8) * 8;
-        const uint64_t row = row0 + r;
-        if (row >= n_rows || col >= int(D)) continue;
+        if (row0 + r >= n_rows || col >= int(D)) continue;
         float M = kNone, W = kNone, L = 0.0f, x[8] = {};
 #pragma unroll
         for (int w = 0; w < kWarps; w++) M = fmaxf(M, mg.m[w][r]), W = fmaxf(W, mg.mw[w][r]);
@@ -328,29 +397,167 @@ template <int DT, int DP> __global__ void __launch_bounds__(kThreads, 3) rows_ke
 #pragma unroll
             for (int k = 0; k < 8; k++) x[k] += mg.o[w][r][col + k] * f;
         }
-        // out = sum / L in the units of M; a row that sees no key is 0. (L is NaN where a score was.)
-        const float by = L == 0.0f ? 0.0f : (W == kNone ? 0.0f : ex2(W - M)) / L;
-        uint32_t w[4];
+        if (part) {
+            float4 *p = reinterpret_cast<float4 *>(&part->o[r][col]);
+            __stcg(p, make_float4(x[0], x[1], x[2], x[3]));
+            __stcg(p + 1, make_float4(x[4], x[5], x[6], x[7]));
+            if (col == 0) __stcg(&part->m[r], M), __stcg(&part->mw[r], W), __stcg(&part->l[r], L);
+        } else {
+            emit<DT>(a, seq, h, row0 + r, col, x, 8, M, W, L);
+        }
+    }
+}
+
+// An item's parts together: the `first` one in its CTA's second slot (a piece
+// that begins an item), the others in the first slots of the CTAs after it.
+template <int DT, int DP>
+__device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
+                                     const Part<DP> *parts, uint32_t first, uint32_t n) {
+    constexpr int kBatch = 128;  // parts whose factors are in shared memory at a time
+    float (*fo)[kRows] = reinterpret_cast<float (*)[kRows]>(smem);
+    float *sM = reinterpret_cast<float *>(fo + kBatch), *sW = sM + kRows, *sL = sW + kRows;
+    const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
+    const int rows = int(min(uint64_t(kRows), n_rows - row0)), D = int(a.c.dim);
+    auto part = [&](uint32_t i) -> const Part<DP> & { return parts[2 * (first + i) + (i ? 0 : 1)]; };
+    // each row's units, by 8 threads
+    {
+        const int r = threadIdx.x / 8, k = threadIdx.x % 8;
+        float M = kNone, W = kNone, L = 0.0f;
+        if (r < rows)
+            for (uint32_t i = k; i < n; i += 8) M = fmaxf(M, __ldcg(&part(i).m[r])), W = fmaxf(W, __ldcg(&part(i).mw[r]));
 #pragma unroll
-        for (int k = 0; k < 4; k++) w[k] = L == 0.0f ? 0u : pack2<DT>(x[2 * k] * by, x[2 * k + 1] * by);
-        const int64_t token = int64_t(seq.first) + int64_t(row / a.group), head = int64_t(h) * a.group + int64_t(row % a.group);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out.p) + token * a.out.token + head * a.out.head + col) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-        if (a.lse && col == 0)
-            a.lse[token * a.heads + head] = L == 0.0f ? kNone : (M + log2f(L)) * 0.6931471805599453f;
+        for (int d = 1; d < 8; d *= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d)), W = fmaxf(W, __shfl_xor_sync(0xFFFFFFFFu, W, d));
+        if (r < rows)
+            for (uint32_t i = k; i < n; i += 8) L += __ldcg(&part(i).l[r]) * ratio2(__ldcg(&part(i).m[r]), M);
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+        if (k == 0) sM[r] = M, sW[r] = W, sL[r] = L;
+    }
+    __syncthreads();
+    // 4 columns of a row a thread
+    constexpr int kCols = DP / 4, kMost = kRows * kCols / kThreads;
+    float4 x[kMost];
+#pragma unroll
+    for (int j = 0; j < kMost; j++) x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (uint32_t i0 = 0; i0 < n; i0 += kBatch) {
+        const uint32_t m = min(uint32_t(kBatch), n - i0);
+        for (uint32_t i = threadIdx.x; i < m * kRows; i += kThreads)
+            if (int(i % kRows) < rows) fo[i / kRows][i % kRows] = ratio2(__ldcg(&part(i0 + i / kRows).mw[i % kRows]), sW[i % kRows]);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kMost; j++) {
+            const int r = (j * kThreads + threadIdx.x) / kCols, col = (j * kThreads + threadIdx.x) % kCols * 4;
+            if (r >= rows || col >= D) continue;
+#pragma unroll 8
+            for (uint32_t i = 0; i < m; i++) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(&part(i0 + i).o[r][col]));
+                const float f = fo[i][r];
+                x[j].x += v.x * f, x[j].y += v.y * f, x[j].z += v.z * f, x[j].w += v.w * f;
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kMost; j++) {
+        const int r = (j * kThreads + threadIdx.x) / kCols, col = (j * kThreads + threadIdx.x) % kCols * 4;
+        if (r >= rows || col >= D) continue;
+        const float y[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        emit<DT>(a, seq, h, row0 + r, col, y, 4, sM[r], sW[r], sL[r]);
+    }
+}
+
+template <int DT, int DP> __global__ void __launch_bounds__(kThreads, kResident) rows_kernel(AttendArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint64_t s_warp[kWarps], s_at;
+    __shared__ uint32_t s_seq;
+    __shared__ int s_last;
+    Part<DP> *parts = reinterpret_cast<Part<DP> *>(a.parts);
+    const uint32_t B = a.c.tokens, cta = blockIdx.x;
+
+    // The line of work, and this CTA's piece [w0, w1) of it.
+    uint64_t sum = 0, W;
+    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += kThreads) sum += work_of(a, read_seq(a.b, s, a.d_status, B, cta == 0));
+    block_scan(sum, s_warp, W);
+    const uint64_t G = min(uint64_t(gridDim.x), W);  // no CTA between two that have work is without
+    if (cta >= G) return;
+    const uint64_t w0 = W * cta / G, w1 = W * (cta + 1) / G;
+    uint64_t before = 0;
+    for (uint32_t s0 = 0; s0 < a.b.n_seqs; s0 += kThreads) {
+        const uint32_t s = s0 + threadIdx.x;
+        const uint64_t mine = s < a.b.n_seqs ? work_of(a, read_seq(a.b, s, a.d_status, B, false)) : 0;
+        uint64_t all;
+        const uint64_t upto = before + block_scan(mine, s_warp, all);
+        if (mine && upto > w0 && upto - mine <= w0) s_seq = s, s_at = upto - mine;
+        before += all;
+        if (before > w0) break;
+    }
+    __syncthreads();
+    uint32_t s = s_seq;
+    uint64_t at = s_at;  // where the sequence's work begins
+
+    uint64_t w = w0;
+    while (w < w1) {
+        const Seq seq = read_seq(a.b, s, a.d_status, B, false);
+        const uint64_t work = work_of(a, seq);
+        if (w >= at + work) {
+            at += work;
+            s++;
+            continue;
+        }
+        const uint32_t units = units_of(a, seq);
+        const uint64_t item = (w - at) / units, i0 = at + item * units, i1 = i0 + units;
+        const uint64_t upto = min(w1, i1);
+        const uint64_t tile = item / a.c.heads;
+        const uint32_t h = uint32_t(item % a.c.heads);
+        const bool whole = w == i0 && upto == i1;
+        piece<DT, DP>(a, smem, seq, tile, h, first_unit(a, seq) + uint32_t(w - i0), uint32_t(upto - w),
+                      whole ? nullptr : parts + 2 * cta + (w == i0 ? 1 : 0));
+        if (!whole) {
+            // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
+            // W c / G <= u < W (c + 1) / G, rounded down, so c = (u G + G - 1) / W
+            const uint32_t c0 = uint32_t((i0 * G + G - 1) / W), c1 = uint32_t(((i1 - 1) * G + G - 1) / W);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                uint32_t *counter = a.counters + (slot_of(seq.first, s, a.group, kRows, 1) + tile) * a.c.heads + h;
+                const bool last = atomicAdd(counter, 1u) == c1 - c0;
+                if (last) *counter = 0;
+                s_last = last;
+                __threadfence();
+            }
+            __syncthreads();
+            if (s_last) join<DT, DP>(a, smem, seq, tile, h, parts, c0, c1 - c0 + 1);
+        }
+        __syncthreads();  // shared memory is free for the next piece
+        w = upto;
     }
 }
 
 template <int DT, int DP> int launch(const AttendArgs &a, cudaStream_t s) {
-    const uint64_t slots = slots_of(a.b.total, a.b.n_seqs, a.group, kRows, 1);
-    if (slots > 0x7FFFFFFFull) return ZC_EINVAL;
-    if (cudaFuncSetAttribute(rows_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<DP>())) != cudaSuccess)
-        return ZC_ECUDA;
-    rows_kernel<DT, DP><<<dim3(uint32_t(slots), a.c.heads), kThreads, smem_bytes<DP>(), s>>>(a);
+    static std::atomic<uint64_t> ready{0};  // devices whose kernel may use this much shared memory
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(rows_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<DP>())) != cudaSuccess)
+            return ZC_ECUDA;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    rows_kernel<DT, DP><<<rows_ctas(), kThreads, smem_bytes<DP>(), s>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }
 
 } // namespace
+
+uint32_t rows_ctas() { return uint32_t(sm_count()) * kResident; }
+
+uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group) {
+    return slots_of(b.total, b.n_seqs, group, kRows, 1) * c.heads;
+}
+
+uint64_t rows_part_bytes(uint32_t dim) {
+    return uint64_t(rows_ctas()) * 2 * (dim <= 64 ? sizeof(Part<64>) : sizeof(Part<128>));
+}
 
 int launch_attend(int dtype, const AttendArgs &a, cudaStream_t s) {
     if (dtype == ZC_BF16) return a.c.dim <= 64 ? launch<ZC_BF16, 64>(a, s) : launch<ZC_BF16, 128>(a, s);

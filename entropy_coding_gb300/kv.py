@@ -38,24 +38,35 @@ class _Rows(ctypes.Structure):
     _fields_ = [("d_data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+_entry = None  # (zc_kv_write, zc_kv_read, zc_kv_attend) once the library is loaded
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _fail(what: str):
     from . import EINVAL, ZcError
     raise ZcError(EINVAL, what)
 
 
-def _lib():
-    from . import lib
-    return lib()
-
-
 def declare(L: ctypes.CDLL) -> None:
     """Argument types of the zc_kv_* entry points."""
-    vp, u32, i32 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int
+    vp, u32, u64, i32 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int
     for f in (L.zc_kv_write, L.zc_kv_read):
         f.restype = i32
         f.argtypes = [vp, vp, i32, vp, vp, vp, vp]
     L.zc_kv_attend.restype = i32
-    L.zc_kv_attend.argtypes = [vp, vp, i32, u32, vp, vp, vp, ctypes.c_double, u32, u32, vp, vp]
+    L.zc_kv_attend.argtypes = [vp, vp, i32, u32, vp, vp, vp, ctypes.c_double, u32, u32, vp, u64, vp, vp]
+    L.zc_kv_attend_workspace_size.restype = u64
+    L.zc_kv_attend_workspace_size.argtypes = [vp, vp, u32]
+
+
+def _entries():
+    """The entry points, kept: a decoding step calls them for every layer."""
+    global _entry
+    if _entry is None:
+        from . import lib
+        L = lib()
+        _entry = (L.zc_kv_write, L.zc_kv_read, L.zc_kv_attend)
+    return _entry
 
 
 class KVCache:
@@ -84,7 +95,7 @@ class KVCache:
             _fail("KVCache expects CUDA tensors of one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_blocks, self.kv_heads, self.block_tokens, self.head_dim = n, h, b, d
-        self.device = k.device
+        self.device, self._index = k.device, k.device.index
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                          max(k.stride(0), h * b * d), max(k_scale.stride(0), h), n, h, b, d)
@@ -118,7 +129,8 @@ class KVBatch:
     int32 [n_seqs]: tokens of each sequence, those rows being its last.
     ``total_tokens`` and ``max_tokens`` (of one sequence) are the host's
     numbers. The tensors may change between calls (a captured graph is
-    replayed with new lengths) as long as the totals hold."""
+    replayed with new lengths) as long as the totals hold. The batch keeps
+    attention's workspace: calls that may overlap use batches of their own."""
 
     def __init__(self, block_table: torch.Tensor, cu_tokens: torch.Tensor, lens: torch.Tensor, total_tokens: int,
                  max_tokens: int):
@@ -136,22 +148,39 @@ class KVBatch:
         self._c = _Batch(block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]) if n else 0,
                          cu_tokens.data_ptr(), lens.data_ptr(), n, total_tokens, max_tokens, block_table.shape[1])
         self._ref = ctypes.addressof(self._c)
+        self._ws: dict = {}
+
+    def workspace(self, cache: KVCache, heads: int, stream=None) -> tuple:
+        """(address, bytes) of the zeroed workspace for attention of this batch
+        over such a cache, made on the first call and kept."""
+        key = (cache.kv_heads, cache.head_dim, heads)
+        ws = self._ws.get(key)
+        if ws is None:
+            from . import lib
+            n = int(lib().zc_kv_attend_workspace_size(cache._ref, self._ref, heads))
+            with _on(stream, cache.device):
+                t = torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.device)
+            ws = self._ws[key] = (t.data_ptr(), n, t)
+        return ws
 
 
 def _rows(t: torch.Tensor, shape, device, what: str) -> _Rows:
-    if t.shape != shape or t.stride(2) != 1 or t.device != device:
-        _fail(f"{what} is a tensor {tuple(shape)} on the cache's device, contiguous in its last dimension")
-    return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    if t.shape != shape or t.device != device:
+        _fail(f"{what} is a tensor {tuple(shape)} on the cache's device")
+    token, head, one = t.stride()
+    if one != 1:
+        _fail(f"{what} is contiguous in its last dimension")
+    return _Rows(t.data_ptr(), token, head)
 
 
-def _stream(stream, device) -> int:
+def _handle(stream, cache: KVCache) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(cache._index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _on(stream, device):
-    """Outputs of a call belong to the stream that it runs on."""
+    """Memory made for a call belongs to the stream that it runs on."""
     if stream is None:
         return torch.cuda.device(device)
     s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
@@ -165,31 +194,39 @@ def _check(st: int, what: str) -> None:
 
 
 def _move(fn, what, cache, batch, k, v, stream):
-    if k.dtype not in _CODE or v.dtype != k.dtype:
+    code = _CODE.get(k.dtype)
+    if code is None or v.dtype != k.dtype:
         _fail(f"{what}: k and v are bfloat16, float16 or float32")
     shape = (batch.total_tokens, cache.kv_heads, cache.head_dim)
     rk, rv = _rows(k, shape, cache.device, "k"), _rows(v, shape, cache.device, "v")
-    _check(fn(cache._ref, batch._ref, _CODE[k.dtype], ctypes.byref(rk), ctypes.byref(rv), cache._status,
-              _stream(stream, cache.device)), what)
+    _check(fn(cache._ref, batch._ref, code, ctypes.addressof(rk), ctypes.addressof(rv), cache._status,
+              _handle(stream, cache)), what)
 
 
 def kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """Quantise the batch's tokens into the cache (zc_kv_write). ``k``, ``v``:
     [total_tokens, kv_heads, head_dim] in bfloat16, float16 or float32, any
     strides that are multiples of 16 bytes (views of a fused projection)."""
-    _move(_lib().zc_kv_write, "zc_kv_write", cache, batch, k, v, stream)
+    _move(_entries()[0], "zc_kv_write", cache, batch, k, v, stream)
 
 
 def kv_read_into(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """Read the batch's tokens back into ``k`` and ``v`` (zc_kv_read)."""
-    _move(_lib().zc_kv_read, "zc_kv_read", cache, batch, k, v, stream)
+    _move(_entries()[1], "zc_kv_read", cache, batch, k, v, stream)
+
+
+def _pair(make, stream, device):
+    if stream is None:
+        return make()
+    with _on(stream, device):
+        return make()
 
 
 def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16, stream=None):
     """The batch's tokens as (k, v), [total_tokens, kv_heads, head_dim]."""
     shape = (batch.total_tokens, cache.kv_heads, cache.head_dim)
-    with _on(stream, cache.device):
-        k, v = (torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    k, v = _pair(lambda: (torch.empty(shape, dtype=dtype, device=cache.device),
+                          torch.empty(shape, dtype=dtype, device=cache.device)), stream, cache.device)
     kv_read_into(cache, batch, k, v, stream)
     return k, v
 
@@ -198,7 +235,8 @@ def kv_attend_into(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.T
                    scale: float | None = None, causal: bool = True, window: int = 0, stream=None) -> None:
     """Attention of the batch's tokens over the cache (zc_kv_attend) into
     ``out`` and, if given, ``lse`` (float32 [total_tokens, heads])."""
-    if q.dtype not in (torch.bfloat16, torch.float16) or out.dtype != q.dtype:
+    code = _CODE.get(q.dtype)
+    if code is None or code == _FP32 or out.dtype != q.dtype:
         _fail("zc_kv_attend: q and out are bfloat16 or float16")
     heads = q.shape[1] if q.dim() == 3 else 0
     shape = (batch.total_tokens, heads, cache.head_dim)
@@ -206,12 +244,13 @@ def kv_attend_into(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.T
     if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous() or
                             lse.device != cache.device):
         _fail("zc_kv_attend: lse is float32 [total_tokens, heads]")
-    if window < 0 or window > 0x7FFFFFFF:
+    if not 0 <= window <= 0x7FFFFFFF:
         _fail("zc_kv_attend: window >= 0")
-    _check(_lib().zc_kv_attend(cache._ref, batch._ref, _CODE[q.dtype], heads, ctypes.byref(rq), ctypes.byref(ro),
-                               lse.data_ptr() if lse is not None else None,
-                               cache.head_dim ** -0.5 if scale is None else scale, _CAUSAL if causal else 0, window,
-                               cache._status, _stream(stream, cache.device)), "zc_kv_attend")
+    ws = batch.workspace(cache, heads, stream)
+    _check(_entries()[2](cache._ref, batch._ref, code, heads, ctypes.addressof(rq), ctypes.addressof(ro),
+                         None if lse is None else lse.data_ptr(), cache.head_dim ** -0.5 if scale is None else scale,
+                         _CAUSAL if causal else 0, window, ws[0], ws[1], cache._status, _handle(stream, cache)),
+           "zc_kv_attend")
 
 
 def kv_attend(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | None = None, causal: bool = True,
@@ -223,8 +262,7 @@ def kv_attend(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | No
     with j <= p (``causal``) and j > p - window (``window`` > 0). ``scale``
     defaults to head_dim ** -0.5. The tokens' own keys and values are in the
     cache already (kv_write first)."""
-    with _on(stream, cache.device):
-        out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device)
+    out, lse = _pair(lambda: (torch.empty(q.shape, dtype=q.dtype, device=cache.device),
+                              torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device)), stream, cache.device)
     kv_attend_into(cache, batch, q, out, lse, scale, causal, window, stream)
     return out, lse

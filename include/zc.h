@@ -447,12 +447,19 @@ ZC_API int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, int dt
  *   heads   query heads, a multiple of kv_heads
  *   q, out  [total_tokens][heads][head_dim]
  *   d_lse   NULL or float [total_tokens][heads]
+ *   d_ws    workspace of ws_bytes >= zc_kv_attend_workspace_size(...), zeroed
+ *           before its first use; every call leaves it ready for the next with
+ *           a batch of these sizes. Calls that may overlap need their own.
  * Scores, weights' sums and outputs are accumulated in float32; weights are
  * rounded to half, in units of the row's largest contribution. */
 #define ZC_KV_CAUSAL 1u
 ZC_API int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
                         const zc_kv_rows *q, const zc_kv_rows *out, float *d_lse, double scale, uint32_t flags,
-                        uint32_t window, int32_t *d_status, void *stream);
+                        uint32_t window, void *d_ws, uint64_t ws_bytes, int32_t *d_status, void *stream);
+
+/* Workspace bytes of zc_kv_attend for this cache, batch and number of query
+ * heads (0 for invalid ones). Queries the device's SM count; host only. */
+ZC_API uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads);
 
 #ifdef __cplusplus
 }

@@ -33,10 +33,10 @@ def _call(name, cache=None, batch=None, dtype=zc.BF16, k=None, v=None, status=P)
     return f(ref(cache or _cache()), ref(batch or _batch()), dtype, ref(k or _rows()), ref(v or _rows()), status, None)
 
 
-def _attend(cache=None, batch=None, dtype=zc.BF16, heads=4, q=None, out=None, lse=None, scale=0.1, flags=1, window=0, status=P):
+def _attend(cache=None, batch=None, dtype=zc.BF16, heads=4, q=None, out=None, lse=None, scale=0.1, flags=1, window=0, ws=P, ws_bytes=1 << 30, status=P):
     return zc.lib().zc_kv_attend(ctypes.byref(cache or _cache()), ctypes.byref(batch or _batch()), dtype, heads,
                                  ctypes.byref(q or _rows(token=128)), ctypes.byref(out or _rows(token=128)), lse, scale,
-                                 flags, window, status, None)
+                                 flags, window, ws, ws_bytes, status, None)
 
 
 BAD_CACHES = [dict(d_k=None), dict(d_v_scale=None), dict(d_k=P + 8), dict(d_k_scale=P + 2), dict(head_dim=0),
@@ -75,7 +75,18 @@ def test_attend_refuses_its_own_arguments():
         assert _attend(heads=heads) == zc.EINVAL
     for scale in (float("nan"), float("inf"), 1e30):
         assert _attend(scale=scale) == zc.EINVAL
+    assert _attend(ws=None) == zc.EINVAL and _attend(ws=P + 8) == zc.EINVAL and _attend(ws_bytes=1000) == zc.ECAPACITY
     assert _attend(flags=2) == zc.EINVAL and _attend(lse=P + 2) == zc.EINVAL and _attend(status=None) == zc.EINVAL
+
+
+def test_workspace_size_of_valid_arguments_only():
+    size = lambda c, b, h: zc.lib().zc_kv_attend_workspace_size(ctypes.byref(c), ctypes.byref(b), h)  # noqa: E731
+    assert size(_cache(), _batch(), 4) > 0
+    for kw in BAD_CACHES:
+        assert size(_cache(**kw), _batch(), 4) == 0, kw
+    for kw in BAD_BATCHES:
+        assert size(_cache(), _batch(**kw), 4) == 0, kw
+    assert size(_cache(), _batch(), 3) == 0 and size(_cache(), _batch(), 0) == 0
 
 
 def test_a_batch_without_tokens_launches_nothing():
