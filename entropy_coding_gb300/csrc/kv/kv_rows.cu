@@ -151,14 +151,14 @@ __device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32
 
 // The piece [unit0, unit0 + units) of item (seq, tile, h); part: where its
 // partial result goes, or null if the piece is the whole item.
-template <int DT, int DP>
+template <int DT, int DP, bool kFull>
 __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
                                       uint32_t unit0, uint32_t units, Part<DP> *part) {
     constexpr int kSteps = DP / 16;      // inner steps of q k
     constexpr int kTiles = DP / 8;       // column tiles of the output
     constexpr int kRun = DP / 4;         // columns of q and k that a thread of a quad holds
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const uint32_t D = a.c.dim, B = a.c.tokens, s = seq.s;
+    const uint32_t D = kFull ? DP : a.c.dim, B = a.c.tokens, s = seq.s;
     const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
 
     // The keys that each of the thread's two rows sees: [lo, hi).
@@ -227,24 +227,37 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
     int first = int(unit0) * kWarps + warp;
     if (first < all_lo / kSlice) first += (all_lo / kSlice - first + kWarps - 1) / kWarps * kWarps;
 
-    // Fetches slice i into stage st; rows outside the keys that someone sees, and
-    // columns from D on, are zeros.
-    auto fetch = [&](int i, int st) {
+    // Fetches slice i, of block `id`, into stage st. A lane copies the same 16 columns of every
+    // kLaneRows-th row; rows outside the keys that someone sees, and columns from D on, are zeros.
+    constexpr int kChunks = DP / 16, kLaneRows = 32 / kChunks;
+    const int lr = lane / kChunks, lc = lane % kChunks * 16;
+    const bool col_ok = kFull || lc < int(D);
+    auto block_of = [&](int i) -> int64_t { return i < end ? read_block(a.b, a.c, s, uint32_t(i * kSlice) / B, a.d_status) : -1; };
+    auto fetch = [&](int i, int64_t id, int st) {
         if (i < end) {
             const int key0 = i * kSlice;
-            const int64_t id = read_block(a.b, a.c, s, uint32_t(key0) / B, a.d_status);
             const uint32_t in_block = uint32_t(key0) % B;
-            const int64_t base = max(id, int64_t(0)) * a.c.block_stride + (int64_t(h) * B + in_block) * D;
-            constexpr int kChunks = DP / 16;
+            const bool whole = id >= 0 && key0 >= all_lo && key0 + kSlice <= all_hi;
+            if (id < 0) id = 0;
+            const int64_t off = id * a.c.block_stride + (int64_t(h) * B + in_block + lr) * D + (col_ok ? lc : 0);
+            const uint8_t *kp = a.c.code[0] + off, *vp = a.c.code[1] + off;
+            uint8_t *ks = &stages[st].k[lr][lc], *vs = &stages[st].v[lr][lc];
+            if (whole) {
 #pragma unroll
-            for (int j = 0; j < kSlice * kChunks / 32; j++) {
-                const int r = (j * 32 + lane) / kChunks, c = (j * 32 + lane) % kChunks * 16;
-                const bool take = id >= 0 && key0 + r >= all_lo && key0 + r < all_hi && c < int(D);
-                const int64_t off = take ? base + int64_t(r) * D + c : 0;
-                cp16(&stages[st].k[r][c], a.c.code[0] + off, take);
-                cp16(&stages[st].v[r][c], a.c.code[1] + off, take);
+                for (int j = 0; j < kSlice / kLaneRows; j++) {
+                    cp16(ks + j * kLaneRows * (DP + 16), kp + j * kLaneRows * D, col_ok);
+                    cp16(vs + j * kLaneRows * (DP + 16), vp + j * kLaneRows * D, col_ok);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kSlice / kLaneRows; j++) {
+                    const int key = key0 + lr + j * kLaneRows;
+                    const bool take = col_ok && key >= all_lo && key < all_hi;
+                    cp16(ks + j * kLaneRows * (DP + 16), kp + j * kLaneRows * D, take);
+                    cp16(vs + j * kLaneRows * (DP + 16), vp + j * kLaneRows * D, take);
+                }
             }
-            if (lane < 2) cp4(&stages[st].scale[lane], a.c.scale[lane] + max(id, int64_t(0)) * a.c.scale_stride + h, id >= 0);
+            if (lane < 2) cp4(&stages[st].scale[lane], a.c.scale[lane] + id * a.c.scale_stride + h, true);
         }
         cp_commit();
     };
@@ -254,15 +267,29 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
     for (int i = 0; i < kTiles; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) o[i][j] = 0.0f;
-    float m[2] = {kNone, kNone}, mw[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
+    // Running maxima (the scores', and with the value scales), 2^(m - mw), and the weights' sums.
+    float m[2] = {kNone, kNone}, mw[2] = {kNone, kNone}, unit[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
 
+    int64_t id = block_of(first);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; i++) fetch(first + i * kWarps, i);
+    for (int i = 0; i < kStages - 1; i++) {
+        const int64_t next = block_of(first + (i + 1) * kWarps);
+        fetch(first + i * kWarps, id, i);
+        id = next;
+    }
     int st = 0;
     for (int i = first; i < end; i += kWarps) {
         cp_wait<kStages - 2>();
         __syncwarp();
+        // The stage before this one was read a step ago: it is fetched into, and the block of the
+        // fetch after that is looked up a step ahead of its use.
+        {
+            const int64_t next = block_of(i + kStages * kWarps);
+            fetch(i + (kStages - 1) * kWarps, id, st == 0 ? kStages - 1 : st - 1);
+            id = next;
+        }
         Stage<DP> &sl = stages[st];
+        st = st + 1 == kStages ? 0 : st + 1;
         // scores of 16 rows and 16 keys
         float sc[2][4] = {};
 #pragma unroll
@@ -280,46 +307,51 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
         const int key0 = i * kSlice;
         const bool edge = key0 < x_lo || key0 + kSlice > x_hi;  // some row does not see all of it
         const float ks = sl.scale[0], vs = sl.scale[1];
-        float top[2] = {kNone, kNone};
+        const float by[2] = {row_scale[0] * ks, row_scale[1] * ks};
+        float top[2];
 #pragma unroll
         for (int n = 0; n < 2; n++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int r = j >> 1, key = key0 + 8 * n + 2 * t + (j & 1);
-                float x = sc[n][j] * (row_scale[r] * ks);
-                if (edge && (key < lo[r] || key >= hi[r])) x = kNone;
-                sc[n][j] = x;
-                top[r] = fmaxf(top[r], x);
-            }
-        const float lvs = __log2f(vs);
-        float f[2], down[2];
+            for (int j = 0; j < 4; j++) sc[n][j] *= by[j >> 1];
+        if (edge) {
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
-            const float m1 = fmaxf(m[r], top[r]), w1 = fmaxf(mw[r], top[r] + lvs);
-            l[r] *= ratio2(m[r], m1);
-            down[r] = ratio2(mw[r], w1);
-            m[r] = m1, mw[r] = w1;
-            // weights in the output's units: p * f, f = 2^(m + log2 vs - mw)
-            f[r] = w1 == kNone || m1 == kNone ? 0.0f : vs * ex2(fminf(m1 - w1, 126.0f));
+            for (int n = 0; n < 2; n++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int r = j >> 1, key = key0 + 8 * n + 2 * t + (j & 1);
+                    if (key < lo[r] || key >= hi[r]) sc[n][j] = kNone;
+                }
         }
-        if (__any_sync(0xFFFFFFFFu, down[0] != 1.0f || down[1] != 1.0f)) {
+#pragma unroll
+        for (int r = 0; r < 2; r++) top[r] = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+        // The maxima seldom grow after the first steps; while none does, nothing is rescaled.
+        const float lvs = __log2f(vs);
+        if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1] || top[0] + lvs > mw[0] || top[1] + lvs > mw[1])) {
+            float down[2];
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
+                const float m1 = fmaxf(m[r], top[r]), w1 = fmaxf(mw[r], top[r] + lvs);
+                l[r] *= ratio2(m[r], m1);
+                down[r] = ratio2(mw[r], w1);
+                m[r] = m1, mw[r] = w1;
+                unit[r] = w1 == kNone || m1 == kNone ? 0.0f : ex2(fminf(m1 - w1, 126.0f));
+            }
 #pragma unroll
             for (int c = 0; c < kTiles; c++) o[c][0] *= down[0], o[c][1] *= down[0], o[c][2] *= down[1], o[c][3] *= down[1];
         }
+        // Weights p = 2^(s - m), and in the output's units p * 2^(m + log2 vs - mw).
         uint32_t pf[4];
 #pragma unroll
-        for (int n = 0; n < 2; n++) {
-            float p[4];
+        for (int r = 0; r < 2; r++) {
+            const float base = m[r] == kNone ? 0.0f : m[r], f = vs * unit[r];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int r = j >> 1;
-                p[j] = sc[n][j] == kNone ? 0.0f : ex2(sc[n][j] - m[r]);
-                l[r] += p[j];
+            for (int n = 0; n < 2; n++) {
+                const float p0 = ex2(sc[n][2 * r] - base), p1 = ex2(sc[n][2 * r + 1] - base);
+                l[r] += p0 + p1;
+                pf[2 * n + r] = half2_of(p0 * f, p1 * f);
             }
-            pf[2 * n] = half2_of(p[0] * f[0], p[1] * f[0]);
-            pf[2 * n + 1] = half2_of(p[2] * f[1], p[3] * f[1]);
         }
         // Values: the thread's keys are 2t, 2t + 1, 2t + 8, 2t + 9, its columns [kTiles g, kTiles g + kTiles).
         const int keys[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
@@ -359,14 +391,12 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             }
         }
 #pragma unroll
-        for (int c = 0; c < kTiles; c++) {
-            const uint32_t sel = (c & 3) | ((c & 3) + 4) << 4;  // byte c of two keys
+        for (int c = 0; c < kTiles; c += 2) {
+            const uint32_t sel = (c & 3) | ((c & 3) + 4) << 4 | ((c & 3) + 1) << 8 | ((c & 3) + 5) << 12;  // bytes c, c + 1 of two keys
             const uint32_t b0 = __byte_perm(vw[0][c / 4], vw[1][c / 4], sel), b1 = __byte_perm(vw[2][c / 4], vw[3][c / 4], sel);
             mma(o[c], pf, e4m3x2_to_half2(uint16_t(b0)), e4m3x2_to_half2(uint16_t(b1)));
+            mma(o[c + 1], pf, e4m3x2_to_half2(uint16_t(b0 >> 16)), e4m3x2_to_half2(uint16_t(b1 >> 16)));
         }
-        __syncwarp();  // the stage before this one is free: it was read a step ago
-        fetch(i + (kStages - 1) * kWarps, (st + kStages - 1) % kStages);
-        st = (st + 1) % kStages;
     }
     cp_wait<0>();
 
@@ -466,7 +496,7 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const S
     }
 }
 
-template <int DT, int DP> __global__ void __launch_bounds__(kThreads, kResident) rows_kernel(AttendArgs a) {
+template <int DT, int DP, bool kFull> __global__ void __launch_bounds__(kThreads, kResident) rows_kernel(AttendArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint64_t s_warp[kWarps], s_at;
     __shared__ uint32_t s_seq;
@@ -510,7 +540,7 @@ template <int DT, int DP> __global__ void __launch_bounds__(kThreads, kResident)
         const uint64_t tile = item / a.c.heads;
         const uint32_t h = uint32_t(item % a.c.heads);
         const bool whole = w == i0 && upto == i1;
-        piece<DT, DP>(a, smem, seq, tile, h, first_unit(a, seq) + uint32_t(w - i0), uint32_t(upto - w),
+        piece<DT, DP, kFull>(a, smem, seq, tile, h, first_unit(a, seq) + uint32_t(w - i0), uint32_t(upto - w),
                       whole ? nullptr : parts + 2 * cta + (w == i0 ? 1 : 0));
         if (!whole) {
             // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
@@ -533,17 +563,17 @@ template <int DT, int DP> __global__ void __launch_bounds__(kThreads, kResident)
     }
 }
 
-template <int DT, int DP> int launch(const AttendArgs &a, cudaStream_t s) {
+template <int DT, int DP, bool kFull> int launch(const AttendArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose kernel may use this much shared memory
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(rows_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<DP>())) != cudaSuccess)
+        if (cudaFuncSetAttribute(rows_kernel<DT, DP, kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<DP>())) != cudaSuccess)
             return ZC_ECUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    rows_kernel<DT, DP><<<rows_ctas(), kThreads, smem_bytes<DP>(), s>>>(a);
+    rows_kernel<DT, DP, kFull><<<rows_ctas(), kThreads, smem_bytes<DP>(), s>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }
 
@@ -559,9 +589,14 @@ uint64_t rows_part_bytes(uint32_t dim) {
     return uint64_t(rows_ctas()) * 2 * (dim <= 64 ? sizeof(Part<64>) : sizeof(Part<128>));
 }
 
+template <int DT> static int launch_type(const AttendArgs &a, cudaStream_t s) {
+    if (a.c.dim == 128) return launch<DT, 128, true>(a, s);
+    if (a.c.dim == 64) return launch<DT, 64, true>(a, s);
+    return a.c.dim < 64 ? launch<DT, 64, false>(a, s) : launch<DT, 128, false>(a, s);
+}
+
 int launch_attend(int dtype, const AttendArgs &a, cudaStream_t s) {
-    if (dtype == ZC_BF16) return a.c.dim <= 64 ? launch<ZC_BF16, 64>(a, s) : launch<ZC_BF16, 128>(a, s);
-    return a.c.dim <= 64 ? launch<ZC_FP16, 64>(a, s) : launch<ZC_FP16, 128>(a, s);
+    return dtype == ZC_BF16 ? launch_type<ZC_BF16>(a, s) : launch_type<ZC_FP16>(a, s);
 }
 
 } // namespace kv
