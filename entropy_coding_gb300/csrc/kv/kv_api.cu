@@ -122,7 +122,7 @@ extern "C" uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const 
     Batch b{};
     if (make_cache(cache, c) != ZC_OK || make_batch(batch, b) != ZC_OK) return 0;
     if (heads == 0 || heads % c.heads || heads > 65535) return 0;
-    return pad256(4 * rows_counters(b, c, heads / c.heads)) + pad256(rows_part_bytes(c.dim));
+    return pad256(4 * rows_counters(b, c, heads / c.heads)) + pad256(rows_part_bytes(b, c, heads / c.heads));
 }
 
 extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
@@ -139,15 +139,16 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
     if ((st = make_rows(*q, 2, a.q)) != ZC_OK || (st = make_rows(*out, 2, a.out)) != ZC_OK) return st;
     a.lse = d_lse;
     a.heads = heads;
+    a.dtype = dtype;
     a.group = heads / a.c.heads;
     const uint64_t counters = pad256(4 * rows_counters(a.b, a.c, a.group));
     if (!d_ws || !aligned(d_ws, 16)) return ZC_EINVAL;
-    if (ws_bytes < counters + rows_part_bytes(a.c.dim)) return ZC_ECAPACITY;
+    if (ws_bytes < counters + rows_part_bytes(a.b, a.c, a.group)) return ZC_ECAPACITY;
     a.counters = static_cast<uint32_t *>(d_ws);
     a.parts = static_cast<uint8_t *>(d_ws) + counters;
     a.scale_log2 = float(scale * 1.4426950408889634);
     a.causal = flags & ZC_KV_CAUSAL;
     a.window = window;
     a.d_status = d_status;
-    return launch_attend(dtype, a, static_cast<cudaStream_t>(stream));
+    return launch_attend(a, static_cast<cudaStream_t>(stream));
 }

@@ -57,6 +57,7 @@ struct AttendArgs {
     Rows q, out;
     float *lse;            // [total][heads] or null
     uint32_t heads, group;
+    int dtype;             // of q and out
     float scale_log2;      // softmax scale * log2(e)
     uint32_t causal, window;
     uint32_t *counters;    // workspace: an item's parts that are done, zero between calls
@@ -67,11 +68,10 @@ struct AttendArgs {
 int launch_write(int dtype, const MoveArgs &a, cudaStream_t s);
 int launch_read(int dtype, const MoveArgs &a, cudaStream_t s);
 int sm_count();
-// CTAs of the attention kernel's grid, and what its workspace holds.
-uint32_t rows_ctas();
+// What attention's workspace holds: counters, and bytes of partial results.
 uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group);
-uint64_t rows_part_bytes(uint32_t dim);
-int launch_attend(int dtype, const AttendArgs &a, cudaStream_t s);
+uint64_t rows_part_bytes(const Batch &b, const Cache &c, uint32_t group);
+int launch_attend(const AttendArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
 

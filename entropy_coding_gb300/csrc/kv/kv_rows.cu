@@ -6,7 +6,7 @@
 //   s_ij = scale * ks_b(j) * (q_i . kc_j)
 //   out_i = sum_j 2^(s_ij log2e - m) vs_b(j) vc_j / sum_j 2^(s_ij log2e - m)
 //
-// An item is 16 rows of one sequence and key/value head. Decoding has few
+// An item is the rows (at most 32) of one sequence and key/value head. Decoding has few
 // items and long key axes, so items are cut along the keys: the batch's work
 // is one line of 64-key units, items one after another, and each CTA of a
 // resident grid takes an equal piece of it (a few whole items and a part of
@@ -17,15 +17,16 @@
 // is left at zero for the next call.
 //
 // A CTA has 4 warps; a warp takes 16 keys at a time, and both products run on
-// mma.m16n8k16 with half operands and float accumulators. E4M3 codes are
-// exact in half. A query row is exact in half too after it is multiplied by a
-// power of two that brings its largest element to [2^14, 2^15) (what falls
-// below 2^-24 then is 2^-38 of it). A row's weights w are rounded to half;
-// they are kept in units of the row's running maximum of s + log2 vs, not of
-// s alone, so that the largest contribution to the output is always 1 and
-// blocks whose scales differ by any factor keep their precision. The sum of
-// the weights is taken before that rounding, in units of the running maximum
-// of s.
+// mma.m16n8k16 with half operands and float accumulators, transposed: keys (or
+// the output's columns) are the 16 and the query rows the 8, so that a decoding
+// step's 4 or 8 rows of a head fill the tile. E4M3 codes are exact in half. A
+// query row is exact in half too after it is multiplied by a power of two that
+// brings its largest element to [2^14, 2^15) (what falls below 2^-24 then is
+// 2^-38 of it). A row's weights w are rounded to half; they are kept in units
+// of the row's running maximum of s + log2 vs, not of s alone, so that the
+// largest contribution to the output is always 1 and blocks whose scales
+// differ by any factor keep their precision. The sum of the weights is taken
+// before that rounding, in units of the running maximum of s.
 //
 // Each warp streams its own keys and values through shared memory with
 // cp.async, kStages slices of 16 rows deep, and the warps meet only at an
@@ -41,11 +42,15 @@ namespace zc {
 namespace kv {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kStages = 4;
-constexpr int kRows = 16, kSlice = 16;  // rows of an item; keys of a warp's step
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kSlice = 16;              // keys of a warp's step
 constexpr int kUnit = kWarps * kSlice;  // keys of a unit of work
-constexpr int kResident = 3;            // CTAs of an SM
 constexpr float kNone = -INFINITY;
+
+// By tiles of 8 rows: CTAs of an SM, as many as their registers allow, and the
+// slices that fill the SM's shared memory.
+constexpr int resident(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+constexpr int stages(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 6; }
 
 template <int DP> struct Stage {
     uint8_t k[kSlice][DP + 16];
@@ -53,19 +58,20 @@ template <int DP> struct Stage {
     float scale[4];  // ks, vs
 };
 
-template <int DP> struct Merge {  // over the stages, once the loop is done
-    float o[kWarps][kRows][DP + 4];
-    float m[kWarps][kRows], mw[kWarps][kRows], l[kWarps][kRows];
+template <int DP, int NT> struct Merge {  // over the stages, once the loop is done
+    float o[kWarps][8 * NT][DP + 4];
+    float m[kWarps][8 * NT], mw[kWarps][8 * NT], l[kWarps][8 * NT];
 };
 
 // A part of an item: rows in units of 2^mw (o) and 2^m (l).
-template <int DP> struct Part {
-    float o[kRows][DP];
-    float m[kRows], mw[kRows], l[kRows];
+template <int DP, int NT> struct Part {
+    float o[8 * NT][DP];
+    float m[8 * NT], mw[8 * NT], l[8 * NT];
 };
 
-template <int DP> constexpr size_t smem_bytes() {
-    return sizeof(Stage<DP>) * kStages * kWarps > sizeof(Merge<DP>) ? sizeof(Stage<DP>) * kStages * kWarps : sizeof(Merge<DP>);
+template <int DP, int NT> constexpr size_t smem_bytes() {
+    const size_t a = sizeof(Stage<DP>) * stages(NT) * kWarps, b = sizeof(Merge<DP, NT>);
+    return a > b ? a : b;
 }
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool take) {
@@ -83,6 +89,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The 8x8 matrix of halves whose rows the quads hold, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -106,11 +118,8 @@ __device__ __forceinline__ uint32_t first_unit(const AttendArgs &a, const Seq &q
 __device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &q) {
     return max((uint32_t(q.len) + kUnit - 1) / kUnit, first_unit(a, q) + 1) - first_unit(a, q);
 }
-__device__ __forceinline__ uint64_t tiles_of(const AttendArgs &a, const Seq &q) {
-    return (uint64_t(q.n) * a.group + kRows - 1) / kRows;
-}
-__device__ __forceinline__ uint64_t work_of(const AttendArgs &a, const Seq &q) {
-    return q.ok ? tiles_of(a, q) * a.c.heads * units_of(a, q) : 0;
+template <int NT> __device__ __forceinline__ uint64_t work_of(const AttendArgs &a, const Seq &q) {
+    return q.ok ? (uint64_t(q.n) * a.group + 8 * NT - 1) / (8 * NT) * a.c.heads * units_of(a, q) : 0;
 }
 
 // Inclusive sum of the threads before and including this one; `total`: of all.
@@ -133,66 +142,63 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t *s_warp, uin
     return v;
 }
 
-// The finished row: 8 columns from `col` on, in units (M, W, L).
-template <int DT>
-__device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32_t h, uint64_t row, int col, const float *x,
-                                     int n, float M, float W, float L) {
+// Two numbers of the output's type.
+__device__ __forceinline__ uint32_t pack_out(const AttendArgs &a, float x, float y) {
+    return a.dtype == ZC_BF16 ? pack2<ZC_BF16>(x, y) : pack2<ZC_FP16>(x, y);
+}
+
+// n columns (4 or 8) of a finished row from `col` on, in units (M, W, L).
+template <int n>
+__device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32_t h, uint64_t row, int col,
+                                     const float (&x)[n], float M, float W, float L) {
     // out = x / L in the units of M; a row that sees no key is 0. (L is NaN where a score was.)
     const float by = L == 0.0f ? 0.0f : (W == kNone ? 0.0f : ex2(W - M)) / L;
     const int64_t token = int64_t(seq.first) + int64_t(row / a.group), head = int64_t(h) * a.group + int64_t(row % a.group);
     uint16_t *o = static_cast<uint16_t *>(a.out.p) + token * a.out.token + head * a.out.head + col;
-    uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < n / 2; k++) w[k] = L == 0.0f ? 0u : pack2<DT>(x[2 * k] * by, x[2 * k + 1] * by);
-    if (n == 8) *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    for (int k = 0; k < n; k += 4)
+        *reinterpret_cast<uint2 *>(o + k) = L == 0.0f ? make_uint2(0, 0) : make_uint2(pack_out(a, x[k] * by, x[k + 1] * by),
+                                                                                      pack_out(a, x[k + 2] * by, x[k + 3] * by));
     if (a.lse && col == 0) a.lse[token * a.heads + head] = L == 0.0f ? kNone : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // The piece [unit0, unit0 + units) of item (seq, tile, h); part: where its
 // partial result goes, or null if the piece is the whole item.
-template <int DT, int DP, bool kFull>
+template <int DP, int NT, bool kFull>
 __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
-                                      uint32_t unit0, uint32_t units, Part<DP> *part) {
-    constexpr int kSteps = DP / 16;      // inner steps of q k
-    constexpr int kTiles = DP / 8;       // column tiles of the output
+                                      uint32_t unit0, uint32_t units, Part<DP, NT> *part) {
+    constexpr int kRows = 8 * NT, kStages = stages(NT);
+    constexpr int kSteps = DP / 16;      // inner steps of k q, and column tiles of the output
     constexpr int kRun = DP / 4;         // columns of q and k that a thread of a quad holds
+    constexpr int kCols = DP / 8;        // columns of v that a thread's quad holds
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t D = kFull ? DP : a.c.dim, B = a.c.tokens, s = seq.s;
     const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
 
-    // The keys that each of the thread's two rows sees: [lo, hi).
+    // The keys that a row sees: [l, e).
     const int64_t pos0 = int64_t(seq.len) - int64_t(seq.n);  // position of the sequence's first new token
-    int lo[2], hi[2];
-    bool row_ok[2];
     auto bounds = [&](uint64_t row, int &l, int &e) {
         const int64_t pos = pos0 + int64_t(row / a.group);
         e = int(a.causal ? max(pos + 1, int64_t(0)) : int64_t(seq.len));
         l = a.window ? int(max(pos - int64_t(a.window) + 1, int64_t(0))) : 0;
         if (l > e) l = e;
     };
-#pragma unroll
-    for (int r = 0; r < 2; r++) {
-        const uint64_t row = row0 + g + 8 * r;
-        row_ok[r] = row < n_rows;
-        bounds(row_ok[r] ? row : n_rows - 1, lo[r], hi[r]);
-    }
     int all_lo, all_hi, x_lo, x_hi;  // seen by some row; by every row
     bounds(row0, all_lo, x_hi);
     bounds(min(row0 + kRows, n_rows) - 1, x_lo, all_hi);
 
-    // Query fragments: the thread's rows, columns [kRun t, kRun t + kRun).
-    uint32_t qf[kSteps][4];
-    float row_scale[2];
+    // Query fragments: row g of each tile, columns [kRun t, kRun t + kRun).
+    uint32_t qf[NT][kSteps][2];
+    float row_scale[NT][2];  // of rows 2t, 2t + 1 of each tile
 #pragma unroll
-    for (int r = 0; r < 2; r++) {
-        const uint64_t row = row0 + g + 8 * r;
+    for (int n = 0; n < NT; n++) {
+        const uint64_t row = row0 + 8 * n + g;
         uint32_t w[kRun / 2];
 #pragma unroll
         for (int i = 0; i < kRun / 8; i++) {
             uint4 v = make_uint4(0, 0, 0, 0);
             const uint32_t col = kRun * t + 8 * i;
-            if (row_ok[r] && col < D) {
+            if (row < n_rows && col < D) {
                 const uint16_t *q = static_cast<const uint16_t *>(a.q.p) +
                                     (int64_t(seq.first) + int64_t(row / a.group)) * a.q.token +
                                     (int64_t(h) * a.group + int64_t(row % a.group)) * a.q.head + col;
@@ -200,8 +206,8 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             }
             w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
         }
-        row_scale[r] = a.scale_log2;
-        if (DT == ZC_BF16) {
+        float scale = a.scale_log2;
+        if (a.dtype == ZC_BF16) {
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < kRun / 2; i++) top = max(top, max(w[i] << 16 & 0x7FFF0000u, w[i] & 0x7FFF0000u));
@@ -210,18 +216,20 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             // 2^(14 - e) for the largest element's exponent e, within float's normal range
             const int field = min(max(127 + 14 - (int(top >> 23) - 127), 1), 253);
             const float up = __uint_as_float(uint32_t(field) << 23), down = __uint_as_float(uint32_t(254 - field) << 23);
-            row_scale[r] = a.scale_log2 * down;
+            scale = a.scale_log2 * down;
 #pragma unroll
             for (int i = 0; i < kRun / 2; i++) {
-                const float2 f = unpack2<DT>(w[i]);
+                const float2 f = unpack2<ZC_BF16>(w[i]);
                 w[i] = half2_of(f.x * up, f.y * up);
             }
         }
 #pragma unroll
-        for (int i = 0; i < kSteps; i++) qf[i][r] = w[2 * i], qf[i][2 + r] = w[2 * i + 1];
+        for (int e = 0; e < 2; e++) row_scale[n][e] = __shfl_sync(0xFFFFFFFFu, scale, 4 * (2 * t + e));
+#pragma unroll
+        for (int i = 0; i < kSteps; i++) qf[n][i][0] = w[2 * i], qf[n][i][1] = w[2 * i + 1];
     }
 
-    Stage<DP> *stages = reinterpret_cast<Stage<DP> *>(smem) + warp * kStages;
+    Stage<DP> *ring = reinterpret_cast<Stage<DP> *>(smem) + warp * kStages;
     // Slices of this warp: first, first + kWarps, ... below end.
     const int end = min((all_hi + kSlice - 1) / kSlice, int((unit0 + units) * kWarps));
     int first = int(unit0) * kWarps + warp;
@@ -238,10 +246,11 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             const int key0 = i * kSlice;
             const uint32_t in_block = uint32_t(key0) % B;
             const bool whole = id >= 0 && key0 >= all_lo && key0 + kSlice <= all_hi;
-            if (id < 0) id = 0;
+            const bool none = id < 0;
+            if (none) id = 0;
             const int64_t off = id * a.c.block_stride + (int64_t(h) * B + in_block + lr) * D + (col_ok ? lc : 0);
             const uint8_t *kp = a.c.code[0] + off, *vp = a.c.code[1] + off;
-            uint8_t *ks = &stages[st].k[lr][lc], *vs = &stages[st].v[lr][lc];
+            uint8_t *ks = &ring[st].k[lr][lc], *vs = &ring[st].v[lr][lc];
             if (whole) {
 #pragma unroll
                 for (int j = 0; j < kSlice / kLaneRows; j++) {
@@ -252,23 +261,30 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
 #pragma unroll
                 for (int j = 0; j < kSlice / kLaneRows; j++) {
                     const int key = key0 + lr + j * kLaneRows;
-                    const bool take = col_ok && key >= all_lo && key < all_hi;
+                    const bool take = col_ok && !none && key >= all_lo && key < all_hi;
                     cp16(ks + j * kLaneRows * (DP + 16), kp + j * kLaneRows * D, take);
                     cp16(vs + j * kLaneRows * (DP + 16), vp + j * kLaneRows * D, take);
                 }
             }
-            if (lane < 2) cp4(&stages[st].scale[lane], a.c.scale[lane] + id * a.c.scale_stride + h, true);
+            if (lane < 2) cp4(&ring[st].scale[lane], a.c.scale[lane] + id * a.c.scale_stride + h, !none);
         }
         cp_commit();
     };
 
-    float o[kTiles][4];
+    float o[NT][kSteps][4];
 #pragma unroll
-    for (int i = 0; i < kTiles; i++)
+    for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) o[i][j] = 0.0f;
-    // Running maxima (the scores', and with the value scales), 2^(m - mw), and the weights' sums.
-    float m[2] = {kNone, kNone}, mw[2] = {kNone, kNone}, unit[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
+        for (int i = 0; i < kSteps; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) o[n][i][j] = 0.0f;
+    // Of rows 2t, 2t + 1 of each tile: running maxima (the scores', and with the value scales),
+    // 2^(m - mw), and the weights' sums over this thread's keys.
+    float m[NT][2], mw[NT][2], unit[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) m[n][e] = mw[n][e] = kNone, unit[n][e] = l[n][e] = 0.0f;
 
     int64_t id = block_of(first);
 #pragma unroll
@@ -288,72 +304,91 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             fetch(i + (kStages - 1) * kWarps, id, st == 0 ? kStages - 1 : st - 1);
             id = next;
         }
-        Stage<DP> &sl = stages[st];
+        Stage<DP> &sl = ring[st];
         st = st + 1 == kStages ? 0 : st + 1;
-        // scores of 16 rows and 16 keys
-        float sc[2][4] = {};
+
+        // scores of 16 keys and the rows: c0, c1 are key g and rows 2t, 2t + 1, c2, c3 key g + 8
+        float sc[NT][4];
 #pragma unroll
-        for (int n = 0; n < 2; n++) {
-            uint32_t kw[kRun / 4];
+        for (int n = 0; n < NT; n++) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
 #pragma unroll
-            for (int c = 0; c < kRun / 16; c++) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(&sl.k[8 * n + g][kRun * t + 16 * c]);
-                kw[4 * c] = v.x, kw[4 * c + 1] = v.y, kw[4 * c + 2] = v.z, kw[4 * c + 3] = v.w;
+        for (int c = 0; c < kRun / 16; c++) {
+            const uint4 v0 = *reinterpret_cast<const uint4 *>(&sl.k[g][kRun * t + 16 * c]);
+            const uint4 v1 = *reinterpret_cast<const uint4 *>(&sl.k[8 + g][kRun * t + 16 * c]);
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const uint32_t kf[4] = {e4m3x2_to_half2(uint16_t(w0[k])), e4m3x2_to_half2(uint16_t(w1[k])),
+                                        e4m3x2_to_half2(uint16_t(w0[k] >> 16)), e4m3x2_to_half2(uint16_t(w1[k] >> 16))};
+#pragma unroll
+                for (int n = 0; n < NT; n++) mma(sc[n], kf, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
             }
-#pragma unroll
-            for (int c = 0; c < kSteps; c++)
-                mma(sc[n], qf[c], e4m3x2_to_half2(uint16_t(kw[c])), e4m3x2_to_half2(uint16_t(kw[c] >> 16)));
         }
         const int key0 = i * kSlice;
         const bool edge = key0 < x_lo || key0 + kSlice > x_hi;  // some row does not see all of it
         const float ks = sl.scale[0], vs = sl.scale[1];
-        const float by[2] = {row_scale[0] * ks, row_scale[1] * ks};
-        float top[2];
 #pragma unroll
-        for (int n = 0; n < 2; n++)
+        for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) sc[n][j] *= by[j >> 1];
+            for (int j = 0; j < 4; j++) sc[n][j] *= row_scale[n][j & 1] * ks;
         if (edge) {
 #pragma unroll
-            for (int n = 0; n < 2; n++)
+            for (int n = 0; n < NT; n++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int r = j >> 1, key = key0 + 8 * n + 2 * t + (j & 1);
-                    if (key < lo[r] || key >= hi[r]) sc[n][j] = kNone;
+                for (int e = 0; e < 2; e++) {
+                    int lo, hi;
+                    bounds(min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+                        if (key0 + g + 8 * j < lo || key0 + g + 8 * j >= hi) sc[n][2 * j + e] = kNone;
                 }
         }
-#pragma unroll
-        for (int r = 0; r < 2; r++) top[r] = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
         // The maxima seldom grow after the first steps; while none does, nothing is rescaled.
         const float lvs = __log2f(vs);
-        if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1] || top[0] + lvs > mw[0] || top[1] + lvs > mw[1])) {
-            float down[2];
+        bool grows = false;
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
-                const float m1 = fmaxf(m[r], top[r]), w1 = fmaxf(mw[r], top[r] + lvs);
-                l[r] *= ratio2(m[r], m1);
-                down[r] = ratio2(mw[r], w1);
-                m[r] = m1, mw[r] = w1;
-                unit[r] = w1 == kNone || m1 == kNone ? 0.0f : ex2(fminf(m1 - w1, 126.0f));
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float top = fmaxf(sc[n][e], sc[n][2 + e]);
+                grows |= top > m[n][e] || top + lvs > mw[n][e];
             }
+        if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
-            for (int c = 0; c < kTiles; c++) o[c][0] *= down[0], o[c][1] *= down[0], o[c][2] *= down[1], o[c][3] *= down[1];
+            for (int n = 0; n < NT; n++) {
+                float down[2];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float top = fmaxf(sc[n][e], sc[n][2 + e]);
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    const float m1 = fmaxf(m[n][e], top), w1 = fmaxf(mw[n][e], top + lvs);
+                    l[n][e] *= ratio2(m[n][e], m1);
+                    down[e] = ratio2(mw[n][e], w1);
+                    m[n][e] = m1, mw[n][e] = w1;
+                    unit[n][e] = w1 == kNone || m1 == kNone ? 0.0f : ex2(fminf(m1 - w1, 126.0f));
+                }
+#pragma unroll
+                for (int c = 0; c < kSteps; c++)
+                    o[n][c][0] *= down[0], o[n][c][1] *= down[1], o[n][c][2] *= down[0], o[n][c][3] *= down[1];
+            }
         }
         // Weights p = 2^(s - m), and in the output's units p * 2^(m + log2 vs - mw).
-        uint32_t pf[4];
+        uint32_t pf[NT][2];
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-            const float base = m[r] == kNone ? 0.0f : m[r], f = vs * unit[r];
+        for (int n = 0; n < NT; n++) {
+            float w[4];
 #pragma unroll
-            for (int n = 0; n < 2; n++) {
-                const float p0 = ex2(sc[n][2 * r] - base), p1 = ex2(sc[n][2 * r + 1] - base);
-                l[r] += p0 + p1;
-                pf[2 * n + r] = half2_of(p0 * f, p1 * f);
+            for (int e = 0; e < 2; e++) {
+                const float base = m[n][e] == kNone ? 0.0f : m[n][e], f = vs * unit[n][e];
+                const float p0 = ex2(sc[n][e] - base), p1 = ex2(sc[n][2 + e] - base);
+                l[n][e] += p0 + p1;
+                w[e] = p0 * f, w[2 + e] = p1 * f;
             }
+            pf[n][0] = transpose8(half2_of(w[0], w[1]));
+            pf[n][1] = transpose8(half2_of(w[2], w[3]));
         }
-        // Values: the thread's keys are 2t, 2t + 1, 2t + 8, 2t + 9, its columns [kTiles g, kTiles g + kTiles).
+        // Values: the thread's keys are 2t, 2t + 1, 2t + 8, 2t + 9, its columns [kCols g, kCols g + kCols).
         const int keys[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
         if (edge) {
             // A row that does not see a key has weight 0 for it, but 0 * NaN is NaN: NaN codes are
@@ -362,16 +397,20 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
 #pragma unroll
             for (int j = 0; j < 4; j++)
 #pragma unroll
-                for (int c = 0; c < kTiles / 4; c++)
-                    bad |= any_nan(*reinterpret_cast<const uint32_t *>(&sl.v[keys[j]][kTiles * g + 4 * c]));
+                for (int c = 0; c < kCols / 4; c++)
+                    bad |= any_nan(*reinterpret_cast<const uint32_t *>(&sl.v[keys[j]][kCols * g + 4 * c]));
             if (__any_sync(0xFFFFFFFFu, bad)) {
                 for (int k = 0; k < kSlice; k++)
 #pragma unroll
-                    for (int c = 0; c < kTiles; c++)
+                    for (int n = 0; n < NT; n++)
 #pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const int r = e >> 1, col = kTiles * (2 * t + (e & 1)) + c;
-                            if ((sl.v[k][col] & 0x7F) == 0x7F && key0 + k >= lo[r] && key0 + k < hi[r]) o[c][e] = NAN;
+                        for (int e = 0; e < 2; e++) {
+                            int lo, hi;
+                            bounds(min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
+                            if (key0 + k < lo || key0 + k >= hi) continue;
+#pragma unroll
+                            for (int c = 0; c < kCols; c++)
+                                if ((sl.v[k][kCols * g + c] & 0x7F) == 0x7F) o[n][c / 2][2 * (c & 1) + e] = NAN;
                         }
                 __syncwarp();
                 for (int j = lane; j < kSlice * DP; j += 32)
@@ -379,40 +418,45 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
                 __syncwarp();
             }
         }
-        uint32_t vw[4][kTiles / 4];
+        uint32_t vw[4][kCols / 4];
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            if (kTiles == 16) {
+            if (kCols == 16) {
                 const uint4 v = *reinterpret_cast<const uint4 *>(&sl.v[keys[j]][16 * g]);
-                vw[j][0] = v.x, vw[j][1] = v.y, vw[j][kTiles / 4 - 2] = v.z, vw[j][kTiles / 4 - 1] = v.w;
+                vw[j][0] = v.x, vw[j][1] = v.y, vw[j][kCols / 4 - 2] = v.z, vw[j][kCols / 4 - 1] = v.w;
             } else {
                 const uint2 v = *reinterpret_cast<const uint2 *>(&sl.v[keys[j]][8 * g]);
                 vw[j][0] = v.x, vw[j][1] = v.y;
             }
         }
 #pragma unroll
-        for (int c = 0; c < kTiles; c += 2) {
-            const uint32_t sel = (c & 3) | ((c & 3) + 4) << 4 | ((c & 3) + 1) << 8 | ((c & 3) + 5) << 12;  // bytes c, c + 1 of two keys
+        for (int c = 0; c < kCols; c += 2) {  // columns kCols g + c and + 1: rows g and g + 8 of the tile
+            const uint32_t sel = (c & 3) | ((c & 3) + 4) << 4 | ((c & 3) + 1) << 8 | ((c & 3) + 5) << 12;
             const uint32_t b0 = __byte_perm(vw[0][c / 4], vw[1][c / 4], sel), b1 = __byte_perm(vw[2][c / 4], vw[3][c / 4], sel);
-            mma(o[c], pf, e4m3x2_to_half2(uint16_t(b0)), e4m3x2_to_half2(uint16_t(b1)));
-            mma(o[c + 1], pf, e4m3x2_to_half2(uint16_t(b0 >> 16)), e4m3x2_to_half2(uint16_t(b1 >> 16)));
+            const uint32_t vf[4] = {e4m3x2_to_half2(uint16_t(b0)), e4m3x2_to_half2(uint16_t(b0 >> 16)),
+                                    e4m3x2_to_half2(uint16_t(b1)), e4m3x2_to_half2(uint16_t(b1 >> 16))};
+#pragma unroll
+            for (int n = 0; n < NT; n++) mma(o[n][c / 2], vf, pf[n][0], pf[n][1]);
         }
     }
     cp_wait<0>();
 
     // The warps' rows together.
     __syncthreads();
-    Merge<DP> &mg = *reinterpret_cast<Merge<DP> *>(smem);
+    Merge<DP, NT> &mg = *reinterpret_cast<Merge<DP, NT> *>(smem);
 #pragma unroll
-    for (int r = 0; r < 2; r++) {
-        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-        if (t == 0) mg.m[warp][g + 8 * r] = m[r], mg.mw[warp][g + 8 * r] = mw[r], mg.l[warp][g + 8 * r] = l[r];
+    for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int e = 0; e < 2; e++)
+        for (int e = 0; e < 2; e++) {
+            const int r = 8 * n + 2 * t + e;
 #pragma unroll
-            for (int c = 0; c < kTiles; c++) mg.o[warp][g + 8 * r][kTiles * (2 * t + e) + c] = o[c][2 * r + e];
-    }
+            for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], d);
+            if (g == 0) mg.m[warp][r] = m[n][e], mg.mw[warp][r] = mw[n][e], mg.l[warp][r] = l[n][e];
+#pragma unroll
+            for (int c = 0; c < kSteps; c += 2)
+                *reinterpret_cast<float4 *>(&mg.o[warp][r][kCols * g + 2 * c]) =
+                    make_float4(o[n][c][e], o[n][c][2 + e], o[n][c + 1][e], o[n][c + 1][2 + e]);
+        }
     __syncthreads();
     for (int i = threadIdx.x; i < kRows * DP / 8; i += kThreads) {
         const int r = i / (DP / 8), col = i % (DP / 8) * 8;
@@ -433,34 +477,36 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             __stcg(p + 1, make_float4(x[4], x[5], x[6], x[7]));
             if (col == 0) __stcg(&part->m[r], M), __stcg(&part->mw[r], W), __stcg(&part->l[r], L);
         } else {
-            emit<DT>(a, seq, h, row0 + r, col, x, 8, M, W, L);
+            emit(a, seq, h, row0 + r, col, x, M, W, L);
         }
     }
 }
 
 // An item's parts together: the `first` one in its CTA's second slot (a piece
 // that begins an item), the others in the first slots of the CTAs after it.
-template <int DT, int DP>
+template <int DP, int NT>
 __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
-                                     const Part<DP> *parts, uint32_t first, uint32_t n) {
-    constexpr int kBatch = 128;  // parts whose factors are in shared memory at a time
+                                     const Part<DP, NT> *parts, uint32_t first, uint32_t n) {
+    constexpr int kRows = 8 * NT;
+    constexpr int kBatch = 64;  // parts whose factors are in shared memory at a time
     float (*fo)[kRows] = reinterpret_cast<float (*)[kRows]>(smem);
     float *sM = reinterpret_cast<float *>(fo + kBatch), *sW = sM + kRows, *sL = sW + kRows;
     const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
     const int rows = int(min(uint64_t(kRows), n_rows - row0)), D = int(a.c.dim);
-    auto part = [&](uint32_t i) -> const Part<DP> & { return parts[2 * (first + i) + (i ? 0 : 1)]; };
-    // each row's units, by 8 threads
-    {
-        const int r = threadIdx.x / 8, k = threadIdx.x % 8;
+    auto part = [&](uint32_t i) -> const Part<DP, NT> & { return parts[2 * (first + i) + (i ? 0 : 1)]; };
+    // each row's units, by 8 threads (a warp's four rows are all in or all out of the loop: kRows is a multiple of 8)
+    for (int r = threadIdx.x / 8; r < kRows; r += kThreads / 8) {
+        const int k = threadIdx.x % 8;
+        const uint32_t group = 0xFFu << (threadIdx.x & 24);
         float M = kNone, W = kNone, L = 0.0f;
         if (r < rows)
             for (uint32_t i = k; i < n; i += 8) M = fmaxf(M, __ldcg(&part(i).m[r])), W = fmaxf(W, __ldcg(&part(i).mw[r]));
 #pragma unroll
-        for (int d = 1; d < 8; d *= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d)), W = fmaxf(W, __shfl_xor_sync(0xFFFFFFFFu, W, d));
+        for (int d = 1; d < 8; d *= 2) M = fmaxf(M, __shfl_xor_sync(group, M, d)), W = fmaxf(W, __shfl_xor_sync(group, W, d));
         if (r < rows)
             for (uint32_t i = k; i < n; i += 8) L += __ldcg(&part(i).l[r]) * ratio2(__ldcg(&part(i).m[r]), M);
 #pragma unroll
-        for (int d = 1; d < 8; d *= 2) L += __shfl_xor_sync(0xFFFFFFFFu, L, d);
+        for (int d = 1; d < 8; d *= 2) L += __shfl_xor_sync(group, L, d);
         if (k == 0) sM[r] = M, sW[r] = W, sL[r] = L;
     }
     __syncthreads();
@@ -492,21 +538,21 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const S
         const int r = (j * kThreads + threadIdx.x) / kCols, col = (j * kThreads + threadIdx.x) % kCols * 4;
         if (r >= rows || col >= D) continue;
         const float y[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        emit<DT>(a, seq, h, row0 + r, col, y, 4, sM[r], sW[r], sL[r]);
+        emit(a, seq, h, row0 + r, col, y, sM[r], sW[r], sL[r]);
     }
 }
 
-template <int DT, int DP, bool kFull> __global__ void __launch_bounds__(kThreads, kResident) rows_kernel(AttendArgs a) {
+template <int DP, int NT, bool kFull> __global__ void __launch_bounds__(kThreads, resident(NT)) rows_kernel(AttendArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint64_t s_warp[kWarps], s_at;
     __shared__ uint32_t s_seq;
     __shared__ int s_last;
-    Part<DP> *parts = reinterpret_cast<Part<DP> *>(a.parts);
+    Part<DP, NT> *parts = reinterpret_cast<Part<DP, NT> *>(a.parts);
     const uint32_t B = a.c.tokens, cta = blockIdx.x;
 
     // The line of work, and this CTA's piece [w0, w1) of it.
     uint64_t sum = 0, W;
-    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += kThreads) sum += work_of(a, read_seq(a.b, s, a.d_status, B, cta == 0));
+    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += kThreads) sum += work_of<NT>(a, read_seq(a.b, s, a.d_status, B, cta == 0));
     block_scan(sum, s_warp, W);
     const uint64_t G = min(uint64_t(gridDim.x), W);  // no CTA between two that have work is without
     if (cta >= G) return;
@@ -514,7 +560,7 @@ template <int DT, int DP, bool kFull> __global__ void __launch_bounds__(kThreads
     uint64_t before = 0;
     for (uint32_t s0 = 0; s0 < a.b.n_seqs; s0 += kThreads) {
         const uint32_t s = s0 + threadIdx.x;
-        const uint64_t mine = s < a.b.n_seqs ? work_of(a, read_seq(a.b, s, a.d_status, B, false)) : 0;
+        const uint64_t mine = s < a.b.n_seqs ? work_of<NT>(a, read_seq(a.b, s, a.d_status, B, false)) : 0;
         uint64_t all;
         const uint64_t upto = before + block_scan(mine, s_warp, all);
         if (mine && upto > w0 && upto - mine <= w0) s_seq = s, s_at = upto - mine;
@@ -528,7 +574,7 @@ template <int DT, int DP, bool kFull> __global__ void __launch_bounds__(kThreads
     uint64_t w = w0;
     while (w < w1) {
         const Seq seq = read_seq(a.b, s, a.d_status, B, false);
-        const uint64_t work = work_of(a, seq);
+        const uint64_t work = work_of<NT>(a, seq);
         if (w >= at + work) {
             at += work;
             s++;
@@ -540,7 +586,7 @@ template <int DT, int DP, bool kFull> __global__ void __launch_bounds__(kThreads
         const uint64_t tile = item / a.c.heads;
         const uint32_t h = uint32_t(item % a.c.heads);
         const bool whole = w == i0 && upto == i1;
-        piece<DT, DP, kFull>(a, smem, seq, tile, h, first_unit(a, seq) + uint32_t(w - i0), uint32_t(upto - w),
+        piece<DP, NT, kFull>(a, smem, seq, tile, h, first_unit(a, seq) + uint32_t(w - i0), uint32_t(upto - w),
                       whole ? nullptr : parts + 2 * cta + (w == i0 ? 1 : 0));
         if (!whole) {
             // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
@@ -549,54 +595,70 @@ template <int DT, int DP, bool kFull> __global__ void __launch_bounds__(kThreads
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
-                uint32_t *counter = a.counters + (slot_of(seq.first, s, a.group, kRows, 1) + tile) * a.c.heads + h;
+                uint32_t *counter = a.counters + (slot_of(seq.first, s, a.group, 8 * NT, 1) + tile) * a.c.heads + h;
                 const bool last = atomicAdd(counter, 1u) == c1 - c0;
                 if (last) *counter = 0;
                 s_last = last;
                 __threadfence();
             }
             __syncthreads();
-            if (s_last) join<DT, DP>(a, smem, seq, tile, h, parts, c0, c1 - c0 + 1);
+            if (s_last) join<DP, NT>(a, smem, seq, tile, h, parts, c0, c1 - c0 + 1);
         }
         __syncthreads();  // shared memory is free for the next piece
         w = upto;
     }
 }
 
-template <int DT, int DP, bool kFull> int launch(const AttendArgs &a, cudaStream_t s) {
+template <int DP, int NT, bool kFull> int launch(const AttendArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose kernel may use this much shared memory
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(rows_kernel<DT, DP, kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<DP>())) != cudaSuccess)
+        if (cudaFuncSetAttribute(rows_kernel<DP, NT, kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<DP, NT>())) != cudaSuccess)
             return ZC_ECUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    rows_kernel<DT, DP, kFull><<<rows_ctas(), kThreads, smem_bytes<DP>(), s>>>(a);
+    rows_kernel<DP, NT, kFull><<<uint32_t(sm_count() * resident(NT)), kThreads, smem_bytes<DP, NT>(), s>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
+}
+
+template <int NT> int launch_rows(const AttendArgs &a, cudaStream_t s) {
+    if (a.c.dim == 128) return launch<128, NT, true>(a, s);
+    if (a.c.dim == 64) return launch<64, NT, true>(a, s);
+    return a.c.dim < 64 ? launch<64, NT, false>(a, s) : launch<128, NT, false>(a, s);
+}
+
+template <int NT> uint64_t part_bytes(uint32_t dim) {
+    return uint64_t(sm_count()) * resident(NT) * 2 * (dim <= 64 ? sizeof(Part<64, NT>) : sizeof(Part<128, NT>));
+}
+
+// Tiles of 8 rows of an item: the fewest that hold a sequence's rows of a head.
+int tiles_for(const Batch &b, uint32_t group) {
+    const uint64_t rows = uint64_t(b.most) * group;
+    return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
 } // namespace
 
-uint32_t rows_ctas() { return uint32_t(sm_count()) * kResident; }
-
 uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group) {
-    return slots_of(b.total, b.n_seqs, group, kRows, 1) * c.heads;
+    return slots_of(b.total, b.n_seqs, group, 8 * tiles_for(b, group), 1) * c.heads;
 }
 
-uint64_t rows_part_bytes(uint32_t dim) {
-    return uint64_t(rows_ctas()) * 2 * (dim <= 64 ? sizeof(Part<64>) : sizeof(Part<128>));
+uint64_t rows_part_bytes(const Batch &b, const Cache &c, uint32_t group) {
+    switch (tiles_for(b, group)) {
+    case 1: return part_bytes<1>(c.dim);
+    case 2: return part_bytes<2>(c.dim);
+    default: return part_bytes<4>(c.dim);
+    }
 }
 
-template <int DT> static int launch_type(const AttendArgs &a, cudaStream_t s) {
-    if (a.c.dim == 128) return launch<DT, 128, true>(a, s);
-    if (a.c.dim == 64) return launch<DT, 64, true>(a, s);
-    return a.c.dim < 64 ? launch<DT, 64, false>(a, s) : launch<DT, 128, false>(a, s);
-}
-
-int launch_attend(int dtype, const AttendArgs &a, cudaStream_t s) {
-    return dtype == ZC_BF16 ? launch_type<ZC_BF16>(a, s) : launch_type<ZC_FP16>(a, s);
+int launch_attend(const AttendArgs &a, cudaStream_t s) {
+    switch (tiles_for(a.b, a.group)) {
+    case 1: return launch_rows<1>(a, s);
+    case 2: return launch_rows<2>(a, s);
+    default: return launch_rows<4>(a, s);
+    }
 }
 
 } // namespace kv
