@@ -58,6 +58,8 @@ int make_cache(const zc_kv_cache *c, Cache &o) {
     o.heads = c->kv_heads;
     o.tokens = c->block_tokens;
     o.dim = c->head_dim;
+    const uint64_t d = o.tokens / 16;
+    o.sixteenths = d == 1 ? 0 : uint32_t(((uint64_t(1) << 32) + d - 1) / d);
     return ZC_OK;
 }
 

@@ -28,6 +28,7 @@ struct Cache {
     int64_t block_stride;  // bytes
     int64_t scale_stride;  // floats
     uint32_t n_blocks, heads, tokens, dim;
+    uint32_t sixteenths;   // 2^32 / (tokens / 16), rounded up; 0 for 16 tokens
 };
 
 struct Batch {
@@ -135,6 +136,12 @@ __device__ __forceinline__ uint32_t find_seq(const Batch &b, uint64_t u, uint32_
     return s;
 }
 
+// Block of a position's 16 (i = position / 16 < 2^27): i / (tokens / 16). With M = 2^32 / d + e, e < 1, and d <= 16,
+// i M / 2^32 exceeds i / d by less than i / 2^32 < 1 / d: the floor is the same.
+__device__ __forceinline__ uint32_t block_of_16(const Cache &c, uint32_t i) {
+    return c.sixteenths ? __umulhi(i, c.sixteenths) : i;
+}
+
 // Block of the table, or -1 (reported) where the entry names none.
 __device__ __forceinline__ int64_t read_block(const Batch &b, const Cache &c, uint32_t s, uint32_t i, int32_t *d_status) {
     const int32_t e = __ldg(b.table + int64_t(s) * b.table_stride + i);
@@ -151,6 +158,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t v) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
     return r;
+}
+// Four codes to four halves, the low two and the high two.
+__device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t v, uint32_t &lo, uint32_t &hi) {
+    asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}" : "=r"(lo), "=r"(hi) : "r"(v));
 }
 // Two floats to two codes, to nearest even, saturating at +-448, NaN stays NaN.
 __device__ __forceinline__ uint16_t float2_to_e4m3x2(float lo, float hi) {

@@ -23,9 +23,9 @@
 // query row is exact in half too after it is multiplied by a power of two that
 // brings its largest element to [2^14, 2^15) (what falls below 2^-24 then is
 // 2^-38 of it). A row's weights w are rounded to half; they are kept in units
-// of the row's running maximum of s + log2 vs, not of s alone, so that the
-// largest contribution to the output is always 1 and blocks whose scales
-// differ by any factor keep their precision. The sum of the weights is taken
+// of the row's running maximum of s + log2 vs (to a factor of 2^8), not of s
+// alone, so that the largest contribution to the output is never below 1 and
+// blocks whose scales differ by any factor keep their precision. The sum of the weights is taken
 // before that rounding, in units of the running maximum of s.
 //
 // Each warp streams its own keys and values through shared memory with
@@ -46,6 +46,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kSlice = 16;              // keys of a warp's step
 constexpr int kUnit = kWarps * kSlice;  // keys of a unit of work
 constexpr float kNone = -INFINITY;
+constexpr float kSlack = 8.0f;          // how far (log2) the running maxima may lag behind
 
 // By tiles of 8 rows: CTAs of an SM, as many as their registers allow, and the
 // slices that fill the SM's shared memory.
@@ -240,11 +241,11 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
     constexpr int kChunks = DP / 16, kLaneRows = 32 / kChunks;
     const int lr = lane / kChunks, lc = lane % kChunks * 16;
     const bool col_ok = kFull || lc < int(D);
-    auto block_of = [&](int i) -> int64_t { return i < end ? read_block(a.b, a.c, s, uint32_t(i * kSlice) / B, a.d_status) : -1; };
+    auto block_of = [&](int i) -> int64_t { return i < end ? read_block(a.b, a.c, s, block_of_16(a.c, uint32_t(i)), a.d_status) : -1; };
     auto fetch = [&](int i, int64_t id, int st) {
         if (i < end) {
             const int key0 = i * kSlice;
-            const uint32_t in_block = uint32_t(key0) % B;
+            const uint32_t in_block = uint32_t(key0) - block_of_16(a.c, uint32_t(i)) * B;
             const bool whole = id >= 0 && key0 >= all_lo && key0 + kSlice <= all_hi;
             const bool none = id < 0;
             if (none) id = 0;
@@ -318,8 +319,9 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
-                const uint32_t kf[4] = {e4m3x2_to_half2(uint16_t(w0[k])), e4m3x2_to_half2(uint16_t(w1[k])),
-                                        e4m3x2_to_half2(uint16_t(w0[k] >> 16)), e4m3x2_to_half2(uint16_t(w1[k] >> 16))};
+                uint32_t kf[4];
+                e4m3x4_to_half2x2(w0[k], kf[0], kf[2]);
+                e4m3x4_to_half2x2(w1[k], kf[1], kf[3]);
 #pragma unroll
                 for (int n = 0; n < NT; n++) mma(sc[n], kf, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
             }
@@ -343,7 +345,8 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
                         if (key0 + g + 8 * j < lo || key0 + g + 8 * j >= hi) sc[n][2 * j + e] = kNone;
                 }
         }
-        // The maxima seldom grow after the first steps; while none does, nothing is rescaled.
+        // m and mw follow the maxima only once these are 2^kSlack above them: weights stay below 2^kSlack, which
+        // half holds as precisely, and after the first step a rescaling is rare.
         const float lvs = __log2f(vs);
         bool grows = false;
 #pragma unroll
@@ -351,7 +354,7 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const float top = fmaxf(sc[n][e], sc[n][2 + e]);
-                grows |= top > m[n][e] || top + lvs > mw[n][e];
+                grows |= top > m[n][e] + kSlack || top + lvs > mw[n][e] + kSlack;
             }
         if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
@@ -433,8 +436,9 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
         for (int c = 0; c < kCols; c += 2) {  // columns kCols g + c and + 1: rows g and g + 8 of the tile
             const uint32_t sel = (c & 3) | ((c & 3) + 4) << 4 | ((c & 3) + 1) << 8 | ((c & 3) + 5) << 12;
             const uint32_t b0 = __byte_perm(vw[0][c / 4], vw[1][c / 4], sel), b1 = __byte_perm(vw[2][c / 4], vw[3][c / 4], sel);
-            const uint32_t vf[4] = {e4m3x2_to_half2(uint16_t(b0)), e4m3x2_to_half2(uint16_t(b0 >> 16)),
-                                    e4m3x2_to_half2(uint16_t(b1)), e4m3x2_to_half2(uint16_t(b1 >> 16))};
+            uint32_t vf[4];
+            e4m3x4_to_half2x2(b0, vf[0], vf[1]);
+            e4m3x4_to_half2x2(b1, vf[2], vf[3]);
 #pragma unroll
             for (int n = 0; n < NT; n++) mma(o[n][c / 2], vf, pf[n][0], pf[n][1]);
         }
@@ -484,61 +488,66 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
 
 // An item's parts together: the `first` one in its CTA's second slot (a piece
 // that begins an item), the others in the first slots of the CTAs after it.
+// A thread takes 4 columns of a row and every kWays-th part, in runs whose
+// loads are in flight together; the ways meet in shared memory.
 template <int DP, int NT>
 __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
                                      const Part<DP, NT> *parts, uint32_t first, uint32_t n) {
-    constexpr int kRows = 8 * NT;
-    constexpr int kBatch = 64;  // parts whose factors are in shared memory at a time
-    float (*fo)[kRows] = reinterpret_cast<float (*)[kRows]>(smem);
-    float *sM = reinterpret_cast<float *>(fo + kBatch), *sW = sM + kRows, *sL = sW + kRows;
+    constexpr int kRows = 8 * NT, kCols = DP / 4, kRun = 8;
+    struct Way {
+        float4 x;
+        float m, mw, l;
+    };
+    Way *met = reinterpret_cast<Way *>(smem);
     const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
     const int rows = int(min(uint64_t(kRows), n_rows - row0)), D = int(a.c.dim);
+    const int jobs = rows * kCols;                             // 4 columns of a row each
+    const int ways = jobs >= kThreads ? 1 : kThreads / jobs;   // threads of a job
     auto part = [&](uint32_t i) -> const Part<DP, NT> & { return parts[2 * (first + i) + (i ? 0 : 1)]; };
-    // each row's units, by 8 threads (a warp's four rows are all in or all out of the loop: kRows is a multiple of 8)
-    for (int r = threadIdx.x / 8; r < kRows; r += kThreads / 8) {
-        const int k = threadIdx.x % 8;
-        const uint32_t group = 0xFFu << (threadIdx.x & 24);
-        float M = kNone, W = kNone, L = 0.0f;
-        if (r < rows)
-            for (uint32_t i = k; i < n; i += 8) M = fmaxf(M, __ldcg(&part(i).m[r])), W = fmaxf(W, __ldcg(&part(i).mw[r]));
+    auto add = [&](Way &w, float4 x, float m, float mw, float l) {
+        const float M = fmaxf(w.m, m), W = fmaxf(w.mw, mw);
+        const float f = ratio2(w.mw, W), g = ratio2(mw, W);
+        w.l = w.l * ratio2(w.m, M) + l * ratio2(m, M);
+        w.x = make_float4(w.x.x * f + x.x * g, w.x.y * f + x.y * g, w.x.z * f + x.z * g, w.x.w * f + x.w * g);
+        w.m = M, w.mw = W;
+    };
+    for (int j0 = 0; j0 < jobs; j0 += kThreads) {
+        const int job = ways == 1 ? j0 + int(threadIdx.x) : int(threadIdx.x) % jobs, way = ways == 1 ? 0 : int(threadIdx.x) / jobs;
+        const bool mine = job < jobs && way < ways;
+        const int r = job / kCols, col = job % kCols * 4;
+        Way w = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), kNone, kNone, 0.0f};
+        if (mine && col < D) {
+            uint32_t i = way;
+            for (; i + (kRun - 1) * ways < n; i += kRun * ways) {
+                float4 x[kRun];
+                float m[kRun], mw[kRun], l[kRun];
 #pragma unroll
-        for (int d = 1; d < 8; d *= 2) M = fmaxf(M, __shfl_xor_sync(group, M, d)), W = fmaxf(W, __shfl_xor_sync(group, W, d));
-        if (r < rows)
-            for (uint32_t i = k; i < n; i += 8) L += __ldcg(&part(i).l[r]) * ratio2(__ldcg(&part(i).m[r]), M);
+                for (int k = 0; k < kRun; k++) {
+                    const Part<DP, NT> &p = part(i + k * ways);
+                    x[k] = __ldcg(reinterpret_cast<const float4 *>(&p.o[r][col]));
+                    m[k] = __ldcg(&p.m[r]), mw[k] = __ldcg(&p.mw[r]), l[k] = __ldcg(&p.l[r]);
+                }
 #pragma unroll
-        for (int d = 1; d < 8; d *= 2) L += __shfl_xor_sync(group, L, d);
-        if (k == 0) sM[r] = M, sW[r] = W, sL[r] = L;
-    }
-    __syncthreads();
-    // 4 columns of a row a thread
-    constexpr int kCols = DP / 4, kMost = kRows * kCols / kThreads;
-    float4 x[kMost];
-#pragma unroll
-    for (int j = 0; j < kMost; j++) x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (uint32_t i0 = 0; i0 < n; i0 += kBatch) {
-        const uint32_t m = min(uint32_t(kBatch), n - i0);
-        for (uint32_t i = threadIdx.x; i < m * kRows; i += kThreads)
-            if (int(i % kRows) < rows) fo[i / kRows][i % kRows] = ratio2(__ldcg(&part(i0 + i / kRows).mw[i % kRows]), sW[i % kRows]);
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kMost; j++) {
-            const int r = (j * kThreads + threadIdx.x) / kCols, col = (j * kThreads + threadIdx.x) % kCols * 4;
-            if (r >= rows || col >= D) continue;
-#pragma unroll 8
-            for (uint32_t i = 0; i < m; i++) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(&part(i0 + i).o[r][col]));
-                const float f = fo[i][r];
-                x[j].x += v.x * f, x[j].y += v.y * f, x[j].z += v.z * f, x[j].w += v.w * f;
+                for (int k = 0; k < kRun; k++) add(w, x[k], m[k], mw[k], l[k]);
+            }
+            for (; i < n; i += ways) {
+                const Part<DP, NT> &p = part(i);
+                add(w, __ldcg(reinterpret_cast<const float4 *>(&p.o[r][col])), __ldcg(&p.m[r]), __ldcg(&p.mw[r]), __ldcg(&p.l[r]));
             }
         }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < kMost; j++) {
-        const int r = (j * kThreads + threadIdx.x) / kCols, col = (j * kThreads + threadIdx.x) % kCols * 4;
-        if (r >= rows || col >= D) continue;
-        const float y[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        emit(a, seq, h, row0 + r, col, y, sM[r], sW[r], sL[r]);
+        if (ways > 1) {
+            met[threadIdx.x] = w;
+            __syncthreads();
+            if (way == 0)
+                for (int k = 1; k < ways; k++) {
+                    const Way &v = met[threadIdx.x + k * jobs];
+                    add(w, v.x, v.m, v.mw, v.l);
+                }
+        }
+        if (mine && way == 0 && col < D) {
+            const float y[4] = {w.x.x, w.x.y, w.x.z, w.x.w};
+            emit(a, seq, h, row0 + r, col, y, w.m, w.mw, w.l);
+        }
     }
 }
 
@@ -592,14 +601,14 @@ template <int DP, int NT, bool kFull> __global__ void __launch_bounds__(kThreads
             // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
             // W c / G <= u < W (c + 1) / G, rounded down, so c = (u G + G - 1) / W
             const uint32_t c0 = uint32_t((i0 * G + G - 1) / W), c1 = uint32_t(((i1 - 1) * G + G - 1) / W);
-            __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
+                // releases the CTA's part (the barrier before it orders the other threads' writes) and acquires the others'
                 uint32_t *counter = a.counters + (slot_of(seq.first, s, a.group, 8 * NT, 1) + tile) * a.c.heads + h;
-                const bool last = atomicAdd(counter, 1u) == c1 - c0;
-                if (last) *counter = 0;
-                s_last = last;
-                __threadfence();
+                uint32_t done;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
+                if (done == c1 - c0) *counter = 0;
+                s_last = done == c1 - c0;
             }
             __syncthreads();
             if (s_last) join<DP, NT>(a, smem, seq, tile, h, parts, c0, c1 - c0 + 1);
