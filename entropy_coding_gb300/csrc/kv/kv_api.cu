@@ -20,6 +20,32 @@ int sm_count() {
     return sms;
 }
 
+int make_maps(const Cache &c, uint32_t columns, uint32_t rows, CodeMaps &m) {
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<Encode> known{nullptr};
+    Encode encode = known.load(std::memory_order_relaxed);
+    if (!encode) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess || !f)
+            return ZC_ECUDA;
+        encode = reinterpret_cast<Encode>(f);
+        known.store(encode, std::memory_order_relaxed);
+    }
+    const cuuint64_t size[3] = {c.dim, cuuint64_t(c.heads) * c.tokens, c.n_blocks};
+    const cuuint64_t stride[2] = {c.dim, cuuint64_t(c.block_stride)};
+    const cuuint32_t box[3] = {columns, rows, 1}, step[3] = {1, 1, 1};
+    for (int i = 0; i < 2; i++)
+        if (encode(&m.code[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.code[i], size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   columns == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return ZC_EINVAL;
+    return ZC_OK;
+}
+
 } // namespace kv
 } // namespace zc
 
@@ -46,6 +72,7 @@ int make_cache(const zc_kv_cache *c, Cache &o) {
     if (c->kv_heads == 0 || c->kv_heads > 65535 || c->n_blocks == 0 || c->n_blocks > 0x7FFFFFFFu) return ZC_EINVAL;
     const int64_t need = int64_t(c->kv_heads) * c->block_tokens * c->head_dim;
     if (c->block_stride < need || c->block_stride % 16 || c->scale_stride < int64_t(c->kv_heads)) return ZC_EINVAL;
+    if (c->block_stride >= int64_t(1) << 40) return ZC_EINVAL;  // of a tensor map
     if (c->block_stride > INT64_MAX / int64_t(c->n_blocks) || c->scale_stride > INT64_MAX / 4 / int64_t(c->n_blocks)) return ZC_EINVAL;
     if (!aligned(c->d_k, 16) || !aligned(c->d_v, 16) || !aligned(c->d_k_scale, 4) || !aligned(c->d_v_scale, 4)) return ZC_EINVAL;
     o.code[0] = static_cast<uint8_t *>(c->d_k);

@@ -9,6 +9,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -65,6 +66,14 @@ struct AttendArgs {
     void *parts;           // workspace: partial results
     int32_t *d_status;
 };
+
+// The codes as tensor maps, K and V: columns, rows of all heads, blocks; a box
+// is `rows` rows of `columns` bytes, swizzled over that width (64 or 128
+// bytes). Columns past head_dim are read as zeros.
+struct CodeMaps {
+    CUtensorMap code[2];
+};
+int make_maps(const Cache &c, uint32_t columns, uint32_t rows, CodeMaps &m);
 
 int launch_write(int dtype, const MoveArgs &a, cudaStream_t s);
 int launch_read(int dtype, const MoveArgs &a, cudaStream_t s);
@@ -148,6 +157,46 @@ __device__ __forceinline__ int64_t read_block(const Batch &b, const Cache &c, ui
     if (uint32_t(e) < c.n_blocks) return e;
     report(d_status, ZC_EFORMAT);
     return -1;
+}
+
+// ---------------------------------------------------------------------------
+// Copies by the tensor memory accelerator, and the barriers that they complete.
+
+constexpr long long kWaitClocks = 1ll << 31;  // about a second; a wait that takes longer is given up
+
+__device__ __forceinline__ uint32_t smem_of(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_init_done() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+// Orders this thread's accesses to shared memory before later ones by copies.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_of(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+                 : "=r"(ok) : "r"(smem_of(bar)), "r"(parity) : "memory");
+    return ok;
+}
+// Waits for the phase of that parity; false after kWaitClocks.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+    if (bar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!bar_try(bar, parity))
+        if (clock64() - t0 > kWaitClocks) return false;
+    return true;
+}
+__device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int row, int block, uint64_t *bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                     smem_of(dst)), "l"(map), "r"(0), "r"(row), "r"(block), "r"(smem_of(bar)) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // ---------------------------------------------------------------------------

@@ -28,12 +28,13 @@
 // blocks whose scales differ by any factor keep their precision. The sum of the weights is taken
 // before that rounding, in units of the running maximum of s.
 //
-// Each warp streams its own keys and values through shared memory with
-// cp.async, kStages slices of 16 rows deep, and the warps meet only at an
-// item's end. Rows are padded by 16 bytes, which spreads a fragment's reads over the
-// banks. Within a row the columns are dealt to the threads of a quad in runs
-// (the order of a product's inner index is free as long as both operands
-// share it), so that fragments are read 16 bytes at a time.
+// Each warp streams its own keys and values through a ring of slices of 16
+// rows in shared memory: one lane asks for two boxes a slice, and the warps
+// meet only at an item's end. The boxes are swizzled, which spreads a
+// fragment's reads over the banks. Within a row the columns are dealt to the
+// threads of a quad in runs (the order of a product's inner index is free as
+// long as both operands share it), so that fragments are read 16 bytes at a
+// time.
 #include <atomic>
 
 #include "kv_common.cuh"
@@ -54,12 +55,20 @@ constexpr int resident(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 constexpr int stages(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 6; }
 
 template <int DP> struct Stage {
-    uint8_t k[kSlice][DP + 16];
-    uint8_t v[kSlice][DP + 16];
-    float scale[4];  // ks, vs
+    uint8_t k[kSlice * DP];
+    uint8_t v[kSlice * DP];
 };
 
-template <int DP, int NT> struct Merge {  // over the stages, once the loop is done
+// What a warp keeps in shared memory besides its ring: the ring's barriers, and
+// the blocks and scales of 64 of its steps, read 32 at a time.
+constexpr int kAhead = 32;
+template <int NT> struct Warp {
+    uint64_t full[stages(NT)];
+    int32_t block[2 * kAhead];
+    float ks[2 * kAhead], vs[2 * kAhead];
+};
+
+template <int DP, int NT> struct Merge {  // over the rings, once the loop is done
     float o[kWarps][8 * NT][DP + 4];
     float m[kWarps][8 * NT], mw[kWarps][8 * NT], l[kWarps][8 * NT];
 };
@@ -75,16 +84,15 @@ template <int DP, int NT> constexpr size_t smem_bytes() {
     return a > b ? a : b;
 }
 
-__device__ __forceinline__ void cp16(void *dst, const void *src, bool take) {
-    const uint32_t d = uint32_t(__cvta_generic_to_shared(dst)), n = take ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+__device__ __forceinline__ void cp4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_of(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp4(void *dst, const void *src, bool take) {
-    const uint32_t d = uint32_t(__cvta_generic_to_shared(dst)), n = take ? 4 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Where a box holds 16-byte chunk c of row r: the swizzle of the tensor maps.
+template <int DP> __device__ __forceinline__ int chunk_at(int r, int c) {
+    return r * DP + 16 * (c ^ (DP == 128 ? r & 7 : r >> 1 & 3));
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -164,16 +172,18 @@ __device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32
 }
 
 // The piece [unit0, unit0 + units) of item (seq, tile, h); part: where its
-// partial result goes, or null if the piece is the whole item.
-template <int DP, int NT, bool kFull>
-__device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
-                                      uint32_t unit0, uint32_t units, Part<DP, NT> *part) {
+// partial result goes, or null if the piece is the whole item. `turn` counts
+// the warp's slices over all pieces. False if a wait was given up.
+template <int DP, int NT>
+__device__ __forceinline__ bool piece(const AttendArgs &a, const CodeMaps &maps, uint8_t *smem, Warp<NT> &wp, uint32_t &turn,
+                                      const Seq &seq, uint64_t tile, uint32_t h, uint32_t unit0, uint32_t units,
+                                      Part<DP, NT> *part) {
     constexpr int kRows = 8 * NT, kStages = stages(NT);
     constexpr int kSteps = DP / 16;      // inner steps of k q, and column tiles of the output
     constexpr int kRun = DP / 4;         // columns of q and k that a thread of a quad holds
     constexpr int kCols = DP / 8;        // columns of v that a thread's quad holds
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const uint32_t D = kFull ? DP : a.c.dim, B = a.c.tokens, s = seq.s;
+    const uint32_t D = a.c.dim, s = seq.s;
     const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
 
     // The keys that a row sees: [l, e).
@@ -235,41 +245,28 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
     const int end = min((all_hi + kSlice - 1) / kSlice, int((unit0 + units) * kWarps));
     int first = int(unit0) * kWarps + warp;
     if (first < all_lo / kSlice) first += (all_lo / kSlice - first + kWarps - 1) / kWarps * kWarps;
+    const int steps = first < end ? (end - first + kWarps - 1) / kWarps : 0;
 
-    // Fetches slice i, of block `id`, into stage st. A lane copies the same 16 columns of every
-    // kLaneRows-th row; rows outside the keys that someone sees, and columns from D on, are zeros.
-    constexpr int kChunks = DP / 16, kLaneRows = 32 / kChunks;
-    const int lr = lane / kChunks, lc = lane % kChunks * 16;
-    const bool col_ok = kFull || lc < int(D);
-    auto block_of = [&](int i) -> int64_t { return i < end ? read_block(a.b, a.c, s, block_of_16(a.c, uint32_t(i)), a.d_status) : -1; };
-    auto fetch = [&](int i, int64_t id, int st) {
-        if (i < end) {
-            const int key0 = i * kSlice;
-            const uint32_t in_block = uint32_t(key0) - block_of_16(a.c, uint32_t(i)) * B;
-            const bool whole = id >= 0 && key0 >= all_lo && key0 + kSlice <= all_hi;
-            const bool none = id < 0;
-            if (none) id = 0;
-            const int64_t off = id * a.c.block_stride + (int64_t(h) * B + in_block + lr) * D + (col_ok ? lc : 0);
-            const uint8_t *kp = a.c.code[0] + off, *vp = a.c.code[1] + off;
-            uint8_t *ks = &ring[st].k[lr][lc], *vs = &ring[st].v[lr][lc];
-            if (whole) {
-#pragma unroll
-                for (int j = 0; j < kSlice / kLaneRows; j++) {
-                    cp16(ks + j * kLaneRows * (DP + 16), kp + j * kLaneRows * D, col_ok);
-                    cp16(vs + j * kLaneRows * (DP + 16), vp + j * kLaneRows * D, col_ok);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kSlice / kLaneRows; j++) {
-                    const int key = key0 + lr + j * kLaneRows;
-                    const bool take = col_ok && !none && key >= all_lo && key < all_hi;
-                    cp16(ks + j * kLaneRows * (DP + 16), kp + j * kLaneRows * D, take);
-                    cp16(vs + j * kLaneRows * (DP + 16), vp + j * kLaneRows * D, take);
-                }
-            }
-            if (lane < 2) cp4(&ring[st].scale[lane], a.c.scale[lane] + id * a.c.scale_stride + h, !none);
+    // The blocks and scales of steps k0 .. k0 + 31, a step a lane. A block that is not there is read as block 0.
+    auto look_up = [&](int k0) {
+        const int k = k0 + lane;
+        if (k < steps) {
+            const int64_t id = max(read_block(a.b, a.c, s, block_of_16(a.c, uint32_t(first + k * kWarps)), a.d_status), int64_t(0));
+            const int at = k & (2 * kAhead - 1);
+            wp.block[at] = int32_t(id);
+            cp4(&wp.ks[at], a.c.scale[0] + id * a.c.scale_stride + h);
+            cp4(&wp.vs[at], a.c.scale[1] + id * a.c.scale_stride + h);
         }
-        cp_commit();
+    };
+    // Asks for step k's keys and values (one lane). Rows that nobody sees come along as they are.
+    auto fetch = [&](int k, uint32_t st) {
+        if (lane == 0 && k < steps) {
+            const uint32_t i = uint32_t(first + k * kWarps);
+            const int row = int(h * a.c.tokens + i * kSlice - block_of_16(a.c, i) * a.c.tokens), id = wp.block[k & (2 * kAhead - 1)];
+            bar_expect(&wp.full[st], sizeof(Stage<DP>));
+            copy_box(ring[st].k, &maps.code[0], row, id, &wp.full[st]);
+            copy_box(ring[st].v, &maps.code[1], row, id, &wp.full[st]);
+        }
     };
 
     float o[NT][kSteps][4];
@@ -287,26 +284,35 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
 #pragma unroll
         for (int e = 0; e < 2; e++) m[n][e] = mw[n][e] = kNone, unit[n][e] = l[n][e] = 0.0f;
 
-    int64_t id = block_of(first);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; i++) {
-        const int64_t next = block_of(first + (i + 1) * kWarps);
-        fetch(first + i * kWarps, id, i);
-        id = next;
-    }
-    int st = 0;
-    for (int i = first; i < end; i += kWarps) {
-        cp_wait<kStages - 2>();
-        __syncwarp();
-        // The stage before this one was read a step ago: it is fetched into, and the block of the
-        // fetch after that is looked up a step ahead of its use.
-        {
-            const int64_t next = block_of(i + kStages * kWarps);
-            fetch(i + (kStages - 1) * kWarps, id, st == 0 ? kStages - 1 : st - 1);
-            id = next;
+    look_up(0);
+    __syncwarp();
+    uint32_t st = turn % kStages, parity = turn / kStages & 1;  // of step k
+    for (int k = 0; k < kStages - 1; k++) fetch(k, (st + k) % kStages);
+    turn += uint32_t(steps);
+    bool ok = true;
+    for (int k = 0; k < steps; k++) {
+        if ((k & (kAhead - 1)) == 0) {
+            cp_wait_all();
+            __syncwarp();
+            look_up(k + kAhead);
         }
+        ok = bar_wait(&wp.full[st], parity);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+            // given up: what is still on its way is waited for (as long again), and the call reports it
+            ok = false;
+            for (int f = k; f < min(k + kStages - 1, steps); f++) {
+                bar_wait(&wp.full[st], parity);
+                if (++st == kStages) st = 0, parity ^= 1;
+            }
+            if (lane == 0) report(a.d_status, ZC_ETIMEOUT);
+            break;
+        }
+        // The stage before this one was read a step ago (the vote above comes after every lane's reads).
+        fetch(k + kStages - 1, st == 0 ? kStages - 1 : st - 1);
         Stage<DP> &sl = ring[st];
-        st = st + 1 == kStages ? 0 : st + 1;
+        if (++st == kStages) st = 0, parity ^= 1;
+        const int key0 = (first + k * kWarps) * kSlice;
+        const float ks = wp.ks[k & (2 * kAhead - 1)], vs = wp.vs[k & (2 * kAhead - 1)];
 
         // scores of 16 keys and the rows: c0, c1 are key g and rows 2t, 2t + 1, c2, c3 key g + 8
         float sc[NT][4];
@@ -314,8 +320,8 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
         for (int n = 0; n < NT; n++) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
 #pragma unroll
         for (int c = 0; c < kRun / 16; c++) {
-            const uint4 v0 = *reinterpret_cast<const uint4 *>(&sl.k[g][kRun * t + 16 * c]);
-            const uint4 v1 = *reinterpret_cast<const uint4 *>(&sl.k[8 + g][kRun * t + 16 * c]);
+            const uint4 v0 = *reinterpret_cast<const uint4 *>(&sl.k[chunk_at<DP>(g, kRun / 16 * t + c)]);
+            const uint4 v1 = *reinterpret_cast<const uint4 *>(&sl.k[chunk_at<DP>(8 + g, kRun / 16 * t + c)]);
             const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
@@ -326,9 +332,7 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
                 for (int n = 0; n < NT; n++) mma(sc[n], kf, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
             }
         }
-        const int key0 = i * kSlice;
         const bool edge = key0 < x_lo || key0 + kSlice > x_hi;  // some row does not see all of it
-        const float ks = sl.scale[0], vs = sl.scale[1];
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -397,11 +401,10 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             // A row that does not see a key has weight 0 for it, but 0 * NaN is NaN: NaN codes are
             // taken out here and given to the rows that do see them.
             bool bad = false;
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-#pragma unroll
-                for (int c = 0; c < kCols / 4; c++)
-                    bad |= any_nan(*reinterpret_cast<const uint32_t *>(&sl.v[keys[j]][kCols * g + 4 * c]));
+            for (int j = lane; j < kSlice * DP / 16; j += 32) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(&sl.v[16 * j]);
+                bad |= any_nan(v.x) || any_nan(v.y) || any_nan(v.z) || any_nan(v.w);
+            }
             if (__any_sync(0xFFFFFFFFu, bad)) {
                 for (int k = 0; k < kSlice; k++)
 #pragma unroll
@@ -410,14 +413,17 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
                         for (int e = 0; e < 2; e++) {
                             int lo, hi;
                             bounds(min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
-                            if (key0 + k < lo || key0 + k >= hi) continue;
+                            const bool sees = key0 + k >= lo && key0 + k < hi;
 #pragma unroll
-                            for (int c = 0; c < kCols; c++)
-                                if ((sl.v[k][kCols * g + c] & 0x7F) == 0x7F) o[n][c / 2][2 * (c & 1) + e] = NAN;
+                            for (int c = 0; c < kCols; c++) {
+                                const int col = kCols * g + c;
+                                if (sees && (sl.v[chunk_at<DP>(k, col / 16) + col % 16] & 0x7F) == 0x7F) o[n][c / 2][2 * (c & 1) + e] = NAN;
+                            }
                         }
                 __syncwarp();
                 for (int j = lane; j < kSlice * DP; j += 32)
-                    if ((sl.v[j / DP][j % DP] & 0x7F) == 0x7F) sl.v[j / DP][j % DP] = 0;
+                    if ((sl.v[j] & 0x7F) == 0x7F) sl.v[j] = 0;
+                fence_async();
                 __syncwarp();
             }
         }
@@ -425,10 +431,10 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             if (kCols == 16) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(&sl.v[keys[j]][16 * g]);
+                const uint4 v = *reinterpret_cast<const uint4 *>(&sl.v[chunk_at<DP>(keys[j], g)]);
                 vw[j][0] = v.x, vw[j][1] = v.y, vw[j][kCols / 4 - 2] = v.z, vw[j][kCols / 4 - 1] = v.w;
             } else {
-                const uint2 v = *reinterpret_cast<const uint2 *>(&sl.v[keys[j]][8 * g]);
+                const uint2 v = *reinterpret_cast<const uint2 *>(&sl.v[chunk_at<DP>(keys[j], g / 2) + 8 * (g & 1)]);
                 vw[j][0] = v.x, vw[j][1] = v.y;
             }
         }
@@ -443,10 +449,9 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             for (int n = 0; n < NT; n++) mma(o[n][c / 2], vf, pf[n][0], pf[n][1]);
         }
     }
-    cp_wait<0>();
 
     // The warps' rows together.
-    __syncthreads();
+    if (__syncthreads_or(!ok)) return false;
     Merge<DP, NT> &mg = *reinterpret_cast<Merge<DP, NT> *>(smem);
 #pragma unroll
     for (int n = 0; n < NT; n++)
@@ -484,6 +489,7 @@ __device__ __forceinline__ void piece(const AttendArgs &a, uint8_t *smem, const 
             emit(a, seq, h, row0 + r, col, x, M, W, L);
         }
     }
+    return true;
 }
 
 // An item's parts together: the `first` one in its CTA's second slot (a piece
@@ -551,8 +557,11 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const S
     }
 }
 
-template <int DP, int NT, bool kFull> __global__ void __launch_bounds__(kThreads, resident(NT)) rows_kernel(AttendArgs a) {
-    extern __shared__ __align__(16) uint8_t smem[];
+template <int DP, int NT>
+__global__ void __launch_bounds__(kThreads, resident(NT)) rows_kernel(const __grid_constant__ AttendArgs a,
+                                                                     const __grid_constant__ CodeMaps maps) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Warp<NT> s_warps[kWarps];
     __shared__ uint64_t s_warp[kWarps], s_at;
     __shared__ uint32_t s_seq;
     __shared__ int s_last;
@@ -576,6 +585,14 @@ template <int DP, int NT, bool kFull> __global__ void __launch_bounds__(kThreads
         before += all;
         if (before > w0) break;
     }
+    Warp<NT> &wp = s_warps[threadIdx.x / 32];
+    if (threadIdx.x % 32 == 0) {
+        for (int i = 0; i < stages(NT); i++) bar_init(&wp.full[i], 1);
+        bar_init_done();
+        prefetch_map(&maps.code[0]);
+        prefetch_map(&maps.code[1]);
+    }
+    uint32_t turn = 0;
     __syncthreads();
     uint32_t s = s_seq;
     uint64_t at = s_at;  // where the sequence's work begins
@@ -595,8 +612,9 @@ template <int DP, int NT, bool kFull> __global__ void __launch_bounds__(kThreads
         const uint64_t tile = item / a.c.heads;
         const uint32_t h = uint32_t(item % a.c.heads);
         const bool whole = w == i0 && upto == i1;
-        piece<DP, NT, kFull>(a, smem, seq, tile, h, first_unit(a, seq) + uint32_t(w - i0), uint32_t(upto - w),
-                      whole ? nullptr : parts + 2 * cta + (w == i0 ? 1 : 0));
+        if (!piece<DP, NT>(a, maps, smem, wp, turn, seq, tile, h, first_unit(a, seq) + uint32_t(w - i0), uint32_t(upto - w),
+                           whole ? nullptr : parts + 2 * cta + (w == i0 ? 1 : 0)))
+            return;
         if (!whole) {
             // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
             // W c / G <= u < W (c + 1) / G, rounded down, so c = (u G + G - 1) / W
@@ -613,29 +631,31 @@ template <int DP, int NT, bool kFull> __global__ void __launch_bounds__(kThreads
             __syncthreads();
             if (s_last) join<DP, NT>(a, smem, seq, tile, h, parts, c0, c1 - c0 + 1);
         }
-        __syncthreads();  // shared memory is free for the next piece
+        fence_async();
+        __syncthreads();  // shared memory is free for the next piece's copies
         w = upto;
     }
 }
 
-template <int DP, int NT, bool kFull> int launch(const AttendArgs &a, cudaStream_t s) {
+template <int DP, int NT> int launch(const AttendArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose kernel may use this much shared memory
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(rows_kernel<DP, NT, kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<DP, NT>())) != cudaSuccess)
+        if (cudaFuncSetAttribute(rows_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<DP, NT>())) != cudaSuccess)
             return ZC_ECUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    rows_kernel<DP, NT, kFull><<<uint32_t(sm_count() * resident(NT)), kThreads, smem_bytes<DP, NT>(), s>>>(a);
+    CodeMaps maps;
+    const int st = make_maps(a.c, DP, kSlice, maps);
+    if (st != ZC_OK) return st;
+    rows_kernel<DP, NT><<<uint32_t(sm_count() * resident(NT)), kThreads, smem_bytes<DP, NT>(), s>>>(a, maps);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }
 
 template <int NT> int launch_rows(const AttendArgs &a, cudaStream_t s) {
-    if (a.c.dim == 128) return launch<128, NT, true>(a, s);
-    if (a.c.dim == 64) return launch<64, NT, true>(a, s);
-    return a.c.dim < 64 ? launch<64, NT, false>(a, s) : launch<128, NT, false>(a, s);
+    return a.c.dim <= 64 ? launch<64, NT>(a, s) : launch<128, NT>(a, s);
 }
 
 template <int NT> uint64_t part_bytes(uint32_t dim) {
