@@ -49,10 +49,10 @@ constexpr int kUnit = kWarps * kSlice;  // keys of a unit of work
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.0f;          // how far (log2) the running maxima may lag behind
 
-// By tiles of 8 rows: CTAs of an SM, as many as their registers allow, and the
-// slices that fill the SM's shared memory.
-constexpr int resident(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
-constexpr int stages(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 6; }
+// By tiles of 8 rows: CTAs of an SM, as many as their registers allow, and
+// slices of a ring, as many as fit the SM's shared memory then.
+constexpr int resident(int nt) { return nt == 4 ? 2 : 3; }
+constexpr int stages(int dp, int nt) { return (nt == 4 ? 5 : 3) * (128 / dp); }
 
 template <int DP> struct Stage {
     uint8_t k[kSlice * DP];
@@ -62,15 +62,15 @@ template <int DP> struct Stage {
 // What a warp keeps in shared memory besides its ring: the ring's barriers, and
 // the blocks and scales of 64 of its steps, read 32 at a time.
 constexpr int kAhead = 32;
-template <int NT> struct Warp {
-    uint64_t full[stages(NT)];
+template <int S> struct Warp {
+    uint64_t full[S];
     int32_t block[2 * kAhead];
     float ks[2 * kAhead], vs[2 * kAhead];
 };
 
-template <int DP, int NT> struct Merge {  // over the rings, once the loop is done
-    float o[kWarps][8 * NT][DP + 4];
-    float m[kWarps][8 * NT], mw[kWarps][8 * NT], l[kWarps][8 * NT];
+template <int DP> struct Merge {  // 8 rows of each warp
+    float o[kWarps][8][DP + 4];
+    float m[kWarps][8], mw[kWarps][8], l[kWarps][8];
 };
 
 // A part of an item: rows in units of 2^mw (o) and 2^m (l).
@@ -79,10 +79,8 @@ template <int DP, int NT> struct Part {
     float m[8 * NT], mw[8 * NT], l[8 * NT];
 };
 
-template <int DP, int NT> constexpr size_t smem_bytes() {
-    const size_t a = sizeof(Stage<DP>) * stages(NT) * kWarps, b = sizeof(Merge<DP, NT>);
-    return a > b ? a : b;
-}
+template <int DP, int NT> constexpr size_t ring_bytes() { return sizeof(Stage<DP>) * stages(DP, NT) * kWarps; }
+template <int DP, int NT> constexpr size_t smem_bytes() { return ring_bytes<DP, NT>() + sizeof(Merge<DP>); }
 
 __device__ __forceinline__ void cp4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_of(dst)), "l"(src) : "memory");
@@ -171,32 +169,121 @@ __device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32
     if (a.lse && col == 0) a.lse[token * a.heads + head] = L == 0.0f ? kNone : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// The piece [unit0, unit0 + units) of item (seq, tile, h); part: where its
-// partial result goes, or null if the piece is the whole item. `turn` counts
-// the warp's slices over all pieces. False if a wait was given up.
-template <int DP, int NT>
-__device__ __forceinline__ bool piece(const AttendArgs &a, const CodeMaps &maps, uint8_t *smem, Warp<NT> &wp, uint32_t &turn,
-                                      const Seq &seq, uint64_t tile, uint32_t h, uint32_t unit0, uint32_t units,
-                                      Part<DP, NT> *part) {
-    constexpr int kRows = 8 * NT, kStages = stages(NT);
+// A piece of work: units of item (seq, tile, h) on the line of work, and what
+// this warp does of it.
+struct Job {
+    Seq seq;
+    uint64_t tile;
+    uint32_t h;
+    uint64_t w, upto, i0, i1;          // the piece [w, upto) of the item's [i0, i1)
+    int all_lo, all_hi, x_lo, x_hi;    // keys seen by some row; by every row
+    int first, steps;                  // this warp's slices: first, first + kWarps, ...
+    __device__ __forceinline__ bool whole() const { return w == i0 && upto == i1; }
+};
+
+// The keys [l, e) that a row sees.
+__device__ __forceinline__ void bounds(const AttendArgs &a, const Seq &seq, uint64_t row, int &l, int &e) {
+    const int64_t pos = int64_t(seq.len) - int64_t(seq.n) + int64_t(row / a.group);
+    e = int(a.causal ? max(pos + 1, int64_t(0)) : int64_t(seq.len));
+    l = a.window ? int(max(pos - int64_t(a.window) + 1, int64_t(0))) : 0;
+    if (l > e) l = e;
+}
+
+// The piece of work at w, whose sequence's work begins at `at` (both moved on).
+template <int NT>
+__device__ __forceinline__ bool next_job(const AttendArgs &a, uint64_t &w, uint64_t w1, uint32_t &s, uint64_t &at, Job &job) {
+    while (w < w1) {
+        const Seq seq = read_seq(a.b, s, a.d_status, a.c.tokens, false);
+        const uint64_t work = work_of<NT>(a, seq);
+        if (w >= at + work) {
+            at += work;
+            s++;
+            continue;
+        }
+        const uint32_t units = units_of(a, seq);
+        const uint64_t item = (w - at) / units;
+        job.seq = seq;
+        job.i0 = at + item * units;
+        job.i1 = job.i0 + units;
+        job.w = w;
+        job.upto = min(w1, job.i1);
+        job.tile = item / a.c.heads;
+        job.h = uint32_t(item % a.c.heads);
+        const uint64_t row0 = job.tile * 8 * NT, n_rows = uint64_t(seq.n) * a.group;
+        bounds(a, seq, row0, job.all_lo, job.x_hi);
+        bounds(a, seq, min(row0 + 8 * NT, n_rows) - 1, job.x_lo, job.all_hi);
+        const int unit0 = int(first_unit(a, seq) + uint32_t(w - job.i0)), warp = threadIdx.x >> 5;
+        const int end = min((job.all_hi + kSlice - 1) / kSlice, (unit0 + int(job.upto - w)) * kWarps);
+        job.first = unit0 * kWarps + warp;
+        if (job.first < job.all_lo / kSlice) job.first += (job.all_lo / kSlice - job.first + kWarps - 1) / kWarps * kWarps;
+        job.steps = job.first < end ? (end - job.first + kWarps - 1) / kWarps : 0;
+        w = job.upto;
+        return true;
+    }
+    return false;
+}
+
+// The blocks and scales of steps k0 .. k0 + 31, a step a lane. A block that is not there is read as block 0.
+template <class Warp> __device__ __forceinline__ void look_up(const AttendArgs &a, Warp &wp, const Job &job, int k0) {
+    const int k = k0 + (threadIdx.x & 31);
+    if (k >= job.steps) return;
+    const int64_t id = max(read_block(a.b, a.c, job.seq.s, block_of_16(a.c, uint32_t(job.first + k * kWarps)), a.d_status), int64_t(0));
+    const int at = k & (2 * kAhead - 1);
+    wp.block[at] = int32_t(id);
+    cp4(&wp.ks[at], a.c.scale[0] + id * a.c.scale_stride + job.h);
+    cp4(&wp.vs[at], a.c.scale[1] + id * a.c.scale_stride + job.h);
+}
+
+// Asks for step k's keys and values (one lane). Rows that nobody sees come along as they are.
+template <int DP, class Warp>
+__device__ __forceinline__ void fetch(const AttendArgs &a, const CodeMaps &maps, Warp &wp, Stage<DP> *ring, const Job &job, int k, uint32_t st) {
+    if ((threadIdx.x & 31) == 0 && k < job.steps) {
+        const uint32_t i = uint32_t(job.first + k * kWarps);
+        const int row = int(job.h * a.c.tokens + i * kSlice - block_of_16(a.c, i) * a.c.tokens), id = wp.block[k & (2 * kAhead - 1)];
+        bar_expect(&wp.full[st], sizeof(Stage<DP>));
+        copy_box(ring[st].k, &maps.code[0], row, id, &wp.full[st]);
+        copy_box(ring[st].v, &maps.code[1], row, id, &wp.full[st]);
+    }
+}
+
+// Looks up a piece's first steps and asks for the first of them. turn: the
+// warp's slices before the piece.
+template <int DP, int S>
+__device__ __forceinline__ void begin(const AttendArgs &a, const CodeMaps &maps, Warp<S> &wp, Stage<DP> *ring, const Job &job, uint32_t turn) {
+    look_up(a, wp, job, 0);
+    __syncwarp();
+    for (int k = 0; k < S - 1; k++) fetch<DP>(a, maps, wp, ring, job, k, (turn + k) % S);
+}
+
+// After a wait was given up: waits (as long again) for the warp's slices [turn, turn + n) that are on their way.
+template <int S> __device__ __forceinline__ void drain(Warp<S> &wp, uint32_t turn, int n) {
+    for (int k = 0; k < min(S - 1, n); k++) bar_wait(&wp.full[(turn + k) % S], (turn + k) / S & 1);
+}
+
+// All of the rows' work, as far as this warp's slices go.
+template <int DP, int NT> struct Rows32 {
+    float o[NT][DP / 16][4];
+    // Of rows 2t, 2t + 1 of each tile: running maxima (the scores', and with the value scales),
+    // 2^(m - mw), and the weights' sums over this thread's keys.
+    float m[NT][2], mw[NT][2], unit[NT][2], l[NT][2];
+};
+
+template <int DP, int NT, int S>
+__device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMaps &maps, Warp<S> &wp, Stage<DP> *ring, const Job &job,
+                                              uint32_t turn, Rows32<DP, NT> &acc) {
+    constexpr int kRows = 8 * NT;
     constexpr int kSteps = DP / 16;      // inner steps of k q, and column tiles of the output
     constexpr int kRun = DP / 4;         // columns of q and k that a thread of a quad holds
     constexpr int kCols = DP / 8;        // columns of v that a thread's quad holds
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const uint32_t D = a.c.dim, s = seq.s;
-    const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
-
-    // The keys that a row sees: [l, e).
-    const int64_t pos0 = int64_t(seq.len) - int64_t(seq.n);  // position of the sequence's first new token
-    auto bounds = [&](uint64_t row, int &l, int &e) {
-        const int64_t pos = pos0 + int64_t(row / a.group);
-        e = int(a.causal ? max(pos + 1, int64_t(0)) : int64_t(seq.len));
-        l = a.window ? int(max(pos - int64_t(a.window) + 1, int64_t(0))) : 0;
-        if (l > e) l = e;
-    };
-    int all_lo, all_hi, x_lo, x_hi;  // seen by some row; by every row
-    bounds(row0, all_lo, x_hi);
-    bounds(min(row0 + kRows, n_rows) - 1, x_lo, all_hi);
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t D = a.c.dim, h = job.h;
+    const Seq &seq = job.seq;
+    const uint64_t row0 = job.tile * kRows, n_rows = uint64_t(seq.n) * a.group;
+    auto &o = acc.o;
+    auto &m = acc.m;
+    auto &mw = acc.mw;
+    auto &unit = acc.unit;
+    auto &l = acc.l;
 
     // Query fragments: row g of each tile, columns [kRun t, kRun t + kRun).
     uint32_t qf[NT][kSteps][2];
@@ -240,84 +327,43 @@ __device__ __forceinline__ bool piece(const AttendArgs &a, const CodeMaps &maps,
         for (int i = 0; i < kSteps; i++) qf[n][i][0] = w[2 * i], qf[n][i][1] = w[2 * i + 1];
     }
 
-    Stage<DP> *ring = reinterpret_cast<Stage<DP> *>(smem) + warp * kStages;
-    // Slices of this warp: first, first + kWarps, ... below end.
-    const int end = min((all_hi + kSlice - 1) / kSlice, int((unit0 + units) * kWarps));
-    int first = int(unit0) * kWarps + warp;
-    if (first < all_lo / kSlice) first += (all_lo / kSlice - first + kWarps - 1) / kWarps * kWarps;
-    const int steps = first < end ? (end - first + kWarps - 1) / kWarps : 0;
-
-    // The blocks and scales of steps k0 .. k0 + 31, a step a lane. A block that is not there is read as block 0.
-    auto look_up = [&](int k0) {
-        const int k = k0 + lane;
-        if (k < steps) {
-            const int64_t id = max(read_block(a.b, a.c, s, block_of_16(a.c, uint32_t(first + k * kWarps)), a.d_status), int64_t(0));
-            const int at = k & (2 * kAhead - 1);
-            wp.block[at] = int32_t(id);
-            cp4(&wp.ks[at], a.c.scale[0] + id * a.c.scale_stride + h);
-            cp4(&wp.vs[at], a.c.scale[1] + id * a.c.scale_stride + h);
-        }
-    };
-    // Asks for step k's keys and values (one lane). Rows that nobody sees come along as they are.
-    auto fetch = [&](int k, uint32_t st) {
-        if (lane == 0 && k < steps) {
-            const uint32_t i = uint32_t(first + k * kWarps);
-            const int row = int(h * a.c.tokens + i * kSlice - block_of_16(a.c, i) * a.c.tokens), id = wp.block[k & (2 * kAhead - 1)];
-            bar_expect(&wp.full[st], sizeof(Stage<DP>));
-            copy_box(ring[st].k, &maps.code[0], row, id, &wp.full[st]);
-            copy_box(ring[st].v, &maps.code[1], row, id, &wp.full[st]);
-        }
-    };
-
-    float o[NT][kSteps][4];
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
         for (int i = 0; i < kSteps; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) o[n][i][j] = 0.0f;
-    // Of rows 2t, 2t + 1 of each tile: running maxima (the scores', and with the value scales),
-    // 2^(m - mw), and the weights' sums over this thread's keys.
-    float m[NT][2], mw[NT][2], unit[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
         for (int e = 0; e < 2; e++) m[n][e] = mw[n][e] = kNone, unit[n][e] = l[n][e] = 0.0f;
 
-    look_up(0);
-    __syncwarp();
-    uint32_t st = turn % kStages, parity = turn / kStages & 1;  // of step k
-    for (int k = 0; k < kStages - 1; k++) fetch(k, (st + k) % kStages);
-    turn += uint32_t(steps);
-    bool ok = true;
-    for (int k = 0; k < steps; k++) {
+    uint32_t st = turn % S, parity = turn / S & 1;  // of step k
+    for (int k = 0; k < job.steps; k++) {
         if ((k & (kAhead - 1)) == 0) {
             cp_wait_all();
             __syncwarp();
-            look_up(k + kAhead);
+            look_up(a, wp, job, k + kAhead);
         }
-        ok = bar_wait(&wp.full[st], parity);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-            // given up: what is still on its way is waited for (as long again), and the call reports it
-            ok = false;
-            for (int f = k; f < min(k + kStages - 1, steps); f++) {
-                bar_wait(&wp.full[st], parity);
-                if (++st == kStages) st = 0, parity ^= 1;
-            }
+        if (!__all_sync(0xFFFFFFFFu, bar_wait(&wp.full[st], parity))) {
+            drain(wp, turn + k, job.steps - k);
             if (lane == 0) report(a.d_status, ZC_ETIMEOUT);
-            break;
+            return false;
         }
         // The stage before this one was read a step ago (the vote above comes after every lane's reads).
-        fetch(k + kStages - 1, st == 0 ? kStages - 1 : st - 1);
+        fetch<DP>(a, maps, wp, ring, job, k + S - 1, st == 0 ? S - 1 : st - 1);
         Stage<DP> &sl = ring[st];
-        if (++st == kStages) st = 0, parity ^= 1;
-        const int key0 = (first + k * kWarps) * kSlice;
+        if (++st == S) st = 0, parity ^= 1;
+        const int key0 = (job.first + k * kWarps) * kSlice;
         const float ks = wp.ks[k & (2 * kAhead - 1)], vs = wp.vs[k & (2 * kAhead - 1)];
 
         // scores of 16 keys and the rows: c0, c1 are key g and rows 2t, 2t + 1, c2, c3 key g + 8
-        float sc[NT][4];
+        // (two sums for a single tile: half the chain of dependent products)
+        constexpr int kSums = NT == 1 ? 2 : 1;
+        float part_sc[kSums][NT][4], sc[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; n++) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+        for (int n = 0; n < kSums * NT; n++)
+            part_sc[n / NT][n % NT][0] = part_sc[n / NT][n % NT][1] = part_sc[n / NT][n % NT][2] = part_sc[n / NT][n % NT][3] = 0.0f;
 #pragma unroll
         for (int c = 0; c < kRun / 16; c++) {
             const uint4 v0 = *reinterpret_cast<const uint4 *>(&sl.k[chunk_at<DP>(g, kRun / 16 * t + c)]);
@@ -329,21 +375,22 @@ __device__ __forceinline__ bool piece(const AttendArgs &a, const CodeMaps &maps,
                 e4m3x4_to_half2x2(w0[k], kf[0], kf[2]);
                 e4m3x4_to_half2x2(w1[k], kf[1], kf[3]);
 #pragma unroll
-                for (int n = 0; n < NT; n++) mma(sc[n], kf, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
+                for (int n = 0; n < NT; n++) mma(part_sc[k % kSums][n], kf, qf[n][4 * c + k][0], qf[n][4 * c + k][1]);
             }
         }
-        const bool edge = key0 < x_lo || key0 + kSlice > x_hi;  // some row does not see all of it
+        const bool edge = key0 < job.x_lo || key0 + kSlice > job.x_hi;  // some row does not see all of it
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) sc[n][j] *= row_scale[n][j & 1] * ks;
+            for (int j = 0; j < 4; j++)
+                sc[n][j] = (kSums == 1 ? part_sc[0][n][j] : part_sc[0][n][j] + part_sc[kSums - 1][n][j]) * (row_scale[n][j & 1] * ks);
         if (edge) {
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     int lo, hi;
-                    bounds(min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
+                    bounds(a, seq, min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
 #pragma unroll
                     for (int j = 0; j < 2; j++)
                         if (key0 + g + 8 * j < lo || key0 + g + 8 * j >= hi) sc[n][2 * j + e] = kNone;
@@ -412,7 +459,7 @@ __device__ __forceinline__ bool piece(const AttendArgs &a, const CodeMaps &maps,
 #pragma unroll
                         for (int e = 0; e < 2; e++) {
                             int lo, hi;
-                            bounds(min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
+                            bounds(a, seq, min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
                             const bool sees = key0 + k >= lo && key0 + k < hi;
 #pragma unroll
                             for (int c = 0; c < kCols; c++) {
@@ -450,46 +497,56 @@ __device__ __forceinline__ bool piece(const AttendArgs &a, const CodeMaps &maps,
         }
     }
 
-    // The warps' rows together.
-    if (__syncthreads_or(!ok)) return false;
-    Merge<DP, NT> &mg = *reinterpret_cast<Merge<DP, NT> *>(smem);
+    return true;
+}
+
+// The warps' rows together, 8 at a time: into `part`, or finished.
+template <int DP, int NT>
+__device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const Job &job, Rows32<DP, NT> &acc, Part<DP, NT> *part) {
+    constexpr int kCols = DP / 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const uint64_t n_rows = uint64_t(job.seq.n) * a.group;
 #pragma unroll
-    for (int n = 0; n < NT; n++)
+    for (int n = 0; n < NT; n++) {
+        const uint64_t row0 = (job.tile * NT + n) * 8;
+        if (n && row0 >= n_rows) break;
+        if (n) __syncthreads();
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-            const int r = 8 * n + 2 * t + e;
+            const int r = 2 * t + e;
+            float l = acc.l[n][e];
 #pragma unroll
-            for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], d);
-            if (g == 0) mg.m[warp][r] = m[n][e], mg.mw[warp][r] = mw[n][e], mg.l[warp][r] = l[n][e];
+            for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+            if (g == 0) mg.m[warp][r] = acc.m[n][e], mg.mw[warp][r] = acc.mw[n][e], mg.l[warp][r] = l;
 #pragma unroll
-            for (int c = 0; c < kSteps; c += 2)
+            for (int c = 0; c < DP / 16; c += 2)
                 *reinterpret_cast<float4 *>(&mg.o[warp][r][kCols * g + 2 * c]) =
-                    make_float4(o[n][c][e], o[n][c][2 + e], o[n][c + 1][e], o[n][c + 1][2 + e]);
+                    make_float4(acc.o[n][c][e], acc.o[n][c][2 + e], acc.o[n][c + 1][e], acc.o[n][c + 1][2 + e]);
         }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRows * DP / 8; i += kThreads) {
-        const int r = i / (DP / 8), col = i % (DP / 8) * 8;
-        if (row0 + r >= n_rows || col >= int(D)) continue;
-        float M = kNone, W = kNone, L = 0.0f, x[8] = {};
+        __syncthreads();
+        for (int i = threadIdx.x; i < DP; i += kThreads) {
+            const int r = i / (DP / 8), col = i % (DP / 8) * 8;
+            if (row0 + r >= n_rows || col >= int(a.c.dim)) continue;
+            float M = kNone, W = kNone, L = 0.0f, x[8] = {};
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) M = fmaxf(M, mg.m[w][r]), W = fmaxf(W, mg.mw[w][r]);
+            for (int w = 0; w < kWarps; w++) M = fmaxf(M, mg.m[w][r]), W = fmaxf(W, mg.mw[w][r]);
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            L += mg.l[w][r] * ratio2(mg.m[w][r], M);
-            const float f = ratio2(mg.mw[w][r], W);
+            for (int w = 0; w < kWarps; w++) {
+                L += mg.l[w][r] * ratio2(mg.m[w][r], M);
+                const float f = ratio2(mg.mw[w][r], W);
 #pragma unroll
-            for (int k = 0; k < 8; k++) x[k] += mg.o[w][r][col + k] * f;
-        }
-        if (part) {
-            float4 *p = reinterpret_cast<float4 *>(&part->o[r][col]);
-            __stcg(p, make_float4(x[0], x[1], x[2], x[3]));
-            __stcg(p + 1, make_float4(x[4], x[5], x[6], x[7]));
-            if (col == 0) __stcg(&part->m[r], M), __stcg(&part->mw[r], W), __stcg(&part->l[r], L);
-        } else {
-            emit(a, seq, h, row0 + r, col, x, M, W, L);
+                for (int k = 0; k < 8; k++) x[k] += mg.o[w][r][col + k] * f;
+            }
+            if (part) {
+                float4 *p = reinterpret_cast<float4 *>(&part->o[8 * n + r][col]);
+                __stcg(p, make_float4(x[0], x[1], x[2], x[3]));
+                __stcg(p + 1, make_float4(x[4], x[5], x[6], x[7]));
+                if (col == 0) __stcg(&part->m[8 * n + r], M), __stcg(&part->mw[8 * n + r], W), __stcg(&part->l[8 * n + r], L);
+            } else {
+                emit(a, job.seq, job.h, row0 + r, col, x, M, W, L);
+            }
         }
     }
-    return true;
 }
 
 // An item's parts together: the `first` one in its CTA's second slot (a piece
@@ -499,7 +556,7 @@ __device__ __forceinline__ bool piece(const AttendArgs &a, const CodeMaps &maps,
 template <int DP, int NT>
 __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
                                      const Part<DP, NT> *parts, uint32_t first, uint32_t n) {
-    constexpr int kRows = 8 * NT, kCols = DP / 4, kRun = 8;
+    constexpr int kRows = 8 * NT, kCols = DP / 4, kRun = 16;
     struct Way {
         float4 x;
         float m, mw, l;
@@ -560,80 +617,85 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const S
 template <int DP, int NT>
 __global__ void __launch_bounds__(kThreads, resident(NT)) rows_kernel(const __grid_constant__ AttendArgs a,
                                                                      const __grid_constant__ CodeMaps maps) {
+    constexpr int S = stages(DP, NT);
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ Warp<NT> s_warps[kWarps];
+    __shared__ Warp<S> s_warps[kWarps];
     __shared__ uint64_t s_warp[kWarps], s_at;
     __shared__ uint32_t s_seq;
     __shared__ int s_last;
+    Merge<DP> &mg = *reinterpret_cast<Merge<DP> *>(smem + ring_bytes<DP, NT>());
     Part<DP, NT> *parts = reinterpret_cast<Part<DP, NT> *>(a.parts);
     const uint32_t B = a.c.tokens, cta = blockIdx.x;
 
+    Warp<S> &wp = s_warps[threadIdx.x / 32];
+    Stage<DP> *ring = reinterpret_cast<Stage<DP> *>(smem) + threadIdx.x / 32 * S;
+    if (threadIdx.x % 32 == 0) {
+        for (int i = 0; i < S; i++) bar_init(&wp.full[i], 1);
+        bar_init_done();
+        prefetch_map(&maps.code[0]);
+        prefetch_map(&maps.code[1]);
+    }
+
     // The line of work, and this CTA's piece [w0, w1) of it.
-    uint64_t sum = 0, W;
-    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += kThreads) sum += work_of<NT>(a, read_seq(a.b, s, a.d_status, B, cta == 0));
-    block_scan(sum, s_warp, W);
+    uint64_t mine = 0, sum, W;
+    for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += kThreads) {
+        const uint64_t work = work_of<NT>(a, read_seq(a.b, s, a.d_status, B, cta == 0));
+        mine += work;
+    }
+    sum = block_scan(mine, s_warp, W);
     const uint64_t G = min(uint64_t(gridDim.x), W);  // no CTA between two that have work is without
     if (cta >= G) return;
     const uint64_t w0 = W * cta / G, w1 = W * (cta + 1) / G;
     uint64_t before = 0;
     for (uint32_t s0 = 0; s0 < a.b.n_seqs; s0 += kThreads) {
-        const uint32_t s = s0 + threadIdx.x;
-        const uint64_t mine = s < a.b.n_seqs ? work_of<NT>(a, read_seq(a.b, s, a.d_status, B, false)) : 0;
-        uint64_t all;
-        const uint64_t upto = before + block_scan(mine, s_warp, all);
-        if (mine && upto > w0 && upto - mine <= w0) s_seq = s, s_at = upto - mine;
-        before += all;
+        if (a.b.n_seqs > kThreads) {  // more than one round: the sums above were not of single sequences
+            const uint32_t s = s0 + threadIdx.x;
+            mine = s < a.b.n_seqs ? work_of<NT>(a, read_seq(a.b, s, a.d_status, B, false)) : 0;
+            uint64_t all;
+            sum = before + block_scan(mine, s_warp, all);
+            before += all;
+        }
+        if (mine && sum > w0 && sum - mine <= w0) s_seq = s0 + threadIdx.x, s_at = sum - mine;
         if (before > w0) break;
     }
-    Warp<NT> &wp = s_warps[threadIdx.x / 32];
-    if (threadIdx.x % 32 == 0) {
-        for (int i = 0; i < stages(NT); i++) bar_init(&wp.full[i], 1);
-        bar_init_done();
-        prefetch_map(&maps.code[0]);
-        prefetch_map(&maps.code[1]);
-    }
-    uint32_t turn = 0;
     __syncthreads();
     uint32_t s = s_seq;
-    uint64_t at = s_at;  // where the sequence's work begins
+    uint64_t at = s_at, w = w0;  // where the sequence's work begins; where this CTA has got to
 
-    uint64_t w = w0;
-    while (w < w1) {
-        const Seq seq = read_seq(a.b, s, a.d_status, B, false);
-        const uint64_t work = work_of<NT>(a, seq);
-        if (w >= at + work) {
-            at += work;
-            s++;
-            continue;
-        }
-        const uint32_t units = units_of(a, seq);
-        const uint64_t item = (w - at) / units, i0 = at + item * units, i1 = i0 + units;
-        const uint64_t upto = min(w1, i1);
-        const uint64_t tile = item / a.c.heads;
-        const uint32_t h = uint32_t(item % a.c.heads);
-        const bool whole = w == i0 && upto == i1;
-        if (!piece<DP, NT>(a, maps, smem, wp, turn, seq, tile, h, first_unit(a, seq) + uint32_t(w - i0), uint32_t(upto - w),
-                           whole ? nullptr : parts + 2 * cta + (w == i0 ? 1 : 0)))
+    uint32_t turn = 0;  // slices that this warp has asked for
+    Job job, next;
+    bool more = next_job<NT>(a, w, w1, s, at, job);
+    begin<DP>(a, maps, wp, ring, job, turn);
+    while (more) {
+        Rows32<DP, NT> acc;
+        const bool ok = attend_slices<DP, NT>(a, maps, wp, ring, job, turn, acc);
+        turn += uint32_t(job.steps);
+        // The next piece's first slices are on their way while this one is finished.
+        more = next_job<NT>(a, w, w1, s, at, next);
+        if (more && ok) begin<DP>(a, maps, wp, ring, next, turn);
+        if (__syncthreads_or(!ok)) {
+            if (more && ok) drain(wp, turn, next.steps);
             return;
+        }
+        const bool whole = job.whole();
+        merge<DP, NT>(a, mg, job, acc, whole ? nullptr : parts + 2 * cta + (job.w == job.i0 ? 1 : 0));
         if (!whole) {
             // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
             // W c / G <= u < W (c + 1) / G, rounded down, so c = (u G + G - 1) / W
-            const uint32_t c0 = uint32_t((i0 * G + G - 1) / W), c1 = uint32_t(((i1 - 1) * G + G - 1) / W);
+            const uint32_t c0 = uint32_t((job.i0 * G + G - 1) / W), c1 = uint32_t(((job.i1 - 1) * G + G - 1) / W);
             __syncthreads();
             if (threadIdx.x == 0) {
                 // releases the CTA's part (the barrier before it orders the other threads' writes) and acquires the others'
-                uint32_t *counter = a.counters + (slot_of(seq.first, s, a.group, 8 * NT, 1) + tile) * a.c.heads + h;
+                uint32_t *counter = a.counters + (slot_of(job.seq.first, job.seq.s, a.group, 8 * NT, 1) + job.tile) * a.c.heads + job.h;
                 uint32_t done;
                 asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
                 if (done == c1 - c0) *counter = 0;
                 s_last = done == c1 - c0;
             }
             __syncthreads();
-            if (s_last) join<DP, NT>(a, smem, seq, tile, h, parts, c0, c1 - c0 + 1);
+            if (s_last) join<DP, NT>(a, reinterpret_cast<uint8_t *>(&mg), job.seq, job.tile, job.h, parts, c0, c1 - c0 + 1);
         }
-        fence_async();
-        __syncthreads();  // shared memory is free for the next piece's copies
-        w = upto;
+        job = next;
     }
 }
 
