@@ -146,12 +146,34 @@ extern "C" int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, in
     return move(false, cache, batch, dtype, k, v, d_status, stream);
 }
 
+namespace {
+
+// Which kernels a batch needs. A sequence's rows of a head are its new tokens times the group. Up to 16 of them the
+// cache's bytes are what counts, and the kernel that streams them does the work; more rows fill the tensor cores'
+// 128-row tiles. A batch of both kinds runs both, each on its own sequences; up to 8 sequences of uneven length are not
+// worth a second launch, and the tiles take them all.
+struct Plan {
+    bool rows, tiles;
+    uint64_t rows_counters, tiles_counters, part_bytes;
+    Plan(const Batch &b, const Cache &c, uint32_t group) {
+        tiles = uint64_t(b.most) * group > kRowsMost;
+        rows = !tiles || (b.n_seqs > 8 && uint64_t(b.n_seqs) * b.most != b.total);
+        rows_counters = rows ? pad256(4 * zc::kv::rows_counters(b, c, group)) : 0;
+        tiles_counters = tiles ? pad256(4 * zc::kv::tiles_counters(b, c, group)) : 0;
+        const uint64_t r = rows ? rows_part_bytes(c) : 0, t = tiles ? tiles_part_bytes(c) : 0;
+        part_bytes = r > t ? r : t;
+    }
+    uint64_t bytes() const { return rows_counters + tiles_counters + part_bytes; }
+};
+
+} // namespace
+
 extern "C" uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads) {
     Cache c{};
     Batch b{};
     if (make_cache(cache, c) != ZC_OK || make_batch(batch, b) != ZC_OK) return 0;
     if (heads == 0 || heads % c.heads || heads > 65535) return 0;
-    return pad256(4 * rows_counters(b, c, heads / c.heads)) + pad256(rows_part_bytes(b, c, heads / c.heads));
+    return Plan(b, c, heads / c.heads).bytes();
 }
 
 extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
@@ -170,14 +192,24 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
     a.heads = heads;
     a.dtype = dtype;
     a.group = heads / a.c.heads;
-    const uint64_t counters = pad256(4 * rows_counters(a.b, a.c, a.group));
+    const Plan plan(a.b, a.c, a.group);
     if (!d_ws || !aligned(d_ws, 16)) return ZC_EINVAL;
-    if (ws_bytes < counters + rows_part_bytes(a.b, a.c, a.group)) return ZC_ECAPACITY;
-    a.counters = static_cast<uint32_t *>(d_ws);
-    a.parts = static_cast<uint8_t *>(d_ws) + counters;
+    if (ws_bytes < plan.bytes()) return ZC_ECAPACITY;
+    uint8_t *ws = static_cast<uint8_t *>(d_ws);
+    a.parts = ws + plan.rows_counters + plan.tiles_counters;
+    a.rows_most = plan.rows ? kRowsMost : 0;
     a.scale_log2 = float(scale * 1.4426950408889634);
     a.causal = flags & ZC_KV_CAUSAL;
     a.window = window;
     a.d_status = d_status;
-    return launch_attend(a, static_cast<cudaStream_t>(stream));
+    cudaStream_t str = static_cast<cudaStream_t>(stream);
+    if (plan.tiles) {
+        a.counters = reinterpret_cast<uint32_t *>(ws + plan.rows_counters);
+        if ((st = launch_tiles(a, str)) != ZC_OK) return st;
+    }
+    if (plan.rows) {
+        a.counters = reinterpret_cast<uint32_t *>(ws);
+        st = launch_rows(a, str);
+    }
+    return st;
 }

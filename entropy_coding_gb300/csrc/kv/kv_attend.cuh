@@ -1,0 +1,88 @@
+// kv_attend.cuh — what the attention kernels share: arithmetic of weights,
+// the keys that a row sees, sums over a CTA, and finished rows.
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace zc {
+namespace kv {
+
+constexpr float kNone = -INFINITY;
+constexpr float kSlack = 8.0f;  // how far (log2) the running maxima may lag behind
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// 2^(a - b) with 2^(-inf - anything) = 0
+__device__ __forceinline__ float ratio2(float a, float b) { return a == kNone ? 0.0f : ex2(a - b); }
+// Whether one of the four codes is NaN (0x7F or 0xFF).
+__device__ __forceinline__ bool any_nan(uint32_t v) { return __vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0; }
+
+// The power of two that brings a bfloat16 row whose largest magnitude has these
+// float bits to [2^14, 2^15), and its inverse, within float's normal range.
+__device__ __forceinline__ void row_powers(uint32_t top, float &up, float &down) {
+    const int field = min(max(127 + 14 - (int(top >> 23) - 127), 1), 253);
+    up = __uint_as_float(uint32_t(field) << 23);
+    down = __uint_as_float(uint32_t(254 - field) << 23);
+}
+
+// The keys [l, e) that a row sees.
+__device__ __forceinline__ void bounds(const AttendArgs &a, const Seq &seq, uint64_t row, int &l, int &e) {
+    const int64_t pos = int64_t(seq.len) - int64_t(seq.n) + int64_t(row / a.group);
+    e = int(a.causal ? max(pos + 1, int64_t(0)) : int64_t(seq.len));
+    l = a.window ? int(max(pos - int64_t(a.window) + 1, int64_t(0))) : 0;
+    if (l > e) l = e;
+}
+
+// Inclusive sum over the threads up to this one; `total`: over all of the CTA's kWarps warps.
+template <int kWarps> __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t *s_warp, uint64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) v += s_warp[w];
+        total += s_warp[w];
+    }
+    return v;
+}
+
+// Two numbers of the output's type.
+__device__ __forceinline__ uint32_t pack_out(const AttendArgs &a, float x, float y) {
+    return a.dtype == ZC_BF16 ? pack2<ZC_BF16>(x, y) : pack2<ZC_FP16>(x, y);
+}
+
+// A finished row is its sum (in units of 2^W) by this factor: out = x / L in the units of M. A row that sees no key
+// is 0, whatever x holds. (L is NaN where a score was.)
+__device__ __forceinline__ float row_factor(float M, float W, float L) { return (W == kNone ? 0.0f : ex2(W - M)) / L; }
+__device__ __forceinline__ float row_lse(float M, float L) { return L == 0.0f ? kNone : (M + log2f(L)) * 0.6931471805599453f; }
+
+// n columns (a multiple of 4) of a finished row from `col` on.
+template <int n>
+__device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32_t h, uint64_t row, int col,
+                                     const float (&x)[n], float M, float W, float L) {
+    const float by = row_factor(M, W, L);
+    const int64_t token = int64_t(seq.first) + int64_t(row / a.group), head = int64_t(h) * a.group + int64_t(row % a.group);
+    uint16_t *o = static_cast<uint16_t *>(a.out.p) + token * a.out.token + head * a.out.head + col;
+#pragma unroll
+    for (int k = 0; k < n; k += 4)
+        *reinterpret_cast<uint2 *>(o + k) = L == 0.0f ? make_uint2(0, 0) : make_uint2(pack_out(a, x[k] * by, x[k + 1] * by),
+                                                                                      pack_out(a, x[k + 2] * by, x[k + 3] * by));
+    if (a.lse && col == 0) a.lse[token * a.heads + head] = row_lse(M, L);
+}
+
+} // namespace kv
+} // namespace zc

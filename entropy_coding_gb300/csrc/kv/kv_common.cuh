@@ -62,6 +62,7 @@ struct AttendArgs {
     int dtype;             // of q and out
     float scale_log2;      // softmax scale * log2(e)
     uint32_t causal, window;
+    uint32_t rows_most;    // a sequence of no more rows of a head goes to kv_rows.cu
     uint32_t *counters;    // workspace: an item's parts that are done, zero between calls
     void *parts;           // workspace: partial results
     int32_t *d_status;
@@ -78,10 +79,15 @@ int make_maps(const Cache &c, uint32_t columns, uint32_t rows, CodeMaps &m);
 int launch_write(int dtype, const MoveArgs &a, cudaStream_t s);
 int launch_read(int dtype, const MoveArgs &a, cudaStream_t s);
 int sm_count();
-// What attention's workspace holds: counters, and bytes of partial results.
+// Attention of sequences with at most rows_most rows of a head (kv_rows.cu) and
+// of those with more (kv_tiles.cu), and what their workspaces hold.
+constexpr uint32_t kRowsMost = 16;
 uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group);
-uint64_t rows_part_bytes(const Batch &b, const Cache &c, uint32_t group);
-int launch_attend(const AttendArgs &a, cudaStream_t s);
+uint64_t rows_part_bytes(const Cache &c);
+int launch_rows(const AttendArgs &a, cudaStream_t s);
+uint64_t tiles_counters(const Batch &b, const Cache &c, uint32_t group);
+uint64_t tiles_part_bytes(const Cache &c);
+int launch_tiles(const AttendArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
 

@@ -6,7 +6,7 @@
 //   s_ij = scale * ks_b(j) * (q_i . kc_j)
 //   out_i = sum_j 2^(s_ij log2e - m) vs_b(j) vc_j / sum_j 2^(s_ij log2e - m)
 //
-// An item is the rows (at most 32) of one sequence and key/value head. Decoding has few
+// An item is the rows (at most 16) of one sequence and key/value head. Decoding has few
 // items and long key axes, so items are cut along the keys: the batch's work
 // is one line of 64-key units, items one after another, and each CTA of a
 // resident grid takes an equal piece of it (a few whole items and a part of
@@ -35,9 +35,10 @@
 // threads of a quad in runs (the order of a product's inner index is free as
 // long as both operands share it), so that fragments are read 16 bytes at a
 // time.
+#include <algorithm>
 #include <atomic>
 
-#include "kv_common.cuh"
+#include "kv_attend.cuh"
 
 namespace zc {
 namespace kv {
@@ -46,13 +47,11 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kSlice = 16;              // keys of a warp's step
 constexpr int kUnit = kWarps * kSlice;  // keys of a unit of work
-constexpr float kNone = -INFINITY;
-constexpr float kSlack = 8.0f;          // how far (log2) the running maxima may lag behind
 
-// By tiles of 8 rows: CTAs of an SM, as many as their registers allow, and
-// slices of a ring, as many as fit the SM's shared memory then.
-constexpr int resident(int nt) { return nt == 4 ? 2 : 3; }
-constexpr int stages(int dp, int nt) { return (nt == 4 ? 5 : 3) * (128 / dp); }
+// CTAs of an SM, as many as their registers allow, and slices of a ring, as
+// many as fit the SM's shared memory then.
+constexpr int kResident = 3;
+constexpr int stages(int dp) { return 3 * (128 / dp); }
 
 template <int DP> struct Stage {
     uint8_t k[kSlice * DP];
@@ -79,7 +78,7 @@ template <int DP, int NT> struct Part {
     float m[8 * NT], mw[8 * NT], l[8 * NT];
 };
 
-template <int DP, int NT> constexpr size_t ring_bytes() { return sizeof(Stage<DP>) * stages(DP, NT) * kWarps; }
+template <int DP, int NT> constexpr size_t ring_bytes() { return sizeof(Stage<DP>) * stages(DP) * kWarps; }
 template <int DP, int NT> constexpr size_t smem_bytes() { return ring_bytes<DP, NT>() + sizeof(Merge<DP>); }
 
 __device__ __forceinline__ void cp4(void *dst, const void *src) {
@@ -103,20 +102,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t half2_of(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-// 2^(a - b) with 2^(-inf - anything) = 0
-__device__ __forceinline__ float ratio2(float a, float b) { return a == kNone ? 0.0f : ex2(a - b); }
-// Whether one of the four codes is NaN (0x7F or 0xFF).
-__device__ __forceinline__ bool any_nan(uint32_t v) { return __vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0; }
-
 // Units of work of a sequence's items (the same for all of them).
 __device__ __forceinline__ uint32_t first_unit(const AttendArgs &a, const Seq &q) {
     const int64_t lo = a.window ? int64_t(q.len) - int64_t(q.n) - int64_t(a.window) + 1 : 0;
@@ -126,47 +111,7 @@ __device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &q) 
     return max((uint32_t(q.len) + kUnit - 1) / kUnit, first_unit(a, q) + 1) - first_unit(a, q);
 }
 template <int NT> __device__ __forceinline__ uint64_t work_of(const AttendArgs &a, const Seq &q) {
-    return q.ok ? (uint64_t(q.n) * a.group + 8 * NT - 1) / (8 * NT) * a.c.heads * units_of(a, q) : 0;
-}
-
-// Inclusive sum of the threads before and including this one; `total`: of all.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t *s_warp, uint64_t &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const uint64_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
-        if (lane >= d) v += u;
-    }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-        if (w < warp) v += s_warp[w];
-        total += s_warp[w];
-    }
-    return v;
-}
-
-// Two numbers of the output's type.
-__device__ __forceinline__ uint32_t pack_out(const AttendArgs &a, float x, float y) {
-    return a.dtype == ZC_BF16 ? pack2<ZC_BF16>(x, y) : pack2<ZC_FP16>(x, y);
-}
-
-// n columns (4 or 8) of a finished row from `col` on, in units (M, W, L).
-template <int n>
-__device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32_t h, uint64_t row, int col,
-                                     const float (&x)[n], float M, float W, float L) {
-    // out = x / L in the units of M; a row that sees no key is 0. (L is NaN where a score was.)
-    const float by = L == 0.0f ? 0.0f : (W == kNone ? 0.0f : ex2(W - M)) / L;
-    const int64_t token = int64_t(seq.first) + int64_t(row / a.group), head = int64_t(h) * a.group + int64_t(row % a.group);
-    uint16_t *o = static_cast<uint16_t *>(a.out.p) + token * a.out.token + head * a.out.head + col;
-#pragma unroll
-    for (int k = 0; k < n; k += 4)
-        *reinterpret_cast<uint2 *>(o + k) = L == 0.0f ? make_uint2(0, 0) : make_uint2(pack_out(a, x[k] * by, x[k + 1] * by),
-                                                                                      pack_out(a, x[k + 2] * by, x[k + 3] * by));
-    if (a.lse && col == 0) a.lse[token * a.heads + head] = L == 0.0f ? kNone : (M + log2f(L)) * 0.6931471805599453f;
+    return q.ok && uint64_t(q.n) * a.group <= a.rows_most ? (uint64_t(q.n) * a.group + 8 * NT - 1) / (8 * NT) * a.c.heads * units_of(a, q) : 0;
 }
 
 // A piece of work: units of item (seq, tile, h) on the line of work, and what
@@ -180,14 +125,6 @@ struct Job {
     int first, steps;                  // this warp's slices: first, first + kWarps, ...
     __device__ __forceinline__ bool whole() const { return w == i0 && upto == i1; }
 };
-
-// The keys [l, e) that a row sees.
-__device__ __forceinline__ void bounds(const AttendArgs &a, const Seq &seq, uint64_t row, int &l, int &e) {
-    const int64_t pos = int64_t(seq.len) - int64_t(seq.n) + int64_t(row / a.group);
-    e = int(a.causal ? max(pos + 1, int64_t(0)) : int64_t(seq.len));
-    l = a.window ? int(max(pos - int64_t(a.window) + 1, int64_t(0))) : 0;
-    if (l > e) l = e;
-}
 
 // The piece of work at w, whose sequence's work begins at `at` (both moved on).
 template <int NT>
@@ -261,7 +198,7 @@ template <int S> __device__ __forceinline__ void drain(Warp<S> &wp, uint32_t tur
 }
 
 // All of the rows' work, as far as this warp's slices go.
-template <int DP, int NT> struct Rows32 {
+template <int DP, int NT> struct Sums {
     float o[NT][DP / 16][4];
     // Of rows 2t, 2t + 1 of each tile: running maxima (the scores', and with the value scales),
     // 2^(m - mw), and the weights' sums over this thread's keys.
@@ -270,7 +207,7 @@ template <int DP, int NT> struct Rows32 {
 
 template <int DP, int NT, int S>
 __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMaps &maps, Warp<S> &wp, Stage<DP> *ring, const Job &job,
-                                              uint32_t turn, Rows32<DP, NT> &acc) {
+                                              uint32_t turn, Sums<DP, NT> &acc) {
     constexpr int kRows = 8 * NT;
     constexpr int kSteps = DP / 16;      // inner steps of k q, and column tiles of the output
     constexpr int kRun = DP / 4;         // columns of q and k that a thread of a quad holds
@@ -311,9 +248,8 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
             for (int i = 0; i < kRun / 2; i++) top = max(top, max(w[i] << 16 & 0x7FFF0000u, w[i] & 0x7FFF0000u));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            // 2^(14 - e) for the largest element's exponent e, within float's normal range
-            const int field = min(max(127 + 14 - (int(top >> 23) - 127), 1), 253);
-            const float up = __uint_as_float(uint32_t(field) << 23), down = __uint_as_float(uint32_t(254 - field) << 23);
+            float up, down;
+            row_powers(top, up, down);
             scale = a.scale_log2 * down;
 #pragma unroll
             for (int i = 0; i < kRun / 2; i++) {
@@ -502,7 +438,7 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
 
 // The warps' rows together, 8 at a time: into `part`, or finished.
 template <int DP, int NT>
-__device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const Job &job, Rows32<DP, NT> &acc, Part<DP, NT> *part) {
+__device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const Job &job, Sums<DP, NT> &acc, Part<DP, NT> *part) {
     constexpr int kCols = DP / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const uint64_t n_rows = uint64_t(job.seq.n) * a.group;
@@ -615,9 +551,9 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const S
 }
 
 template <int DP, int NT>
-__global__ void __launch_bounds__(kThreads, resident(NT)) rows_kernel(const __grid_constant__ AttendArgs a,
+__global__ void __launch_bounds__(kThreads, kResident) rows_kernel(const __grid_constant__ AttendArgs a,
                                                                      const __grid_constant__ CodeMaps maps) {
-    constexpr int S = stages(DP, NT);
+    constexpr int S = stages(DP);
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Warp<S> s_warps[kWarps];
     __shared__ uint64_t s_warp[kWarps], s_at;
@@ -642,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) rows_kernel(const __gr
         const uint64_t work = work_of<NT>(a, read_seq(a.b, s, a.d_status, B, cta == 0));
         mine += work;
     }
-    sum = block_scan(mine, s_warp, W);
+    sum = block_scan<kWarps>(mine, s_warp, W);
     const uint64_t G = min(uint64_t(gridDim.x), W);  // no CTA between two that have work is without
     if (cta >= G) return;
     const uint64_t w0 = W * cta / G, w1 = W * (cta + 1) / G;
@@ -652,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) rows_kernel(const __gr
             const uint32_t s = s0 + threadIdx.x;
             mine = s < a.b.n_seqs ? work_of<NT>(a, read_seq(a.b, s, a.d_status, B, false)) : 0;
             uint64_t all;
-            sum = before + block_scan(mine, s_warp, all);
+            sum = before + block_scan<kWarps>(mine, s_warp, all);
             before += all;
         }
         if (mine && sum > w0 && sum - mine <= w0) s_seq = s0 + threadIdx.x, s_at = sum - mine;
@@ -667,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) rows_kernel(const __gr
     bool more = next_job<NT>(a, w, w1, s, at, job);
     begin<DP>(a, maps, wp, ring, job, turn);
     while (more) {
-        Rows32<DP, NT> acc;
+        Sums<DP, NT> acc;
         const bool ok = attend_slices<DP, NT>(a, maps, wp, ring, job, turn, acc);
         turn += uint32_t(job.steps);
         // The next piece's first slices are on their way while this one is finished.
@@ -712,44 +648,28 @@ template <int DP, int NT> int launch(const AttendArgs &a, cudaStream_t s) {
     CodeMaps maps;
     const int st = make_maps(a.c, DP, kSlice, maps);
     if (st != ZC_OK) return st;
-    rows_kernel<DP, NT><<<uint32_t(sm_count() * resident(NT)), kThreads, smem_bytes<DP, NT>(), s>>>(a, maps);
+    rows_kernel<DP, NT><<<uint32_t(sm_count() * kResident), kThreads, smem_bytes<DP, NT>(), s>>>(a, maps);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }
 
-template <int NT> int launch_rows(const AttendArgs &a, cudaStream_t s) {
+template <int NT> int launch_tiles_of(const AttendArgs &a, cudaStream_t s) {
     return a.c.dim <= 64 ? launch<64, NT>(a, s) : launch<128, NT>(a, s);
 }
 
 template <int NT> uint64_t part_bytes(uint32_t dim) {
-    return uint64_t(sm_count()) * resident(NT) * 2 * (dim <= 64 ? sizeof(Part<64, NT>) : sizeof(Part<128, NT>));
-}
-
-// Tiles of 8 rows of an item: the fewest that hold a sequence's rows of a head.
-int tiles_for(const Batch &b, uint32_t group) {
-    const uint64_t rows = uint64_t(b.most) * group;
-    return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    return uint64_t(sm_count()) * kResident * 2 * (dim <= 64 ? sizeof(Part<64, NT>) : sizeof(Part<128, NT>));
 }
 
 } // namespace
 
 uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group) {
-    return slots_of(b.total, b.n_seqs, group, 8 * tiles_for(b, group), 1) * c.heads;
+    return slots_of(b.total, b.n_seqs, group, 8, 1) * c.heads;
 }
 
-uint64_t rows_part_bytes(const Batch &b, const Cache &c, uint32_t group) {
-    switch (tiles_for(b, group)) {
-    case 1: return part_bytes<1>(c.dim);
-    case 2: return part_bytes<2>(c.dim);
-    default: return part_bytes<4>(c.dim);
-    }
-}
+uint64_t rows_part_bytes(const Cache &c) { return part_bytes<2>(c.dim); }
 
-int launch_attend(const AttendArgs &a, cudaStream_t s) {
-    switch (tiles_for(a.b, a.group)) {
-    case 1: return launch_rows<1>(a, s);
-    case 2: return launch_rows<2>(a, s);
-    default: return launch_rows<4>(a, s);
-    }
+int launch_rows(const AttendArgs &a, cudaStream_t s) {
+    return std::min<uint64_t>(uint64_t(a.b.most) * a.group, a.rows_most) <= 8 ? launch_tiles_of<1>(a, s) : launch_tiles_of<2>(a, s);
 }
 
 } // namespace kv

@@ -1,0 +1,697 @@
+// kv_tiles.cu — attention of many query rows (prompts, chunks of prompts,
+// longer drafts) over the 8-bit cache, on the fifth-generation tensor cores.
+//
+// An item is up to 256 rows of one sequence and key/value head, in two tiles
+// of 128 (a row is one query token and query head, as in kv_rows.cu). Over
+// tiles of 128 keys, with codes kc, vc and block scales ks, vs:
+//   S = Q Kc^T            128 x 128 x dim, half operands, float32 in tensor memory
+//   s_ij = S_ij ks_b c_i  (c_i: the row's power of two and the softmax scale, log2)
+//   w_ij = 2^(s_ij + log2 vs_b - mw_i), rounded to half, back into tensor memory
+//   O += W Vc             128 x dim x 128
+//   l_i += sum_b (sum_{j in b} w_ij before rounding) 2^(mw_i - m_i - log2 vs_b)
+// m_i and mw_i follow the row's maxima of s and of s + log2 vs (and may lag by
+// 2^8), so O is in units of the largest contribution and l in units of the
+// largest weight: block scales cost an exponent's bias for 16 columns, and no
+// spread between them loses precision. A block whose scale is 2^60 below the
+// unit adds less than 2^-51 of it and counts as 2^-60. out = O 2^(mw - m) / l.
+//
+// Work: as in kv_rows.cu, one line of key tiles over all items, an equal
+// piece for each of one CTA an SM; items cut by a piece's end leave partial
+// results, which the last CTA of the item joins.
+//
+// A CTA is 16 warps in roles, which meet at barriers in shared memory:
+//   warps 0-3, 4-7   a row a thread of the first and second tile: scores from
+//                    tensor memory, weights back, the output's rescaling and end
+//   warps 8-11       codes to halves, from the ring of code tiles to the ring of
+//                    operand tiles, swizzled over 128 bytes as the products read them
+//   warp 12          one thread issues the products, as operands and weights come
+//   warp 13          copies: 8 boxes of 16 keys a code tile, by block table
+// While one tile's rows turn scores into weights, the other tile's products
+// run: 4 products of 128 x 128 x 128 a key tile, 2048 clocks of the tensor
+// cores, against about 1000 issue slots of the weights and 300 of the codes on
+// each scheduler.
+#include <atomic>
+
+#include "kv_attend.cuh"
+
+namespace zc {
+namespace kv {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kTile = 128;              // rows of a tile, keys of a key tile
+constexpr int kRows = 2 * kTile;        // rows of an item
+constexpr int kBoxes = kTile / 16;      // boxes of a code tile
+constexpr int kRaw = 3, kOps = 3;       // rings of code tiles and operand tiles (keys and values in turn)
+constexpr int kSlots = 8;               // key tiles whose scales are held: the copies run up to 3 ahead of the weights
+constexpr uint32_t kColumns = 512;      // of tensor memory: S (and W in its place) 0, 128, O 256, 384
+
+struct Bars {
+    uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], scale_full[kSlots];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], rows, drained;
+};
+
+template <int DP> struct Smem {
+    uint8_t q[2][kTile * DP * 2];       // panels of 64 columns: 128-byte rows, swizzled
+    uint8_t op[kOps][kTile * DP * 2];
+    uint8_t raw[kRaw][kTile * DP];
+    float ks[kSlots][kBoxes], lvs[kSlots][kBoxes];
+    Bars bars;
+    uint64_t sums[kWarps], at;
+    uint32_t slot, seq, tmem;
+    int last, poison;
+};
+
+// A part of an item, rows in units of 2^mw (o) and 2^m (l), for a row a thread.
+template <int DP> struct Part {
+    float4 o[DP / 4][kRows];
+    float m[kRows], mw[kRows], l[kRows];
+};
+
+// ---------------------------------------------------------------------------
+// Tensor memory and tensor cores
+
+__device__ __forceinline__ void tm_load32(uint32_t at, float *x) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(x);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tm_store32(uint32_t at, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+                   "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+                   "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+__device__ __forceinline__ void tm_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Operand descriptors: 128-byte rows swizzled over 8-row atoms of 1024 bytes, atoms 1024 bytes apart. Of keys and
+// queries the rows are rows and the inner index runs along them (the leading offset is not used); of values the inner
+// index are the rows, and panels of 64 columns are `panel` bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t smem, uint32_t panel) {
+    return uint64_t(smem >> 4 & 0x3FFF) | uint64_t(panel >> 4 & 0x3FFF) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
+           uint64_t(2) << 61;
+}
+// Float32 sums of half products, 128 rows, n columns; the second operand's inner index along its rows or columns.
+__host__ __device__ constexpr uint32_t product(uint32_t n, bool values) {
+    return 1u << 4 | uint32_t(values) << 16 | n / 8 << 17 | 128u / 16 << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, uint32_t add) {
+    asm volatile("{.reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d), "l"(a),
+                 "l"(b), "r"(kind), "r"(add) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, uint32_t add) {
+    asm volatile("{.reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d), "r"(a),
+                 "l"(b), "r"(kind), "r"(add) : "memory");
+}
+// The barrier is arrived at when all products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {  // x, y = a0 b + c, a1 b + c
+    asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5}; fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}"
+        : "=f"(x), "=f"(y) : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+// ---------------------------------------------------------------------------
+// The line of work
+
+struct Job {
+    Seq seq;
+    uint64_t tile;
+    uint32_t h;
+    uint64_t w, upto, i0, i1;        // the piece [w, upto) of the item's [i0, i1)
+    int all_lo, all_hi, x_lo, x_hi;  // keys seen by some row; by every row
+    int j0, n;                       // key tiles of the piece
+    int tiles;                       // of 128 rows
+    __device__ __forceinline__ bool whole() const { return w == i0 && upto == i1; }
+    __device__ __forceinline__ bool edge(int j) const { return j * kTile < x_lo || (j + 1) * kTile > x_hi; }
+};
+
+__device__ __forceinline__ void see(const AttendArgs &a, Job &job) {
+    const uint64_t row0 = job.tile * kRows, n_rows = uint64_t(job.seq.n) * a.group;
+    bounds(a, job.seq, row0, job.all_lo, job.x_hi);
+    bounds(a, job.seq, min(row0 + kRows, n_rows) - 1, job.x_lo, job.all_hi);
+    job.tiles = n_rows - row0 > kTile ? 2 : 1;
+}
+__device__ __forceinline__ uint32_t units_of(const Job &job) {
+    return uint32_t(max((job.all_hi + kTile - 1) / kTile - job.all_lo / kTile, 1));
+}
+
+// Work of a slot (sequence and item of 256 rows) over all heads, in key tiles; 0 if it is empty or not this kernel's.
+__device__ __forceinline__ uint64_t work_of(const AttendArgs &a, const Seq &seq, uint64_t tile, Job &job) {
+    const uint64_t n_rows = uint64_t(seq.n) * a.group;
+    if (!seq.ok || n_rows <= a.rows_most || tile * kRows >= n_rows) return 0;
+    job.seq = seq;
+    job.tile = tile;
+    see(a, job);
+    return uint64_t(units_of(job)) * a.c.heads;
+}
+
+// The sequence that slot u belongs to, by halving.
+__device__ __forceinline__ uint32_t seq_of_slot(const AttendArgs &a, uint64_t u) {
+    uint32_t lo = 0, hi = a.b.n_seqs;
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (slot_of(uint32_t(max(__ldg(a.b.cu + mid), 0)), mid, a.group, kRows, 1) <= u) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Where a role has got to on the line: every role walks the same pieces.
+struct Walk {
+    uint64_t w, w1, at, slot;  // next work; the end; where the slot's work begins
+    uint32_t s;
+    __device__ __forceinline__ bool next(const AttendArgs &a, Job &job) {
+        while (w < w1) {
+            const Seq seq = read_seq(a.b, s, a.d_status, a.c.tokens, false);
+            const uint64_t first = slot_of(uint32_t(max(__ldg(a.b.cu + s), 0)), s, a.group, kRows, 1);
+            const uint64_t work = work_of(a, seq, slot - first, job);
+            if (w >= at + work) {
+                at += work;
+                slot++;
+                while (s + 1 < a.b.n_seqs && slot_of(uint32_t(max(__ldg(a.b.cu + s + 1), 0)), s + 1, a.group, kRows, 1) <= slot) s++;
+                continue;
+            }
+            const uint32_t units = units_of(job);
+            const uint64_t item = (w - at) / units;
+            job.h = uint32_t(item);
+            job.i0 = at + item * units;
+            job.i1 = job.i0 + units;
+            job.w = w;
+            job.upto = min(w1, job.i1);
+            job.j0 = job.all_lo / kTile + int(w - job.i0);
+            job.n = max(min(int(job.upto - w), (job.all_hi + kTile - 1) / kTile - job.j0), 0);
+            w = job.upto;
+            return true;
+        }
+        return false;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Roles. Each returns false if a wait was given up.
+
+template <int DP>
+__device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &maps, Smem<DP> &sm, Walk walk) {
+    const int lane = threadIdx.x & 31;
+    uint32_t item = 0, tile = 0;
+    bool ok = true;
+    Job job;
+    while (ok && walk.next(a, job)) {
+        const int least = job.all_lo / 16, last = (job.all_hi - 1) / 16;  // boxes without a key that is seen hold others again
+        for (int j = job.j0; j < job.j0 + job.n && ok; j++, tile++) {
+            const int slot = tile % kSlots;
+            int id = 0, row = 0;
+            if (lane < kBoxes) {
+                const uint32_t i = uint32_t(min(max(j * kBoxes + lane, least), last)), blk = block_of_16(a.c, i);
+                id = int(max(read_block(a.b, a.c, job.seq.s, blk, a.d_status), int64_t(0)));
+                row = int(job.h * a.c.tokens + i * 16 - blk * a.c.tokens);
+                const int64_t at = id * a.c.scale_stride + job.h;
+                sm.ks[slot][lane] = __ldg(a.c.scale[0] + at);
+                sm.lvs[slot][lane] = __log2f(__ldg(a.c.scale[1] + at));
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.bars.scale_full[slot]);
+#pragma unroll
+            for (int kv = 0; kv < 2 && ok; kv++, item++) {
+                const int r = item % kRaw;
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.raw_empty[r], (item / kRaw & 1) ^ 1));
+                if (!ok) break;
+                if (lane == 0) bar_expect(&sm.bars.raw_full[r], kTile * DP);
+                __syncwarp();
+                if (lane < kBoxes) copy_box(sm.raw[r] + lane * 16 * DP, &maps.code[kv], row, id, &sm.bars.raw_full[r]);
+            }
+        }
+    }
+    // The CTA outlives its copies, also those of a call that is given up.
+    for (uint32_t k = item > kRaw ? item - kRaw : 0; k < item; k++) ok &= bar_wait(&sm.bars.raw_full[k % kRaw], k / kRaw & 1);
+    return ok;
+}
+
+template <int DP> __device__ __forceinline__ bool convert_role(const AttendArgs &a, Smem<DP> &sm, Walk walk) {
+    const int t = threadIdx.x - 256, lane = t & 31;
+    uint32_t item = 0;
+    Job job;
+    while (walk.next(a, job)) {
+        for (int j = job.j0; j < job.j0 + job.n; j++)
+#pragma unroll 1
+            for (int kv = 0; kv < 2; kv++, item++) {
+                const int r = item % kRaw, c = item % kOps;
+                if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.raw_full[r], item / kRaw & 1) &&
+                                                 bar_wait(&sm.bars.op_empty[c], (item / kOps & 1) ^ 1)))
+                    return false;
+                // A row that does not see a key has weight 0 for it, but 0 * NaN is NaN: where some row does not see all
+                // keys, NaN codes of values are taken out, and rows that see them get them at the end.
+                const bool edge = kv && job.edge(j);
+                constexpr int kChunks = DP / 16;
+#pragma unroll
+                for (int i = 0; i < kTile * kChunks / 128; i++) {
+                    // 8 lanes take 8 rows of one chunk: reads and writes of a quarter warp meet all banks
+                    const int u = i * 128 + t, row = u % 8 + u / (8 * kChunks) * 8, ch = u / 8 % kChunks;
+                    uint4 v = *reinterpret_cast<const uint4 *>(sm.raw[r] + row * DP + 16 * (ch ^ (DP == 128 ? row & 7 : row >> 1 & 3)));
+                    if (edge && (any_nan(v.x) || any_nan(v.y) || any_nan(v.z) || any_nan(v.w))) {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                        for (int k = 0; k < 4; k++) w[k] &= ~__vcmpeq4(w[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        if (j * kTile + row >= job.all_lo && j * kTile + row < job.all_hi) sm.poison = 1;
+                    }
+                    uint4 lo, hi;
+                    e4m3x4_to_half2x2(v.x, lo.x, lo.y);
+                    e4m3x4_to_half2x2(v.y, lo.z, lo.w);
+                    e4m3x4_to_half2x2(v.z, hi.x, hi.y);
+                    e4m3x4_to_half2x2(v.w, hi.z, hi.w);
+                    uint8_t *dst = sm.op[c] + ch / 4 * (kTile * 128) + row * 128;
+                    const int q = ch % 4 * 2;
+                    *reinterpret_cast<uint4 *>(dst + 16 * (q ^ (row & 7))) = lo;
+                    *reinterpret_cast<uint4 *>(dst + 16 * ((q + 1) ^ (row & 7))) = hi;
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sm.bars.raw_empty[r]), bar_arrive(&sm.bars.op_full[c]);
+            }
+    }
+    return true;
+}
+
+// One thread.
+template <int DP> __device__ __forceinline__ bool product_role(const AttendArgs &a, Smem<DP> &sm, Walk walk) {
+    constexpr uint32_t kPanel = kTile * 128;
+    const uint32_t tm = sm.tmem;
+    uint32_t item = 0, queries[2] = {0, 0}, weights[2] = {0, 0};
+    auto scores = [&](int t, uint32_t c) {
+        const uint64_t q = operand(smem_of(sm.q[t]), 0), k = operand(smem_of(sm.op[c]), 0);
+#pragma unroll
+        for (int i = 0; i < DP / 16; i++) {  // 16 columns: 32 bytes on within a panel
+            const uint32_t at = (i / 4 * kPanel + i % 4 * 32) >> 4;
+            mma_ss(tm + t * 128, q + at, k + at, product(kTile, false), i > 0);
+        }
+    };
+    auto sums = [&](int t, uint32_t c, bool add) {
+        const uint64_t v = operand(smem_of(sm.op[c]), kPanel);
+#pragma unroll
+        for (int i = 0; i < kTile / 16; i++)  // 16 keys: 8 columns of weights, 16 rows of values
+            mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * i, v + (i * 16 * 128 >> 4), product(DP, true), add || i > 0);
+    };
+    bool ok = true;
+    Job job;
+    while (ok && walk.next(a, job)) {
+        if (!job.n) continue;
+        ok = bar_wait(&sm.bars.op_full[item % kOps], item / kOps & 1);
+        for (int t = 0; t < job.tiles && ok; t++) {
+            ok = bar_wait(&sm.bars.q_full[t], queries[t]++ & 1);
+            if (!ok) break;
+            tm_after();
+            scores(t, item % kOps);
+            mma_commit(&sm.bars.s_full[t]);
+        }
+        if (!ok) break;
+        mma_commit(&sm.bars.op_empty[item % kOps]);
+        item++;
+        for (int j = 0; j < job.n && ok; j++) {
+            const uint32_t v = item, k = item + 1;
+            item += j + 1 < job.n ? 2 : 1;
+            ok = bar_wait(&sm.bars.op_full[v % kOps], v / kOps & 1);
+            for (int t = 0; t < job.tiles && ok; t++) {
+                ok = bar_wait(&sm.bars.p_full[t], weights[t]++ & 1);
+                if (!ok) break;
+                tm_after();
+                sums(t, v % kOps, j > 0);
+                if (t == job.tiles - 1) mma_commit(&sm.bars.op_empty[v % kOps]);
+                if (j + 1 < job.n) {
+                    if (t == 0) ok = bar_wait(&sm.bars.op_full[k % kOps], k / kOps & 1);
+                    if (!ok) break;
+                    tm_after();
+                    scores(t, k % kOps);
+                    mma_commit(&sm.bars.s_full[t]);
+                    if (t == job.tiles - 1) mma_commit(&sm.bars.op_empty[k % kOps]);
+                } else {
+                    mma_commit(&sm.bars.o_full[t]);
+                }
+            }
+        }
+    }
+    // Tensor memory is freed once the products are done, also those of a call that is given up.
+    mma_commit(&sm.bars.drained);
+    return bar_wait(&sm.bars.drained, 0) && ok;
+}
+
+// Columns [col, col + 32) of values that are NaN at keys that the row [lo, hi) sees, among the piece's key tiles where
+// NaN was taken out; a bit a column.
+__device__ __forceinline__ uint32_t poisoned(const AttendArgs &a, const Job &job, int lo, int hi, int col) {
+    uint32_t mask = 0;
+    for (int j = job.j0; j < job.j0 + job.n; j++) {
+        if (!job.edge(j)) continue;
+        for (int key = max(j * kTile, lo); key < min((j + 1) * kTile, hi); key++) {
+            const uint32_t blk = block_of_16(a.c, uint32_t(key) / 16);
+            const int64_t id = max(read_block(a.b, a.c, job.seq.s, blk, a.d_status), int64_t(0));
+            const uint8_t *v = a.c.code[1] + id * a.c.block_stride + (int64_t(job.h) * a.c.tokens + (key - blk * a.c.tokens)) * a.c.dim + col;
+            for (int i = 0; i < min(32, int(a.c.dim) - col); i++)
+                if ((__ldg(v + i) & 0x7F) == 0x7F) mask |= 1u << i;
+        }
+    }
+    return mask;
+}
+
+// The 256 row threads meet; false if that was given up.
+__device__ __forceinline__ bool rows_meet(uint64_t *bar, uint32_t turn) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, turn & 1));
+}
+
+template <int DP>
+__device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Walk walk, uint64_t W, uint64_t G, Part<DP> *parts) {
+    const int r = threadIdx.x, half = r / kTile;                 // row of the item; its tile
+    const int lane = r & 31;
+    const uint32_t lanes = uint32_t(r / 32 % 4 * 32) << 16;      // of tensor memory
+    const uint32_t tmS = sm.tmem + half * 128 + lanes, tmO = sm.tmem + 256 + half * 128 + lanes;
+    uint32_t tile = 0, scored = 0, summed = 0, met = 0;
+    Job job;
+    while (walk.next(a, job)) {
+        const uint64_t row = job.tile * kRows + r, n_rows = uint64_t(job.seq.n) * a.group;
+        const bool mine = row < n_rows;
+        const int64_t token = int64_t(job.seq.first) + int64_t(row / a.group), head = int64_t(job.h) * a.group + int64_t(row % a.group);
+        const uint16_t *src = static_cast<const uint16_t *>(a.q.p) + token * a.q.token + head * a.q.head;
+        int lo = 0, hi = 0;
+        if (mine) bounds(a, job.seq, row, lo, hi);
+        float m = kNone, mw = kNone, l = 0.0f;
+        if (job.n && half >= job.tiles) tile += job.n;  // no rows in this tile
+        if (job.n && half < job.tiles) {
+            // The query row, exact in half by a power of two, with the sign of the scale.
+            const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+            float c = fabsf(a.scale_log2), up = 1.0f;
+            if (a.dtype == ZC_BF16) {
+                uint32_t top = 0;
+                if (mine)
+                    for (uint32_t i = 0; i < a.c.dim; i += 8) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + i));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; k++) top = max(top, max(w[k] << 16 & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+                    }
+                float down;
+                row_powers(top, up, down);
+                c *= down;
+            }
+#pragma unroll 4
+            for (int i = 0; i < DP / 8; i++) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (mine && i * 8 < int(a.c.dim)) v = __ldg(reinterpret_cast<const uint4 *>(src + i * 8));
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    if (a.dtype == ZC_BF16) {
+                        const float2 f = unpack2<ZC_BF16>(w[k]);
+                        w[k] = half2_of(f.x * up, f.y * up);
+                    }
+                    w[k] ^= sign;
+                }
+                *reinterpret_cast<uint4 *>(sm.q[half] + i / 8 * (kTile * 128) + r % kTile * 128 + 16 * (i % 8 ^ (r & 7))) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.bars.q_full[half]);
+
+            {
+                for (int j = job.j0; j < job.j0 + job.n; j++, tile++, scored++) {
+                    const int slot = tile % kSlots;
+                    if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.scale_full[slot], tile / kSlots & 1) &&
+                                                     bar_wait(&sm.bars.s_full[half], scored & 1)))
+                        return false;
+                    tm_after();
+                    float x[kTile];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) tm_load32(tmS + 32 * i, x + 32 * i);
+                    tm_wait_load();
+                    if (job.edge(j)) {
+                        const int from = lo - j * kTile, to = hi - j * kTile;
+#pragma unroll
+                        for (int i = 0; i < kTile; i++)
+                            if (i < from || i >= to) x[i] = kNone;
+                    }
+                    float top = kNone, topw = kNone;
+#pragma unroll
+                    for (int b = 0; b < kBoxes; b++) {
+                        float g = x[16 * b];
+#pragma unroll
+                        for (int i = 1; i < 16; i++) g = fmaxf(g, x[16 * b + i]);
+                        g *= fmaxf(c * sm.ks[slot][b], 1e-37f);  // (0 * -infinity would be NaN)
+                        top = fmaxf(top, g);
+                        topw = fmaxf(topw, g + sm.lvs[slot][b]);
+                    }
+                    // As in kv_rows.cu: the maxima are followed once they have grown by 2^kSlack.
+                    const bool grows = top > m + kSlack || topw > mw + kSlack;
+                    if (__any_sync(0xFFFFFFFFu, grows)) {
+                        float down = 1.0f;
+                        if (grows) {
+                            const float m1 = fmaxf(m, top), w1 = fmaxf(mw, topw);
+                            l *= ratio2(m, m1);
+                            down = ratio2(mw, w1);
+                            m = m1, mw = w1;
+                        }
+                        // the last sums are done: the scores were issued after them
+                        if (j > job.j0) {
+#pragma unroll 1
+                            for (int i = 0; i < DP; i += 32) {
+                                float o[32];
+                                tm_load32(tmO + i, o);
+                                tm_wait_load();
+#pragma unroll
+                                for (int k = 0; k < 32; k++) o[k] *= down;
+                                tm_store32(tmO + i, reinterpret_cast<uint32_t *>(o));
+                            }
+                        }
+                    }
+                    const float base = m == kNone ? 0.0f : m;
+                    uint32_t *p = reinterpret_cast<uint32_t *>(x);
+#pragma unroll
+                    for (int b = 0; b < kBoxes; b++) {
+                        const float by = fmaxf(c * sm.ks[slot][b], 1e-37f);
+                        const float lf = fminf(fmaxf(sm.lvs[slot][b] + (base - mw), -60.0f), 120.0f);  // (mw = -infinity: every vs is 0)
+                        const float bias = lf - base;
+                        float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            float y0, y1;
+                            fma2(y0, y1, x[16 * b + i], x[16 * b + i + 1], by, bias);
+                            y0 = ex2(y0), y1 = ex2(y1);
+                            sum0 += y0, sum1 += y1;
+                            p[8 * b + i / 2] = half2_of(y0, y1);
+                        }
+                        l += (sum0 + sum1) * ex2(-lf);
+                    }
+                    tm_store32(tmS, p);
+                    tm_store32(tmS + 32, p + 32);
+                    tm_wait_store();
+                    tm_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&sm.bars.p_full[half]);
+                }
+                if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.o_full[half], summed++ & 1))) return false;
+                tm_after();
+            }
+        }
+
+        // The rows' ends: finished, or a part.
+        const bool whole = job.whole();
+        Part<DP> *part = parts + 2 * blockIdx.x + (job.w == job.i0 ? 1 : 0);
+        if (half < job.tiles) {
+            const float by = whole ? (l == 0.0f ? 0.0f : row_factor(m, mw, l)) : 1.0f;
+            const bool poison = job.n && *reinterpret_cast<volatile int *>(&sm.poison);
+            uint16_t *dst = static_cast<uint16_t *>(a.out.p) + token * a.out.token + head * a.out.head;
+#pragma unroll 1
+            for (int i = 0; i < DP; i += 32) {
+                float o[32];
+                if (job.n) {
+                    tm_load32(tmO + i, o);
+                    tm_wait_load();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k++) o[k] = 0.0f;
+                }
+                if (poison && mine && i < int(a.c.dim)) {
+                    const uint32_t mask = poisoned(a, job, lo, hi, i);
+#pragma unroll
+                    for (int k = 0; k < 32; k++)
+                        if (mask >> k & 1) o[k] = NAN;
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) __stcg(&part->o[(i + k) / 4][r], make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
+                } else if (mine) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8)
+                        if (i + k < int(a.c.dim))
+                            *reinterpret_cast<uint4 *>(dst + i + k) =
+                                l == 0.0f ? make_uint4(0, 0, 0, 0)
+                                          : make_uint4(pack_out(a, o[k] * by, o[k + 1] * by), pack_out(a, o[k + 2] * by, o[k + 3] * by),
+                                                       pack_out(a, o[k + 4] * by, o[k + 5] * by), pack_out(a, o[k + 6] * by, o[k + 7] * by));
+                }
+            }
+            if (!whole) __stcg(&part->m[r], m), __stcg(&part->mw[r], mw), __stcg(&part->l[r], l);
+            else if (mine && a.lse) a.lse[token * a.heads + head] = row_lse(m, l);
+            tm_before();
+        }
+        if (!whole) {
+            const uint32_t c0 = uint32_t((job.i0 * G + G - 1) / W), c1 = uint32_t(((job.i1 - 1) * G + G - 1) / W);  // as in kv_rows.cu
+            if (!rows_meet(&sm.bars.rows, met++)) return false;
+            if (r == 0) {
+                uint32_t *counter = a.counters + (slot_of(job.seq.first, job.seq.s, a.group, kRows, 1) + job.tile) * a.c.heads + job.h;
+                uint32_t done;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
+                if (done == c1 - c0) *counter = 0;
+                sm.last = done == c1 - c0;
+            }
+            if (!rows_meet(&sm.bars.rows, met++)) return false;
+            if (*reinterpret_cast<volatile int *>(&sm.last) && mine) {
+                // the first part is in its CTA's second slot, the others in the first slots of the CTAs after it
+                auto at = [&](uint32_t c) -> const Part<DP> & { return parts[2 * c + (c == c0 ? 1 : 0)]; };
+                float M = kNone, Wt = kNone, L = 0.0f;
+                for (uint32_t c = c0; c <= c1; c++) M = fmaxf(M, __ldcg(&at(c).m[r])), Wt = fmaxf(Wt, __ldcg(&at(c).mw[r]));
+                for (uint32_t c = c0; c <= c1; c++) L += __ldcg(&at(c).l[r]) * ratio2(__ldcg(&at(c).m[r]), M);
+#pragma unroll 1
+                for (int i = 0; i < int(a.c.dim); i += 16) {
+                    float o[16];
+#pragma unroll
+                    for (int k = 0; k < 16; k++) o[k] = 0.0f;
+#pragma unroll 2
+                    for (uint32_t c = c0; c <= c1; c++) {
+                        const float f = ratio2(__ldcg(&at(c).mw[r]), Wt);
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const float4 v = __ldcg(&at(c).o[i / 4 + k][r]);
+                            o[4 * k] += v.x * f, o[4 * k + 1] += v.y * f, o[4 * k + 2] += v.z * f, o[4 * k + 3] += v.w * f;
+                        }
+                    }
+                    emit(a, job.seq, job.h, row, i, o, M, Wt, L);
+                }
+            }
+        }
+    }
+    return true;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CodeMaps maps) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Smem<DP> &sm = *reinterpret_cast<Smem<DP> *>(smem);
+    const uint32_t cta = blockIdx.x;
+    const int warp = threadIdx.x / 32;
+
+    // The line of work, and this CTA's piece of it.
+    const uint64_t slots = slots_of(a.b.total, a.b.n_seqs, a.group, kRows, 1);
+    auto work_at = [&](uint64_t u, uint32_t &s, bool speak) -> uint64_t {
+        Job job;
+        s = seq_of_slot(a, u);
+        const Seq seq = read_seq(a.b, s, a.d_status, a.c.tokens, speak);
+        return work_of(a, seq, u - slot_of(uint32_t(max(__ldg(a.b.cu + s), 0)), s, a.group, kRows, 1), job);
+    };
+    uint64_t mine = 0, sum, W;
+    uint32_t s = 0;
+    for (uint64_t u = threadIdx.x; u < slots; u += kThreads) mine += work_at(u, s, cta == 0);
+    sum = block_scan<kWarps>(mine, sm.sums, W);
+    const uint64_t G = min(uint64_t(gridDim.x), W);  // no CTA between two that have work is without
+    if (cta >= G) return;
+    const uint64_t w0 = W * cta / G, w1 = W * (cta + 1) / G;
+    uint64_t before = 0;
+    for (uint64_t u0 = 0; u0 < slots; u0 += kThreads) {
+        if (slots > kThreads) {  // more than one round: the sums above were not of single slots
+            mine = u0 + threadIdx.x < slots ? work_at(u0 + threadIdx.x, s, false) : 0;
+            uint64_t all;
+            sum = before + block_scan<kWarps>(mine, sm.sums, all);
+            before += all;
+        }
+        if (mine && sum > w0 && sum - mine <= w0) sm.slot = uint32_t(u0 + threadIdx.x), sm.seq = s, sm.at = sum - mine;
+        if (before > w0) break;
+    }
+    if (threadIdx.x == 0) {
+        Bars &b = sm.bars;
+        for (int i = 0; i < kRaw; i++) bar_init(&b.raw_full[i], 1), bar_init(&b.raw_empty[i], 4);
+        for (int i = 0; i < kOps; i++) bar_init(&b.op_full[i], 4), bar_init(&b.op_empty[i], 1);
+        for (int i = 0; i < kSlots; i++) bar_init(&b.scale_full[i], 1);
+        for (int i = 0; i < 2; i++) bar_init(&b.q_full[i], 4), bar_init(&b.s_full[i], 1), bar_init(&b.p_full[i], 4), bar_init(&b.o_full[i], 1);
+        bar_init(&b.rows, 8);
+        bar_init(&b.drained, 1);
+        bar_init_done();
+        prefetch_map(&maps.code[0]);
+        prefetch_map(&maps.code[1]);
+        sm.poison = 0;
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&sm.tmem)), "r"(kColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tm_before();
+    }
+    __syncthreads();
+    tm_after();
+    const Walk walk = {w0, w1, sm.at, sm.slot, sm.seq};
+
+    bool ok = true;
+    // 512 registers a lane over the four warpgroups, as at launch
+    if (warp < 8) {
+        more_registers<192>();
+        ok = rows_role<DP>(a, sm, walk, W, G, reinterpret_cast<Part<DP> *>(a.parts));
+    } else if (warp < 12) {
+        fewer_registers<72>();
+        ok = convert_role<DP>(a, sm, walk);
+    } else {
+        fewer_registers<56>();
+        if (warp == 12 && threadIdx.x % 32 == 0) ok = product_role<DP>(a, sm, walk);
+        if (warp == 13) ok = copy_role<DP>(a, maps, sm, walk);
+    }
+    if (!ok) report(a.d_status, ZC_ETIMEOUT);
+    __syncwarp();
+    tm_before();
+    __syncthreads();
+    tm_after();
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem), "r"(kColumns));
+}
+
+template <int DP> int launch(const AttendArgs &a, cudaStream_t s) {
+    static std::atomic<uint64_t> ready{0};  // devices whose kernel may use this much shared memory
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(tiles_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Smem<DP>))) != cudaSuccess)
+            return ZC_ECUDA;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    CodeMaps maps;
+    const int st = make_maps(a.c, DP, 16, maps);
+    if (st != ZC_OK) return st;
+    tiles_kernel<DP><<<uint32_t(sm_count()), kThreads, sizeof(Smem<DP>), s>>>(a, maps);
+    return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
+}
+
+} // namespace
+
+uint64_t tiles_counters(const Batch &b, const Cache &c, uint32_t group) {
+    return slots_of(b.total, b.n_seqs, group, kRows, 1) * c.heads;
+}
+
+uint64_t tiles_part_bytes(const Cache &c) {
+    return uint64_t(sm_count()) * 2 * (c.dim <= 64 ? sizeof(Part<64>) : sizeof(Part<128>));
+}
+
+int launch_tiles(const AttendArgs &a, cudaStream_t s) { return a.c.dim <= 64 ? launch<64>(a, s) : launch<128>(a, s); }
+
+} // namespace kv
+} // namespace zc
