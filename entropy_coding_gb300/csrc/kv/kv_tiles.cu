@@ -127,6 +127,9 @@ __device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, flo
         : "=f"(x), "=f"(y) : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
 
+// Where an operand tile holds 16-byte chunk c of row r.
+__device__ __forceinline__ int panel_at(int r, int c) { return c / 8 * (kTile * 128) + r * 128 + 16 * (c % 8 ^ (r & 7)); }
+
 // ---------------------------------------------------------------------------
 // The line of work
 
@@ -276,10 +279,8 @@ template <int DP> __device__ __forceinline__ bool convert_role(const AttendArgs 
                     e4m3x4_to_half2x2(v.y, lo.z, lo.w);
                     e4m3x4_to_half2x2(v.z, hi.x, hi.y);
                     e4m3x4_to_half2x2(v.w, hi.z, hi.w);
-                    uint8_t *dst = sm.op[c] + ch / 4 * (kTile * 128) + row * 128;
-                    const int q = ch % 4 * 2;
-                    *reinterpret_cast<uint4 *>(dst + 16 * (q ^ (row & 7))) = lo;
-                    *reinterpret_cast<uint4 *>(dst + 16 * ((q + 1) ^ (row & 7))) = hi;
+                    *reinterpret_cast<uint4 *>(sm.op[c] + panel_at(row, 2 * ch)) = lo;
+                    *reinterpret_cast<uint4 *>(sm.op[c] + panel_at(row, 2 * ch + 1)) = hi;
                 }
                 fence_async();
                 __syncwarp();
@@ -381,49 +382,53 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
     const int lane = r & 31;
     const uint32_t lanes = uint32_t(r / 32 % 4 * 32) << 16;      // of tensor memory
     const uint32_t tmS = sm.tmem + half * 128 + lanes, tmO = sm.tmem + 256 + half * 128 + lanes;
+    constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes, kPasses = 32 / kAtOnce;  // lanes of a row of q or out, 16 bytes each
     uint32_t tile = 0, scored = 0, summed = 0, met = 0;
     Job job;
     while (walk.next(a, job)) {
         const uint64_t row = job.tile * kRows + r, n_rows = uint64_t(job.seq.n) * a.group;
         const bool mine = row < n_rows;
         const int64_t token = int64_t(job.seq.first) + int64_t(row / a.group), head = int64_t(job.h) * a.group + int64_t(row % a.group);
-        const uint16_t *src = static_cast<const uint16_t *>(a.q.p) + token * a.q.token + head * a.q.head;
         int lo = 0, hi = 0;
         if (mine) bounds(a, job.seq, row, lo, hi);
-        float m = kNone, mw = kNone, l = 0.0f;
+        float m = kNone, mw = kNone, l = 0.0f, c = 0.0f;
         if (job.n && half >= job.tiles) tile += job.n;  // no rows in this tile
         if (job.n && half < job.tiles) {
-            // The query row, exact in half by a power of two, with the sign of the scale.
+            // The warp's query rows, whole rows at a time: exact in half by a power of two, with the sign of the scale.
             const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-            float c = fabsf(a.scale_log2), up = 1.0f;
-            if (a.dtype == ZC_BF16) {
-                uint32_t top = 0;
-                if (mine)
-                    for (uint32_t i = 0; i < a.c.dim; i += 8) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + i));
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const int64_t from = mine ? token * a.q.token + head * a.q.head : -1;
+            const int ch = lane % kLanes;
+            c = fabsf(a.scale_log2);
+            uint4 v[kPasses];
 #pragma unroll
-                        for (int k = 0; k < 4; k++) top = max(top, max(w[k] << 16 & 0x7FFF0000u, w[k] & 0x7FFF0000u));
-                    }
-                float down;
-                row_powers(top, up, down);
-                c *= down;
+            for (int i = 0; i < kPasses; i++) {
+                const int64_t at = __shfl_sync(0xFFFFFFFFu, from, i * kAtOnce + lane / kLanes);
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (at >= 0 && ch * 8 < int(a.c.dim)) v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + at + ch * 8));
             }
-#pragma unroll 4
-            for (int i = 0; i < DP / 8; i++) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (mine && i * 8 < int(a.c.dim)) v = __ldg(reinterpret_cast<const uint4 *>(src + i * 8));
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    if (a.dtype == ZC_BF16) {
+            for (int i = 0; i < kPasses; i++) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(&v[i]);
+                if (a.dtype == ZC_BF16) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; k++) top = max(top, max(w[k] << 16 & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+#pragma unroll
+                    for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    float up, down;
+                    row_powers(top, up, down);
+                    down = __shfl_sync(0xFFFFFFFFu, down, lane % kAtOnce * kLanes);
+                    if (lane / kAtOnce == i) c *= down;
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
                         const float2 f = unpack2<ZC_BF16>(w[k]);
                         w[k] = half2_of(f.x * up, f.y * up);
                     }
-                    w[k] ^= sign;
                 }
-                *reinterpret_cast<uint4 *>(sm.q[half] + i / 8 * (kTile * 128) + r % kTile * 128 + 16 * (i % 8 ^ (r & 7))) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int k = 0; k < 4; k++) w[k] ^= sign;
+                const int to = r % kTile - lane + i * kAtOnce + lane / kLanes;
+                *reinterpret_cast<uint4 *>(sm.q[half] + panel_at(to, ch)) = v[i];
             }
             fence_async();
             __syncwarp();
@@ -513,9 +518,8 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
         const bool whole = job.whole();
         Part<DP> *part = parts + 2 * blockIdx.x + (job.w == job.i0 ? 1 : 0);
         if (half < job.tiles) {
-            const float by = whole ? (l == 0.0f ? 0.0f : row_factor(m, mw, l)) : 1.0f;
+            const float by = row_factor(m, mw, l);
             const bool poison = job.n && *reinterpret_cast<volatile int *>(&sm.poison);
-            uint16_t *dst = static_cast<uint16_t *>(a.out.p) + token * a.out.token + head * a.out.head;
 #pragma unroll 1
             for (int i = 0; i < DP; i += 32) {
                 float o[32];
@@ -535,18 +539,31 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
                 if (!whole) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) __stcg(&part->o[(i + k) / 4][r], make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
-                } else if (mine) {
+                } else {
+                    // through the query tile's memory, so that whole rows are written
 #pragma unroll
                     for (int k = 0; k < 32; k += 8)
-                        if (i + k < int(a.c.dim))
-                            *reinterpret_cast<uint4 *>(dst + i + k) =
-                                l == 0.0f ? make_uint4(0, 0, 0, 0)
-                                          : make_uint4(pack_out(a, o[k] * by, o[k + 1] * by), pack_out(a, o[k + 2] * by, o[k + 3] * by),
-                                                       pack_out(a, o[k + 4] * by, o[k + 5] * by), pack_out(a, o[k + 6] * by, o[k + 7] * by));
+                        *reinterpret_cast<uint4 *>(sm.q[half] + panel_at(r % kTile, (i + k) / 8)) =
+                            l == 0.0f ? make_uint4(0, 0, 0, 0)
+                                      : make_uint4(pack_out(a, o[k] * by, o[k + 1] * by), pack_out(a, o[k + 2] * by, o[k + 3] * by),
+                                                   pack_out(a, o[k + 4] * by, o[k + 5] * by), pack_out(a, o[k + 6] * by, o[k + 7] * by));
                 }
             }
-            if (!whole) __stcg(&part->m[r], m), __stcg(&part->mw[r], mw), __stcg(&part->l[r], l);
-            else if (mine && a.lse) a.lse[token * a.heads + head] = row_lse(m, l);
+            if (whole) {
+                const int64_t to = mine ? token * a.out.token + head * a.out.head : -1;
+                const int ch = lane % kLanes;
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < kPasses; i++) {
+                    const int64_t at = __shfl_sync(0xFFFFFFFFu, to, i * kAtOnce + lane / kLanes);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(sm.q[half] + panel_at(r % kTile - lane + i * kAtOnce + lane / kLanes, ch));
+                    if (at >= 0 && ch * 8 < int(a.c.dim)) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out.p) + at + ch * 8) = v;
+                }
+                __syncwarp();
+                if (mine && a.lse) a.lse[token * a.heads + head] = row_lse(m, l);
+            } else {
+                __stcg(&part->m[r], m), __stcg(&part->mw[r], mw), __stcg(&part->l[r], l);
+            }
             tm_before();
         }
         if (!whole) {
@@ -560,25 +577,41 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
                 sm.last = done == c1 - c0;
             }
             if (!rows_meet(&sm.bars.rows, met++)) return false;
-            if (*reinterpret_cast<volatile int *>(&sm.last) && mine) {
+            // With one tile of rows its 128 rows take two threads each, half of the columns a thread.
+            const int jr = job.tiles == 1 ? r % kTile : r, span = job.tiles == 1 ? DP / 2 : DP;
+            const uint64_t row = job.tile * kRows + jr;
+            if (*reinterpret_cast<volatile int *>(&sm.last) && row < n_rows) {
                 // the first part is in its CTA's second slot, the others in the first slots of the CTAs after it
                 auto at = [&](uint32_t c) -> const Part<DP> & { return parts[2 * c + (c == c0 ? 1 : 0)]; };
                 float M = kNone, Wt = kNone, L = 0.0f;
-                for (uint32_t c = c0; c <= c1; c++) M = fmaxf(M, __ldcg(&at(c).m[r])), Wt = fmaxf(Wt, __ldcg(&at(c).mw[r]));
-                for (uint32_t c = c0; c <= c1; c++) L += __ldcg(&at(c).l[r]) * ratio2(__ldcg(&at(c).m[r]), M);
+#pragma unroll 4
+                for (uint32_t c = c0; c <= c1; c++) M = fmaxf(M, __ldcg(&at(c).m[jr])), Wt = fmaxf(Wt, __ldcg(&at(c).mw[jr]));
+#pragma unroll 4
+                for (uint32_t c = c0; c <= c1; c++) L += __ldcg(&at(c).l[jr]) * ratio2(__ldcg(&at(c).m[jr]), M);
+                const int from = job.tiles == 1 ? half * span : 0;
 #pragma unroll 1
-                for (int i = 0; i < int(a.c.dim); i += 16) {
+                for (int i = from; i < from + span && i < int(a.c.dim); i += 16) {
                     float o[16];
 #pragma unroll
                     for (int k = 0; k < 16; k++) o[k] = 0.0f;
-#pragma unroll 2
-                    for (uint32_t c = c0; c <= c1; c++) {
-                        const float f = ratio2(__ldcg(&at(c).mw[r]), Wt);
+                    auto add = [&](const float4 (&v)[4], float f) {
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const float4 v = __ldcg(&at(c).o[i / 4 + k][r]);
-                            o[4 * k] += v.x * f, o[4 * k + 1] += v.y * f, o[4 * k + 2] += v.z * f, o[4 * k + 3] += v.w * f;
+                        for (int k = 0; k < 4; k++) o[4 * k] += v[k].x * f, o[4 * k + 1] += v[k].y * f, o[4 * k + 2] += v[k].z * f, o[4 * k + 3] += v[k].w * f;
+                    };
+                    constexpr int kRun = 4;
+                    for (uint32_t c = c0; c <= c1; c += kRun) {  // 16 reads in flight
+                        float4 v[kRun][4];
+                        float f[kRun];
+#pragma unroll
+                        for (int n = 0; n < kRun; n++) {
+                            const uint32_t cn = min(c + n, c1);
+                            f[n] = __ldcg(&at(cn).mw[jr]);
+#pragma unroll
+                            for (int k = 0; k < 4; k++) v[n][k] = __ldcg(&at(cn).o[i / 4 + k][jr]);
                         }
+#pragma unroll
+                        for (int n = 0; n < kRun; n++)
+                            if (c + n <= c1) add(v[n], ratio2(f[n], Wt));
                     }
                     emit(a, job.seq, job.h, row, i, o, M, Wt, L);
                 }
