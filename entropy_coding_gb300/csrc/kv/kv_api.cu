@@ -172,7 +172,7 @@ extern "C" uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const 
     Cache c{};
     Batch b{};
     if (make_cache(cache, c) != ZC_OK || make_batch(batch, b) != ZC_OK) return 0;
-    if (heads == 0 || heads % c.heads || heads > 65535) return 0;
+    if (heads == 0 || heads % c.heads || heads > 65535 || uint64_t(b.total) * heads > 0x7FFFFFFFu) return 0;
     return Plan(b, c, heads / c.heads).bytes();
 }
 
@@ -185,7 +185,7 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
     int st = make_cache(cache, a.c);
     if (st == ZC_OK) st = make_batch(batch, a.b);
     if (st != ZC_OK) return st;
-    if (heads == 0 || heads % a.c.heads || heads > 65535) return ZC_EINVAL;
+    if (heads == 0 || heads % a.c.heads || heads > 65535 || uint64_t(a.b.total) * heads > 0x7FFFFFFFu) return ZC_EINVAL;
     if (a.b.total == 0) return ZC_OK;
     if ((st = make_rows(*q, 2, a.q)) != ZC_OK || (st = make_rows(*out, 2, a.out)) != ZC_OK) return st;
     a.lse = d_lse;

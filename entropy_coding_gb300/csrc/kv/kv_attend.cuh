@@ -33,11 +33,21 @@ __device__ __forceinline__ void row_powers(uint32_t top, float &up, float &down)
 }
 
 // The keys [l, e) that a row sees.
-__device__ __forceinline__ void bounds(const AttendArgs &a, const Seq &seq, uint64_t row, int &l, int &e) {
-    const int64_t pos = int64_t(seq.len) - int64_t(seq.n) + int64_t(row / a.group);
-    e = int(a.causal ? max(pos + 1, int64_t(0)) : int64_t(seq.len));
-    l = a.window ? int(max(pos - int64_t(a.window) + 1, int64_t(0))) : 0;
+__device__ __forceinline__ void bounds(const AttendArgs &a, const Seq &seq, uint32_t row, int &l, int &e) {
+    const int pos = seq.len - int(seq.n) + int(row / a.group);  // (may be below 0: more new tokens than the sequence has)
+    e = a.causal ? max(pos + 1, 0) : seq.len;
+    l = a.window && pos >= int(a.window) ? pos - int(a.window) + 1 : 0;
     if (l > e) l = e;
+}
+
+// Where a row's query head is among the tensor's (q or out), in elements.
+__device__ __forceinline__ int64_t row_at(const AttendArgs &a, const Rows &x, const Seq &seq, uint32_t h, uint32_t row) {
+    const uint32_t token = row / a.group, head = row - token * a.group;
+    return int64_t(seq.first + token) * x.token + int64_t(h * a.group + head) * x.head;
+}
+__device__ __forceinline__ float *lse_at(const AttendArgs &a, const Seq &seq, uint32_t h, uint32_t row) {
+    const uint32_t token = row / a.group, head = row - token * a.group;
+    return a.lse + int64_t(seq.first + token) * a.heads + h * a.group + head;
 }
 
 // Inclusive sum over the threads up to this one; `total`: over all of the CTA's kWarps warps.
@@ -72,16 +82,15 @@ __device__ __forceinline__ float row_lse(float M, float L) { return L == 0.0f ? 
 
 // n columns (a multiple of 4) of a finished row from `col` on.
 template <int n>
-__device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32_t h, uint64_t row, int col,
+__device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32_t h, uint32_t row, int col,
                                      const float (&x)[n], float M, float W, float L) {
     const float by = row_factor(M, W, L);
-    const int64_t token = int64_t(seq.first) + int64_t(row / a.group), head = int64_t(h) * a.group + int64_t(row % a.group);
-    uint16_t *o = static_cast<uint16_t *>(a.out.p) + token * a.out.token + head * a.out.head + col;
+    uint16_t *o = static_cast<uint16_t *>(a.out.p) + row_at(a, a.out, seq, h, row) + col;
 #pragma unroll
     for (int k = 0; k < n; k += 4)
         *reinterpret_cast<uint2 *>(o + k) = L == 0.0f ? make_uint2(0, 0) : make_uint2(pack_out(a, x[k] * by, x[k + 1] * by),
                                                                                       pack_out(a, x[k + 2] * by, x[k + 3] * by));
-    if (a.lse && col == 0) a.lse[token * a.heads + head] = row_lse(M, L);
+    if (a.lse && col == 0) *lse_at(a, seq, h, row) = row_lse(M, L);
 }
 
 } // namespace kv

@@ -127,27 +127,27 @@ __device__ __forceinline__ Seq read_seq(const Batch &b, uint32_t s, int32_t *d_s
 // counts the f(s) at or below its slot: one round of loads for any batch up
 // to the CTA's size, where a binary search would take one dependent load for
 // each halving.
-__device__ __forceinline__ uint64_t slot_of(uint64_t tokens, uint32_t s, uint32_t per, uint32_t unit, uint32_t extra) {
-    return tokens * per / unit + uint64_t(extra) * s;
+// (tokens * per < 2^31 and sequences < 2^24: the entry points see to it)
+__host__ __device__ inline uint32_t slot_of(uint32_t tokens, uint32_t s, uint32_t per, uint32_t unit, uint32_t extra) {
+    return tokens * per / unit + extra * s;
 }
-__host__ __device__ inline uint64_t slots_of(uint64_t total, uint32_t n_seqs, uint32_t per, uint32_t unit, uint32_t extra) {
-    return total * per / unit + uint64_t(extra) * n_seqs;
-}
+
+__device__ __forceinline__ uint32_t tokens_before(const Batch &b, uint32_t s) { return uint32_t(min(max(__ldg(b.cu + s), 0), int(b.total))); }
 
 // The sequence of slot u (the whole CTA calls this); `at`: the slot's index
 // within the sequence.
-__device__ __forceinline__ uint32_t find_seq(const Batch &b, uint64_t u, uint32_t per, uint32_t unit, uint32_t extra, uint64_t &at) {
+__device__ __forceinline__ uint32_t find_seq(const Batch &b, uint32_t u, uint32_t per, uint32_t unit, uint32_t extra, uint32_t &at) {
     uint32_t below = 0;
     for (uint32_t s0 = 0; s0 < b.n_seqs; s0 += blockDim.x) {
         const uint32_t s = s0 + threadIdx.x;
         bool in = false;
-        if (s < b.n_seqs) in = slot_of(uint32_t(max(__ldg(b.cu + s), 0)), s, per, unit, extra) <= u;
+        if (s < b.n_seqs) in = slot_of(tokens_before(b, s), s, per, unit, extra) <= u;
         const uint32_t n = __syncthreads_count(in);
         below += n;
         if (n < blockDim.x) break;  // f grows with s
     }
     const uint32_t s = below ? below - 1 : 0;
-    at = u - slot_of(uint32_t(max(__ldg(b.cu + s), 0)), s, per, unit, extra);
+    at = u - slot_of(tokens_before(b, s), s, per, unit, extra);
     return s;
 }
 

@@ -25,7 +25,7 @@ template <int DT> __device__ __forceinline__ void store16(void *p, const float (
 }
 
 template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(MoveArgs a) {
-    uint64_t at;
+    uint32_t at;
     const uint32_t s = find_seq(a.b, blockIdx.x, 1, kTokens, 1, at);
     const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, threadIdx.x == 0 && at == 0);
     if (!q.ok || q.n == 0) return;
@@ -36,9 +36,9 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(MoveAr
     const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y, kvi = blockIdx.z;
     const uint32_t per_row = D / 16;
     for (uint32_t i = threadIdx.x; i < kTokens * per_row; i += kThreads) {
-        const uint64_t t = at * kTokens + i / per_row;
+        const uint32_t t = at * kTokens + i / per_row;
         if (t >= q.n) break;
-        const uint32_t pos = uint32_t(q.len) - q.n + uint32_t(t), col = i % per_row * 16;
+        const uint32_t pos = uint32_t(q.len) - q.n + t, col = i % per_row * 16;
         const int64_t id = read_block(a.b, a.c, s, pos / B, a.d_status);
         if (id < 0) continue;
         const uint4 c = __ldg(reinterpret_cast<const uint4 *>(a.c.code[kvi] + id * a.c.block_stride +
@@ -60,9 +60,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(MoveAr
 } // namespace
 
 int launch_read(int dtype, const MoveArgs &a, cudaStream_t s) {
-    const uint64_t slots = slots_of(a.b.total, a.b.n_seqs, 1, kTokens, 1);
-    if (slots > 0x7FFFFFFFull) return ZC_EINVAL;
-    const dim3 grid(uint32_t(slots), a.c.heads, 2);
+    const dim3 grid(slot_of(a.b.total, a.b.n_seqs, 1, kTokens, 1), a.c.heads, 2);
     switch (dtype) {
     case ZC_BF16: read_kernel<ZC_BF16><<<grid, kThreads, 0, s>>>(a); break;
     case ZC_FP16: read_kernel<ZC_FP16><<<grid, kThreads, 0, s>>>(a); break;

@@ -104,22 +104,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 }
 // Units of work of a sequence's items (the same for all of them).
 __device__ __forceinline__ uint32_t first_unit(const AttendArgs &a, const Seq &q) {
-    const int64_t lo = a.window ? int64_t(q.len) - int64_t(q.n) - int64_t(a.window) + 1 : 0;
-    return uint32_t(max(lo, int64_t(0)) / kUnit);
+    const int pos = q.len - int(q.n);
+    return a.window && pos >= int(a.window) ? uint32_t(pos - int(a.window) + 1) / kUnit : 0;
 }
 __device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &q) {
     return max((uint32_t(q.len) + kUnit - 1) / kUnit, first_unit(a, q) + 1) - first_unit(a, q);
 }
 template <int NT> __device__ __forceinline__ uint64_t work_of(const AttendArgs &a, const Seq &q) {
-    return q.ok && uint64_t(q.n) * a.group <= a.rows_most ? (uint64_t(q.n) * a.group + 8 * NT - 1) / (8 * NT) * a.c.heads * units_of(a, q) : 0;
+    return q.ok && q.n * a.group <= a.rows_most ? uint64_t((q.n * a.group + 8 * NT - 1) / (8 * NT)) * a.c.heads * units_of(a, q) : 0;
 }
 
 // A piece of work: units of item (seq, tile, h) on the line of work, and what
 // this warp does of it.
 struct Job {
     Seq seq;
-    uint64_t tile;
-    uint32_t h;
+    uint32_t tile, h;
     uint64_t w, upto, i0, i1;          // the piece [w, upto) of the item's [i0, i1)
     int all_lo, all_hi, x_lo, x_hi;    // keys seen by some row; by every row
     int first, steps;                  // this warp's slices: first, first + kWarps, ...
@@ -138,15 +137,16 @@ __device__ __forceinline__ bool next_job(const AttendArgs &a, uint64_t &w, uint6
             continue;
         }
         const uint32_t units = units_of(a, seq);
-        const uint64_t item = (w - at) / units;
+        const uint64_t past = w - at;
+        const uint32_t item = past >> 32 ? uint32_t(past / units) : uint32_t(past) / units;
         job.seq = seq;
         job.i0 = at + item * units;
         job.i1 = job.i0 + units;
         job.w = w;
         job.upto = min(w1, job.i1);
         job.tile = item / a.c.heads;
-        job.h = uint32_t(item % a.c.heads);
-        const uint64_t row0 = job.tile * 8 * NT, n_rows = uint64_t(seq.n) * a.group;
+        job.h = item - job.tile * a.c.heads;
+        const uint32_t row0 = job.tile * 8 * NT, n_rows = seq.n * a.group;
         bounds(a, seq, row0, job.all_lo, job.x_hi);
         bounds(a, seq, min(row0 + 8 * NT, n_rows) - 1, job.x_lo, job.all_hi);
         const int unit0 = int(first_unit(a, seq) + uint32_t(w - job.i0)), warp = threadIdx.x >> 5;
@@ -215,7 +215,7 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t D = a.c.dim, h = job.h;
     const Seq &seq = job.seq;
-    const uint64_t row0 = job.tile * kRows, n_rows = uint64_t(seq.n) * a.group;
+    const uint32_t row0 = job.tile * kRows, n_rows = seq.n * a.group;
     auto &o = acc.o;
     auto &m = acc.m;
     auto &mw = acc.mw;
@@ -227,17 +227,14 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
     float row_scale[NT][2];  // of rows 2t, 2t + 1 of each tile
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-        const uint64_t row = row0 + 8 * n + g;
+        const uint32_t row = row0 + 8 * n + g;
         uint32_t w[kRun / 2];
 #pragma unroll
         for (int i = 0; i < kRun / 8; i++) {
             uint4 v = make_uint4(0, 0, 0, 0);
             const uint32_t col = kRun * t + 8 * i;
             if (row < n_rows && col < D) {
-                const uint16_t *q = static_cast<const uint16_t *>(a.q.p) +
-                                    (int64_t(seq.first) + int64_t(row / a.group)) * a.q.token +
-                                    (int64_t(h) * a.group + int64_t(row % a.group)) * a.q.head + col;
-                v = __ldg(reinterpret_cast<const uint4 *>(q));
+                v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + row_at(a, a.q, seq, h, row) + col));
             }
             w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
         }
@@ -441,10 +438,10 @@ template <int DP, int NT>
 __device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const Job &job, Sums<DP, NT> &acc, Part<DP, NT> *part) {
     constexpr int kCols = DP / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const uint64_t n_rows = uint64_t(job.seq.n) * a.group;
+    const uint32_t n_rows = job.seq.n * a.group;
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-        const uint64_t row0 = (job.tile * NT + n) * 8;
+        const uint32_t row0 = (job.tile * NT + n) * 8;
         if (n && row0 >= n_rows) break;
         if (n) __syncthreads();
 #pragma unroll
@@ -490,7 +487,7 @@ __device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const 
 // A thread takes 4 columns of a row and every kWays-th part, in runs whose
 // loads are in flight together; the ways meet in shared memory.
 template <int DP, int NT>
-__device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint64_t tile, uint32_t h,
+__device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint32_t tile, uint32_t h,
                                      const Part<DP, NT> *parts, uint32_t first, uint32_t n) {
     constexpr int kRows = 8 * NT, kCols = DP / 4, kRun = 16;
     struct Way {
@@ -498,8 +495,8 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const S
         float m, mw, l;
     };
     Way *met = reinterpret_cast<Way *>(smem);
-    const uint64_t row0 = tile * kRows, n_rows = uint64_t(seq.n) * a.group;
-    const int rows = int(min(uint64_t(kRows), n_rows - row0)), D = int(a.c.dim);
+    const uint32_t row0 = tile * kRows, n_rows = seq.n * a.group;
+    const int rows = int(min(uint32_t(kRows), n_rows - row0)), D = int(a.c.dim);
     const int jobs = rows * kCols;                             // 4 columns of a row each
     const int ways = jobs >= kThreads ? 1 : kThreads / jobs;   // threads of a job
     auto part = [&](uint32_t i) -> const Part<DP, NT> & { return parts[2 * (first + i) + (i ? 0 : 1)]; };
@@ -622,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rows_kernel(const __grid_
             __syncthreads();
             if (threadIdx.x == 0) {
                 // releases the CTA's part (the barrier before it orders the other threads' writes) and acquires the others'
-                uint32_t *counter = a.counters + (slot_of(job.seq.first, job.seq.s, a.group, 8 * NT, 1) + job.tile) * a.c.heads + job.h;
+                uint32_t *counter = a.counters + uint64_t(slot_of(job.seq.first, job.seq.s, a.group, 8 * NT, 1) + job.tile) * a.c.heads + job.h;
                 uint32_t done;
                 asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
                 if (done == c1 - c0) *counter = 0;
@@ -663,7 +660,7 @@ template <int NT> uint64_t part_bytes(uint32_t dim) {
 } // namespace
 
 uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group) {
-    return slots_of(b.total, b.n_seqs, group, 8, 1) * c.heads;
+    return uint64_t(slot_of(b.total, b.n_seqs, group, 8, 1)) * c.heads;
 }
 
 uint64_t rows_part_bytes(const Cache &c) { return part_bytes<2>(c.dim); }

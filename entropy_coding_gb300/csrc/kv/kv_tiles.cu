@@ -55,10 +55,11 @@ template <int DP> struct Smem {
     uint8_t q[2][kTile * DP * 2];       // panels of 64 columns: 128-byte rows, swizzled
     uint8_t op[kOps][kTile * DP * 2];
     uint8_t raw[kRaw][kTile * DP];
+    uint8_t out[8][32 * 64];            // a warp's rows, 32 columns at a time
     float ks[kSlots][kBoxes], lvs[kSlots][kBoxes];
     Bars bars;
-    uint64_t sums[kWarps], at;
-    uint32_t slot, seq, tmem;
+    uint64_t sums[kWarps], i0;
+    uint32_t slot, seq, h, tmem;
     int last, poison;
 };
 
@@ -135,8 +136,7 @@ __device__ __forceinline__ int panel_at(int r, int c) { return c / 8 * (kTile * 
 
 struct Job {
     Seq seq;
-    uint64_t tile;
-    uint32_t h;
+    uint32_t tile, h;
     uint64_t w, upto, i0, i1;        // the piece [w, upto) of the item's [i0, i1)
     int all_lo, all_hi, x_lo, x_hi;  // keys seen by some row; by every row
     int j0, n;                       // key tiles of the piece
@@ -145,32 +145,28 @@ struct Job {
     __device__ __forceinline__ bool edge(int j) const { return j * kTile < x_lo || (j + 1) * kTile > x_hi; }
 };
 
-__device__ __forceinline__ void see(const AttendArgs &a, Job &job) {
-    const uint64_t row0 = job.tile * kRows, n_rows = uint64_t(job.seq.n) * a.group;
-    bounds(a, job.seq, row0, job.all_lo, job.x_hi);
-    bounds(a, job.seq, min(row0 + kRows, n_rows) - 1, job.x_lo, job.all_hi);
+// Work of an item of this slot (a sequence's run of 256 rows), in key tiles; 0 if it is empty or not this kernel's.
+__device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &seq, uint32_t tile, Job &job) {
+    const uint32_t n_rows = seq.n * a.group, row0 = tile * kRows;
+    if (!seq.ok || n_rows <= a.rows_most || row0 >= n_rows) return 0;
+    job.seq = seq;
+    job.tile = tile;
+    bounds(a, seq, row0, job.all_lo, job.x_hi);
+    bounds(a, seq, min(row0 + kRows, n_rows) - 1, job.x_lo, job.all_hi);
     job.tiles = n_rows - row0 > kTile ? 2 : 1;
-}
-__device__ __forceinline__ uint32_t units_of(const Job &job) {
     return uint32_t(max((job.all_hi + kTile - 1) / kTile - job.all_lo / kTile, 1));
 }
 
-// Work of a slot (sequence and item of 256 rows) over all heads, in key tiles; 0 if it is empty or not this kernel's.
-__device__ __forceinline__ uint64_t work_of(const AttendArgs &a, const Seq &seq, uint64_t tile, Job &job) {
-    const uint64_t n_rows = uint64_t(seq.n) * a.group;
-    if (!seq.ok || n_rows <= a.rows_most || tile * kRows >= n_rows) return 0;
-    job.seq = seq;
-    job.tile = tile;
-    see(a, job);
-    return uint64_t(units_of(job)) * a.c.heads;
+__device__ __forceinline__ uint32_t first_slot(const AttendArgs &a, uint32_t s) {
+    return slot_of(tokens_before(a.b, s), s, a.group, kRows, 1);
 }
 
 // The sequence that slot u belongs to, by halving.
-__device__ __forceinline__ uint32_t seq_of_slot(const AttendArgs &a, uint64_t u) {
+__device__ __forceinline__ uint32_t seq_of_slot(const AttendArgs &a, uint32_t u) {
     uint32_t lo = 0, hi = a.b.n_seqs;
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) / 2;
-        if (slot_of(uint32_t(max(__ldg(a.b.cu + mid), 0)), mid, a.group, kRows, 1) <= u) lo = mid;
+        if (first_slot(a, mid) <= u) lo = mid;
         else hi = mid;
     }
     return lo;
@@ -178,27 +174,25 @@ __device__ __forceinline__ uint32_t seq_of_slot(const AttendArgs &a, uint64_t u)
 
 // Where a role has got to on the line: every role walks the same pieces.
 struct Walk {
-    uint64_t w, w1, at, slot;  // next work; the end; where the slot's work begins
-    uint32_t s;
+    uint64_t w, w1, i0;   // next work; the end; where the item begins
+    uint32_t slot, s, h;  // the item
     __device__ __forceinline__ bool next(const AttendArgs &a, Job &job) {
         while (w < w1) {
-            const Seq seq = read_seq(a.b, s, a.d_status, a.c.tokens, false);
-            const uint64_t first = slot_of(uint32_t(max(__ldg(a.b.cu + s), 0)), s, a.group, kRows, 1);
-            const uint64_t work = work_of(a, seq, slot - first, job);
-            if (w >= at + work) {
-                at += work;
+            const uint32_t units = units_of(a, read_seq(a.b, s, a.d_status, a.c.tokens, false), slot - first_slot(a, s), job);
+            if (w >= i0 + units) {
+                i0 += units;
+                if (units && ++h < a.c.heads) continue;
+                h = 0;
                 slot++;
-                while (s + 1 < a.b.n_seqs && slot_of(uint32_t(max(__ldg(a.b.cu + s + 1), 0)), s + 1, a.group, kRows, 1) <= slot) s++;
+                while (s + 1 < a.b.n_seqs && first_slot(a, s + 1) <= slot) s++;
                 continue;
             }
-            const uint32_t units = units_of(job);
-            const uint64_t item = (w - at) / units;
-            job.h = uint32_t(item);
-            job.i0 = at + item * units;
-            job.i1 = job.i0 + units;
+            job.h = h;
+            job.i0 = i0;
+            job.i1 = i0 + units;
             job.w = w;
             job.upto = min(w1, job.i1);
-            job.j0 = job.all_lo / kTile + int(w - job.i0);
+            job.j0 = job.all_lo / kTile + int(w - i0);
             job.n = max(min(int(job.upto - w), (job.all_hi + kTile - 1) / kTile - job.j0), 0);
             w = job.upto;
             return true;
@@ -376,64 +370,88 @@ __device__ __forceinline__ bool rows_meet(uint64_t *bar, uint32_t turn) {
     return __all_sync(0xFFFFFFFFu, bar_wait(bar, turn & 1));
 }
 
+constexpr int kNoRow = -1;
+
+// Asks for the warp's query rows of a piece, whole rows at a time (the tile's memory is not in use).
+template <int DP> __device__ __forceinline__ void fetch_queries(const AttendArgs &a, Smem<DP> &sm, const Job &job) {
+    constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes;  // lanes of a row, 16 bytes each
+    const int r = threadIdx.x, half = r / kTile, lane = r & 31, ch = lane % kLanes;
+    if (!job.n || half >= job.tiles) return;
+    const uint32_t row = job.tile * kRows + r;
+    const int64_t from = row < job.seq.n * a.group ? row_at(a, a.q, job.seq, job.h, row) : kNoRow;
+#pragma unroll 2
+    for (int i = 0; i < kLanes; i++) {
+        const int of = i * kAtOnce + lane / kLanes;
+        const int64_t at = __shfl_sync(0xFFFFFFFFu, from, of);
+        const bool take = at != kNoRow && ch * 8 < int(a.c.dim);
+        const uint32_t dst = smem_of(sm.q[half] + panel_at(r % kTile - lane + of, ch)), n = take ? 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(static_cast<const uint16_t *>(a.q.p) + (take ? at + ch * 8 : 0)),
+                     "r"(n) : "memory");
+    }
+}
+
+// The row is there: exact in half by a power of two, with the sign of the scale. Returns the scale of its scores.
+template <int DP> __device__ __forceinline__ float ready_query(const AttendArgs &a, Smem<DP> &sm) {
+    const int r = threadIdx.x, half = r / kTile;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    float c = fabsf(a.scale_log2), up = 1.0f;
+    if (a.dtype == ZC_BF16) {
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int i = 0; i < DP / 8; i++) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(sm.q[half] + panel_at(r % kTile, i));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) top = max(top, max(w[k] << 16 & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+        }
+        float down;
+        row_powers(top, up, down);
+        c *= down;
+    }
+    if (a.dtype == ZC_BF16 || sign) {
+#pragma unroll 4
+        for (int i = 0; i < DP / 8; i++) {
+            uint4 *at = reinterpret_cast<uint4 *>(sm.q[half] + panel_at(r % kTile, i));
+            const uint4 v = *at;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if (a.dtype == ZC_BF16) {
+                    const float2 f = unpack2<ZC_BF16>(w[k]);
+                    w[k] = half2_of(f.x * up, f.y * up);
+                }
+                w[k] ^= sign;
+            }
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    fence_async();
+    __syncwarp();
+    if ((r & 31) == 0) bar_arrive(&sm.bars.q_full[half]);
+    return c;
+}
+
 template <int DP>
 __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Walk walk, uint64_t W, uint64_t G, Part<DP> *parts) {
     const int r = threadIdx.x, half = r / kTile;                 // row of the item; its tile
     const int lane = r & 31;
     const uint32_t lanes = uint32_t(r / 32 % 4 * 32) << 16;      // of tensor memory
     const uint32_t tmS = sm.tmem + half * 128 + lanes, tmO = sm.tmem + 256 + half * 128 + lanes;
-    constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes, kPasses = 32 / kAtOnce;  // lanes of a row of q or out, 16 bytes each
     uint32_t tile = 0, scored = 0, summed = 0, met = 0;
-    Job job;
-    while (walk.next(a, job)) {
-        const uint64_t row = job.tile * kRows + r, n_rows = uint64_t(job.seq.n) * a.group;
+    Job job, next;
+    bool more = walk.next(a, job);
+    fetch_queries(a, sm, job);
+    for (; more; job = next) {
+        const uint32_t row = job.tile * kRows + r, n_rows = job.seq.n * a.group;
         const bool mine = row < n_rows;
-        const int64_t token = int64_t(job.seq.first) + int64_t(row / a.group), head = int64_t(job.h) * a.group + int64_t(row % a.group);
         int lo = 0, hi = 0;
         if (mine) bounds(a, job.seq, row, lo, hi);
-        float m = kNone, mw = kNone, l = 0.0f, c = 0.0f;
+        float m = kNone, mw = kNone, l = 0.0f;
         if (job.n && half >= job.tiles) tile += job.n;  // no rows in this tile
         if (job.n && half < job.tiles) {
-            // The warp's query rows, whole rows at a time: exact in half by a power of two, with the sign of the scale.
-            const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-            const int64_t from = mine ? token * a.q.token + head * a.q.head : -1;
-            const int ch = lane % kLanes;
-            c = fabsf(a.scale_log2);
-            uint4 v[kPasses];
-#pragma unroll
-            for (int i = 0; i < kPasses; i++) {
-                const int64_t at = __shfl_sync(0xFFFFFFFFu, from, i * kAtOnce + lane / kLanes);
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (at >= 0 && ch * 8 < int(a.c.dim)) v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + at + ch * 8));
-            }
-#pragma unroll
-            for (int i = 0; i < kPasses; i++) {
-                uint32_t *w = reinterpret_cast<uint32_t *>(&v[i]);
-                if (a.dtype == ZC_BF16) {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; k++) top = max(top, max(w[k] << 16 & 0x7FFF0000u, w[k] & 0x7FFF0000u));
-#pragma unroll
-                    for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    float up, down;
-                    row_powers(top, up, down);
-                    down = __shfl_sync(0xFFFFFFFFu, down, lane % kAtOnce * kLanes);
-                    if (lane / kAtOnce == i) c *= down;
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const float2 f = unpack2<ZC_BF16>(w[k]);
-                        w[k] = half2_of(f.x * up, f.y * up);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 4; k++) w[k] ^= sign;
-                const int to = r % kTile - lane + i * kAtOnce + lane / kLanes;
-                *reinterpret_cast<uint4 *>(sm.q[half] + panel_at(to, ch)) = v[i];
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&sm.bars.q_full[half]);
-
+            const float c = ready_query(a, sm);
             {
                 for (int j = job.j0; j < job.j0 + job.n; j++, tile++, scored++) {
                     const int slot = tile % kSlots;
@@ -514,12 +532,18 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
             }
         }
 
+        // The next piece's queries are on their way while this one is finished.
+        more = walk.next(a, next);
+        if (more) fetch_queries(a, sm, next);
+
         // The rows' ends: finished, or a part.
         const bool whole = job.whole();
         Part<DP> *part = parts + 2 * blockIdx.x + (job.w == job.i0 ? 1 : 0);
         if (half < job.tiles) {
             const float by = row_factor(m, mw, l);
             const bool poison = job.n && *reinterpret_cast<volatile int *>(&sm.poison);
+            const int64_t to = mine ? row_at(a, a.out, job.seq, job.h, row) : kNoRow;
+            uint8_t *stage = sm.out[r / 32];
 #pragma unroll 1
             for (int i = 0; i < DP; i += 32) {
                 float o[32];
@@ -540,37 +564,43 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) __stcg(&part->o[(i + k) / 4][r], make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
                 } else {
-                    // through the query tile's memory, so that whole rows are written
+                    // through shared memory, so that a warp writes 64 bytes of each of 8 rows at a time
+                    uint32_t w[16];
+                    if (l == 0.0f) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8)
-                        *reinterpret_cast<uint4 *>(sm.q[half] + panel_at(r % kTile, (i + k) / 8)) =
-                            l == 0.0f ? make_uint4(0, 0, 0, 0)
-                                      : make_uint4(pack_out(a, o[k] * by, o[k + 1] * by), pack_out(a, o[k + 2] * by, o[k + 3] * by),
-                                                   pack_out(a, o[k + 4] * by, o[k + 5] * by), pack_out(a, o[k + 6] * by, o[k + 7] * by));
+                        for (int k = 0; k < 16; k++) w[k] = 0;
+                    } else if (a.dtype == ZC_BF16) {
+#pragma unroll
+                        for (int k = 0; k < 16; k++) w[k] = pack2<ZC_BF16>(o[2 * k] * by, o[2 * k + 1] * by);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; k++) w[k] = pack2<ZC_FP16>(o[2 * k] * by, o[2 * k + 1] * by);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        *reinterpret_cast<uint4 *>(stage + lane * 64 + 16 * (k ^ (lane >> 1 & 3))) =
+                            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const int of = 8 * k + lane / 4, ch = lane % 4;
+                        const int64_t at = __shfl_sync(0xFFFFFFFFu, to, of);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + of * 64 + 16 * (ch ^ (of >> 1 & 3)));
+                        if (at != kNoRow && i + ch * 8 < int(a.c.dim))
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out.p) + at + i + ch * 8) = v;
+                    }
                 }
             }
-            if (whole) {
-                const int64_t to = mine ? token * a.out.token + head * a.out.head : -1;
-                const int ch = lane % kLanes;
-                __syncwarp();
-#pragma unroll 4
-                for (int i = 0; i < kPasses; i++) {
-                    const int64_t at = __shfl_sync(0xFFFFFFFFu, to, i * kAtOnce + lane / kLanes);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(sm.q[half] + panel_at(r % kTile - lane + i * kAtOnce + lane / kLanes, ch));
-                    if (at >= 0 && ch * 8 < int(a.c.dim)) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out.p) + at + ch * 8) = v;
-                }
-                __syncwarp();
-                if (mine && a.lse) a.lse[token * a.heads + head] = row_lse(m, l);
-            } else {
-                __stcg(&part->m[r], m), __stcg(&part->mw[r], mw), __stcg(&part->l[r], l);
-            }
+            if (!whole) __stcg(&part->m[r], m), __stcg(&part->mw[r], mw), __stcg(&part->l[r], l);
+            else if (mine && a.lse) *lse_at(a, job.seq, job.h, row) = row_lse(m, l);
             tm_before();
         }
         if (!whole) {
             const uint32_t c0 = uint32_t((job.i0 * G + G - 1) / W), c1 = uint32_t(((job.i1 - 1) * G + G - 1) / W);  // as in kv_rows.cu
             if (!rows_meet(&sm.bars.rows, met++)) return false;
             if (r == 0) {
-                uint32_t *counter = a.counters + (slot_of(job.seq.first, job.seq.s, a.group, kRows, 1) + job.tile) * a.c.heads + job.h;
+                uint32_t *counter = a.counters + uint64_t(first_slot(a, job.seq.s) + job.tile) * a.c.heads + job.h;
                 uint32_t done;
                 asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
                 if (done == c1 - c0) *counter = 0;
@@ -579,7 +609,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
             if (!rows_meet(&sm.bars.rows, met++)) return false;
             // With one tile of rows its 128 rows take two threads each, half of the columns a thread.
             const int jr = job.tiles == 1 ? r % kTile : r, span = job.tiles == 1 ? DP / 2 : DP;
-            const uint64_t row = job.tile * kRows + jr;
+            const uint32_t row = job.tile * kRows + jr;
             if (*reinterpret_cast<volatile int *>(&sm.last) && row < n_rows) {
                 // the first part is in its CTA's second slot, the others in the first slots of the CTAs after it
                 auto at = [&](uint32_t c) -> const Part<DP> & { return parts[2 * c + (c == c0 ? 1 : 0)]; };
@@ -590,30 +620,31 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
                 for (uint32_t c = c0; c <= c1; c++) L += __ldcg(&at(c).l[jr]) * ratio2(__ldcg(&at(c).m[jr]), M);
                 const int from = job.tiles == 1 ? half * span : 0;
 #pragma unroll 1
-                for (int i = from; i < from + span && i < int(a.c.dim); i += 16) {
-                    float o[16];
+                for (int i = from; i < from + span && i < int(a.c.dim); i += 32) {
+                    float o[32];
 #pragma unroll
-                    for (int k = 0; k < 16; k++) o[k] = 0.0f;
-                    auto add = [&](const float4 (&v)[4], float f) {
+                    for (int k = 0; k < 32; k++) o[k] = 0.0f;
+                    for (uint32_t c = c0; c <= c1; c += 2) {  // 16 reads in flight
+                        const Part<DP> &p0 = at(c), &p1 = at(min(c + 1, c1));
+                        float4 v[2][8];
 #pragma unroll
-                        for (int k = 0; k < 4; k++) o[4 * k] += v[k].x * f, o[4 * k + 1] += v[k].y * f, o[4 * k + 2] += v[k].z * f, o[4 * k + 3] += v[k].w * f;
-                    };
-                    constexpr int kRun = 4;
-                    for (uint32_t c = c0; c <= c1; c += kRun) {  // 16 reads in flight
-                        float4 v[kRun][4];
-                        float f[kRun];
+                        for (int k = 0; k < 8; k++) v[0][k] = __ldcg(&p0.o[i / 4 + k][jr]), v[1][k] = __ldcg(&p1.o[i / 4 + k][jr]);
+                        const float f0 = ratio2(__ldcg(&p0.mw[jr]), Wt);
 #pragma unroll
-                        for (int n = 0; n < kRun; n++) {
-                            const uint32_t cn = min(c + n, c1);
-                            f[n] = __ldcg(&at(cn).mw[jr]);
+                        for (int k = 0; k < 8; k++) o[4 * k] += v[0][k].x * f0, o[4 * k + 1] += v[0][k].y * f0, o[4 * k + 2] += v[0][k].z * f0, o[4 * k + 3] += v[0][k].w * f0;
+                        if (c < c1) {
+                            const float f1 = ratio2(__ldcg(&p1.mw[jr]), Wt);
 #pragma unroll
-                            for (int k = 0; k < 4; k++) v[n][k] = __ldcg(&at(cn).o[i / 4 + k][jr]);
+                            for (int k = 0; k < 8; k++) o[4 * k] += v[1][k].x * f1, o[4 * k + 1] += v[1][k].y * f1, o[4 * k + 2] += v[1][k].z * f1, o[4 * k + 3] += v[1][k].w * f1;
                         }
-#pragma unroll
-                        for (int n = 0; n < kRun; n++)
-                            if (c + n <= c1) add(v[n], ratio2(f[n], Wt));
                     }
-                    emit(a, job.seq, job.h, row, i, o, M, Wt, L);
+                    float y[16];
+#pragma unroll
+                    for (int k = 0; k < 16; k++) y[k] = o[k];
+                    emit(a, job.seq, job.h, row, i, y, M, Wt, L);
+#pragma unroll
+                    for (int k = 0; k < 16; k++) y[k] = o[16 + k];
+                    if (i + 16 < int(a.c.dim)) emit(a, job.seq, job.h, row, i + 16, y, M, Wt, L);
                 }
             }
         }
@@ -629,29 +660,33 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const int warp = threadIdx.x / 32;
 
     // The line of work, and this CTA's piece of it.
-    const uint64_t slots = slots_of(a.b.total, a.b.n_seqs, a.group, kRows, 1);
-    auto work_at = [&](uint64_t u, uint32_t &s, bool speak) -> uint64_t {
+    const uint32_t slots = slot_of(a.b.total, a.b.n_seqs, a.group, kRows, 1);
+    auto work_at = [&](uint32_t u, uint32_t &s, uint32_t &units, bool speak) -> uint64_t {
         Job job;
         s = seq_of_slot(a, u);
-        const Seq seq = read_seq(a.b, s, a.d_status, a.c.tokens, speak);
-        return work_of(a, seq, u - slot_of(uint32_t(max(__ldg(a.b.cu + s), 0)), s, a.group, kRows, 1), job);
+        units = units_of(a, read_seq(a.b, s, a.d_status, a.c.tokens, speak), u - first_slot(a, s), job);
+        return uint64_t(units) * a.c.heads;
     };
     uint64_t mine = 0, sum, W;
-    uint32_t s = 0;
-    for (uint64_t u = threadIdx.x; u < slots; u += kThreads) mine += work_at(u, s, cta == 0);
+    uint32_t s = 0, units = 0;
+    for (uint32_t u = threadIdx.x; u < slots; u += kThreads) mine += work_at(u, s, units, cta == 0);
     sum = block_scan<kWarps>(mine, sm.sums, W);
     const uint64_t G = min(uint64_t(gridDim.x), W);  // no CTA between two that have work is without
     if (cta >= G) return;
     const uint64_t w0 = W * cta / G, w1 = W * (cta + 1) / G;
     uint64_t before = 0;
-    for (uint64_t u0 = 0; u0 < slots; u0 += kThreads) {
+    for (uint32_t u0 = 0; u0 < slots; u0 += kThreads) {
         if (slots > kThreads) {  // more than one round: the sums above were not of single slots
-            mine = u0 + threadIdx.x < slots ? work_at(u0 + threadIdx.x, s, false) : 0;
+            mine = u0 + threadIdx.x < slots ? work_at(u0 + threadIdx.x, s, units, false) : 0;
             uint64_t all;
             sum = before + block_scan<kWarps>(mine, sm.sums, all);
             before += all;
         }
-        if (mine && sum > w0 && sum - mine <= w0) sm.slot = uint32_t(u0 + threadIdx.x), sm.seq = s, sm.at = sum - mine;
+        if (mine && sum > w0 && sum - mine <= w0) {
+            sm.slot = u0 + threadIdx.x, sm.seq = s;
+            sm.h = uint32_t((w0 - (sum - mine)) / units);
+            sm.i0 = sum - mine + uint64_t(sm.h) * units;
+        }
         if (before > w0) break;
     }
     if (threadIdx.x == 0) {
@@ -674,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     }
     __syncthreads();
     tm_after();
-    const Walk walk = {w0, w1, sm.at, sm.slot, sm.seq};
+    const Walk walk = {w0, w1, sm.i0, sm.slot, sm.seq, sm.h};
 
     bool ok = true;
     // 512 registers a lane over the four warpgroups, as at launch
@@ -690,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         if (warp == 13) ok = copy_role<DP>(a, maps, sm, walk);
     }
     if (!ok) report(a.d_status, ZC_ETIMEOUT);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     tm_before();
     __syncthreads();
@@ -717,7 +753,7 @@ template <int DP> int launch(const AttendArgs &a, cudaStream_t s) {
 } // namespace
 
 uint64_t tiles_counters(const Batch &b, const Cache &c, uint32_t group) {
-    return slots_of(b.total, b.n_seqs, group, kRows, 1) * c.heads;
+    return uint64_t(slot_of(b.total, b.n_seqs, group, kRows, 1)) * c.heads;
 }
 
 uint64_t tiles_part_bytes(const Cache &c) {

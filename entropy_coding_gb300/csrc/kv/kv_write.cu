@@ -52,7 +52,7 @@ __device__ __forceinline__ float two_to(int field) {  // 2^(field - 127), fields
 
 template <int DT> __global__ void __launch_bounds__(kThreads) write_kernel(MoveArgs a) {
     __shared__ uint32_t s_max;
-    uint64_t at;
+    uint32_t at;
     const uint32_t s = find_seq(a.b, blockIdx.x, 1, a.c.tokens, 2, at);
     const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, threadIdx.x == 0 && at == 0);
     if (!q.ok || q.n == 0) return;
@@ -62,11 +62,11 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write_kernel(MoveA
         return;
     }
     const uint32_t start = uint32_t(q.len) - q.n;
-    const uint64_t blk = uint64_t(start / B) + at;
-    if (blk * B >= uint64_t(q.len)) return;
-    const uint32_t lo = max(start, uint32_t(blk) * B), hi = min(uint32_t(q.len), uint32_t(blk + 1) * B);
-    const uint32_t n0 = lo - uint32_t(blk) * B, rows = hi - lo;
-    const int64_t id = read_block(a.b, a.c, s, uint32_t(blk), a.d_status);
+    const uint32_t blk = start / B + at;
+    if (uint64_t(blk) * B >= uint64_t(q.len)) return;
+    const uint32_t lo = max(start, blk * B), hi = min(uint32_t(q.len), (blk + 1) * B);
+    const uint32_t n0 = lo - blk * B, rows = hi - lo;
+    const int64_t id = read_block(a.b, a.c, s, blk, a.d_status);
     if (id < 0) return;
 
     const int elt = DT == ZC_FP32 ? 4 : 2;
@@ -130,9 +130,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write_kernel(MoveA
 } // namespace
 
 int launch_write(int dtype, const MoveArgs &a, cudaStream_t s) {
-    const uint64_t slots = slots_of(a.b.total, a.b.n_seqs, 1, a.c.tokens, 2);
-    if (slots > 0x7FFFFFFFull) return ZC_EINVAL;
-    const dim3 grid(uint32_t(slots), a.c.heads, 2);
+    const dim3 grid(slot_of(a.b.total, a.b.n_seqs, 1, a.c.tokens, 2), a.c.heads, 2);
     switch (dtype) {
     case ZC_BF16: write_kernel<ZC_BF16><<<grid, kThreads, 0, s>>>(a); break;
     case ZC_FP16: write_kernel<ZC_FP16><<<grid, kThreads, 0, s>>>(a); break;

@@ -444,7 +444,7 @@ ZC_API int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, int dt
  * scores of -infinity) is 0 with lse = -infinity; keys that a row does not
  * see have no influence on it, whatever they hold.
  *   dtype   ZC_BF16 or ZC_FP16: the type of q and out
- *   heads   query heads, a multiple of kv_heads
+ *   heads   query heads, a multiple of kv_heads; total_tokens * heads < 2^31
  *   q, out  [total_tokens][heads][head_dim]
  *   d_lse   NULL or float [total_tokens][heads]
  *   d_ws    workspace of ws_bytes >= zc_kv_attend_workspace_size(...), zeroed
