@@ -26,6 +26,7 @@
 //                    operand tiles, swizzled over 128 bytes as the products read them
 //   warp 12          one thread issues the products, as operands and weights come
 //   warp 13          copies: 8 boxes of 16 keys a code tile, by block table
+//   warp 14          one thread finds the CTA's pieces of work ahead of the others
 // While one tile's rows turn scores into weights, the other tile's products
 // run: 4 products of 128 x 128 x 128 a key tile, 2048 clocks of the tensor
 // cores, against about 1000 issue slots of the weights and 300 of the codes on
@@ -43,12 +44,30 @@ constexpr int kTile = 128;              // rows of a tile, keys of a key tile
 constexpr int kRows = 2 * kTile;        // rows of an item
 constexpr int kBoxes = kTile / 16;      // boxes of a code tile
 constexpr int kRaw = 3, kOps = 3;       // rings of code tiles and operand tiles (keys and values in turn)
+constexpr int kJobs = 4;                // pieces of work that are known ahead
+constexpr int kReaders = 8 + 4 + 1 + 1; // warps (and the products' thread) that read them
 constexpr int kSlots = 8;               // key tiles whose scales are held: the copies run up to 3 ahead of the weights
 constexpr uint32_t kColumns = 512;      // of tensor memory: S (and W in its place) 0, 128, O 256, 384
 
 struct Bars {
     uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], scale_full[kSlots];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], rows, drained;
+    uint64_t job_full[kJobs], job_empty[kJobs];
+};
+
+// A piece of work: key tiles of an item.
+struct Job {
+    Seq seq;
+    uint32_t tile, h;
+    int end;                         // no piece: the line's end
+    int whole;                       // the piece is the whole item; else:
+    uint32_t part;                   // where its partial result goes
+    uint32_t c0, c1;                 // the CTAs that have the item's first and last units
+    uint64_t counter;                // the item's
+    int all_lo, all_hi, x_lo, x_hi;  // keys seen by some row; by every row
+    int j0, n;                       // key tiles of the piece
+    int tiles;                       // of 128 rows
+    __device__ __forceinline__ bool edge(int j) const { return j * kTile < x_lo || (j + 1) * kTile > x_hi; }
 };
 
 template <int DP> struct Smem {
@@ -58,6 +77,7 @@ template <int DP> struct Smem {
     uint8_t out[8][32 * 64];            // a warp's rows, 32 columns at a time
     float ks[kSlots][kBoxes], lvs[kSlots][kBoxes];
     Bars bars;
+    Job jobs[kJobs];
     uint64_t sums[kWarps], i0;
     uint32_t slot, seq, h, tmem;
     int last, poison;
@@ -134,17 +154,6 @@ __device__ __forceinline__ int panel_at(int r, int c) { return c / 8 * (kTile * 
 // ---------------------------------------------------------------------------
 // The line of work
 
-struct Job {
-    Seq seq;
-    uint32_t tile, h;
-    uint64_t w, upto, i0, i1;        // the piece [w, upto) of the item's [i0, i1)
-    int all_lo, all_hi, x_lo, x_hi;  // keys seen by some row; by every row
-    int j0, n;                       // key tiles of the piece
-    int tiles;                       // of 128 rows
-    __device__ __forceinline__ bool whole() const { return w == i0 && upto == i1; }
-    __device__ __forceinline__ bool edge(int j) const { return j * kTile < x_lo || (j + 1) * kTile > x_hi; }
-};
-
 // Work of an item of this slot (a sequence's run of 256 rows), in key tiles; 0 if it is empty or not this kernel's.
 __device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &seq, uint32_t tile, Job &job) {
     const uint32_t n_rows = seq.n * a.group, row0 = tile * kRows;
@@ -172,9 +181,10 @@ __device__ __forceinline__ uint32_t seq_of_slot(const AttendArgs &a, uint32_t u)
     return lo;
 }
 
-// Where a role has got to on the line: every role walks the same pieces.
+// Where the CTA has got to on the line.
 struct Walk {
     uint64_t w, w1, i0;   // next work; the end; where the item begins
+    uint64_t W, G;        // all work; the CTAs that share it
     uint32_t slot, s, h;  // the item
     __device__ __forceinline__ bool next(const AttendArgs &a, Job &job) {
         while (w < w1) {
@@ -187,14 +197,20 @@ struct Walk {
                 while (s + 1 < a.b.n_seqs && first_slot(a, s + 1) <= slot) s++;
                 continue;
             }
+            const uint64_t i1 = i0 + units, upto = min(w1, i1);
             job.h = h;
-            job.i0 = i0;
-            job.i1 = i0 + units;
-            job.w = w;
-            job.upto = min(w1, job.i1);
             job.j0 = job.all_lo / kTile + int(w - i0);
-            job.n = max(min(int(job.upto - w), (job.all_hi + kTile - 1) / kTile - job.j0), 0);
-            w = job.upto;
+            job.n = max(min(int(upto - w), (job.all_hi + kTile - 1) / kTile - job.j0), 0);
+            job.whole = w == i0 && upto == i1;
+            job.part = 2 * blockIdx.x + (w == i0 ? 1 : 0);
+            if (!job.whole) {
+                // CTA c has the units [W c / G, W (c + 1) / G), rounded down: unit u is CTA (u G + G - 1) / W's
+                job.c0 = uint32_t((i0 * G + G - 1) / W);
+                job.c1 = uint32_t(((i1 - 1) * G + G - 1) / W);
+                job.counter = uint64_t(first_slot(a, s) + job.tile) * a.c.heads + h;
+            }
+            job.end = 0;
+            w = upto;
             return true;
         }
         return false;
@@ -204,13 +220,33 @@ struct Walk {
 // ---------------------------------------------------------------------------
 // Roles. Each returns false if a wait was given up.
 
+// Finds the CTA's pieces of work ahead of the others (one thread).
+template <int DP> __device__ __forceinline__ bool find_role(const AttendArgs &a, Smem<DP> &sm, Walk walk) {
+    for (uint32_t k = 0;; k++) {
+        Job job;
+        const bool more = walk.next(a, job);
+        if (!bar_wait(&sm.bars.job_empty[k % kJobs], (k / kJobs & 1) ^ 1)) return false;
+        job.end = !more;
+        sm.jobs[k % kJobs] = job;
+        bar_arrive(&sm.bars.job_full[k % kJobs]);
+        if (!more) return true;
+    }
+}
+template <int DP> __device__ __forceinline__ bool job_ready(Smem<DP> &sm, uint32_t k) {
+    return bar_wait(&sm.bars.job_full[k % kJobs], k / kJobs & 1);
+}
+// A reader is done with piece k (a warp, or the products' thread).
+template <int DP> __device__ __forceinline__ void job_done(Smem<DP> &sm, uint32_t k) { bar_arrive(&sm.bars.job_empty[k % kJobs]); }
+
 template <int DP>
-__device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &maps, Smem<DP> &sm, Walk walk) {
+__device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &maps, Smem<DP> &sm) {
     const int lane = threadIdx.x & 31;
     uint32_t item = 0, tile = 0;
     bool ok = true;
-    Job job;
-    while (ok && walk.next(a, job)) {
+    for (uint32_t k = 0; ok; k++) {
+        if (!(ok = __all_sync(0xFFFFFFFFu, job_ready(sm, k)))) break;
+        const Job &job = sm.jobs[k % kJobs];
+        if (job.end) break;
         const int least = job.all_lo / 16, last = (job.all_hi - 1) / 16;  // boxes without a key that is seen hold others again
         for (int j = job.j0; j < job.j0 + job.n && ok; j++, tile++) {
             const int slot = tile % kSlots;
@@ -235,17 +271,21 @@ __device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &m
                 if (lane < kBoxes) copy_box(sm.raw[r] + lane * 16 * DP, &maps.code[kv], row, id, &sm.bars.raw_full[r]);
             }
         }
+        __syncwarp();
+        if (lane == 0) job_done(sm, k);
     }
     // The CTA outlives its copies, also those of a call that is given up.
     for (uint32_t k = item > kRaw ? item - kRaw : 0; k < item; k++) ok &= bar_wait(&sm.bars.raw_full[k % kRaw], k / kRaw & 1);
     return ok;
 }
 
-template <int DP> __device__ __forceinline__ bool convert_role(const AttendArgs &a, Smem<DP> &sm, Walk walk) {
+template <int DP> __device__ __forceinline__ bool convert_role(Smem<DP> &sm) {
     const int t = threadIdx.x - 256, lane = t & 31;
     uint32_t item = 0;
-    Job job;
-    while (walk.next(a, job)) {
+    for (uint32_t k = 0;; k++) {
+        if (!__all_sync(0xFFFFFFFFu, job_ready(sm, k))) return false;
+        const Job &job = sm.jobs[k % kJobs];
+        if (job.end) return true;
         for (int j = job.j0; j < job.j0 + job.n; j++)
 #pragma unroll 1
             for (int kv = 0; kv < 2; kv++, item++) {
@@ -280,12 +320,13 @@ template <int DP> __device__ __forceinline__ bool convert_role(const AttendArgs 
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sm.bars.raw_empty[r]), bar_arrive(&sm.bars.op_full[c]);
             }
+        __syncwarp();
+        if (lane == 0) job_done(sm, k);
     }
-    return true;
 }
 
 // One thread.
-template <int DP> __device__ __forceinline__ bool product_role(const AttendArgs &a, Smem<DP> &sm, Walk walk) {
+template <int DP> __device__ __forceinline__ bool product_role(Smem<DP> &sm) {
     constexpr uint32_t kPanel = kTile * 128;
     const uint32_t tm = sm.tmem;
     uint32_t item = 0, queries[2] = {0, 0}, weights[2] = {0, 0};
@@ -304,8 +345,10 @@ template <int DP> __device__ __forceinline__ bool product_role(const AttendArgs 
             mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * i, v + (i * 16 * 128 >> 4), product(DP, true), add || i > 0);
     };
     bool ok = true;
-    Job job;
-    while (ok && walk.next(a, job)) {
+    for (uint32_t k = 0; ok; job_done(sm, k), k++) {
+        if (!(ok = job_ready(sm, k))) break;
+        const Job &job = sm.jobs[k % kJobs];
+        if (job.end) break;
         if (!job.n) continue;
         ok = bar_wait(&sm.bars.op_full[item % kOps], item / kOps & 1);
         for (int t = 0; t < job.tiles && ok; t++) {
@@ -319,7 +362,7 @@ template <int DP> __device__ __forceinline__ bool product_role(const AttendArgs 
         mma_commit(&sm.bars.op_empty[item % kOps]);
         item++;
         for (int j = 0; j < job.n && ok; j++) {
-            const uint32_t v = item, k = item + 1;
+            const uint32_t v = item, next = item + 1;
             item += j + 1 < job.n ? 2 : 1;
             ok = bar_wait(&sm.bars.op_full[v % kOps], v / kOps & 1);
             for (int t = 0; t < job.tiles && ok; t++) {
@@ -329,12 +372,12 @@ template <int DP> __device__ __forceinline__ bool product_role(const AttendArgs 
                 sums(t, v % kOps, j > 0);
                 if (t == job.tiles - 1) mma_commit(&sm.bars.op_empty[v % kOps]);
                 if (j + 1 < job.n) {
-                    if (t == 0) ok = bar_wait(&sm.bars.op_full[k % kOps], k / kOps & 1);
+                    if (t == 0) ok = bar_wait(&sm.bars.op_full[next % kOps], next / kOps & 1);
                     if (!ok) break;
                     tm_after();
-                    scores(t, k % kOps);
+                    scores(t, next % kOps);
                     mma_commit(&sm.bars.s_full[t]);
-                    if (t == job.tiles - 1) mma_commit(&sm.bars.op_empty[k % kOps]);
+                    if (t == job.tiles - 1) mma_commit(&sm.bars.op_empty[next % kOps]);
                 } else {
                     mma_commit(&sm.bars.o_full[t]);
                 }
@@ -376,7 +419,7 @@ constexpr int kNoRow = -1;
 template <int DP> __device__ __forceinline__ void fetch_queries(const AttendArgs &a, Smem<DP> &sm, const Job &job) {
     constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes;  // lanes of a row, 16 bytes each
     const int r = threadIdx.x, half = r / kTile, lane = r & 31, ch = lane % kLanes;
-    if (!job.n || half >= job.tiles) return;
+    if (job.end || !job.n || half >= job.tiles) return;
     const uint32_t row = job.tile * kRows + r;
     const int64_t from = row < job.seq.n * a.group ? row_at(a, a.q, job.seq, job.h, row) : kNoRow;
 #pragma unroll 2
@@ -434,16 +477,18 @@ template <int DP> __device__ __forceinline__ float ready_query(const AttendArgs 
 }
 
 template <int DP>
-__device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Walk walk, uint64_t W, uint64_t G, Part<DP> *parts) {
+__device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
+    Part<DP> *parts = reinterpret_cast<Part<DP> *>(a.parts);
     const int r = threadIdx.x, half = r / kTile;                 // row of the item; its tile
     const int lane = r & 31;
     const uint32_t lanes = uint32_t(r / 32 % 4 * 32) << 16;      // of tensor memory
     const uint32_t tmS = sm.tmem + half * 128 + lanes, tmO = sm.tmem + 256 + half * 128 + lanes;
     uint32_t tile = 0, scored = 0, summed = 0, met = 0;
-    Job job, next;
-    bool more = walk.next(a, job);
-    fetch_queries(a, sm, job);
-    for (; more; job = next) {
+    if (!__all_sync(0xFFFFFFFFu, job_ready(sm, 0))) return false;
+    fetch_queries(a, sm, sm.jobs[0]);
+    for (uint32_t k = 0;; k++) {
+        const Job &job = sm.jobs[k % kJobs], &next = sm.jobs[(k + 1) % kJobs];
+        if (job.end) return true;
         const uint32_t row = job.tile * kRows + r, n_rows = job.seq.n * a.group;
         const bool mine = row < n_rows;
         int lo = 0, hi = 0;
@@ -533,12 +578,12 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
         }
 
         // The next piece's queries are on their way while this one is finished.
-        more = walk.next(a, next);
-        if (more) fetch_queries(a, sm, next);
+        if (!__all_sync(0xFFFFFFFFu, job_ready(sm, k + 1))) return false;
+        fetch_queries(a, sm, next);
 
         // The rows' ends: finished, or a part.
-        const bool whole = job.whole();
-        Part<DP> *part = parts + 2 * blockIdx.x + (job.w == job.i0 ? 1 : 0);
+        const bool whole = job.whole;
+        Part<DP> *part = parts + job.part;
         if (half < job.tiles) {
             const float by = row_factor(m, mw, l);
             const bool poison = job.n && *reinterpret_cast<volatile int *>(&sm.poison);
@@ -597,10 +642,10 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
             tm_before();
         }
         if (!whole) {
-            const uint32_t c0 = uint32_t((job.i0 * G + G - 1) / W), c1 = uint32_t(((job.i1 - 1) * G + G - 1) / W);  // as in kv_rows.cu
+            const uint32_t c0 = job.c0, c1 = job.c1;
             if (!rows_meet(&sm.bars.rows, met++)) return false;
             if (r == 0) {
-                uint32_t *counter = a.counters + uint64_t(first_slot(a, job.seq.s) + job.tile) * a.c.heads + job.h;
+                uint32_t *counter = a.counters + job.counter;
                 uint32_t done;
                 asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
                 if (done == c1 - c0) *counter = 0;
@@ -648,8 +693,9 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm, Wal
                 }
             }
         }
+        __syncwarp();
+        if (lane == 0) job_done(sm, k);
     }
-    return true;
 }
 
 template <int DP>
@@ -695,6 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         for (int i = 0; i < kOps; i++) bar_init(&b.op_full[i], 4), bar_init(&b.op_empty[i], 1);
         for (int i = 0; i < kSlots; i++) bar_init(&b.scale_full[i], 1);
         for (int i = 0; i < 2; i++) bar_init(&b.q_full[i], 4), bar_init(&b.s_full[i], 1), bar_init(&b.p_full[i], 4), bar_init(&b.o_full[i], 1);
+        for (int i = 0; i < kJobs; i++) bar_init(&b.job_full[i], 1), bar_init(&b.job_empty[i], kReaders);
         bar_init(&b.rows, 8);
         bar_init(&b.drained, 1);
         bar_init_done();
@@ -709,20 +756,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     }
     __syncthreads();
     tm_after();
-    const Walk walk = {w0, w1, sm.i0, sm.slot, sm.seq, sm.h};
-
+    
     bool ok = true;
     // 512 registers a lane over the four warpgroups, as at launch
     if (warp < 8) {
         more_registers<192>();
-        ok = rows_role<DP>(a, sm, walk, W, G, reinterpret_cast<Part<DP> *>(a.parts));
+        ok = rows_role<DP>(a, sm);
     } else if (warp < 12) {
         fewer_registers<72>();
-        ok = convert_role<DP>(a, sm, walk);
+        ok = convert_role<DP>(sm);
     } else {
         fewer_registers<56>();
-        if (warp == 12 && threadIdx.x % 32 == 0) ok = product_role<DP>(a, sm, walk);
-        if (warp == 13) ok = copy_role<DP>(a, maps, sm, walk);
+        if (warp == 12 && threadIdx.x % 32 == 0) ok = product_role<DP>(sm);
+        if (warp == 13) ok = copy_role<DP>(a, maps, sm);
+        if (warp == 14 && threadIdx.x % 32 == 0) ok = find_role<DP>(a, sm, Walk{w0, w1, sm.i0, W, G, sm.slot, sm.seq, sm.h});
     }
     if (!ok) report(a.d_status, ZC_ETIMEOUT);
     asm volatile("cp.async.wait_all;" ::: "memory");
