@@ -24,7 +24,7 @@
 //                    tensor memory, weights back, the output's rescaling and end
 //   warps 8-11       codes to halves, from the ring of code tiles to the ring of
 //                    operand tiles, swizzled over 128 bytes as the products read them
-//   warp 12          one thread issues the products, as operands and weights come
+//   warp 12          issues the products, as operands and weights come
 //   warp 13          copies: 8 boxes of 16 keys a code tile, by block table
 //   warp 14          one thread finds the CTA's pieces of work ahead of the others
 // While one tile's rows turn scores into weights, the other tile's products
@@ -51,7 +51,7 @@ constexpr uint32_t kColumns = 512;      // of tensor memory: S (and W in its pla
 
 struct Bars {
     uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], scale_full[kSlots];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], rows, drained;
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], rows, drained;
     uint64_t job_full[kJobs], job_empty[kJobs];
 };
 
@@ -138,6 +138,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 // The barrier is arrived at when all products issued so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_of(bar)) : "memory");
+}
+
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{.reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p;}" : "=r"(p));
+    return p;
 }
 
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -325,68 +331,91 @@ template <int DP> __device__ __forceinline__ bool convert_role(Smem<DP> &sm) {
     }
 }
 
-// One thread.
+// A warp whose elected thread issues; the others keep its addresses uniform, as the products want them.
 template <int DP> __device__ __forceinline__ bool product_role(Smem<DP> &sm) {
     constexpr uint32_t kPanel = kTile * 128;
-    const uint32_t tm = sm.tmem;
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, sm.tmem, 0);
+    const bool one = elected();
+    const uint64_t q0 = operand(smem_of(sm.q[0]), 0), k0 = operand(smem_of(sm.op[0]), 0), v0 = operand(smem_of(sm.op[0]), kPanel);
+    constexpr uint32_t kQ = sizeof(sm.q[0]) >> 4, kOp = sizeof(sm.op[0]) >> 4;
     uint32_t item = 0, queries[2] = {0, 0}, weights[2] = {0, 0};
     auto scores = [&](int t, uint32_t c) {
-        const uint64_t q = operand(smem_of(sm.q[t]), 0), k = operand(smem_of(sm.op[c]), 0);
+        const uint64_t q = q0 + t * kQ, k = k0 + c * kOp;
+        if (one) {
 #pragma unroll
-        for (int i = 0; i < DP / 16; i++) {  // 16 columns: 32 bytes on within a panel
-            const uint32_t at = (i / 4 * kPanel + i % 4 * 32) >> 4;
-            mma_ss(tm + t * 128, q + at, k + at, product(kTile, false), i > 0);
+            for (int i = 0; i < DP / 16; i++) {  // 16 columns: 32 bytes on within a panel
+                const uint32_t at = (i / 4 * kPanel + i % 4 * 32) >> 4;
+                mma_ss(tm + t * 128, q + at, k + at, product(kTile, false), i > 0);
+            }
         }
+        __syncwarp();
     };
-    auto sums = [&](int t, uint32_t c, bool add) {
-        const uint64_t v = operand(smem_of(sm.op[c]), kPanel);
+    // half of the key tile's sums: 64 keys
+    auto sums = [&](int t, uint32_t c, int part, bool add) {
+        const uint64_t v = v0 + c * kOp;
+        if (one) {
 #pragma unroll
-        for (int i = 0; i < kTile / 16; i++)  // 16 keys: 8 columns of weights, 16 rows of values
-            mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * i, v + (i * 16 * 128 >> 4), product(DP, true), add || i > 0);
+            for (int i = 0; i < kTile / 32; i++) {  // 16 keys: 8 columns of weights, 16 rows of values
+                const int at = part * (kTile / 32) + i;
+                mma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * at, v + (at * 16 * 128 >> 4), product(DP, true), add || i > 0);
+            }
+        }
+        __syncwarp();
     };
+    auto commit = [&](uint64_t *bar) {
+        if (one) mma_commit(bar);
+        __syncwarp();
+    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return bool(__all_sync(0xFFFFFFFFu, bar_wait(bar, parity))); };
     bool ok = true;
-    for (uint32_t k = 0; ok; job_done(sm, k), k++) {
-        if (!(ok = job_ready(sm, k))) break;
+    for (uint32_t k = 0; ok; k++) {
+        if (!(ok = __all_sync(0xFFFFFFFFu, job_ready(sm, k)))) break;
         const Job &job = sm.jobs[k % kJobs];
-        if (job.end) break;
-        if (!job.n) continue;
-        ok = bar_wait(&sm.bars.op_full[item % kOps], item / kOps & 1);
-        for (int t = 0; t < job.tiles && ok; t++) {
-            ok = bar_wait(&sm.bars.q_full[t], queries[t]++ & 1);
+        const int n = __shfl_sync(0xFFFFFFFFu, job.n, 0), tiles = __shfl_sync(0xFFFFFFFFu, job.tiles, 0);
+        if (__shfl_sync(0xFFFFFFFFu, job.end, 0)) break;
+        if (one) job_done(sm, k);
+        if (!n) continue;
+        ok = wait(&sm.bars.op_full[item % kOps], item / kOps & 1);
+        for (int t = 0; t < tiles && ok; t++) {
+            ok = wait(&sm.bars.q_full[t], queries[t]++ & 1);
             if (!ok) break;
             tm_after();
             scores(t, item % kOps);
-            mma_commit(&sm.bars.s_full[t]);
+            commit(&sm.bars.s_full[t]);
         }
         if (!ok) break;
-        mma_commit(&sm.bars.op_empty[item % kOps]);
+        commit(&sm.bars.op_empty[item % kOps]);
         item++;
-        for (int j = 0; j < job.n && ok; j++) {
+        for (int j = 0; j < n && ok; j++) {
             const uint32_t v = item, next = item + 1;
-            item += j + 1 < job.n ? 2 : 1;
-            ok = bar_wait(&sm.bars.op_full[v % kOps], v / kOps & 1);
-            for (int t = 0; t < job.tiles && ok; t++) {
-                ok = bar_wait(&sm.bars.p_full[t], weights[t]++ & 1);
+            item += j + 1 < n ? 2 : 1;
+            ok = wait(&sm.bars.op_full[v % kOps], v / kOps & 1);
+            for (int t = 0; t < tiles && ok; t++) {
+                for (int part = 0; part < 2 && ok; part++) {
+                    ok = wait(&sm.bars.p_full[t][part], weights[t] & 1);
+                    if (!ok) break;
+                    tm_after();
+                    sums(t, v % kOps, part, j > 0 || part > 0);
+                }
                 if (!ok) break;
-                tm_after();
-                sums(t, v % kOps, j > 0);
-                if (t == job.tiles - 1) mma_commit(&sm.bars.op_empty[v % kOps]);
-                if (j + 1 < job.n) {
-                    if (t == 0) ok = bar_wait(&sm.bars.op_full[next % kOps], next / kOps & 1);
+                weights[t]++;
+                if (t == tiles - 1) commit(&sm.bars.op_empty[v % kOps]);
+                if (j + 1 < n) {
+                    if (t == 0) ok = wait(&sm.bars.op_full[next % kOps], next / kOps & 1);
                     if (!ok) break;
                     tm_after();
                     scores(t, next % kOps);
-                    mma_commit(&sm.bars.s_full[t]);
-                    if (t == job.tiles - 1) mma_commit(&sm.bars.op_empty[next % kOps]);
+                    commit(&sm.bars.s_full[t]);
+                    if (t == tiles - 1) commit(&sm.bars.op_empty[next % kOps]);
                 } else {
-                    mma_commit(&sm.bars.o_full[t]);
+                    commit(&sm.bars.o_full[t]);
                 }
             }
         }
     }
     // Tensor memory is freed once the products are done, also those of a call that is given up.
-    mma_commit(&sm.bars.drained);
-    return bar_wait(&sm.bars.drained, 0) && ok;
+    commit(&sm.bars.drained);
+    return wait(&sm.bars.drained, 0) && ok;
 }
 
 // Columns [col, col + 32) of values that are NaN at keys that the row [lo, hi) sees, among the piece's key tiles where
@@ -500,15 +529,24 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
             {
                 for (int j = job.j0; j < job.j0 + job.n; j++, tile++, scored++) {
                     const int slot = tile % kSlots;
-                    if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.scale_full[slot], tile / kSlots & 1) &&
-                                                     bar_wait(&sm.bars.s_full[half], scored & 1)))
-                        return false;
+                    if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.scale_full[slot], tile / kSlots & 1))) return false;
+                    float by[kBoxes], lvs[kBoxes];  // read early: the products keep shared memory busy
+#pragma unroll
+                    for (int b = 0; b < kBoxes; b += 4) {
+                        const float4 u = *reinterpret_cast<const float4 *>(&sm.ks[slot][b]), v = *reinterpret_cast<const float4 *>(&sm.lvs[slot][b]);
+                        by[b] = u.x, by[b + 1] = u.y, by[b + 2] = u.z, by[b + 3] = u.w;
+                        lvs[b] = v.x, lvs[b + 1] = v.y, lvs[b + 2] = v.z, lvs[b + 3] = v.w;
+                    }
+                    const bool edge = job.edge(j);
+#pragma unroll
+                    for (int b = 0; b < kBoxes; b++) by[b] = fmaxf(c * by[b], 1e-37f);  // (0 * -infinity would be NaN)
+                    if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.s_full[half], scored & 1))) return false;
                     tm_after();
                     float x[kTile];
 #pragma unroll
                     for (int i = 0; i < 4; i++) tm_load32(tmS + 32 * i, x + 32 * i);
                     tm_wait_load();
-                    if (job.edge(j)) {
+                    if (edge) {
                         const int from = lo - j * kTile, to = hi - j * kTile;
 #pragma unroll
                         for (int i = 0; i < kTile; i++)
@@ -520,9 +558,9 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                         float g = x[16 * b];
 #pragma unroll
                         for (int i = 1; i < 16; i++) g = fmaxf(g, x[16 * b + i]);
-                        g *= fmaxf(c * sm.ks[slot][b], 1e-37f);  // (0 * -infinity would be NaN)
+                        g *= by[b];
                         top = fmaxf(top, g);
-                        topw = fmaxf(topw, g + sm.lvs[slot][b]);
+                        topw = fmaxf(topw, g + lvs[b]);
                     }
                     // As in kv_rows.cu: the maxima are followed once they have grown by 2^kSlack.
                     const bool grows = top > m + kSlack || topw > mw + kSlack;
@@ -550,27 +588,28 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                     const float base = m == kNone ? 0.0f : m;
                     uint32_t *p = reinterpret_cast<uint32_t *>(x);
 #pragma unroll
-                    for (int b = 0; b < kBoxes; b++) {
-                        const float by = fmaxf(c * sm.ks[slot][b], 1e-37f);
-                        const float lf = fminf(fmaxf(sm.lvs[slot][b] + (base - mw), -60.0f), 120.0f);  // (mw = -infinity: every vs is 0)
-                        const float bias = lf - base;
-                        float sum0 = 0.0f, sum1 = 0.0f;
+                    for (int part = 0; part < 2; part++) {  // the products start on the first 64 keys' weights
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float y0, y1;
-                            fma2(y0, y1, x[16 * b + i], x[16 * b + i + 1], by, bias);
-                            y0 = ex2(y0), y1 = ex2(y1);
-                            sum0 += y0, sum1 += y1;
-                            p[8 * b + i / 2] = half2_of(y0, y1);
+                        for (int b = part * kBoxes / 2; b < (part + 1) * kBoxes / 2; b++) {
+                            const float lf = fminf(fmaxf(lvs[b] + (base - mw), -60.0f), 120.0f);  // (mw = -infinity: every vs is 0)
+                            const float bias = lf - base;
+                            float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                float y0, y1;
+                                fma2(y0, y1, x[16 * b + i], x[16 * b + i + 1], by[b], bias);
+                                y0 = ex2(y0), y1 = ex2(y1);
+                                sum0 += y0, sum1 += y1;
+                                p[8 * b + i / 2] = half2_of(y0, y1);
+                            }
+                            l += (sum0 + sum1) * ex2(-lf);
                         }
-                        l += (sum0 + sum1) * ex2(-lf);
+                        tm_store32(tmS + 32 * part, p + 32 * part);
+                        tm_wait_store();
+                        tm_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&sm.bars.p_full[half][part]);
                     }
-                    tm_store32(tmS, p);
-                    tm_store32(tmS + 32, p + 32);
-                    tm_wait_store();
-                    tm_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(&sm.bars.p_full[half]);
                 }
                 if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.o_full[half], summed++ & 1))) return false;
                 tm_after();
@@ -740,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         for (int i = 0; i < kRaw; i++) bar_init(&b.raw_full[i], 1), bar_init(&b.raw_empty[i], 4);
         for (int i = 0; i < kOps; i++) bar_init(&b.op_full[i], 4), bar_init(&b.op_empty[i], 1);
         for (int i = 0; i < kSlots; i++) bar_init(&b.scale_full[i], 1);
-        for (int i = 0; i < 2; i++) bar_init(&b.q_full[i], 4), bar_init(&b.s_full[i], 1), bar_init(&b.p_full[i], 4), bar_init(&b.o_full[i], 1);
+        for (int i = 0; i < 2; i++) bar_init(&b.q_full[i], 4), bar_init(&b.s_full[i], 1), bar_init(&b.p_full[i][0], 4), bar_init(&b.p_full[i][1], 4), bar_init(&b.o_full[i], 1);
         for (int i = 0; i < kJobs; i++) bar_init(&b.job_full[i], 1), bar_init(&b.job_empty[i], kReaders);
         bar_init(&b.rows, 8);
         bar_init(&b.drained, 1);
@@ -767,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         ok = convert_role<DP>(sm);
     } else {
         fewer_registers<56>();
-        if (warp == 12 && threadIdx.x % 32 == 0) ok = product_role<DP>(sm);
+        if (warp == 12) ok = product_role<DP>(sm);
         if (warp == 13) ok = copy_role<DP>(a, maps, sm);
         if (warp == 14 && threadIdx.x % 32 == 0) ok = find_role<DP>(a, sm, Walk{w0, w1, sm.i0, W, G, sm.slot, sm.seq, sm.h});
     }
