@@ -189,6 +189,7 @@ template <int DP, int S>
 __device__ __forceinline__ void begin(const AttendArgs &a, const CodeMaps &maps, Warp<S> &wp, Stage<DP> *ring, const Job &job, uint32_t turn) {
     look_up(a, wp, job, 0);
     __syncwarp();
+#pragma unroll 1
     for (int k = 0; k < S - 1; k++) fetch<DP>(a, maps, wp, ring, job, k, (turn + k) % S);
 }
 
@@ -203,6 +204,7 @@ template <int DP, int NT> struct Sums {
     // Of rows 2t, 2t + 1 of each tile: running maxima (the scores', and with the value scales),
     // 2^(m - mw), and the weights' sums over this thread's keys.
     float m[NT][2], mw[NT][2], unit[NT][2], l[NT][2];
+    uint32_t poison[NT][2];  // of this thread's columns: where a value that the row sees is NaN, and was taken out
 };
 
 template <int DP, int NT, int S>
@@ -269,7 +271,7 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int e = 0; e < 2; e++) m[n][e] = mw[n][e] = kNone, unit[n][e] = l[n][e] = 0.0f;
+        for (int e = 0; e < 2; e++) m[n][e] = mw[n][e] = kNone, unit[n][e] = l[n][e] = 0.0f, acc.poison[n][e] = 0;
 
     uint32_t st = turn % S, parity = turn / S & 1;  // of step k
     for (int k = 0; k < job.steps; k++) {
@@ -381,26 +383,26 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
             // A row that does not see a key has weight 0 for it, but 0 * NaN is NaN: NaN codes are
             // taken out here and given to the rows that do see them.
             bool bad = false;
+#pragma unroll 1
             for (int j = lane; j < kSlice * DP / 16; j += 32) {
                 const uint4 v = *reinterpret_cast<const uint4 *>(&sl.v[16 * j]);
                 bad |= any_nan(v.x) || any_nan(v.y) || any_nan(v.z) || any_nan(v.w);
             }
             if (__any_sync(0xFFFFFFFFu, bad)) {
-                for (int k = 0; k < kSlice; k++)
 #pragma unroll
-                    for (int n = 0; n < NT; n++)
+                for (int n = 0; n < NT; n++)
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            int lo, hi;
-                            bounds(a, seq, min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
-                            const bool sees = key0 + k >= lo && key0 + k < hi;
-#pragma unroll
-                            for (int c = 0; c < kCols; c++) {
-                                const int col = kCols * g + c;
-                                if (sees && (sl.v[chunk_at<DP>(k, col / 16) + col % 16] & 0x7F) == 0x7F) o[n][c / 2][2 * (c & 1) + e] = NAN;
-                            }
-                        }
+                    for (int e = 0; e < 2; e++) {
+                        int lo, hi;
+                        bounds(a, seq, min(row0 + 8 * n + 2 * t + e, n_rows - 1), lo, hi);
+#pragma unroll 1
+                        for (int k = max(lo - key0, 0); k < min(hi - key0, kSlice); k++)
+#pragma unroll 1
+                            for (int c = 0; c < kCols; c++)
+                                if ((sl.v[chunk_at<DP>(k, (kCols * g + c) / 16) + (kCols * g + c) % 16] & 0x7F) == 0x7F) acc.poison[n][e] |= 1u << c;
+                    }
                 __syncwarp();
+#pragma unroll 1
                 for (int j = lane; j < kSlice * DP; j += 32)
                     if ((sl.v[j] & 0x7F) == 0x7F) sl.v[j] = 0;
                 fence_async();
@@ -450,6 +452,11 @@ __device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const 
             float l = acc.l[n][e];
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+            if (acc.poison[n][e]) {
+#pragma unroll
+                for (int c = 0; c < kCols; c++)
+                    if (acc.poison[n][e] >> c & 1) acc.o[n][c / 2][2 * (c & 1) + e] = NAN;
+            }
             if (g == 0) mg.m[warp][r] = acc.m[n][e], mg.mw[warp][r] = acc.mw[n][e], mg.l[warp][r] = l;
 #pragma unroll
             for (int c = 0; c < DP / 16; c += 2)

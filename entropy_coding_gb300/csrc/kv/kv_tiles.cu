@@ -15,8 +15,8 @@
 // spread between them loses precision. A block whose scale is 2^60 below the
 // unit adds less than 2^-51 of it and counts as 2^-60. out = O 2^(mw - m) / l.
 //
-// Work: as in kv_rows.cu, one line of key tiles over all items, an equal
-// piece for each of one CTA an SM; items cut by a piece's end leave partial
+// Work: as in kv_rows.cu, one line of key tiles over all items (an item's
+// beginning and end count as 4 tiles), an equal piece for each of one CTA an SM; items cut by a piece's end leave partial
 // results, which the last CTA of the item joins.
 //
 // A CTA is 16 warps in roles, which meet at barriers in shared memory:
@@ -44,6 +44,7 @@ constexpr int kTile = 128;              // rows of a tile, keys of a key tile
 constexpr int kRows = 2 * kTile;        // rows of an item
 constexpr int kBoxes = kTile / 16;      // boxes of a code tile
 constexpr int kRaw = 3, kOps = 3;       // rings of code tiles and operand tiles (keys and values in turn)
+constexpr uint32_t kFixed = 4;          // units of work of an item besides its key tiles: its beginning and end
 constexpr int kJobs = 4;                // pieces of work that are known ahead
 constexpr int kReaders = 8 + 4 + 1 + 1; // warps (and the products' thread) that read them
 constexpr int kSlots = 8;               // key tiles whose scales are held: the copies run up to 3 ahead of the weights
@@ -160,7 +161,8 @@ __device__ __forceinline__ int panel_at(int r, int c) { return c / 8 * (kTile * 
 // ---------------------------------------------------------------------------
 // The line of work
 
-// Work of an item of this slot (a sequence's run of 256 rows), in key tiles; 0 if it is empty or not this kernel's.
+// Work of an item of this slot (a sequence's run of 256 rows): kFixed units and one for each of its key tiles (or one);
+// 0 if it is empty or not this kernel's.
 __device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &seq, uint32_t tile, Job &job) {
     const uint32_t n_rows = seq.n * a.group, row0 = tile * kRows;
     if (!seq.ok || n_rows <= a.rows_most || row0 >= n_rows) return 0;
@@ -169,7 +171,7 @@ __device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &seq
     bounds(a, seq, row0, job.all_lo, job.x_hi);
     bounds(a, seq, min(row0 + kRows, n_rows) - 1, job.x_lo, job.all_hi);
     job.tiles = n_rows - row0 > kTile ? 2 : 1;
-    return uint32_t(max((job.all_hi + kTile - 1) / kTile - job.all_lo / kTile, 1));
+    return kFixed + uint32_t(max((job.all_hi + kTile - 1) / kTile - job.all_lo / kTile, 1));
 }
 
 __device__ __forceinline__ uint32_t first_slot(const AttendArgs &a, uint32_t s) {
@@ -203,20 +205,21 @@ struct Walk {
                 while (s + 1 < a.b.n_seqs && first_slot(a, s + 1) <= slot) s++;
                 continue;
             }
-            const uint64_t i1 = i0 + units, upto = min(w1, i1);
+            const uint64_t first = i0 + kFixed, i1 = i0 + units, from = max(w, first), upto = min(w1, i1);
+            w = upto;
+            if (upto <= first) continue;  // the piece ends within the item's beginning, which belongs to the first tile's piece
             job.h = h;
-            job.j0 = job.all_lo / kTile + int(w - i0);
-            job.n = max(min(int(upto - w), (job.all_hi + kTile - 1) / kTile - job.j0), 0);
-            job.whole = w == i0 && upto == i1;
-            job.part = 2 * blockIdx.x + (w == i0 ? 1 : 0);
+            job.j0 = job.all_lo / kTile + int(from - first);
+            job.n = max(min(int(upto - from), (job.all_hi + kTile - 1) / kTile - job.j0), 0);
+            job.whole = from == first && upto == i1;
+            job.part = 2 * blockIdx.x + (from == first ? 1 : 0);
             if (!job.whole) {
                 // CTA c has the units [W c / G, W (c + 1) / G), rounded down: unit u is CTA (u G + G - 1) / W's
-                job.c0 = uint32_t((i0 * G + G - 1) / W);
+                job.c0 = uint32_t((first * G + G - 1) / W);
                 job.c1 = uint32_t(((i1 - 1) * G + G - 1) / W);
                 job.counter = uint64_t(first_slot(a, s) + job.tile) * a.c.heads + h;
             }
             job.end = 0;
-            w = upto;
             return true;
         }
         return false;
@@ -303,17 +306,32 @@ template <int DP> __device__ __forceinline__ bool convert_role(Smem<DP> &sm) {
                 // keys, NaN codes of values are taken out, and rows that see them get them at the end.
                 const bool edge = kv && job.edge(j);
                 constexpr int kChunks = DP / 16;
+                // 8 lanes take 8 rows of one chunk: reads and writes of a quarter warp meet all banks
+                auto chunk = [&](int i, int &row, int &ch) {
+                    const int u = i * 128 + t;
+                    row = u % 8 + u / (8 * kChunks) * 8, ch = u / 8 % kChunks;
+                    return reinterpret_cast<uint4 *>(sm.raw[r] + row * DP + 16 * (ch ^ (DP == 128 ? row & 7 : row >> 1 & 3)));
+                };
+                int row, ch;
+                if (edge) {
+#pragma unroll 1
+                    for (int i = 0; i < kTile * kChunks / 128; i++) {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(chunk(i, row, ch));
+#pragma unroll 1
+                        for (int k = 0; k < 4; k++) {
+                            if (!any_nan(w[k])) continue;
+                            w[k] &= ~__vcmpeq4(w[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                            if (j * kTile + row >= job.all_lo && j * kTile + row < job.all_hi) sm.poison = 1;
+                        }
+                    }
+                }
+                uint4 in[kTile * kChunks / 128];  // all reads first: the products' reads of shared memory go before them
+#pragma unroll
+                for (int i = 0; i < kTile * kChunks / 128; i++) in[i] = *chunk(i, row, ch);
 #pragma unroll
                 for (int i = 0; i < kTile * kChunks / 128; i++) {
-                    // 8 lanes take 8 rows of one chunk: reads and writes of a quarter warp meet all banks
-                    const int u = i * 128 + t, row = u % 8 + u / (8 * kChunks) * 8, ch = u / 8 % kChunks;
-                    uint4 v = *reinterpret_cast<const uint4 *>(sm.raw[r] + row * DP + 16 * (ch ^ (DP == 128 ? row & 7 : row >> 1 & 3)));
-                    if (edge && (any_nan(v.x) || any_nan(v.y) || any_nan(v.z) || any_nan(v.w))) {
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                        for (int k = 0; k < 4; k++) w[k] &= ~__vcmpeq4(w[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                        if (j * kTile + row >= job.all_lo && j * kTile + row < job.all_hi) sm.poison = 1;
-                    }
+                    const uint4 v = in[i];
+                    chunk(i, row, ch);
                     uint4 lo, hi;
                     e4m3x4_to_half2x2(v.x, lo.x, lo.y);
                     e4m3x4_to_half2x2(v.y, lo.z, lo.w);
@@ -420,19 +438,71 @@ template <int DP> __device__ __forceinline__ bool product_role(Smem<DP> &sm) {
 
 // Columns [col, col + 32) of values that are NaN at keys that the row [lo, hi) sees, among the piece's key tiles where
 // NaN was taken out; a bit a column.
-__device__ __forceinline__ uint32_t poisoned(const AttendArgs &a, const Job &job, int lo, int hi, int col) {
+__device__ __noinline__ uint32_t poisoned(const AttendArgs &a, const Job &job, int lo, int hi, int col) {
     uint32_t mask = 0;
+#pragma unroll 1
     for (int j = job.j0; j < job.j0 + job.n; j++) {
         if (!job.edge(j)) continue;
+#pragma unroll 1
         for (int key = max(j * kTile, lo); key < min((j + 1) * kTile, hi); key++) {
             const uint32_t blk = block_of_16(a.c, uint32_t(key) / 16);
             const int64_t id = max(read_block(a.b, a.c, job.seq.s, blk, a.d_status), int64_t(0));
             const uint8_t *v = a.c.code[1] + id * a.c.block_stride + (int64_t(job.h) * a.c.tokens + (key - blk * a.c.tokens)) * a.c.dim + col;
+#pragma unroll 1
             for (int i = 0; i < min(32, int(a.c.dim) - col); i++)
                 if ((__ldg(v + i) & 0x7F) == 0x7F) mask |= 1u << i;
         }
     }
     return mask;
+}
+
+// An item's parts together, by the 256 row threads. Apart from the loop over key tiles, whose registers are all taken.
+template <int DP> __device__ __noinline__ void join(const AttendArgs &a, const Job &job) {
+    const Part<DP> *parts = static_cast<const Part<DP> *>(a.parts);
+    const uint32_t c0 = job.c0, c1 = job.c1;
+    // the first part is in its CTA's second slot, the others in the first slots of the CTAs after it
+    auto at = [&](uint32_t c) -> const Part<DP> & { return parts[2 * c + (c == c0 ? 1 : 0)]; };
+    // With one tile of rows its 128 rows take two threads each, half of the columns a thread.
+    const int r = job.tiles == 1 ? threadIdx.x % kTile : threadIdx.x, span = job.tiles == 1 ? DP / 2 : DP;
+    const int from = job.tiles == 1 ? int(threadIdx.x) / kTile * span : 0, to = min(from + span, int(a.c.dim));
+    const uint32_t row = job.tile * kRows + r;
+    if (row >= job.seq.n * a.group) return;
+#pragma unroll 1
+    for (int i = from; i < to; i += 16) {
+        float o[16], M = kNone, W = kNone, L = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; k++) o[k] = 0.0f;
+        constexpr int kRun = 4;  // parts whose reads are in flight together
+#pragma unroll 1
+        for (uint32_t c = c0; c <= c1; c += kRun) {
+            float4 v[kRun][4];
+            float pm[kRun], pw[kRun], pl[kRun];
+#pragma unroll
+            for (int n = 0; n < kRun; n++) {
+                const bool there = c + n <= c1;
+                const Part<DP> &p = at(there ? c + n : c1);
+                pm[n] = there ? __ldcg(&p.m[r]) : kNone, pw[n] = there ? __ldcg(&p.mw[r]) : kNone, pl[n] = there ? __ldcg(&p.l[r]) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; k++) v[n][k] = there ? __ldcg(&p.o[i / 4 + k][r]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            float m1 = M, w1 = W;
+#pragma unroll
+            for (int n = 0; n < kRun; n++) m1 = fmaxf(m1, pm[n]), w1 = fmaxf(w1, pw[n]);
+            const float down = ratio2(W, w1);
+            L *= ratio2(M, m1);
+#pragma unroll
+            for (int k = 0; k < 16; k++) o[k] *= down;
+#pragma unroll
+            for (int n = 0; n < kRun; n++) {
+                L += pl[n] * ratio2(pm[n], m1);
+                const float f = ratio2(pw[n], w1);
+#pragma unroll
+                for (int k = 0; k < 4; k++) o[4 * k] += v[n][k].x * f, o[4 * k + 1] += v[n][k].y * f, o[4 * k + 2] += v[n][k].z * f, o[4 * k + 3] += v[n][k].w * f;
+            }
+            M = m1, W = w1;
+        }
+        emit(a, job.seq, job.h, row, i, o, M, W, L);
+    }
 }
 
 // The 256 row threads meet; false if that was given up.
@@ -451,7 +521,7 @@ template <int DP> __device__ __forceinline__ void fetch_queries(const AttendArgs
     if (job.end || !job.n || half >= job.tiles) return;
     const uint32_t row = job.tile * kRows + r;
     const int64_t from = row < job.seq.n * a.group ? row_at(a, a.q, job.seq, job.h, row) : kNoRow;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = 0; i < kLanes; i++) {
         const int of = i * kAtOnce + lane / kLanes;
         const int64_t at = __shfl_sync(0xFFFFFFFFu, from, of);
@@ -471,7 +541,7 @@ template <int DP> __device__ __forceinline__ float ready_query(const AttendArgs 
     float c = fabsf(a.scale_log2), up = 1.0f;
     if (a.dtype == ZC_BF16) {
         uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < DP / 8; i++) {
             const uint4 v = *reinterpret_cast<const uint4 *>(sm.q[half] + panel_at(r % kTile, i));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -483,7 +553,7 @@ template <int DP> __device__ __forceinline__ float ready_query(const AttendArgs 
         c *= down;
     }
     if (a.dtype == ZC_BF16 || sign) {
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < DP / 8; i++) {
             uint4 *at = reinterpret_cast<uint4 *>(sm.q[half] + panel_at(r % kTile, i));
             const uint4 v = *at;
@@ -681,56 +751,17 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
             tm_before();
         }
         if (!whole) {
-            const uint32_t c0 = job.c0, c1 = job.c1;
             if (!rows_meet(&sm.bars.rows, met++)) return false;
             if (r == 0) {
                 uint32_t *counter = a.counters + job.counter;
                 uint32_t done;
                 asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
-                if (done == c1 - c0) *counter = 0;
-                sm.last = done == c1 - c0;
+                const bool last = done == job.c1 - job.c0;
+                if (last) *counter = 0;
+                sm.last = last;
             }
             if (!rows_meet(&sm.bars.rows, met++)) return false;
-            // With one tile of rows its 128 rows take two threads each, half of the columns a thread.
-            const int jr = job.tiles == 1 ? r % kTile : r, span = job.tiles == 1 ? DP / 2 : DP;
-            const uint32_t row = job.tile * kRows + jr;
-            if (*reinterpret_cast<volatile int *>(&sm.last) && row < n_rows) {
-                // the first part is in its CTA's second slot, the others in the first slots of the CTAs after it
-                auto at = [&](uint32_t c) -> const Part<DP> & { return parts[2 * c + (c == c0 ? 1 : 0)]; };
-                float M = kNone, Wt = kNone, L = 0.0f;
-#pragma unroll 4
-                for (uint32_t c = c0; c <= c1; c++) M = fmaxf(M, __ldcg(&at(c).m[jr])), Wt = fmaxf(Wt, __ldcg(&at(c).mw[jr]));
-#pragma unroll 4
-                for (uint32_t c = c0; c <= c1; c++) L += __ldcg(&at(c).l[jr]) * ratio2(__ldcg(&at(c).m[jr]), M);
-                const int from = job.tiles == 1 ? half * span : 0;
-#pragma unroll 1
-                for (int i = from; i < from + span && i < int(a.c.dim); i += 32) {
-                    float o[32];
-#pragma unroll
-                    for (int k = 0; k < 32; k++) o[k] = 0.0f;
-                    for (uint32_t c = c0; c <= c1; c += 2) {  // 16 reads in flight
-                        const Part<DP> &p0 = at(c), &p1 = at(min(c + 1, c1));
-                        float4 v[2][8];
-#pragma unroll
-                        for (int k = 0; k < 8; k++) v[0][k] = __ldcg(&p0.o[i / 4 + k][jr]), v[1][k] = __ldcg(&p1.o[i / 4 + k][jr]);
-                        const float f0 = ratio2(__ldcg(&p0.mw[jr]), Wt);
-#pragma unroll
-                        for (int k = 0; k < 8; k++) o[4 * k] += v[0][k].x * f0, o[4 * k + 1] += v[0][k].y * f0, o[4 * k + 2] += v[0][k].z * f0, o[4 * k + 3] += v[0][k].w * f0;
-                        if (c < c1) {
-                            const float f1 = ratio2(__ldcg(&p1.mw[jr]), Wt);
-#pragma unroll
-                            for (int k = 0; k < 8; k++) o[4 * k] += v[1][k].x * f1, o[4 * k + 1] += v[1][k].y * f1, o[4 * k + 2] += v[1][k].z * f1, o[4 * k + 3] += v[1][k].w * f1;
-                        }
-                    }
-                    float y[16];
-#pragma unroll
-                    for (int k = 0; k < 16; k++) y[k] = o[k];
-                    emit(a, job.seq, job.h, row, i, y, M, Wt, L);
-#pragma unroll
-                    for (int k = 0; k < 16; k++) y[k] = o[16 + k];
-                    if (i + 16 < int(a.c.dim)) emit(a, job.seq, job.h, row, i + 16, y, M, Wt, L);
-                }
-            }
+            if (*reinterpret_cast<volatile int *>(&sm.last)) join<DP>(a, job);
         }
         __syncwarp();
         if (lane == 0) job_done(sm, k);
