@@ -505,6 +505,9 @@ template <int DP> __device__ __noinline__ void join(const AttendArgs &a, const J
     }
 }
 
+// The lowest n bits (none for n < 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
+
 // The 256 row threads meet; false if that was given up.
 __device__ __forceinline__ bool rows_meet(uint64_t *bar, uint32_t turn) {
     __syncwarp();
@@ -521,7 +524,7 @@ template <int DP> __device__ __forceinline__ void fetch_queries(const AttendArgs
     if (job.end || !job.n || half >= job.tiles) return;
     const uint32_t row = job.tile * kRows + r;
     const int64_t from = row < job.seq.n * a.group ? row_at(a, a.q, job.seq, job.h, row) : kNoRow;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < kLanes; i++) {
         const int of = i * kAtOnce + lane / kLanes;
         const int64_t at = __shfl_sync(0xFFFFFFFFu, from, of);
@@ -540,33 +543,32 @@ template <int DP> __device__ __forceinline__ float ready_query(const AttendArgs 
     const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
     float c = fabsf(a.scale_log2), up = 1.0f;
     if (a.dtype == ZC_BF16) {
-        uint32_t top = 0;
-#pragma unroll 2
+        __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
+#pragma unroll 4
         for (int i = 0; i < DP / 8; i++) {
             const uint4 v = *reinterpret_cast<const uint4 *>(sm.q[half] + panel_at(r % kTile, i));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; k++) top = max(top, max(w[k] << 16 & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+            for (int k = 0; k < 4; k++) most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k])));
         }
         float down;
-        row_powers(top, up, down);
+        row_powers(__float_as_uint(fmaxf(__low2float(most), __high2float(most))), up, down);
         c *= down;
     }
     if (a.dtype == ZC_BF16 || sign) {
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < DP / 8; i++) {
             uint4 *at = reinterpret_cast<uint4 *>(sm.q[half] + panel_at(r % kTile, i));
             const uint4 v = *at;
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if (a.dtype == ZC_BF16) {
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                if (a.dtype == ZC_BF16) {
+                for (int k = 0; k < 4; k++) {
                     const float2 f = unpack2<ZC_BF16>(w[k]);
                     w[k] = half2_of(f.x * up, f.y * up);
                 }
-                w[k] ^= sign;
             }
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            *at = make_uint4(w[0] ^ sign, w[1] ^ sign, w[2] ^ sign, w[3] ^ sign);
         }
     }
     fence_async();
@@ -619,8 +621,11 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                     if (edge) {
                         const int from = lo - j * kTile, to = hi - j * kTile;
 #pragma unroll
-                        for (int i = 0; i < kTile; i++)
-                            if (i < from || i >= to) x[i] = kNone;
+                        for (int q = 0; q < kTile; q += 32) {
+                            const uint32_t seen = below(to - q) & ~below(from - q);
+#pragma unroll
+                            for (int i = 0; i < 32; i++) x[q + i] = seen >> i & 1 ? x[q + i] : kNone;
+                        }
                     }
                     float top = kNone, topw = kNone;
 #pragma unroll
@@ -830,13 +835,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     bool ok = true;
     // 512 registers a lane over the four warpgroups, as at launch
     if (warp < 8) {
-        more_registers<192>();
+        more_registers<184>();
         ok = rows_role<DP>(a, sm);
     } else if (warp < 12) {
-        fewer_registers<72>();
+        fewer_registers<80>();
         ok = convert_role<DP>(sm);
     } else {
-        fewer_registers<56>();
+        fewer_registers<64>();
         if (warp == 12) ok = product_role<DP>(sm);
         if (warp == 13) ok = copy_role<DP>(a, maps, sm);
         if (warp == 14 && threadIdx.x % 32 == 0) ok = find_role<DP>(a, sm, Walk{w0, w1, sm.i0, W, G, sm.slot, sm.seq, sm.h});
