@@ -158,6 +158,10 @@ __device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, flo
 // Where an operand tile holds 16-byte chunk c of row r.
 __device__ __forceinline__ int panel_at(int r, int c) { return c / 8 * (kTile * 128) + r * 128 + 16 * (c % 8 ^ (r & 7)); }
 
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {  // x + a, y + b
+    asm("{.reg .b64 c, d; mov.b64 c, {%0, %1}; mov.b64 d, {%2, %3}; add.rn.f32x2 c, c, d; mov.b64 {%0, %1}, c;}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+
 // ---------------------------------------------------------------------------
 // The line of work
 
@@ -674,7 +678,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                                 float y0, y1;
                                 fma2(y0, y1, x[16 * b + i], x[16 * b + i + 1], by[b], bias);
                                 y0 = ex2(y0), y1 = ex2(y1);
-                                sum0 += y0, sum1 += y1;
+                                add2(sum0, sum1, y0, y1);
                                 p[8 * b + i / 2] = half2_of(y0, y1);
                             }
                             l += (sum0 + sum1) * ex2(-lf);
