@@ -1,15 +1,17 @@
 // kv_read.cu — tokens of the 8-bit cache as numbers: value(code) * scale,
 // rounded once to the type asked for.
 //
-// One CTA does kTokens packed tokens of one head, K or V: the tokens' places
-// first, then 16 codes (16 bytes) a thread.
+// One CTA does kTokens packed tokens of one head, K and V, 16 codes (16 bytes)
+// a piece. A thread asks for all of its pieces before it converts the first:
+// 8 reads in flight a thread for 128 columns.
 #include "kv_common.cuh"
 
 namespace zc {
 namespace kv {
 namespace {
 
-constexpr int kThreads = 128, kTokens = 16;
+constexpr int kThreads = 128, kTokens = 64;
+constexpr int kPieces = kTokens * (kMaxHeadDim / 16) / kThreads;  // of K and of V, at most
 
 template <int DT> __device__ __forceinline__ void store16(void *p, const float (&x)[16]) {
     if (DT == ZC_FP32) {
@@ -24,7 +26,7 @@ template <int DT> __device__ __forceinline__ void store16(void *p, const float (
     }
 }
 
-template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(MoveArgs a) {
+template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ MoveArgs a) {
     uint32_t at;
     const uint32_t s = find_seq(a.b, blockIdx.x, 1, kTokens, 1, at);
     const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, threadIdx.x == 0 && at == 0);
@@ -33,34 +35,52 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(MoveAr
         if (threadIdx.x == 0 && at == 0) report(a.d_status, ZC_EFORMAT);
         return;
     }
-    const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y, kvi = blockIdx.z;
-    const uint32_t per_row = D / 16;
-    for (uint32_t i = threadIdx.x; i < kTokens * per_row; i += kThreads) {
-        const uint32_t t = at * kTokens + i / per_row;
-        if (t >= q.n) break;
-        const uint32_t pos = uint32_t(q.len) - q.n + t, col = i % per_row * 16;
-        const int64_t id = read_block(a.b, a.c, s, pos / B, a.d_status);
-        if (id < 0) continue;
-        const uint4 c = __ldg(reinterpret_cast<const uint4 *>(a.c.code[kvi] + id * a.c.block_stride +
-                                                              (int64_t(h) * B + pos % B) * D + col));
-        const float scale = __ldg(a.c.scale[kvi] + id * a.c.scale_stride + h);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        float x[16];
+    const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y;
+    const uint32_t per_row = D / 16, t0 = at * kTokens, n = min(uint32_t(kTokens), q.n - min(q.n, t0)) * per_row;
+    const uint32_t pos0 = uint32_t(q.len) - q.n + t0;
+    uint4 c[2][kPieces];
+    float scale[2][kPieces];
+    bool there[kPieces];
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const float2 f = e4m3x2_to_float2(uint16_t(w[k / 2] >> (16 * (k & 1))));
-            x[2 * k] = f.x * scale, x[2 * k + 1] = f.y * scale;
+    for (int p = 0; p < kPieces; p++) {
+        const uint32_t i = threadIdx.x + p * kThreads, pos = pos0 + i / per_row;
+        there[p] = false;
+        if (i >= n) continue;
+        const uint32_t blk = block_of_16(a.c, pos / 16);
+        const int64_t id = read_block(a.b, a.c, s, blk, a.d_status);
+        if (id < 0) continue;
+        there[p] = true;
+        const int64_t off = id * a.c.block_stride + (int64_t(h) * B + (pos - blk * B)) * D + i % per_row * 16;
+#pragma unroll
+        for (int kv = 0; kv < 2; kv++) {
+            c[kv][p] = __ldg(reinterpret_cast<const uint4 *>(a.c.code[kv] + off));
+            scale[kv][p] = __ldg(a.c.scale[kv] + id * a.c.scale_stride + h);
         }
-        const int elt = DT == ZC_FP32 ? 4 : 2;
-        store16<DT>(static_cast<uint8_t *>(a.x[kvi].p) +
-                        ((int64_t(q.first) + int64_t(t)) * a.x[kvi].token + int64_t(h) * a.x[kvi].head + col) * elt, x);
+    }
+#pragma unroll
+    for (int p = 0; p < kPieces; p++) {
+        if (!there[p]) continue;
+        const uint32_t i = threadIdx.x + p * kThreads;
+#pragma unroll
+        for (int kv = 0; kv < 2; kv++) {
+            const uint32_t w[4] = {c[kv][p].x, c[kv][p].y, c[kv][p].z, c[kv][p].w};
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const float2 f = e4m3x2_to_float2(uint16_t(w[k / 2] >> (16 * (k & 1))));
+                x[2 * k] = f.x * scale[kv][p], x[2 * k + 1] = f.y * scale[kv][p];
+            }
+            const int elt = DT == ZC_FP32 ? 4 : 2;
+            store16<DT>(static_cast<uint8_t *>(a.x[kv].p) +
+                            (int64_t(q.first + t0 + i / per_row) * a.x[kv].token + int64_t(h) * a.x[kv].head + i % per_row * 16) * elt, x);
+        }
     }
 }
 
 } // namespace
 
 int launch_read(int dtype, const MoveArgs &a, cudaStream_t s) {
-    const dim3 grid(slot_of(a.b.total, a.b.n_seqs, 1, kTokens, 1), a.c.heads, 2);
+    const dim3 grid(slot_of(a.b.total, a.b.n_seqs, 1, kTokens, 1), a.c.heads);
     switch (dtype) {
     case ZC_BF16: read_kernel<ZC_BF16><<<grid, kThreads, 0, s>>>(a); break;
     case ZC_FP16: read_kernel<ZC_FP16><<<grid, kThreads, 0, s>>>(a); break;

@@ -10,30 +10,51 @@
 // significant bits, and moving old codes rounds again only those that leave
 // E4M3's normal range.
 //
-// One CTA does one block of one head: first the magnitudes, then the codes.
+// One CTA does one block of one head, K or V, in one pass over its new rows:
+// a thread keeps kHold pieces of 8 elements in registers while the CTA finds
+// the largest magnitude, and then quantises them (256 threads hold 128 rows of
+// 128 columns; rows beyond that are read again). The CTA is as small as that
+// allows: what bounds it is the latency of its few dependent reads, which only
+// more CTAs on an SM hide.
 #include "kv_common.cuh"
 
 namespace zc {
 namespace kv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kHold = 8;
 
-// Eight elements from 16-byte aligned memory.
-template <int DT> __device__ __forceinline__ void load8(const void *p, float (&x)[8]) {
-    if (DT == ZC_FP32) {
-        const float4 a = __ldg(static_cast<const float4 *>(p)), b = __ldg(static_cast<const float4 *>(p) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 v = __ldg(static_cast<const uint4 *>(p));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight elements from 16-byte aligned memory, as they are, and as floats.
+template <int DT> struct Eight {
+    uint4 v[DT == ZC_FP32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *p) {
+        v[0] = __ldg(static_cast<const uint4 *>(p));
+        if (DT == ZC_FP32) v[DT == ZC_FP32 ? 1 : 0] = __ldg(static_cast<const uint4 *>(p) + 1);
+    }
+    __device__ __forceinline__ float2 pair(int i) const {  // elements 2i, 2i + 1
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+        return DT == ZC_FP32 ? make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])) : unpack2<DT>(w[i]);
+    }
+    __device__ __forceinline__ uint32_t top() const {  // bits of the largest finite magnitude
+        uint32_t t = 0;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const float2 f = unpack2<DT>(w[i]);
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            const float2 f = pair(i);
+            const uint32_t a = __float_as_uint(f.x) & 0x7FFFFFFFu, b = __float_as_uint(f.y) & 0x7FFFFFFFu;
+            t = max(t, max(a < 0x7F800000u ? a : 0u, b < 0x7F800000u ? b : 0u));
         }
+        return t;
     }
-}
+    __device__ __forceinline__ uint2 codes(float inv) const {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float2 f = pair(2 * i), g = pair(2 * i + 1);
+            w[i] = float2_to_e4m3x2(f.x * inv, f.y * inv) | uint32_t(float2_to_e4m3x2(g.x * inv, g.y * inv)) << 16;
+        }
+        return make_uint2(w[0], w[1]);
+    }
+};
 
 // Exponent field of the least power of two s >= 2^-126 with a <= 448 s, for
 // the bits of a finite a >= 0: 448 = 1.75 2^8.
@@ -50,7 +71,7 @@ __device__ __forceinline__ float two_to(int field) {  // 2^(field - 127), fields
     return __uint_as_float(uint32_t(min(max(field, 1), 254)) << 23);
 }
 
-template <int DT> __global__ void __launch_bounds__(kThreads) write_kernel(MoveArgs a) {
+template <int DT, int kThreads> __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ MoveArgs a) {
     __shared__ uint32_t s_max;
     uint32_t at;
     const uint32_t s = find_seq(a.b, blockIdx.x, 1, a.c.tokens, 2, at);
@@ -66,27 +87,32 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write_kernel(MoveA
     if (uint64_t(blk) * B >= uint64_t(q.len)) return;
     const uint32_t lo = max(start, blk * B), hi = min(uint32_t(q.len), (blk + 1) * B);
     const uint32_t n0 = lo - blk * B, rows = hi - lo;
-    const int64_t id = read_block(a.b, a.c, s, blk, a.d_status);
-    if (id < 0) return;
-
     const int elt = DT == ZC_FP32 ? 4 : 2;
     const uint8_t *x = static_cast<const uint8_t *>(a.x[kvi].p) +
                        ((int64_t(q.first) + (lo - start)) * a.x[kvi].token + int64_t(h) * a.x[kvi].head) * elt;
-    uint8_t *codes = a.c.code[kvi] + id * a.c.block_stride + int64_t(h) * B * D;
-    float *scale = a.c.scale[kvi] + id * a.c.scale_stride + h;
     const uint32_t per_row = D / 8, chunks = rows * per_row;
 
+    auto piece_of = [&](uint32_t i) { return x + (int64_t(i / per_row) * a.x[kvi].token + (i % per_row) * 8) * elt; };
+    Eight<DT> held[kHold];
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < kHold; n++)
+        if (threadIdx.x + n * kThreads < chunks) held[n].load(piece_of(threadIdx.x + n * kThreads));
+    // (the block is looked up while the rows are on their way)
+    const int64_t id = read_block(a.b, a.c, s, blk, a.d_status);
+    if (id < 0) return;
+    uint8_t *codes = a.c.code[kvi] + id * a.c.block_stride + int64_t(h) * B * D;
+    float *scale = a.c.scale[kvi] + id * a.c.scale_stride + h;
+    const float old = n0 ? *scale : 0.0f;
     if (threadIdx.x == 0) s_max = 0;
     __syncthreads();
-    uint32_t top = 0;  // bits of the largest finite magnitude
-    for (uint32_t i = threadIdx.x; i < chunks; i += kThreads) {
-        float v[8];
-        load8<DT>(x + (int64_t(i / per_row) * a.x[kvi].token + (i % per_row) * 8) * elt, v);
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const uint32_t u = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-            if (u < 0x7F800000u) top = max(top, u);
-        }
+    for (int n = 0; n < kHold; n++)
+        if (threadIdx.x + n * kThreads < chunks) top = max(top, held[n].top());
+    for (uint32_t i = threadIdx.x + kHold * kThreads; i < chunks; i += kThreads) {
+        Eight<DT> e;
+        e.load(piece_of(i));
+        top = max(top, e.top());
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if ((threadIdx.x & 31) == 0) atomicMax(&s_max, top);
@@ -94,7 +120,6 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write_kernel(MoveA
 
     uint32_t field = need_exponent(s_max);
     if (n0) {
-        const float old = *scale;
         field = max(field, ceil_exponent(old));
         const float now = two_to(int(field));
         if (now != old) {
@@ -112,29 +137,36 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write_kernel(MoveA
                 *p = make_uint2(w[0] | uint32_t(w[1]) << 16, w[2] | uint32_t(w[3]) << 16);
             }
         }
-        __syncthreads();  // everyone has read the old scale
     }
     const float inv = 1.0f / two_to(int(field));
     if (threadIdx.x == 0) *scale = two_to(int(field));
-    for (uint32_t i = threadIdx.x; i < chunks; i += kThreads) {
-        float v[8];
-        load8<DT>(x + (int64_t(i / per_row) * a.x[kvi].token + (i % per_row) * 8) * elt, v);
-        uint16_t w[4];
+    uint2 *to = reinterpret_cast<uint2 *>(codes + int64_t(n0) * D);
 #pragma unroll
-        for (int k = 0; k < 4; k++) w[k] = float2_to_e4m3x2(v[2 * k] * inv, v[2 * k + 1] * inv);
-        reinterpret_cast<uint2 *>(codes + int64_t(n0) * D)[i] =
-            make_uint2(w[0] | uint32_t(w[1]) << 16, w[2] | uint32_t(w[3]) << 16);
+    for (int n = 0; n < kHold; n++)
+        if (threadIdx.x + n * kThreads < chunks) to[threadIdx.x + n * kThreads] = held[n].codes(inv);
+    for (uint32_t i = threadIdx.x + kHold * kThreads; i < chunks; i += kThreads) {
+        Eight<DT> e;
+        e.load(piece_of(i));
+        to[i] = e.codes(inv);
     }
+}
+
+// Threads by the pieces of a block that a call may write.
+template <int DT> void launch(const MoveArgs &a, cudaStream_t s) {
+    const dim3 grid(slot_of(a.b.total, a.b.n_seqs, 1, a.c.tokens, 2), a.c.heads, 2);
+    const uint32_t rows = a.b.most < a.c.tokens ? a.b.most : a.c.tokens, pieces = rows * (a.c.dim / 8);
+    if (pieces <= 64 * kHold) write_kernel<DT, 64><<<grid, 64, 0, s>>>(a);
+    else if (pieces <= 128 * kHold) write_kernel<DT, 128><<<grid, 128, 0, s>>>(a);
+    else write_kernel<DT, 256><<<grid, 256, 0, s>>>(a);
 }
 
 } // namespace
 
 int launch_write(int dtype, const MoveArgs &a, cudaStream_t s) {
-    const dim3 grid(slot_of(a.b.total, a.b.n_seqs, 1, a.c.tokens, 2), a.c.heads, 2);
     switch (dtype) {
-    case ZC_BF16: write_kernel<ZC_BF16><<<grid, kThreads, 0, s>>>(a); break;
-    case ZC_FP16: write_kernel<ZC_FP16><<<grid, kThreads, 0, s>>>(a); break;
-    default: write_kernel<ZC_FP32><<<grid, kThreads, 0, s>>>(a); break;
+    case ZC_BF16: launch<ZC_BF16>(a, s); break;
+    case ZC_FP16: launch<ZC_FP16>(a, s); break;
+    default: launch<ZC_FP32>(a, s); break;
     }
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }
