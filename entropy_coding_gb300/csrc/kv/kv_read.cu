@@ -21,8 +21,8 @@ template <int DT> __device__ __forceinline__ void store16(void *p, const float (
     } else {
 #pragma unroll
         for (int i = 0; i < 2; i++)
-            static_cast<uint4 *>(p)[i] = make_uint4(pack2<DT>(x[8 * i], x[8 * i + 1]), pack2<DT>(x[8 * i + 2], x[8 * i + 3]),
-                                                    pack2<DT>(x[8 * i + 4], x[8 * i + 5]), pack2<DT>(x[8 * i + 6], x[8 * i + 7]));
+            __stcs(static_cast<uint4 *>(p) + i, make_uint4(pack2<DT>(x[8 * i], x[8 * i + 1]), pack2<DT>(x[8 * i + 2], x[8 * i + 3]),
+                                                    pack2<DT>(x[8 * i + 4], x[8 * i + 5]), pack2<DT>(x[8 * i + 6], x[8 * i + 7])));
     }
 }
 
@@ -38,29 +38,31 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(const 
     const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y;
     const uint32_t per_row = D / 16, t0 = at * kTokens, n = min(uint32_t(kTokens), q.n - min(q.n, t0)) * per_row;
     const uint32_t pos0 = uint32_t(q.len) - q.n + t0;
+    const uint32_t inverse = 0xFFFFFFFFu / per_row + 1;  // i / per_row = i * inverse / 2^32 (1 piece a row: 0)
+    auto row_of = [&](uint32_t i) { return inverse ? __umulhi(i, inverse) : i; };
     uint4 c[2][kPieces];
     float scale[2][kPieces];
     bool there[kPieces];
 #pragma unroll
     for (int p = 0; p < kPieces; p++) {
-        const uint32_t i = threadIdx.x + p * kThreads, pos = pos0 + i / per_row;
+        const uint32_t i = threadIdx.x + p * kThreads, row = row_of(i), pos = pos0 + row;
         there[p] = false;
         if (i >= n) continue;
         const uint32_t blk = block_of_16(a.c, pos / 16);
         const int64_t id = read_block(a.b, a.c, s, blk, a.d_status);
         if (id < 0) continue;
         there[p] = true;
-        const int64_t off = id * a.c.block_stride + (int64_t(h) * B + (pos - blk * B)) * D + i % per_row * 16;
+        const int64_t off = id * a.c.block_stride + (int64_t(h) * B + (pos - blk * B)) * D + (i - row * per_row) * 16;
 #pragma unroll
         for (int kv = 0; kv < 2; kv++) {
-            c[kv][p] = __ldg(reinterpret_cast<const uint4 *>(a.c.code[kv] + off));
+            c[kv][p] = __ldcs(reinterpret_cast<const uint4 *>(a.c.code[kv] + off));
             scale[kv][p] = __ldg(a.c.scale[kv] + id * a.c.scale_stride + h);
         }
     }
 #pragma unroll
     for (int p = 0; p < kPieces; p++) {
         if (!there[p]) continue;
-        const uint32_t i = threadIdx.x + p * kThreads;
+        const uint32_t i = threadIdx.x + p * kThreads, row = row_of(i);
 #pragma unroll
         for (int kv = 0; kv < 2; kv++) {
             const uint32_t w[4] = {c[kv][p].x, c[kv][p].y, c[kv][p].z, c[kv][p].w};
@@ -72,7 +74,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(const 
             }
             const int elt = DT == ZC_FP32 ? 4 : 2;
             store16<DT>(static_cast<uint8_t *>(a.x[kv].p) +
-                            (int64_t(q.first + t0 + i / per_row) * a.x[kv].token + int64_t(h) * a.x[kv].head + i % per_row * 16) * elt, x);
+                            (int64_t(q.first + t0 + row) * a.x[kv].token + int64_t(h) * a.x[kv].head + (i - row * per_row) * 16) * elt, x);
         }
     }
 }

@@ -28,14 +28,22 @@ constexpr int kHold = 8;
 template <int DT> struct Eight {
     uint4 v[DT == ZC_FP32 ? 2 : 1];
     __device__ __forceinline__ void load(const void *p) {
-        v[0] = __ldg(static_cast<const uint4 *>(p));
-        if (DT == ZC_FP32) v[DT == ZC_FP32 ? 1 : 0] = __ldg(static_cast<const uint4 *>(p) + 1);
+        v[0] = __ldcs(static_cast<const uint4 *>(p));
+        if (DT == ZC_FP32) v[DT == ZC_FP32 ? 1 : 0] = __ldcs(static_cast<const uint4 *>(p) + 1);
     }
     __device__ __forceinline__ float2 pair(int i) const {  // elements 2i, 2i + 1
         const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
         return DT == ZC_FP32 ? make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])) : unpack2<DT>(w[i]);
     }
-    __device__ __forceinline__ uint32_t top() const {  // bits of the largest finite magnitude
+    __device__ __forceinline__ uint32_t top() const {  // bits of the largest finite magnitude, as a float
+        constexpr uint32_t kInf = DT == ZC_BF16 ? 0x7F80u : 0x7C00u;
+        if (DT != ZC_FP32) {
+            // two elements at a time, and one by one only where that finds an infinity or NaN
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+            const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+            const uint32_t t = max(m >> 16, m & 0xFFFFu);
+            if (t < kInf) return __float_as_uint(DT == ZC_BF16 ? __uint_as_float(t << 16) : unpack2<DT>(t).x);
+        }
         uint32_t t = 0;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -92,7 +100,12 @@ template <int DT, int kThreads> __global__ void __launch_bounds__(kThreads) writ
                        ((int64_t(q.first) + (lo - start)) * a.x[kvi].token + int64_t(h) * a.x[kvi].head) * elt;
     const uint32_t per_row = D / 8, chunks = rows * per_row;
 
-    auto piece_of = [&](uint32_t i) { return x + (int64_t(i / per_row) * a.x[kvi].token + (i % per_row) * 8) * elt; };
+    const uint32_t inverse = 0xFFFFFFFFu / per_row + 1;  // i / per_row = i * inverse / 2^32 for the few thousand pieces of a block
+    const int64_t stride = a.x[kvi].token * elt;
+    auto piece_of = [&](uint32_t i) {
+        const uint32_t row = __umulhi(i, inverse);
+        return x + row * stride + (i - row * per_row) * (8 * elt);
+    };
     Eight<DT> held[kHold];
     uint32_t top = 0;
 #pragma unroll
