@@ -605,6 +605,9 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
             {
                 for (int j = job.j0; j < job.j0 + job.n; j++, tile++, scored++) {
                     const int slot = tile % kSlots;
+                    // A half that had no rows in the pieces before may be ahead of the copies by more than the ring of scales,
+                    // where a wait for a phase tells nothing: its first scores come after their scales.
+                    if (j == job.j0 && !__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.s_full[half], scored & 1))) return false;
                     if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.scale_full[slot], tile / kSlots & 1))) return false;
                     float by[kBoxes], lvs[kBoxes];  // read early: the products keep shared memory busy
 #pragma unroll

@@ -250,6 +250,15 @@ def test_attend_matches_its_definition(dtype, block, hkv, group, dim, lens, news
     _attend_case(dtype, block, hkv, group, dim, lens, news, causal, window, strides=strides)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_items_of_one_row_tile_among_items_of_two(dim):
+    """More items than the GPU has multiprocessors, over many key tiles whose block scales differ: the row threads of the
+    second tile have nothing to do in some items and must not take the scales of others."""
+    lens = [1700, 1300, 2100, 1500, 1900, 1200]
+    news = [30, 150, 20, 140, 25, 160]
+    _attend_case("fp16", 32, 40, 1, dim, lens, news, True, 0, spread=6)
+
+
 SHAPES = [([700], [1], 0), ([333, 40], [3, 2], 50), ([300], [260], 0), ([600], [300], 100)]  # lens, new, window
 
 
