@@ -491,65 +491,74 @@ __device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const 
 
 // An item's parts together: the `first` one in its CTA's second slot (a piece
 // that begins an item), the others in the first slots of the CTAs after it.
-// A thread takes 4 columns of a row and every kWays-th part, in runs whose
-// loads are in flight together; the ways meet in shared memory.
+// A thread takes 4 columns of a row and every ways-th part, kRun parts in
+// flight together; the ways meet in shared memory.
 template <int DP, int NT>
-__device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Seq &seq, uint32_t tile, uint32_t h,
-                                     const Part<DP, NT> *parts, uint32_t first, uint32_t n) {
-    constexpr int kRows = 8 * NT, kCols = DP / 4, kRun = 16;
+__device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Job &item, uint32_t first, uint32_t n) {
+    constexpr int kCols = DP / 4, kRun = 8;
     struct Way {
         float4 x;
         float m, mw, l;
     };
     Way *met = reinterpret_cast<Way *>(smem);
-    const uint32_t row0 = tile * kRows, n_rows = seq.n * a.group;
-    const int rows = int(min(uint32_t(kRows), n_rows - row0)), D = int(a.c.dim);
+    const Part<DP, NT> *parts = static_cast<const Part<DP, NT> *>(a.parts);
+    const uint32_t row0 = item.tile * 8 * NT;
+    const int rows = int(min(uint32_t(8 * NT), item.seq.n * a.group - row0)), D = int(a.c.dim);
     const int jobs = rows * kCols;                             // 4 columns of a row each
     const int ways = jobs >= kThreads ? 1 : kThreads / jobs;   // threads of a job
-    auto part = [&](uint32_t i) -> const Part<DP, NT> & { return parts[2 * (first + i) + (i ? 0 : 1)]; };
-    auto add = [&](Way &w, float4 x, float m, float mw, float l) {
-        const float M = fmaxf(w.m, m), W = fmaxf(w.mw, mw);
-        const float f = ratio2(w.mw, W), g = ratio2(mw, W);
-        w.l = w.l * ratio2(w.m, M) + l * ratio2(m, M);
-        w.x = make_float4(w.x.x * f + x.x * g, w.x.y * f + x.y * g, w.x.z * f + x.z * g, w.x.w * f + x.w * g);
-        w.m = M, w.mw = W;
-    };
+#pragma unroll 1
     for (int j0 = 0; j0 < jobs; j0 += kThreads) {
         const int job = ways == 1 ? j0 + int(threadIdx.x) : int(threadIdx.x) % jobs, way = ways == 1 ? 0 : int(threadIdx.x) / jobs;
-        const bool mine = job < jobs && way < ways;
         const int r = job / kCols, col = job % kCols * 4;
+        const bool mine = job < jobs && way < ways && col < D;
         Way w = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), kNone, kNone, 0.0f};
-        if (mine && col < D) {
-            uint32_t i = way;
-            for (; i + (kRun - 1) * ways < n; i += kRun * ways) {
+        // brings w to the units (m, mw)
+        auto to_units = [&](float m, float mw) {
+            const float f = ratio2(w.mw, mw);
+            w.l *= ratio2(w.m, m);
+            w.x.x *= f, w.x.y *= f, w.x.z *= f, w.x.w *= f;
+            w.m = m, w.mw = mw;
+        };
+        auto add = [&](float4 x, float m, float mw, float l) {
+            const float f = ratio2(mw, w.mw);
+            w.l += l * ratio2(m, w.m);
+            w.x.x += x.x * f, w.x.y += x.y * f, w.x.z += x.z * f, w.x.w += x.w * f;
+        };
+        if (mine) {
+#pragma unroll 1
+            for (uint32_t i = way; i < n; i += kRun * ways) {
                 float4 x[kRun];
                 float m[kRun], mw[kRun], l[kRun];
 #pragma unroll
                 for (int k = 0; k < kRun; k++) {
-                    const Part<DP, NT> &p = part(i + k * ways);
-                    x[k] = __ldcg(reinterpret_cast<const float4 *>(&p.o[r][col]));
-                    m[k] = __ldcg(&p.m[r]), mw[k] = __ldcg(&p.mw[r]), l[k] = __ldcg(&p.l[r]);
+                    const uint32_t of = i + k * ways;
+                    const bool there = of < n;
+                    const Part<DP, NT> &p = parts[2 * (first + (there ? of : 0)) + (there && of ? 0 : 1)];
+                    x[k] = there ? __ldcg(reinterpret_cast<const float4 *>(&p.o[r][col])) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    m[k] = there ? __ldcg(&p.m[r]) : kNone, mw[k] = there ? __ldcg(&p.mw[r]) : kNone, l[k] = there ? __ldcg(&p.l[r]) : 0.0f;
                 }
+                float m1 = w.m, w1 = w.mw;
 #pragma unroll
-                for (int k = 0; k < kRun; k++) add(w, x[k], m[k], mw[k], l[k]);
-            }
-            for (; i < n; i += ways) {
-                const Part<DP, NT> &p = part(i);
-                add(w, __ldcg(reinterpret_cast<const float4 *>(&p.o[r][col])), __ldcg(&p.m[r]), __ldcg(&p.mw[r]), __ldcg(&p.l[r]));
+                for (int k = 0; k < kRun; k++) m1 = fmaxf(m1, m[k]), w1 = fmaxf(w1, mw[k]);
+                to_units(m1, w1);
+#pragma unroll
+                for (int k = 0; k < kRun; k++) add(x[k], m[k], mw[k], l[k]);
             }
         }
         if (ways > 1) {
             met[threadIdx.x] = w;
             __syncthreads();
             if (way == 0)
+#pragma unroll 1
                 for (int k = 1; k < ways; k++) {
-                    const Way &v = met[threadIdx.x + k * jobs];
-                    add(w, v.x, v.m, v.mw, v.l);
+                    const Way v = met[threadIdx.x + k * jobs];
+                    to_units(fmaxf(w.m, v.m), fmaxf(w.mw, v.mw));
+                    add(v.x, v.m, v.mw, v.l);
                 }
         }
-        if (mine && way == 0 && col < D) {
+        if (mine && way == 0) {
             const float y[4] = {w.x.x, w.x.y, w.x.z, w.x.w};
-            emit(a, seq, h, row0 + r, col, y, w.m, w.mw, w.l);
+            emit(a, item.seq, item.h, row0 + r, col, y, w.m, w.mw, w.l);
         }
     }
 }
@@ -633,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rows_kernel(const __grid_
                 s_last = done == c1 - c0;
             }
             __syncthreads();
-            if (s_last) join<DP, NT>(a, reinterpret_cast<uint8_t *>(&mg), job.seq, job.tile, job.h, parts, c0, c1 - c0 + 1);
+            if (s_last) join<DP, NT>(a, reinterpret_cast<uint8_t *>(&mg), job, c0, c1 - c0 + 1);
         }
         job = next;
     }
