@@ -53,6 +53,8 @@ namespace {
 
 using namespace zc::kv;
 
+std::atomic<uint32_t> g_hooks{0};
+
 uint64_t pad256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -136,6 +138,8 @@ int move(bool write, const zc_kv_cache *cache, const zc_kv_batch *batch, int dty
 
 } // namespace
 
+extern "C" void zc_kv_set_test_hooks(uint32_t hooks) { g_hooks.store(hooks & ZC_HOOK_KV_COPY_STALL, std::memory_order_relaxed); }
+
 extern "C" int zc_kv_write(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, const zc_kv_rows *k,
                            const zc_kv_rows *v, int32_t *d_status, void *stream) {
     return move(true, cache, batch, dtype, k, v, d_status, stream);
@@ -202,6 +206,8 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
     a.causal = flags & ZC_KV_CAUSAL;
     a.window = window;
     a.d_status = d_status;
+    a.stall = g_hooks.load(std::memory_order_relaxed) & ZC_HOOK_KV_COPY_STALL;
+    a.limit = a.stall ? kWaitClocksTest : kWaitClocks;
     cudaStream_t str = static_cast<cudaStream_t>(stream);
     if (plan.tiles) {
         a.counters = reinterpret_cast<uint32_t *>(ws + plan.rows_counters);

@@ -22,6 +22,9 @@ namespace kv {
 constexpr uint32_t kMaxHeadDim = 128, kMaxBlockTokens = 256;
 constexpr float kCodeMax = 448.0f;  // the largest E4M3 value
 
+// Clocks after which a wait is given up: about a second, or a short time under the test hook that makes it run out.
+constexpr long long kWaitClocks = 1ll << 31, kWaitClocksTest = 1ll << 20;
+
 // The cache and the batch as the kernels take them.
 struct Cache {
     uint8_t *code[2];    // K, V
@@ -65,6 +68,8 @@ struct AttendArgs {
     uint32_t rows_most;    // a sequence of no more rows of a head goes to kv_rows.cu
     uint32_t *counters;    // workspace: an item's parts that are done, zero between calls
     void *parts;           // workspace: partial results
+    long long limit;       // clocks of a wait
+    uint32_t stall;        // test hook: the copies are never asked for
     int32_t *d_status;
 };
 
@@ -168,7 +173,6 @@ __device__ __forceinline__ int64_t read_block(const Batch &b, const Cache &c, ui
 // ---------------------------------------------------------------------------
 // Copies by the tensor memory accelerator, and the barriers that they complete.
 
-constexpr long long kWaitClocks = 1ll << 31;  // about a second; a wait that takes longer is given up
 
 __device__ __forceinline__ uint32_t smem_of(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
@@ -189,12 +193,12 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
                  : "=r"(ok) : "r"(smem_of(bar)), "r"(parity) : "memory");
     return ok;
 }
-// Waits for the phase of that parity; false after kWaitClocks.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
+// Waits for the phase of that parity; false after `limit` clocks.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, long long limit) {
     if (bar_try(bar, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try(bar, parity))
-        if (clock64() - t0 > kWaitClocks) return false;
+        if (clock64() - t0 > limit) return false;
     return true;
 }
 __device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int row, int block, uint64_t *bar) {

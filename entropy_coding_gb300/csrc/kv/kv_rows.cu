@@ -174,7 +174,7 @@ template <class Warp> __device__ __forceinline__ void look_up(const AttendArgs &
 // Asks for step k's keys and values (one lane). Rows that nobody sees come along as they are.
 template <int DP, class Warp>
 __device__ __forceinline__ void fetch(const AttendArgs &a, const CodeMaps &maps, Warp &wp, Stage<DP> *ring, const Job &job, int k, uint32_t st) {
-    if ((threadIdx.x & 31) == 0 && k < job.steps) {
+    if ((threadIdx.x & 31) == 0 && k < job.steps && !a.stall) {
         const uint32_t i = uint32_t(job.first + k * kWarps);
         const int row = int(job.h * a.c.tokens + i * kSlice - block_of_16(a.c, i) * a.c.tokens), id = wp.block[k & (2 * kAhead - 1)];
         bar_expect(&wp.full[st], sizeof(Stage<DP>));
@@ -194,8 +194,8 @@ __device__ __forceinline__ void begin(const AttendArgs &a, const CodeMaps &maps,
 }
 
 // After a wait was given up: waits (as long again) for the warp's slices [turn, turn + n) that are on their way.
-template <int S> __device__ __forceinline__ void drain(Warp<S> &wp, uint32_t turn, int n) {
-    for (int k = 0; k < min(S - 1, n); k++) bar_wait(&wp.full[(turn + k) % S], (turn + k) / S & 1);
+template <int S> __device__ __forceinline__ void drain(const AttendArgs &a, Warp<S> &wp, uint32_t turn, int n) {
+    for (int k = 0; k < min(S - 1, n); k++) bar_wait(&wp.full[(turn + k) % S], (turn + k) / S & 1, a.limit);
 }
 
 // All of the rows' work, as far as this warp's slices go.
@@ -280,8 +280,8 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
             __syncwarp();
             look_up(a, wp, job, k + kAhead);
         }
-        if (!__all_sync(0xFFFFFFFFu, bar_wait(&wp.full[st], parity))) {
-            drain(wp, turn + k, job.steps - k);
+        if (!__all_sync(0xFFFFFFFFu, bar_wait(&wp.full[st], parity, a.limit))) {
+            drain(a, wp, turn + k, job.steps - k);
             if (lane == 0) report(a.d_status, ZC_ETIMEOUT);
             return false;
         }
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rows_kernel(const __grid_
         more = next_job<NT>(a, w, w1, s, at, next);
         if (more && ok) begin<DP>(a, maps, wp, ring, next, turn);
         if (__syncthreads_or(!ok)) {
-            if (more && ok) drain(wp, turn, next.steps);
+            if (more && ok) drain(a, wp, turn, next.steps);
             return;
         }
         const bool whole = job.whole();

@@ -238,15 +238,15 @@ template <int DP> __device__ __forceinline__ bool find_role(const AttendArgs &a,
     for (uint32_t k = 0;; k++) {
         Job job;
         const bool more = walk.next(a, job);
-        if (!bar_wait(&sm.bars.job_empty[k % kJobs], (k / kJobs & 1) ^ 1)) return false;
+        if (!bar_wait(&sm.bars.job_empty[k % kJobs], (k / kJobs & 1) ^ 1, a.limit)) return false;
         job.end = !more;
         sm.jobs[k % kJobs] = job;
         bar_arrive(&sm.bars.job_full[k % kJobs]);
         if (!more) return true;
     }
 }
-template <int DP> __device__ __forceinline__ bool job_ready(Smem<DP> &sm, uint32_t k) {
-    return bar_wait(&sm.bars.job_full[k % kJobs], k / kJobs & 1);
+template <int DP> __device__ __forceinline__ bool job_ready(Smem<DP> &sm, uint32_t k, long long limit) {
+    return bar_wait(&sm.bars.job_full[k % kJobs], k / kJobs & 1, limit);
 }
 // A reader is done with piece k (a warp, or the products' thread).
 template <int DP> __device__ __forceinline__ void job_done(Smem<DP> &sm, uint32_t k) { bar_arrive(&sm.bars.job_empty[k % kJobs]); }
@@ -257,7 +257,7 @@ __device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &m
     uint32_t item = 0, tile = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; k++) {
-        if (!(ok = __all_sync(0xFFFFFFFFu, job_ready(sm, k)))) break;
+        if (!(ok = __all_sync(0xFFFFFFFFu, job_ready(sm, k, a.limit)))) break;
         const Job &job = sm.jobs[k % kJobs];
         if (job.end) break;
         const int least = job.all_lo / 16, last = (job.all_hi - 1) / 16;  // boxes without a key that is seen hold others again
@@ -276,8 +276,9 @@ __device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &m
             if (lane == 0) bar_arrive(&sm.bars.scale_full[slot]);
 #pragma unroll
             for (int kv = 0; kv < 2 && ok; kv++, item++) {
+                if (a.stall) return true;
                 const int r = item % kRaw;
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.raw_empty[r], (item / kRaw & 1) ^ 1));
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.raw_empty[r], (item / kRaw & 1) ^ 1, a.limit));
                 if (!ok) break;
                 if (lane == 0) bar_expect(&sm.bars.raw_full[r], kTile * DP);
                 __syncwarp();
@@ -288,23 +289,23 @@ __device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &m
         if (lane == 0) job_done(sm, k);
     }
     // The CTA outlives its copies, also those of a call that is given up.
-    for (uint32_t k = item > kRaw ? item - kRaw : 0; k < item; k++) ok &= bar_wait(&sm.bars.raw_full[k % kRaw], k / kRaw & 1);
+    for (uint32_t k = item > kRaw ? item - kRaw : 0; k < item; k++) ok &= bar_wait(&sm.bars.raw_full[k % kRaw], k / kRaw & 1, a.limit);
     return ok;
 }
 
-template <int DP> __device__ __forceinline__ bool convert_role(Smem<DP> &sm) {
+template <int DP> __device__ __forceinline__ bool convert_role(Smem<DP> &sm, long long limit) {
     const int t = threadIdx.x - 256, lane = t & 31;
     uint32_t item = 0;
     for (uint32_t k = 0;; k++) {
-        if (!__all_sync(0xFFFFFFFFu, job_ready(sm, k))) return false;
+        if (!__all_sync(0xFFFFFFFFu, job_ready(sm, k, limit))) return false;
         const Job &job = sm.jobs[k % kJobs];
         if (job.end) return true;
         for (int j = job.j0; j < job.j0 + job.n; j++)
 #pragma unroll 1
             for (int kv = 0; kv < 2; kv++, item++) {
                 const int r = item % kRaw, c = item % kOps;
-                if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.raw_full[r], item / kRaw & 1) &&
-                                                 bar_wait(&sm.bars.op_empty[c], (item / kOps & 1) ^ 1)))
+                if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.raw_full[r], item / kRaw & 1, limit) &&
+                                                 bar_wait(&sm.bars.op_empty[c], (item / kOps & 1) ^ 1, limit)))
                     return false;
                 // A row that does not see a key has weight 0 for it, but 0 * NaN is NaN: where some row does not see all
                 // keys, NaN codes of values are taken out, and rows that see them get them at the end.
@@ -354,7 +355,7 @@ template <int DP> __device__ __forceinline__ bool convert_role(Smem<DP> &sm) {
 }
 
 // A warp whose elected thread issues; the others keep its addresses uniform, as the products want them.
-template <int DP> __device__ __forceinline__ bool product_role(Smem<DP> &sm) {
+template <int DP> __device__ __forceinline__ bool product_role(Smem<DP> &sm, long long limit) {
     constexpr uint32_t kPanel = kTile * 128;
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, sm.tmem, 0);
     const bool one = elected();
@@ -388,10 +389,10 @@ template <int DP> __device__ __forceinline__ bool product_role(Smem<DP> &sm) {
         if (one) mma_commit(bar);
         __syncwarp();
     };
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return bool(__all_sync(0xFFFFFFFFu, bar_wait(bar, parity))); };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return bool(__all_sync(0xFFFFFFFFu, bar_wait(bar, parity, limit))); };
     bool ok = true;
     for (uint32_t k = 0; ok; k++) {
-        if (!(ok = __all_sync(0xFFFFFFFFu, job_ready(sm, k)))) break;
+        if (!(ok = __all_sync(0xFFFFFFFFu, job_ready(sm, k, limit)))) break;
         const Job &job = sm.jobs[k % kJobs];
         const int n = __shfl_sync(0xFFFFFFFFu, job.n, 0), tiles = __shfl_sync(0xFFFFFFFFu, job.tiles, 0);
         if (__shfl_sync(0xFFFFFFFFu, job.end, 0)) break;
@@ -513,10 +514,10 @@ template <int DP> __device__ __noinline__ void join(const AttendArgs &a, const J
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; }
 
 // The 256 row threads meet; false if that was given up.
-__device__ __forceinline__ bool rows_meet(uint64_t *bar, uint32_t turn) {
+__device__ __forceinline__ bool rows_meet(uint64_t *bar, uint32_t turn, long long limit) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) bar_arrive(bar);
-    return __all_sync(0xFFFFFFFFu, bar_wait(bar, turn & 1));
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, turn & 1, limit));
 }
 
 constexpr int kNoRow = -1;
@@ -589,7 +590,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
     const uint32_t lanes = uint32_t(r / 32 % 4 * 32) << 16;      // of tensor memory
     const uint32_t tmS = sm.tmem + half * 128 + lanes, tmO = sm.tmem + 256 + half * 128 + lanes;
     uint32_t tile = 0, scored = 0, summed = 0, met = 0;
-    if (!__all_sync(0xFFFFFFFFu, job_ready(sm, 0))) return false;
+    if (!__all_sync(0xFFFFFFFFu, job_ready(sm, 0, a.limit))) return false;
     fetch_queries(a, sm, sm.jobs[0]);
     for (uint32_t k = 0;; k++) {
         const Job &job = sm.jobs[k % kJobs], &next = sm.jobs[(k + 1) % kJobs];
@@ -607,8 +608,8 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                     const int slot = tile % kSlots;
                     // A half that had no rows in the pieces before may be ahead of the copies by more than the ring of scales,
                     // where a wait for a phase tells nothing: its first scores come after their scales.
-                    if (j == job.j0 && !__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.s_full[half], scored & 1))) return false;
-                    if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.scale_full[slot], tile / kSlots & 1))) return false;
+                    if (j == job.j0 && !__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.s_full[half], scored & 1, a.limit))) return false;
+                    if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.scale_full[slot], tile / kSlots & 1, a.limit))) return false;
                     float by[kBoxes], lvs[kBoxes];  // read early: the products keep shared memory busy
 #pragma unroll
                     for (int b = 0; b < kBoxes; b += 4) {
@@ -619,7 +620,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                     const bool edge = job.edge(j);
 #pragma unroll
                     for (int b = 0; b < kBoxes; b++) by[b] = fmaxf(c * by[b], 1e-37f);  // (0 * -infinity would be NaN)
-                    if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.s_full[half], scored & 1))) return false;
+                    if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.s_full[half], scored & 1, a.limit))) return false;
                     tm_after();
                     float x[kTile];
 #pragma unroll
@@ -693,13 +694,13 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                         if (lane == 0) bar_arrive(&sm.bars.p_full[half][part]);
                     }
                 }
-                if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.o_full[half], summed++ & 1))) return false;
+                if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.o_full[half], summed++ & 1, a.limit))) return false;
                 tm_after();
             }
         }
 
         // The next piece's queries are on their way while this one is finished.
-        if (!__all_sync(0xFFFFFFFFu, job_ready(sm, k + 1))) return false;
+        if (!__all_sync(0xFFFFFFFFu, job_ready(sm, k + 1, a.limit))) return false;
         fetch_queries(a, sm, next);
 
         // The rows' ends: finished, or a part.
@@ -763,7 +764,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
             tm_before();
         }
         if (!whole) {
-            if (!rows_meet(&sm.bars.rows, met++)) return false;
+            if (!rows_meet(&sm.bars.rows, met++, a.limit)) return false;
             if (r == 0) {
                 uint32_t *counter = a.counters + job.counter;
                 uint32_t done;
@@ -772,7 +773,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                 if (last) *counter = 0;
                 sm.last = last;
             }
-            if (!rows_meet(&sm.bars.rows, met++)) return false;
+            if (!rows_meet(&sm.bars.rows, met++, a.limit)) return false;
             if (*reinterpret_cast<volatile int *>(&sm.last)) join<DP>(a, job);
         }
         __syncwarp();
@@ -846,10 +847,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         ok = rows_role<DP>(a, sm);
     } else if (warp < 12) {
         fewer_registers<80>();
-        ok = convert_role<DP>(sm);
+        ok = convert_role<DP>(sm, a.limit);
     } else {
         fewer_registers<64>();
-        if (warp == 12) ok = product_role<DP>(sm);
+        if (warp == 12) ok = product_role<DP>(sm, a.limit);
         if (warp == 13) ok = copy_role<DP>(a, maps, sm);
         if (warp == 14 && threadIdx.x % 32 == 0) ok = find_role<DP>(a, sm, Walk{w0, w1, sm.i0, W, G, sm.slot, sm.seq, sm.h});
     }

@@ -19,6 +19,7 @@ __all__ = ["KVCache", "KVBatch", "kv_write", "kv_read", "kv_read_into", "kv_atte
 _BF16, _FP16, _FP32 = 4, 5, 6
 _CODE = {torch.bfloat16: _BF16, torch.float16: _FP16, torch.float32: _FP32}
 _CAUSAL = 1
+HOOK_COPY_STALL = 1  # test hook (zc_kv_set_test_hooks)
 
 
 class _Cache(ctypes.Structure):
@@ -55,6 +56,8 @@ def declare(L: ctypes.CDLL) -> None:
         f.argtypes = [vp, vp, i32, vp, vp, vp, vp]
     L.zc_kv_attend.restype = i32
     L.zc_kv_attend.argtypes = [vp, vp, i32, u32, vp, vp, vp, ctypes.c_double, u32, u32, vp, u64, vp, vp]
+    L.zc_kv_set_test_hooks.restype = None
+    L.zc_kv_set_test_hooks.argtypes = [u32]
     L.zc_kv_attend_workspace_size.restype = u64
     L.zc_kv_attend_workspace_size.argtypes = [vp, vp, u32]
 

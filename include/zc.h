@@ -449,13 +449,22 @@ ZC_API int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, int dt
  *   d_lse   NULL or float [total_tokens][heads]
  *   d_ws    workspace of ws_bytes >= zc_kv_attend_workspace_size(...), zeroed
  *           before its first use; every call leaves it ready for the next with
- *           a batch of these sizes. Calls that may overlap need their own.
+ *           a batch of these sizes (zero it again after a call that reported an
+ *           error). Calls that may overlap need their own.
+ * Every wait inside the kernels gives up after about a second and reports
+ * ZC_ETIMEOUT; the outputs are unspecified then.
  * Scores, weights' sums and outputs are accumulated in float32; weights are
  * rounded to half, in units of the row's largest contribution. */
 #define ZC_KV_CAUSAL 1u
 ZC_API int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
                         const zc_kv_rows *q, const zc_kv_rows *out, float *d_lse, double scale, uint32_t flags,
                         uint32_t window, void *d_ws, uint64_t ws_bytes, int32_t *d_status, void *stream);
+
+/* Test hook, like zc_set_test_hooks: with ZC_HOOK_KV_COPY_STALL, attention's
+ * copies of keys and values are never asked for, so that the waits for them
+ * run out (after about a millisecond). */
+#define ZC_HOOK_KV_COPY_STALL 1u
+ZC_API void zc_kv_set_test_hooks(uint32_t hooks);
 
 /* Workspace bytes of zc_kv_attend for this cache, batch and number of query
  * heads (0 for invalid ones). Queries the device's SM count; host only. */

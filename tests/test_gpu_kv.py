@@ -24,6 +24,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import entropy_coding_gb300 as zc  # noqa: E402
+from entropy_coding_gb300 import kv  # noqa: E402
 
 from kv_reference import VALUES, attend, rows_of, to_codes, write  # noqa: E402
 
@@ -429,6 +430,25 @@ def test_device_errors_are_reported_and_nothing_else_is_touched():
     zc.kv_write(cache, good, x, x)
     cache.check()
     assert not cache.k.view(torch.uint8)[2:].any()
+
+
+@pytest.mark.parametrize("lens,news", [([900, 300], [1, 1]), ([900, 300], [300, 10])])
+def test_a_wait_that_runs_out_is_reported(lens, news):
+    """With the test hook the copies of keys and values are never asked for: the kernels give up, return and report it,
+    and a call after that, with a workspace of its own, is right."""
+    cache, batch, q, out, lse = _attend_case("bf16", 64, 2, 4, 128, lens, news, True, 0)
+    again = zc.KVBatch(batch.block_table, batch.cu_tokens, batch.lens, batch.total_tokens, batch.max_tokens)
+    zc.lib().zc_kv_set_test_hooks(kv.HOOK_COPY_STALL)
+    try:
+        zc.kv_attend(cache, again, q)
+        with pytest.raises(zc.ZcError) as e:
+            cache.check()
+    finally:
+        zc.lib().zc_kv_set_test_hooks(0)
+    assert e.value.status == zc.ETIMEOUT
+    o2, l2 = zc.kv_attend(cache, batch, q)
+    cache.check()
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
 
 
 def test_arguments_that_the_host_refuses():
