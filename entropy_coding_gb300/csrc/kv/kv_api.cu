@@ -154,14 +154,15 @@ namespace {
 
 // Which kernels a batch needs. A sequence's rows of a head are its new tokens times the group. Up to 16 of them the
 // cache's bytes are what counts, and the kernel that streams them does the work; more rows fill the tensor cores'
-// 128-row tiles. A batch of prompts (more than a tile's rows) and single tokens runs both, each on its own sequences; up to 8
-// sequences of uneven length, or drafts of uneven length, are not worth a second launch, and the tiles take them all.
+// 128-row tiles. A batch of prompts (more than a tile's rows) among single tokens runs both, each on its own sequences. The
+// host does not know how many sequences are of which kind: where they have a tile's rows on average, or are no more than
+// 8, the few single tokens are not worth a second launch (11 us for two of 24 sequences), nor are drafts of uneven length.
 struct Plan {
     bool rows, tiles;
     uint64_t rows_counters, tiles_counters, part_bytes;
     Plan(const Batch &b, const Cache &c, uint32_t group) {
         tiles = uint64_t(b.most) * group > kRowsMost;
-        rows = !tiles || (b.n_seqs > 8 && uint64_t(b.n_seqs) * b.most != b.total && uint64_t(b.most) * group > 128);
+        rows = !tiles || (b.n_seqs > 8 && uint64_t(b.most) * group > 128 && uint64_t(b.total) * group < 128ull * b.n_seqs);
         rows_counters = rows ? pad256(4 * zc::kv::rows_counters(b, c, group)) : 0;
         tiles_counters = tiles ? pad256(4 * zc::kv::tiles_counters(b, c, group)) : 0;
         const uint64_t r = rows ? rows_part_bytes(c) : 0, t = tiles ? tiles_part_bytes(c) : 0;

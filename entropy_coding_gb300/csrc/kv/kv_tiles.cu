@@ -597,6 +597,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
         if (job.end) return true;
         const uint32_t row = job.tile * kRows + r, n_rows = job.seq.n * a.group;
         const bool mine = row < n_rows;
+        const bool idle = !__any_sync(0xFFFFFFFFu, mine);  // a warp without rows: its weights may be anything
         int lo = 0, hi = 0;
         if (mine) bounds(a, job.seq, row, lo, hi);
         float m = kNone, mw = kNone, l = 0.0f;
@@ -621,6 +622,10 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
 #pragma unroll
                     for (int b = 0; b < kBoxes; b++) by[b] = fmaxf(c * by[b], 1e-37f);  // (0 * -infinity would be NaN)
                     if (!__all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.s_full[half], scored & 1, a.limit))) return false;
+                    if (idle) {
+                        if (lane == 0) bar_arrive(&sm.bars.p_full[half][0]), bar_arrive(&sm.bars.p_full[half][1]);
+                        continue;
+                    }
                     tm_after();
                     float x[kTile];
 #pragma unroll

@@ -241,6 +241,7 @@ ATTENDS = [  # dtype, block, kv heads, group, dim, lens, new, causal, window
     ("fp16", 16, 1, 2, 32, [640, 300], [100, 260], False, 40),
     ("bf16", 256, 1, 16, 128, [600, 270], [64, 1], True, 0),                      # one key/value head for all
     ("fp16", 64, 2, 4, 128, [900, 1, 70, 640, 33], [1, 1, 70, 300, 2], True, 0),  # decoding and prompts
+    ("bf16", 32, 2, 4, 128, [300, 20, 500, 64, 700, 33, 90, 10, 1000, 200], [1, 1, 1, 1, 300, 1, 2, 1, 0, 3], True, 0),  # one prompt among decoding
     ("bf16", 16, 2, 2, 64, [200, 0, 10, 5, 0], [0, 3, 10, 9, 1], True, 0),        # no tokens, no keys, fewer keys than tokens
 ]
 
@@ -487,6 +488,20 @@ def test_arguments_that_the_host_refuses():
     zc.kv_write(cache, empty, x[:0], x[:0])
     assert zc.kv_read(cache, empty)[0].shape == (0, 2, 32) and zc.kv_attend(cache, empty, x[:0])[0].shape == (0, 2, 32)
     cache.check()
+
+
+@pytest.mark.parametrize("args", [[], ["--heads", "10", "--kv-heads", "2", "--dim", "80", "--steps", "3"]])
+def test_the_example_of_a_layer_in_service(args):
+    """Writing, attention, reading back, and a sequence parked without loss in host memory and restored: the outputs of
+    a run in which it never left."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_cache.py")
+    spec = importlib.util.spec_from_file_location("serve_cache", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    r = m.main(args)
+    assert r["same"] and r["ratio"] < 1.0 and r["error"] < 2 ** -6
 
 
 def test_reference_codes_are_torchs():
