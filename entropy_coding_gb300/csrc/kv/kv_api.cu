@@ -163,7 +163,7 @@ struct Plan {
     Plan(const Batch &b, const Cache &c, uint32_t group) {
         tiles = uint64_t(b.most) * group > kRowsMost;
         rows = !tiles || (b.n_seqs > 8 && uint64_t(b.most) * group > 128 && uint64_t(b.total) * group < 128ull * b.n_seqs);
-        rows_counters = rows ? pad256(4 * zc::kv::rows_counters(b, c, group)) : 0;
+        rows_counters = rows ? pad256(4 * zc::kv::rows_counters(b, c, group)) + pad256(4 * rows_group_counters()) : 0;
         tiles_counters = tiles ? pad256(4 * zc::kv::tiles_counters(b, c, group)) : 0;
         const uint64_t r = rows ? rows_part_bytes(c) : 0, t = tiles ? tiles_part_bytes(c) : 0;
         part_bytes = r > t ? r : t;
@@ -215,7 +215,8 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
         if ((st = launch_tiles(a, str)) != ZC_OK) return st;
     }
     if (plan.rows) {
-        a.counters = reinterpret_cast<uint32_t *>(ws);
+        a.group_counters = reinterpret_cast<uint32_t *>(ws);
+        a.counters = reinterpret_cast<uint32_t *>(ws + pad256(4 * rows_group_counters()));
         st = launch_rows(a, str);
     }
     return st;

@@ -67,6 +67,7 @@ struct AttendArgs {
     uint32_t causal, window;
     uint32_t rows_most;    // a sequence of no more rows of a head goes to kv_rows.cu
     uint32_t *counters;    // workspace: an item's parts that are done, zero between calls
+    uint32_t *group_counters;  // (kv_rows.cu) and those of a group of parts
     void *parts;           // workspace: partial results
     long long limit;       // clocks of a wait
     uint32_t stall;        // test hook: the copies are never asked for
@@ -88,6 +89,7 @@ int sm_count();
 // of those with more (kv_tiles.cu), and what their workspaces hold.
 constexpr uint32_t kRowsMost = 16;
 uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group);
+uint64_t rows_group_counters();
 uint64_t rows_part_bytes(const Cache &c);
 int launch_rows(const AttendArgs &a, cudaStream_t s);
 uint64_t tiles_counters(const Batch &b, const Cache &c, uint32_t group);

@@ -51,6 +51,7 @@ constexpr int kUnit = kWarps * kSlice;  // keys of a unit of work
 // CTAs of an SM, as many as their registers allow, and slices of a ring, as
 // many as fit the SM's shared memory then.
 constexpr int kResident = 3;
+constexpr int kGroup = 8;               // parts that are joined at a time, where there are more than twice as many
 constexpr int stages(int dp) { return 3 * (128 / dp); }
 
 template <int DP> struct Stage {
@@ -489,19 +490,23 @@ __device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const 
     }
 }
 
-// An item's parts together: the `first` one in its CTA's second slot (a piece
-// that begins an item), the others in the first slots of the CTAs after it.
+// Parts of an item together: part i is in the first slot of CTA first + i, but
+// the item's own first one (i = 0) in the second, where a piece that begins an
+// item is. Joins parts i0, i0 + step, ... (n of them), into part i0 or, without
+// `on`, into the finished rows.
 // A thread takes 4 columns of a row and every ways-th part, kRun parts in
 // flight together; the ways meet in shared memory.
 template <int DP, int NT>
-__device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Job &item, uint32_t first, uint32_t n) {
+__device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Job &item, uint32_t first, uint32_t i0, uint32_t step,
+                                     uint32_t n, bool on) {
     constexpr int kCols = DP / 4, kRun = 8;
     struct Way {
         float4 x;
         float m, mw, l;
     };
     Way *met = reinterpret_cast<Way *>(smem);
-    const Part<DP, NT> *parts = static_cast<const Part<DP, NT> *>(a.parts);
+    Part<DP, NT> *parts = static_cast<Part<DP, NT> *>(a.parts);
+    auto part = [&](uint32_t i) -> Part<DP, NT> & { return parts[2 * (first + i) + (i ? 0 : 1)]; };
     const uint32_t row0 = item.tile * 8 * NT;
     const int rows = int(min(uint32_t(8 * NT), item.seq.n * a.group - row0)), D = int(a.c.dim);
     const int jobs = rows * kCols;                             // 4 columns of a row each
@@ -533,7 +538,7 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const J
                 for (int k = 0; k < kRun; k++) {
                     const uint32_t of = i + k * ways;
                     const bool there = of < n;
-                    const Part<DP, NT> &p = parts[2 * (first + (there ? of : 0)) + (there && of ? 0 : 1)];
+                    const Part<DP, NT> &p = part(there ? i0 + of * step : i0);
                     x[k] = there ? __ldcg(reinterpret_cast<const float4 *>(&p.o[r][col])) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     m[k] = there ? __ldcg(&p.m[r]) : kNone, mw[k] = there ? __ldcg(&p.mw[r]) : kNone, l[k] = there ? __ldcg(&p.l[r]) : 0.0f;
                 }
@@ -556,11 +561,33 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const J
                     add(v.x, v.m, v.mw, v.l);
                 }
         }
-        if (mine && way == 0) {
+        if (on) {
+            __syncthreads();  // everyone has read part i0
+            if (mine && way == 0) {
+                Part<DP, NT> &p = part(i0);
+                __stcg(reinterpret_cast<float4 *>(&p.o[r][col]), w.x);
+                if (col == 0) __stcg(&p.m[r], w.m), __stcg(&p.mw[r], w.mw), __stcg(&p.l[r], w.l);
+            }
+        } else if (mine && way == 0) {
             const float y[4] = {w.x.x, w.x.y, w.x.z, w.x.w};
             emit(a, item.seq, item.h, row0 + r, col, y, w.m, w.mw, w.l);
         }
     }
+}
+
+// Whether this CTA is the last of n to come to a counter (which is left at zero then): what the others wrote before they
+// came can be read.
+__device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t n, int &s_last) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        // releases what the CTA wrote (the barrier before it orders the other threads' writes) and acquires the others'
+        uint32_t done;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
+        if (done == n - 1) *counter = 0;
+        s_last = done == n - 1;
+    }
+    __syncthreads();
+    return s_last;
 }
 
 template <int DP, int NT>
@@ -632,17 +659,20 @@ __global__ void __launch_bounds__(kThreads, kResident) rows_kernel(const __grid_
             // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
             // W c / G <= u < W (c + 1) / G, rounded down, so c = (u G + G - 1) / W
             const uint32_t c0 = uint32_t((job.i0 * G + G - 1) / W), c1 = uint32_t(((job.i1 - 1) * G + G - 1) / W);
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                // releases the CTA's part (the barrier before it orders the other threads' writes) and acquires the others'
-                uint32_t *counter = a.counters + uint64_t(slot_of(job.seq.first, job.seq.s, a.group, 8 * NT, 1) + job.tile) * a.c.heads + job.h;
-                uint32_t done;
-                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(counter) : "memory");
-                if (done == c1 - c0) *counter = 0;
-                s_last = done == c1 - c0;
+            const uint32_t n = c1 - c0 + 1, mine = cta - c0;
+            uint32_t *counter = a.counters + uint64_t(slot_of(job.seq.first, job.seq.s, a.group, 8 * NT, 1) + job.tile) * a.c.heads + job.h;
+            uint8_t *space = reinterpret_cast<uint8_t *>(&mg);
+            // many parts: each kGroup of them first, by the last CTA of those, then what they make
+            const uint32_t groups = n <= 2 * kGroup ? 1 : (n + kGroup - 1) / kGroup, g = groups == 1 ? 0 : mine / kGroup;
+            uint32_t i0 = g * kGroup, step = 1, parts_of = groups == 1 ? n : min(uint32_t(kGroup), n - i0);
+            uint32_t *first = groups == 1 ? counter : a.group_counters + 2 * (c0 + i0) + (g ? 0 : 1);
+            bool on = groups > 1, go = last_of(first, parts_of, s_last);
+#pragma unroll 1
+            while (go) {
+                join<DP, NT>(a, space, job, c0, i0, step, parts_of, on);
+                go = on && last_of(counter, groups, s_last);
+                i0 = 0, step = kGroup, parts_of = groups, on = false;
             }
-            __syncthreads();
-            if (s_last) join<DP, NT>(a, reinterpret_cast<uint8_t *>(&mg), job, c0, c1 - c0 + 1);
         }
         job = next;
     }
@@ -678,6 +708,8 @@ template <int NT> uint64_t part_bytes(uint32_t dim) {
 uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group) {
     return uint64_t(slot_of(b.total, b.n_seqs, group, 8, 1)) * c.heads;
 }
+
+uint64_t rows_group_counters() { return uint64_t(sm_count()) * kResident * 2; }
 
 uint64_t rows_part_bytes(const Cache &c) { return part_bytes<2>(c.dim); }
 

@@ -467,13 +467,12 @@ template <int DP> __device__ __noinline__ void join(const AttendArgs &a, const J
     const uint32_t c0 = job.c0, c1 = job.c1;
     // the first part is in its CTA's second slot, the others in the first slots of the CTAs after it
     auto at = [&](uint32_t c) -> const Part<DP> & { return parts[2 * c + (c == c0 ? 1 : 0)]; };
-    // With one tile of rows its 128 rows take two threads each, half of the columns a thread.
-    const int r = job.tiles == 1 ? threadIdx.x % kTile : threadIdx.x, span = job.tiles == 1 ? DP / 2 : DP;
-    const int from = job.tiles == 1 ? int(threadIdx.x) / kTile * span : 0, to = min(from + span, int(a.c.dim));
-    const uint32_t row = job.tile * kRows + r;
-    if (row >= job.seq.n * a.group) return;
+    // 16 columns of a row at a time, whichever rows there are
+    const uint32_t rows = min(uint32_t(kRows), job.seq.n * a.group - job.tile * kRows);
 #pragma unroll 1
-    for (int i = from; i < to; i += 16) {
+    for (uint32_t u = threadIdx.x; u < rows * (a.c.dim / 16); u += 256) {
+        const uint32_t r = u % rows, row = job.tile * kRows + r;
+        const int i = int(u / rows) * 16;
         float o[16], M = kNone, W = kNone, L = 0.0f;
 #pragma unroll
         for (int k = 0; k < 16; k++) o[k] = 0.0f;
