@@ -50,6 +50,11 @@ constexpr int kReaders = 8 + 4 + 1 + 1; // warps (and the products' thread) that
 constexpr int kSlots = 8;               // key tiles whose scales are held: the copies run up to 3 ahead of the weights
 constexpr uint32_t kColumns = 512;      // of tensor memory: S (and W in its place) 0, 128, O 256, 384
 
+// Registers of a thread by warpgroup: two of rows, the conversion, the rest. What the groups take together is what the
+// CTA was launched with, 128 for each of 512 threads; a sum above that would wait for registers for ever.
+constexpr int kRowRegs = 184, kConvertRegs = 72, kOtherRegs = 72;
+static_assert(2 * kRowRegs + kConvertRegs + kOtherRegs <= 4 * 128, "more registers than the CTA has");
+
 struct Bars {
     uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], scale_full[kSlots];
     uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], rows, drained;
@@ -845,15 +850,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     tm_after();
     
     bool ok = true;
-    // 512 registers a lane over the four warpgroups, as at launch
     if (warp < 8) {
-        more_registers<184>();
+        more_registers<kRowRegs>();
         ok = rows_role<DP>(a, sm);
     } else if (warp < 12) {
-        fewer_registers<80>();
+        fewer_registers<kConvertRegs>();
         ok = convert_role<DP>(sm, a.limit);
     } else {
-        fewer_registers<64>();
+        fewer_registers<kOtherRegs>();
         if (warp == 12) ok = product_role<DP>(sm, a.limit);
         if (warp == 13) ok = copy_role<DP>(a, maps, sm);
         if (warp == 14 && threadIdx.x % 32 == 0) ok = find_role<DP>(a, sm, Walk{w0, w1, sm.i0, W, G, sm.slot, sm.seq, sm.h});
