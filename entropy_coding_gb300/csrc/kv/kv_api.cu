@@ -154,15 +154,22 @@ namespace {
 
 // Which kernels a batch needs. A sequence's rows of a head are its new tokens times the group. Up to 16 of them the
 // cache's bytes are what counts, and the kernel that streams them does the work; more rows fill the tensor cores'
-// 128-row tiles. A batch of prompts (more than a tile's rows) among single tokens runs both, each on its own sequences. The
-// host does not know how many sequences are of which kind: where they have a tile's rows on average, or are no more than
-// 8, the few single tokens are not worth a second launch (11 us for two of 24 sequences), nor are drafts of uneven length.
+// 128-row tiles. (16 sequences of up to 8000 keys: 16 rows 66 us there and 87 us on tiles; 20 or 32 rows, two passes
+// over the bytes, 94 and 95 us there and 87 us on tiles.)
+// A batch of prompts (more than a tile's rows) among single tokens runs both, each on its own sequences: a prompt of 400
+// tokens among 47 single ones takes 141 us so and 204 us on tiles alone. The host does not know how many sequences are of
+// which kind: where they have a tile's rows on average, or are no more than 8, the few single tokens are not worth a
+// second launch (24 sequences, two of them single tokens: 68 us with both, 56 us on tiles), nor are drafts of uneven
+// length (66 and 36 us). Of such a batch only sequences of up to 8 rows are streamed, where a single token has no more:
+// room for 16 rows costs the streaming 1.35 times the time (168 us for that batch).
 struct Plan {
     bool rows, tiles;
+    uint32_t rows_most;
     uint64_t rows_counters, tiles_counters, part_bytes;
     Plan(const Batch &b, const Cache &c, uint32_t group) {
         tiles = uint64_t(b.most) * group > kRowsMost;
-        rows = !tiles || (b.n_seqs > 8 && uint64_t(b.most) * group > 128 && uint64_t(b.total) * group < 128ull * b.n_seqs);
+        rows = !tiles || (b.n_seqs > 8 && group <= kRowsMost && uint64_t(b.most) * group > 128 && uint64_t(b.total) * group < 128ull * b.n_seqs);
+        rows_most = !rows ? 0 : tiles && group <= 8 ? 8 : kRowsMost;
         rows_counters = rows ? pad256(4 * zc::kv::rows_counters(b, c, group)) + pad256(4 * rows_group_counters()) : 0;
         tiles_counters = tiles ? pad256(4 * zc::kv::tiles_counters(b, c, group)) : 0;
         const uint64_t r = rows ? rows_part_bytes(c) : 0, t = tiles ? tiles_part_bytes(c) : 0;
@@ -202,7 +209,7 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
     if (ws_bytes < plan.bytes()) return ZC_ECAPACITY;
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
     a.parts = ws + plan.rows_counters + plan.tiles_counters;
-    a.rows_most = plan.rows ? kRowsMost : 0;
+    a.rows_most = plan.rows_most;
     a.scale_log2 = float(scale * 1.4426950408889634);
     a.causal = flags & ZC_KV_CAUSAL;
     a.window = window;

@@ -35,6 +35,14 @@
 // threads of a quad in runs (the order of a product's inner index is free as
 // long as both operands share it), so that fragments are read 16 bytes at a
 // time.
+//
+// Measured on a GB300: the next tokens of 64 sequences of up to 8192 keys (8
+// heads of 128, 4 query heads each), 558 MB of cache, in 98 us: 5.7 TB/s, 0.84
+// of the copy rate. While slices stream, memory is the bound (a single long
+// sequence's 268 MB go by in 37 us of the call's 52); the rest is the start (4
+// us until the first slices are there), pieces' ends, and the joining of parts.
+// The transposed products halved the tensor instructions for 4 rows (135 to 122
+// us); fetching the next piece before the last is finished, 113 to 99.
 #include <algorithm>
 #include <atomic>
 
@@ -51,7 +59,9 @@ constexpr int kUnit = kWarps * kSlice;  // keys of a unit of work
 // CTAs of an SM, as many as their registers allow, and slices of a ring, as
 // many as fit the SM's shared memory then.
 constexpr int kResident = 3;
-constexpr int kGroup = 8;               // parts that are joined at a time, where there are more than twice as many
+// Parts that are joined at a time, where there are more than twice as many: 57 parts of a long sequence at once made its
+// call 58 us, in two steps 52; for 16 parts the second step costs what it saves.
+constexpr int kGroup = 8;
 constexpr int stages(int dp) { return 3 * (128 / dp); }
 
 template <int DP> struct Stage {
@@ -713,6 +723,7 @@ uint64_t rows_group_counters() { return uint64_t(sm_count()) * kResident * 2; }
 
 uint64_t rows_part_bytes(const Cache &c) { return part_bytes<2>(c.dim); }
 
+// One tile of 8 rows or two: with two, 64 sequences of 4 rows take 135 us where one takes 100.
 int launch_rows(const AttendArgs &a, cudaStream_t s) {
     return std::min<uint64_t>(uint64_t(a.b.most) * a.group, a.rows_most) <= 8 ? launch_tiles_of<1>(a, s) : launch_tiles_of<2>(a, s);
 }

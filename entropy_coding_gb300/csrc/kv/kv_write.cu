@@ -16,6 +16,14 @@
 // 128 columns; rows beyond that are read again). The CTA is as small as that
 // allows: what bounds it is the latency of its few dependent reads, which only
 // more CTAs on an SM hide.
+//
+// Measured on a GB300: 104 MB of bfloat16 prompts (17138 tokens of 8 heads of
+// 128, blocks of 64) in 20 us, 5.1 TB/s, 0.76 of the copy rate; the arithmetic
+// units are at 48 %, and what is left is the latency of a CTA's start (its
+// place in the batch, its block, its rows: three dependent reads). Divisions
+// by the row's pieces, four a piece at first, were 4 us of it; units of several
+// heads in turn in one CTA, with the next rows on their way, were slower (27 us):
+// they leave fewer CTAs. A decoding step of 32 tokens takes 5 us, a launch.
 #include "kv_common.cuh"
 
 namespace zc {
@@ -164,7 +172,8 @@ template <int DT, int kThreads> __global__ void __launch_bounds__(kThreads) writ
     }
 }
 
-// Threads by the pieces of a block that a call may write.
+// Threads by the pieces of a block that a call may write: as few as hold them. (Blocks of 160 pieces take 8 us with 64
+// threads and 14 with 256, blocks of 1024 pieces 26 us with 128 and 33 with 256.)
 template <int DT> void launch(const MoveArgs &a, cudaStream_t s) {
     const dim3 grid(slot_of(a.b.total, a.b.n_seqs, 1, a.c.tokens, 2), a.c.heads, 2);
     const uint32_t rows = a.b.most < a.c.tokens ? a.b.most : a.c.tokens, pieces = rows * (a.c.dim / 8);
