@@ -117,7 +117,7 @@ __device__ __forceinline__ Seq read_seq(const Batch &b, uint32_t s, int32_t *d_s
     q.first = uint32_t(c0);
     q.n = uint32_t(c1 - c0);
     q.len = __ldg(b.lens + s);
-    q.ok = c0 >= 0 && c1 >= c0 && uint32_t(c1) <= b.total && uint32_t(c1 - c0) <= b.most && q.len >= 0;
+    q.ok = c0 >= 0 && c1 >= c0 && uint32_t(c1) <= b.total && uint32_t(c1 - c0) <= b.most && q.len >= 0 && q.len < (1 << 30);
     if (!q.ok && speak) report(d_status, ZC_EFORMAT);
     if (q.ok && uint64_t(q.len) > uint64_t(b.width) * block_tokens) {
         if (speak) report(d_status, ZC_ECAPACITY);

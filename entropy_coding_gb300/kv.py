@@ -218,42 +218,55 @@ def kv_read_into(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
     _move(_entries()[1], "zc_kv_read", cache, batch, k, v, stream)
 
 
-def _pair(make, stream, device):
-    if stream is None:
-        return make()
-    with _on(stream, device):
-        return make()
-
-
 def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16, stream=None):
     """The batch's tokens as (k, v), [total_tokens, kv_heads, head_dim]."""
-    shape = (batch.total_tokens, cache.kv_heads, cache.head_dim)
-    k, v = _pair(lambda: (torch.empty(shape, dtype=dtype, device=cache.device),
-                          torch.empty(shape, dtype=dtype, device=cache.device)), stream, cache.device)
-    kv_read_into(cache, batch, k, v, stream)
+    code = _CODE.get(dtype)
+    if code is None:
+        _fail("zc_kv_read: bfloat16, float16 or float32")
+    heads, dim, device = cache.kv_heads, cache.head_dim, cache.device
+    shape = (batch.total_tokens, heads, dim)
+    if stream is None:
+        k = torch.empty(shape, dtype=dtype, device=device)
+        v = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        with _on(stream, device):
+            k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+    rk, rv = _Rows(k.data_ptr(), heads * dim, dim), _Rows(v.data_ptr(), heads * dim, dim)
+    _check(_entries()[1](cache._ref, batch._ref, code, ctypes.addressof(rk), ctypes.addressof(rv), cache._status,
+                         _handle(stream, cache)), "zc_kv_read")
     return k, v
+
+
+def _attend(cache, batch, code, heads, q, out, lse, scale, causal, window, stream):
+    if not 0 <= window <= 0x7FFFFFFF:
+        _fail("zc_kv_attend: window >= 0")
+    address, size, _ = batch.workspace(cache, heads, stream)
+    _check(_entries()[2](cache._ref, batch._ref, code, heads, ctypes.addressof(q), ctypes.addressof(out), lse,
+                         cache.head_dim ** -0.5 if scale is None else scale, _CAUSAL if causal else 0, window, address,
+                         size, cache._status, _handle(stream, cache)), "zc_kv_attend")
+
+
+def _query(cache, batch, q):
+    """Type code, heads and rows of a query tensor."""
+    code = _CODE.get(q.dtype)
+    if code is None or code == _FP32:
+        _fail("zc_kv_attend: q is bfloat16 or float16")
+    heads = q.shape[1] if q.dim() == 3 else 0
+    return code, heads, _rows(q, (batch.total_tokens, heads, cache.head_dim), cache.device, "q")
 
 
 def kv_attend_into(cache: KVCache, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None = None,
                    scale: float | None = None, causal: bool = True, window: int = 0, stream=None) -> None:
     """Attention of the batch's tokens over the cache (zc_kv_attend) into
     ``out`` and, if given, ``lse`` (float32 [total_tokens, heads])."""
-    code = _CODE.get(q.dtype)
-    if code is None or code == _FP32 or out.dtype != q.dtype:
-        _fail("zc_kv_attend: q and out are bfloat16 or float16")
-    heads = q.shape[1] if q.dim() == 3 else 0
-    shape = (batch.total_tokens, heads, cache.head_dim)
-    rq, ro = _rows(q, shape, cache.device, "q"), _rows(out, shape, cache.device, "out")
-    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous() or
+    code, heads, rq = _query(cache, batch, q)
+    if out.dtype != q.dtype:
+        _fail("zc_kv_attend: out has q's type")
+    ro = _rows(out, q.shape, cache.device, "out")
+    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous() or
                             lse.device != cache.device):
         _fail("zc_kv_attend: lse is float32 [total_tokens, heads]")
-    if not 0 <= window <= 0x7FFFFFFF:
-        _fail("zc_kv_attend: window >= 0")
-    ws = batch.workspace(cache, heads, stream)
-    _check(_entries()[2](cache._ref, batch._ref, code, heads, ctypes.addressof(rq), ctypes.addressof(ro),
-                         None if lse is None else lse.data_ptr(), cache.head_dim ** -0.5 if scale is None else scale,
-                         _CAUSAL if causal else 0, window, ws[0], ws[1], cache._status, _handle(stream, cache)),
-           "zc_kv_attend")
+    _attend(cache, batch, code, heads, rq, ro, None if lse is None else lse.data_ptr(), scale, causal, window, stream)
 
 
 def kv_attend(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | None = None, causal: bool = True,
@@ -265,7 +278,16 @@ def kv_attend(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | No
     with j <= p (``causal``) and j > p - window (``window`` > 0). ``scale``
     defaults to head_dim ** -0.5. The tokens' own keys and values are in the
     cache already (kv_write first)."""
-    out, lse = _pair(lambda: (torch.empty(q.shape, dtype=q.dtype, device=cache.device),
-                              torch.empty(q.shape[:2], dtype=torch.float32, device=cache.device)), stream, cache.device)
-    kv_attend_into(cache, batch, q, out, lse, scale, causal, window, stream)
+    code, heads, rq = _query(cache, batch, q)
+    shape, device = q.shape, cache.device
+    if stream is None:
+        out = torch.empty(shape, dtype=q.dtype, device=device)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
+    else:
+        with _on(stream, device):
+            out = torch.empty(shape, dtype=q.dtype, device=device)
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
+    dim = cache.head_dim
+    _attend(cache, batch, code, heads, rq, _Rows(out.data_ptr(), heads * dim, dim), lse.data_ptr(), scale, causal, window,
+            stream)
     return out, lse

@@ -393,7 +393,7 @@ typedef struct {
  *   d_table       int32 [n_seqs][table_width], rows table_stride apart: block
  *                 p / block_tokens of sequence s holds its position p
  *   d_cu          int32 [n_seqs + 1], from 0, not falling
- *   d_lens        int32 [n_seqs], at most table_width * block_tokens
+ *   d_lens        int32 [n_seqs], at most table_width * block_tokens, below 2^30
  *   total_tokens  cu[n_seqs], as the host knows it
  *   max_tokens    at least the largest n, at most total_tokens
  * A call skips a sequence whose entries are out of these ranges (ZC_EFORMAT;

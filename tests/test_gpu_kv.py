@@ -242,6 +242,7 @@ ATTENDS = [  # dtype, block, kv heads, group, dim, lens, new, causal, window
     ("bf16", 256, 1, 16, 128, [600, 270], [64, 1], True, 0),                      # one key/value head for all
     ("fp16", 64, 2, 4, 128, [900, 1, 70, 640, 33], [1, 1, 70, 300, 2], True, 0),  # decoding and prompts
     ("bf16", 32, 2, 4, 128, [300, 20, 500, 64, 700, 33, 90, 10, 1000, 200], [1, 1, 1, 1, 300, 1, 2, 1, 0, 3], True, 0),  # one prompt among decoding
+    ("fp16", 32, 1, 71, 64, [300, 50], [1, 2], True, 0),                          # an odd number of heads for one
     ("bf16", 16, 2, 2, 64, [200, 0, 10, 5, 0], [0, 3, 10, 9, 1], True, 0),        # no tokens, no keys, fewer keys than tokens
 ]
 
@@ -469,6 +470,8 @@ def test_arguments_that_the_host_refuses():
         lambda: zc.kv_attend(cache, batch, torch.zeros(6, 4, 32, device=DEV)),
         lambda: zc.kv_attend(cache, batch, x, scale=float("nan")),
         lambda: zc.kv_attend(cache, batch, x, window=-1),
+        lambda: zc.kv_attend(cache, batch, x[0]),
+        lambda: zc.kv_read(cache, batch, dtype=torch.float64),
         lambda: zc.kv_attend_into(cache, batch, x, torch.empty_like(x), torch.zeros(6, device=DEV)),
         lambda: zc.KVBatch(t([[0], [1]]), t([0, 3, 6]), t([3, 16]), 7, 3),
         lambda: zc.KVBatch(t([[0], [1]]), t([0, 3, 6]), t([3, 16]), 2, 3),
