@@ -64,7 +64,7 @@ constexpr uint32_t kColumns = 512;      // of tensor memory: S (and W in its pla
 
 // Registers of a thread by warpgroup: two of rows, the conversion, the rest. What the groups take together is what the
 // CTA was launched with, 128 for each of 512 threads; a sum above that would wait for registers for ever.
-constexpr int kRowRegs = 184, kConvertRegs = 72, kOtherRegs = 72;
+constexpr int kRowRegs = 160, kConvertRegs = 96, kOtherRegs = 96;
 static_assert(2 * kRowRegs + kConvertRegs + kOtherRegs <= 4 * 128, "more registers than the CTA has");
 
 struct Bars {
@@ -130,6 +130,13 @@ __device__ __forceinline__ void tm_store32(uint32_t at, const uint32_t *r) {
                  : "memory");
 }
 __device__ __forceinline__ void tm_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Keeps the uses of 32 loaded registers behind the wait before this: to the compiler they have their values from the load on.
+__device__ __forceinline__ void tm_loaded(float *x) {
+    asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]),
+                 "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]));
+    asm volatile("" : "+f"(x[16]), "+f"(x[17]), "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]),
+                 "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]), "+f"(x[30]), "+f"(x[31]));
+}
 __device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -643,28 +650,38 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                         continue;
                     }
                     tm_after();
-                    float x[kTile];
+                    const int from = lo - j * kTile, to = hi - j * kTile;
+                    // 64 scores at a time, for their maxima and then for the weights: with all 128 in registers the loop spilled
+                    // (drafts 27 us, with 64 25 us)
+                    auto scores64 = [&](int part, float (&x)[64]) {
+                        tm_load32(tmS + 64 * part, x);
+                        tm_load32(tmS + 64 * part + 32, x + 32);
+                        tm_wait_load();
+                        tm_loaded(x);
+                        tm_loaded(x + 32);
+                        if (edge) {
 #pragma unroll
-                    for (int i = 0; i < 4; i++) tm_load32(tmS + 32 * i, x + 32 * i);
-                    tm_wait_load();
-                    if (edge) {
-                        const int from = lo - j * kTile, to = hi - j * kTile;
+                            for (int q = 0; q < 64; q += 32) {
+                                const uint32_t seen = below(to - 64 * part - q) & ~below(from - 64 * part - q);
 #pragma unroll
-                        for (int q = 0; q < kTile; q += 32) {
-                            const uint32_t seen = below(to - q) & ~below(from - q);
-#pragma unroll
-                            for (int i = 0; i < 32; i++) x[q + i] = seen >> i & 1 ? x[q + i] : kNone;
+                                for (int i = 0; i < 32; i++) x[q + i] = seen >> i & 1 ? x[q + i] : kNone;
+                            }
                         }
-                    }
+                    };
                     float top = kNone, topw = kNone;
+                    float x[64];
 #pragma unroll
-                    for (int b = 0; b < kBoxes; b++) {
-                        float g = x[16 * b];
+                    for (int part = 1; part >= 0; part--) {
+                        scores64(part, x);
 #pragma unroll
-                        for (int i = 1; i < 16; i++) g = fmaxf(g, x[16 * b + i]);
-                        g *= by[b];
-                        top = fmaxf(top, g);
-                        topw = fmaxf(topw, g + lvs[b]);
+                        for (int b = 0; b < 4; b++) {
+                            float g = x[16 * b];
+#pragma unroll
+                            for (int i = 1; i < 16; i++) g = fmaxf(g, x[16 * b + i]);
+                            g *= by[4 * part + b];
+                            top = fmaxf(top, g);
+                            topw = fmaxf(topw, g + lvs[4 * part + b]);
+                        }
                     }
                     // As in kv_rows.cu: the maxima are followed once they have grown by 2^kSlack.
                     const bool grows = top > m + kSlack || topw > mw + kSlack;
@@ -683,6 +700,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                                 float o[32];
                                 tm_load32(tmO + i, o);
                                 tm_wait_load();
+                                tm_loaded(o);
 #pragma unroll
                                 for (int k = 0; k < 32; k++) o[k] *= down;
                                 tm_store32(tmO + i, reinterpret_cast<uint32_t *>(o));
@@ -693,22 +711,24 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                     uint32_t *p = reinterpret_cast<uint32_t *>(x);
 #pragma unroll
                     for (int part = 0; part < 2; part++) {  // the products start on the first 64 keys' weights
+                        // (the weights take the columns of scores 0 to 63; those from 64 on are there until the next products)
+                        if (part) scores64(1, x);
 #pragma unroll
-                        for (int b = part * kBoxes / 2; b < (part + 1) * kBoxes / 2; b++) {
-                            const float lf = fminf(fmaxf(lvs[b] + (base - mw), -60.0f), 120.0f);  // (mw = -infinity: every vs is 0)
+                        for (int b = 0; b < 4; b++) {
+                            const float lf = fminf(fmaxf(lvs[4 * part + b] + (base - mw), -60.0f), 120.0f);  // (mw = -infinity: every vs is 0)
                             const float bias = lf - base;
                             float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
                                 float y0, y1;
-                                fma2(y0, y1, x[16 * b + i], x[16 * b + i + 1], by[b], bias);
+                                fma2(y0, y1, x[16 * b + i], x[16 * b + i + 1], by[4 * part + b], bias);
                                 y0 = ex2(y0), y1 = ex2(y1);
                                 add2(sum0, sum1, y0, y1);
                                 p[8 * b + i / 2] = half2_of(y0, y1);
                             }
                             l += (sum0 + sum1) * ex2(-lf);
                         }
-                        tm_store32(tmS + 32 * part, p + 32 * part);
+                        tm_store32(tmS + 32 * part, p);
                         tm_wait_store();
                         tm_before();
                         __syncwarp();
@@ -738,6 +758,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                 if (job.n) {
                     tm_load32(tmO + i, o);
                     tm_wait_load();
+                    tm_loaded(o);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; k++) o[k] = 0.0f;
