@@ -485,33 +485,40 @@ __device__ __noinline__ uint32_t poisoned(const AttendArgs &a, const Job &job, i
     return mask;
 }
 
-// An item's parts together, by the 256 row threads. Apart from the loop over key tiles, whose registers are all taken.
-template <int DP> __device__ __noinline__ void join(const AttendArgs &a, const Job &job) {
+// An item's parts together, by the 256 row threads: kCols columns of a row at a time, kRun parts in flight together.
+// Apart from the loop over key tiles, whose registers are all taken.
+template <int DP, int kCols, int kRun> __device__ __noinline__ void join_rows(const AttendArgs &a, const Job &job) {
     const Part<DP> *parts = static_cast<const Part<DP> *>(a.parts);
     const uint32_t c0 = job.c0, c1 = job.c1;
-    // the first part is in its CTA's second slot, the others in the first slots of the CTAs after it
-    auto at = [&](uint32_t c) -> const Part<DP> & { return parts[2 * c + (c == c0 ? 1 : 0)]; };
     // 16 columns of a row at a time, whichever rows there are
-    const uint32_t rows = min(uint32_t(kRows), job.seq.n * a.group - job.tile * kRows);
+    const uint32_t rows = min(uint32_t(kRows), job.seq.n * a.group - job.tile * kRows), cols = a.c.dim;
 #pragma unroll 1
-    for (uint32_t u = threadIdx.x; u < rows * (a.c.dim / 16); u += 256) {
+    for (uint32_t u = threadIdx.x; u < rows * ((cols + kCols - 1) / kCols); u += 256) {
         const uint32_t r = u % rows, row = job.tile * kRows + r;
-        const int i = int(u / rows) * 16;
-        float o[16], M = kNone, W = kNone, L = 0.0f;
+        const int i = int(u / rows) * kCols;
+        float o[kCols / 16][16], M = kNone, W = kNone, L = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 16; k++) o[k] = 0.0f;
-        constexpr int kRun = 4;  // parts whose reads are in flight together
+        for (int k = 0; k < kCols; k++) o[k / 16][k % 16] = 0.0f;
 #pragma unroll 1
         for (uint32_t c = c0; c <= c1; c += kRun) {
-            float4 v[kRun][4];
+            float4 v[kRun][kCols / 4];
             float pm[kRun], pw[kRun], pl[kRun];
 #pragma unroll
             for (int n = 0; n < kRun; n++) {
-                const bool there = c + n <= c1;
-                const Part<DP> &p = at(there ? c + n : c1);
-                pm[n] = there ? __ldcg(&p.m[r]) : kNone, pw[n] = there ? __ldcg(&p.mw[r]) : kNone, pl[n] = there ? __ldcg(&p.l[r]) : 0.0f;
+                // the first part is in its CTA's second slot, the others in the first slots of the CTAs after it
+                const uint32_t at = min(c + n, c1);
+                const Part<DP> &p = parts[2 * at + (at == c0 ? 1 : 0)];
+                pm[n] = __ldcg(&p.m[r]), pw[n] = __ldcg(&p.mw[r]), pl[n] = __ldcg(&p.l[r]);
 #pragma unroll
-                for (int k = 0; k < 4; k++) v[n][k] = there ? __ldcg(&p.o[i / 4 + k][r]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int k = 0; k < kCols / 4; k++) v[n][k] = __ldcg(&p.o[i / 4 + k][r]);
+            }
+#pragma unroll
+            for (int n = 1; n < kRun; n++) {
+                if (c + n > c1) {
+                    pm[n] = pw[n] = kNone, pl[n] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kCols / 4; k++) v[n][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
             }
             float m1 = M, w1 = W;
 #pragma unroll
@@ -519,17 +526,29 @@ template <int DP> __device__ __noinline__ void join(const AttendArgs &a, const J
             const float down = ratio2(W, w1);
             L *= ratio2(M, m1);
 #pragma unroll
-            for (int k = 0; k < 16; k++) o[k] *= down;
+            for (int k = 0; k < kCols; k++) o[k / 16][k % 16] *= down;
 #pragma unroll
             for (int n = 0; n < kRun; n++) {
                 L += pl[n] * ratio2(pm[n], m1);
                 const float f = ratio2(pw[n], w1);
 #pragma unroll
-                for (int k = 0; k < 4; k++) o[4 * k] += v[n][k].x * f, o[4 * k + 1] += v[n][k].y * f, o[4 * k + 2] += v[n][k].z * f, o[4 * k + 3] += v[n][k].w * f;
+                for (int k = 0; k < kCols / 4; k++) {
+                    float *x = o[k / 4] + k % 4 * 4;
+                    x[0] += v[n][k].x * f, x[1] += v[n][k].y * f, x[2] += v[n][k].z * f, x[3] += v[n][k].w * f;
+                }
             }
             M = m1, W = w1;
         }
-        emit(a, job.seq, job.h, row, i, o, M, W, L);
+        const float by = row_factor(M, W, L);
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out.p) + row_at(a, a.out, job.seq, job.h, row) + i);
+#pragma unroll
+        for (int k = 0; k < kCols; k += 8) {
+            const float *x = o[k / 16] + k % 16;
+            if (i + k < int(cols))
+                out[k / 8] = L == 0.0f ? make_uint4(0, 0, 0, 0) : make_uint4(pack_out(a, x[0] * by, x[1] * by), pack_out(a, x[2] * by, x[3] * by),
+                                                                             pack_out(a, x[4] * by, x[5] * by), pack_out(a, x[6] * by, x[7] * by));
+        }
+        if (a.lse && i == 0) *lse_at(a, job.seq, job.h, row) = row_lse(M, L);
     }
 }
 
@@ -816,7 +835,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                 sm.last = last;
             }
             if (!rows_meet(&sm.bars.rows, met++, a.limit)) return false;
-            if (*reinterpret_cast<volatile int *>(&sm.last)) join<DP>(a, job);
+            if (*reinterpret_cast<volatile int *>(&sm.last)) join_rows<DP, 32, 2>(a, job);
         }
         __syncwarp();
         if (lane == 0) job_done(sm, k);
