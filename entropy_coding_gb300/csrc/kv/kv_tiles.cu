@@ -771,7 +771,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
             const bool poison = job.n && *reinterpret_cast<volatile int *>(&sm.poison);
             const int64_t to = mine ? row_at(a, a.out, job.seq, job.h, row) : kNoRow;
             uint8_t *stage = sm.out[r / 32];
-#pragma unroll 1
+#pragma unroll
             for (int i = 0; i < DP; i += 32) {
                 float o[32];
                 if (job.n) {
