@@ -591,7 +591,7 @@ template <int DP> __device__ __forceinline__ float ready_query(const AttendArgs 
     float c = fabsf(a.scale_log2), up = 1.0f;
     if (a.dtype == ZC_BF16) {
         __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < DP / 8; i++) {
             const uint4 v = *reinterpret_cast<const uint4 *>(sm.q[half] + panel_at(r % kTile, i));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
