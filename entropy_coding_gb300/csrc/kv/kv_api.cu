@@ -154,14 +154,14 @@ namespace {
 
 // Which kernels a batch needs. A sequence's rows of a head are its new tokens times the group. Up to 16 of them the
 // cache's bytes are what counts, and the kernel that streams them does the work; more rows fill the tensor cores'
-// 128-row tiles. (16 sequences of up to 8000 keys: 16 rows 66 us there and 87 us on tiles; 20 or 32 rows, two passes
-// over the bytes, 94 and 95 us there and 87 us on tiles.)
+// 128-row tiles. (16 sequences of up to 8000 keys: 16 rows 66 us there and 78 us on tiles; 20 or 32 rows, two passes
+// over the bytes, 94 and 95 us there and 78 us on tiles.)
 // A batch of prompts (more than a tile's rows) among single tokens runs both, each on its own sequences: a prompt of 400
-// tokens among 47 single ones takes 141 us so and 204 us on tiles alone. The host does not know how many sequences are of
+// tokens among 47 single ones takes 134 us so and 185 us on tiles alone. The host does not know how many sequences are of
 // which kind: where they have a tile's rows on average, or are no more than 8, the few single tokens are not worth a
-// second launch (24 sequences, two of them single tokens: 68 us with both, 56 us on tiles), nor are drafts of uneven
-// length (66 and 36 us). Of such a batch only sequences of up to 8 rows are streamed, where a single token has no more:
-// room for 16 rows costs the streaming 1.35 times the time (168 us for that batch).
+// second launch (24 sequences, two of them single tokens: 63 us with both, 54 us on tiles), nor are drafts of uneven
+// length (16 sequences of 2 to 5 tokens: 29 and 25 us). Of such a batch only sequences of up to 8 rows are streamed, where a single token has no more:
+// room for 16 rows costs the streaming 1.35 times the time.
 struct Plan {
     bool rows, tiles;
     uint32_t rows_most;

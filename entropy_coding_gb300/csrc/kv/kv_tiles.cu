@@ -32,15 +32,20 @@
 // cores.
 //
 // Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads
-// of 128, causal) in 482 us, 1.14 PFLOP/s, 0.61 of the measured bfloat16 rate;
-// 912 tokens of two sequences over 28384 keys in 201 us (1.06 PFLOP/s). The
-// tensor cores are busy half of the time. A key tile takes 1.7 us where its
-// products take 1.05: a row tile's chain of scores, weights (about 1.2 us: 128
-// exponentials a thread on a unit shared by two warps, and the conversions'
-// instructions beside them) and its own products is longer than the other
-// tile's products cover, and the products of queries and keys read shared
-// memory at its full rate, so that the conversion's reads and writes wait for
-// them. An item's beginning and end take about 8 us.
+// of 128, causal) in 452 us, 1.21 PFLOP/s, 0.65 of the measured bfloat16 rate;
+// 912 tokens of two sequences over 28384 keys in 186 us (1.14 PFLOP/s). The
+// tensor cores are busy half of the time. A key tile takes 1.65 us where its
+// products take 1.05: a row tile's chain of scores, weights (about 1.1 us: two
+// passes over the scores, 128 exponentials a thread on a unit shared by two
+// warps, and the conversions' instructions beside them) and its own products is
+// longer than the other tile's products cover. The weights stand where the
+// scores were, so that the next scores wait for these sums: columns for both do
+// not fit. Shared memory is the next limit: by its rate the products take 1536
+// clocks of it a key tile, the conversion 768, the copies 256. An item's
+// beginning and end take about 7 us (queries 1.6, output 3, the first scores and
+// the last sums with nothing beside them), joining a cut item 10: 32 columns and
+// 2 parts at a time, read whether they are there or not (16 columns, 4 parts and
+// predicated reads: 25 us).
 #include <atomic>
 
 #include "kv_attend.cuh"
@@ -54,8 +59,9 @@ constexpr int kTile = 128;              // rows of a tile, keys of a key tile
 constexpr int kRows = 2 * kTile;        // rows of an item
 constexpr int kBoxes = kTile / 16;      // boxes of a code tile
 constexpr int kRaw = 3, kOps = 3;       // rings of code tiles and operand tiles (keys and values in turn)
-// Units of work of an item besides its key tiles: its beginning and end. (An 8192-token prompt: 0 units 1185 us, 2 units
-// 662, 3 units 560, 4 units 484, 8 units 491: with fewer, the CTAs with many short items are last.)
+// Units of work of an item besides its key tiles: its beginning and end. (An 8192-token prompt: 0 units 895 us, 2 units
+// 590, 3 units 491, 4 units 453, 5 units 457; mixed lengths 68, 56, 52, 54 and 58: with fewer, the CTAs with many short
+// items are last.)
 constexpr uint32_t kFixed = 4;
 constexpr int kJobs = 4;                // pieces of work that are known ahead
 constexpr int kReaders = 8 + 4 + 1 + 1; // warps (and the products' thread) that read them
@@ -490,7 +496,7 @@ __device__ __noinline__ uint32_t poisoned(const AttendArgs &a, const Job &job, i
 template <int DP, int kCols, int kRun> __device__ __noinline__ void join_rows(const AttendArgs &a, const Job &job) {
     const Part<DP> *parts = static_cast<const Part<DP> *>(a.parts);
     const uint32_t c0 = job.c0, c1 = job.c1;
-    // 16 columns of a row at a time, whichever rows there are
+    // kCols columns of a row at a time, whichever rows there are
     const uint32_t rows = min(uint32_t(kRows), job.seq.n * a.group - job.tile * kRows), cols = a.c.dim;
 #pragma unroll 1
     for (uint32_t u = threadIdx.x; u < rows * ((cols + kCols - 1) / kCols); u += 256) {
@@ -771,6 +777,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
             const bool poison = job.n && *reinterpret_cast<volatile int *>(&sm.poison);
             const int64_t to = mine ? row_at(a, a.out, job.seq, job.h, row) : kNoRow;
             uint8_t *stage = sm.out[r / 32];
+            // (all columns in flight: an 8192-token prompt in 452 us, 32 at a time in 476)
 #pragma unroll
             for (int i = 0; i < DP; i += 32) {
                 float o[32];
