@@ -34,7 +34,7 @@
 // Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads
 // of 128, causal) in 452 us, 1.21 PFLOP/s, 0.65 of the measured bfloat16 rate;
 // 912 tokens of two sequences over 28384 keys in 186 us (1.14 PFLOP/s). The
-// tensor cores are busy half of the time. A key tile takes 1.65 us where its
+// tensor cores are busy half of the time. A key tile takes 1.7 us where its
 // products take 1.05: a row tile's chain of scores, weights (about 1.1 us: two
 // passes over the scores, 128 exponentials a thread on a unit shared by two
 // warps, and the conversions' instructions beside them) and its own products is
