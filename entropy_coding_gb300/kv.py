@@ -72,6 +72,16 @@ def _entries():
     return _entry
 
 
+def _outer(t: torch.Tensor, least: int, what: str) -> int:
+    """Distance between a tensor's outermost slices, each of ``least`` elements. A single slice has none of its own;
+    slices that overlap (an expanded tensor) are refused, since the kernels step from one to the next."""
+    if t.shape[0] <= 1:
+        return least
+    if t.stride(0) < least:
+        _fail(f"{what} overlap: stride {t.stride(0)} for {least} elements")
+    return t.stride(0)
+
+
 class KVCache:
     """A pool of cache blocks, over tensors that the caller owns.
 
@@ -94,6 +104,7 @@ class KVCache:
                 _fail("KVCache: scales are float32 [n_blocks, kv_heads]")
         if k_scale.stride() != v_scale.stride():
             _fail("KVCache: k_scale and v_scale have the same strides")
+        block_stride, scale_stride = _outer(k, h * b * d, "KVCache: blocks"), _outer(k_scale, h, "KVCache: scales of blocks")
         if not all(t.is_cuda and t.device == k.device for t in (k, v, k_scale, v_scale)):
             _fail("KVCache expects CUDA tensors of one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
@@ -101,7 +112,7 @@ class KVCache:
         self.device, self._index = k.device, k.device.index
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                         max(k.stride(0), h * b * d), max(k_scale.stride(0), h), n, h, b, d)
+                         block_stride, scale_stride, n, h, b, d)
         self._ref = ctypes.addressof(self._c)
         self._status = self.status.data_ptr()
 
@@ -148,7 +159,7 @@ class KVBatch:
             _fail("KVBatch: max_tokens <= total_tokens <= max_tokens * n_seqs")
         self.block_table, self.cu_tokens, self.lens = block_table, cu_tokens, lens
         self.n_seqs, self.total_tokens, self.max_tokens = n, total_tokens, max_tokens
-        self._c = _Batch(block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]) if n else 0,
+        self._c = _Batch(block_table.data_ptr(), _outer(block_table, block_table.shape[1], "KVBatch: rows of the table"),
                          cu_tokens.data_ptr(), lens.data_ptr(), n, total_tokens, max_tokens, block_table.shape[1])
         self._ref = ctypes.addressof(self._c)
         self._ws: dict = {}
