@@ -35,7 +35,8 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    headers = (glob.glob(os.path.join(CSRC, "**", e), recursive=True) for e in ("*.cuh", "*.h"))
+    return _sources() + sum(headers, []) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def needs_build() -> bool:

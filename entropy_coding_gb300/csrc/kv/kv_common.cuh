@@ -14,6 +14,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "kv_slots.h"
 #include "zc.h"  // from include/ (on the -I path)
 
 namespace zc {
@@ -109,7 +110,7 @@ struct Seq {
 };
 
 // Reads and checks sequence s; every thread that asks gets the same answer.
-// `need_table`: whether the tokens' blocks are looked up.
+// `speak`: what is wrong is reported.
 __device__ __forceinline__ Seq read_seq(const Batch &b, uint32_t s, int32_t *d_status, uint32_t block_tokens, bool speak) {
     const int32_t c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1);
     Seq q;
@@ -117,7 +118,7 @@ __device__ __forceinline__ Seq read_seq(const Batch &b, uint32_t s, int32_t *d_s
     q.first = uint32_t(c0);
     q.n = uint32_t(c1 - c0);
     q.len = __ldg(b.lens + s);
-    q.ok = c0 >= 0 && c1 >= c0 && uint32_t(c1) <= b.total && uint32_t(c1 - c0) <= b.most && q.len >= 0 && q.len < (1 << 30);
+    q.ok = counts_ok(c0, c1, q.len, b.total, b.most);
     if (!q.ok && speak) report(d_status, ZC_EFORMAT);
     if (q.ok && uint64_t(q.len) > uint64_t(b.width) * block_tokens) {
         if (speak) report(d_status, ZC_ECAPACITY);
@@ -126,23 +127,22 @@ __device__ __forceinline__ Seq read_seq(const Batch &b, uint32_t s, int32_t *d_s
     return q;
 }
 
-// Work of a ragged batch without a host copy of its lengths. Sequence s takes
-// the slots from f(s) = floor(cu[s] * per / unit) + extra * s on; f(s + 1) -
-// f(s) >= ceil(n * per / unit) + extra - 1, so extra = 1 gives every run of n
-// tokens its ceil(n * per / unit) tiles, and extra = 2 the blocks of a run
-// that may start inside one. The launch covers f(n_seqs) slots. The CTA
-// counts the f(s) at or below its slot: one round of loads for any batch up
-// to the CTA's size, where a binary search would take one dependent load for
-// each halving.
-// (tokens * per < 2^31 and sequences < 2^24: the entry points see to it)
-__host__ __device__ inline uint32_t slot_of(uint32_t tokens, uint32_t s, uint32_t per, uint32_t unit, uint32_t extra) {
-    return tokens * per / unit + extra * s;
+__device__ __forceinline__ uint32_t tokens_before(const Batch &b, uint32_t s) { return clamp_count(__ldg(b.cu + s), b.total); }
+
+// Looks at every sequence of the batch, with threads first, first + step, ... of one CTA of a launch: the slots of a
+// batch whose counts fall need not lead to the sequence that is to be reported. `held`: its new tokens have to be
+// among the sequence's.
+__device__ __forceinline__ void report_batch(const Batch &b, uint32_t block_tokens, int32_t *d_status, uint32_t first, uint32_t step, bool held) {
+    for (uint32_t s = first; s < b.n_seqs; s += step) {
+        const Seq q = read_seq(b, s, d_status, block_tokens, true);
+        if (held && q.ok && uint32_t(q.len) < q.n) report(d_status, ZC_EFORMAT);
+    }
 }
 
-__device__ __forceinline__ uint32_t tokens_before(const Batch &b, uint32_t s) { return uint32_t(min(max(__ldg(b.cu + s), 0), int(b.total))); }
-
 // The sequence of slot u (the whole CTA calls this); `at`: the slot's index
-// within the sequence.
+// within the sequence, or kNoSlot. The CTA counts the f(s) at or below its
+// slot: one round of loads for any batch up to the CTA's size, where a binary
+// search would take one dependent load for each halving.
 __device__ __forceinline__ uint32_t find_seq(const Batch &b, uint32_t u, uint32_t per, uint32_t unit, uint32_t extra, uint32_t &at) {
     uint32_t below = 0;
     for (uint32_t s0 = 0; s0 < b.n_seqs; s0 += blockDim.x) {
@@ -154,7 +154,7 @@ __device__ __forceinline__ uint32_t find_seq(const Batch &b, uint32_t u, uint32_
         if (n < blockDim.x) break;  // f grows with s
     }
     const uint32_t s = below ? below - 1 : 0;
-    at = u - slot_of(tokens_before(b, s), s, per, unit, extra);
+    at = slot_within(u, slot_of(tokens_before(b, s), s, per, unit, extra), slot_of(tokens_before(b, s + 1), s + 1, per, unit, extra));
     return s;
 }
 

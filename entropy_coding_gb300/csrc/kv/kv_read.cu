@@ -30,15 +30,11 @@ template <int DT> __device__ __forceinline__ void store16(void *p, const float (
     }
 }
 
-template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ MoveArgs a) {
+template <int DT> __device__ __forceinline__ void read_tokens(const MoveArgs &a) {
     uint32_t at;
     const uint32_t s = find_seq(a.b, blockIdx.x, 1, kTokens, 1, at);
-    const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, threadIdx.x == 0 && at == 0);
-    if (!q.ok || q.n == 0) return;
-    if (uint32_t(q.len) < q.n) {
-        if (threadIdx.x == 0 && at == 0) report(a.d_status, ZC_EFORMAT);
-        return;
-    }
+    const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, false);
+    if (at == kNoSlot || !q.ok || q.n == 0 || uint32_t(q.len) < q.n) return;
     const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y;
     const uint32_t per_row = D / 16, t0 = at * kTokens, n = min(uint32_t(kTokens), q.n - min(q.n, t0)) * per_row;
     const uint32_t pos0 = uint32_t(q.len) - q.n + t0;
@@ -81,6 +77,11 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(const 
                             (int64_t(q.first + t0 + row) * a.x[kv].token + int64_t(h) * a.x[kv].head + (i - row * per_row) * 16) * elt, x);
         }
     }
+}
+
+template <int DT> __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ MoveArgs a) {
+    read_tokens<DT>(a);
+    if (blockIdx.x == 0 && blockIdx.y == 0) report_batch(a.b, a.c.tokens, a.d_status, threadIdx.x, kThreads, true);
 }
 
 } // namespace

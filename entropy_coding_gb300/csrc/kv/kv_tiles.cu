@@ -27,6 +27,7 @@
 //   warp 12          issues the products, as operands and weights come
 //   warp 13          copies: 8 boxes of 16 keys a code tile, by block table
 //   warp 14          one thread finds the CTA's pieces of work ahead of the others
+//   warp 15          the first CTA's looks over the batch's counts and lengths
 // While one tile's rows turn scores into weights, the other tile's products
 // run: 4 products of 128 x 128 x 128 a key tile, 2048 clocks of the tensor
 // cores.
@@ -199,7 +200,7 @@ __device__ __forceinline__ void add2(float &x, float &y, float a, float b) {  //
 // 0 if it is empty or not this kernel's.
 __device__ __forceinline__ uint32_t units_of(const AttendArgs &a, const Seq &seq, uint32_t tile, Job &job) {
     const uint32_t n_rows = seq.n * a.group, row0 = tile * kRows;
-    if (!seq.ok || n_rows <= a.rows_most || row0 >= n_rows) return 0;
+    if (!seq.ok || n_rows <= a.rows_most || tile > (n_rows - 1) / kRows) return 0;
     job.seq = seq;
     job.tile = tile;
     bounds(a, seq, row0, job.all_lo, job.x_hi);
@@ -223,13 +224,15 @@ __device__ __forceinline__ uint32_t seq_of_slot(const AttendArgs &a, uint32_t u)
     return lo;
 }
 
-// Where the CTA has got to on the line.
+// Where the CTA has got to on the line. Where the counts fall, the slots that the walk passes need not be those that
+// the line's length was taken from (a sequence is looked up by halving there): it ends with the slots and with the line.
 struct Walk {
     uint64_t w, w1, i0;   // next work; the end; where the item begins
     uint64_t W, G;        // all work; the CTAs that share it
     uint32_t slot, s, h;  // the item
+    uint32_t slots;       // of the batch
     __device__ __forceinline__ bool next(const AttendArgs &a, Job &job) {
-        while (w < w1) {
+        while (w < w1 && slot < slots) {
             const uint32_t units = units_of(a, read_seq(a.b, s, a.d_status, a.c.tokens, false), slot - first_slot(a, s), job);
             if (w >= i0 + units) {
                 i0 += units;
@@ -240,6 +243,7 @@ struct Walk {
                 continue;
             }
             const uint64_t first = i0 + kFixed, i1 = i0 + units, from = max(w, first), upto = min(w1, i1);
+            if (i1 > W) return false;
             w = upto;
             if (upto <= first) continue;  // the piece ends within the item's beginning, which belongs to the first tile's piece
             job.h = h;
@@ -858,23 +862,26 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 
     // The line of work, and this CTA's piece of it.
     const uint32_t slots = slot_of(a.b.total, a.b.n_seqs, a.group, kRows, 1);
-    auto work_at = [&](uint32_t u, uint32_t &s, uint32_t &units, bool speak) -> uint64_t {
+    auto work_at = [&](uint32_t u, uint32_t &s, uint32_t &units) -> uint64_t {
         Job job;
         s = seq_of_slot(a, u);
-        units = units_of(a, read_seq(a.b, s, a.d_status, a.c.tokens, speak), u - first_slot(a, s), job);
+        units = units_of(a, read_seq(a.b, s, a.d_status, a.c.tokens, false), u - first_slot(a, s), job);
         return uint64_t(units) * a.c.heads;
     };
     uint64_t mine = 0, sum, W;
     uint32_t s = 0, units = 0;
-    for (uint32_t u = threadIdx.x; u < slots; u += kThreads) mine += work_at(u, s, units, cta == 0);
+    for (uint32_t u = threadIdx.x; u < slots; u += kThreads) mine += work_at(u, s, units);
     sum = block_scan<kWarps>(mine, sm.sums, W);
     const uint64_t G = min(uint64_t(gridDim.x), W);  // no CTA between two that have work is without
-    if (cta >= G) return;
+    if (cta >= G) {
+        if (cta == 0) report_batch(a.b, a.c.tokens, a.d_status, threadIdx.x, kThreads, false);
+        return;
+    }
     const uint64_t w0 = W * cta / G, w1 = W * (cta + 1) / G;
     uint64_t before = 0;
     for (uint32_t u0 = 0; u0 < slots; u0 += kThreads) {
         if (slots > kThreads) {  // more than one round: the sums above were not of single slots
-            mine = u0 + threadIdx.x < slots ? work_at(u0 + threadIdx.x, s, units, false) : 0;
+            mine = u0 + threadIdx.x < slots ? work_at(u0 + threadIdx.x, s, units) : 0;
             uint64_t all;
             sum = before + block_scan<kWarps>(mine, sm.sums, all);
             before += all;
@@ -919,7 +926,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         fewer_registers<kOtherRegs>();
         if (warp == 12) ok = product_role<DP>(sm, a.limit);
         if (warp == 13) ok = copy_role<DP>(a, maps, sm);
-        if (warp == 14 && threadIdx.x % 32 == 0) ok = find_role<DP>(a, sm, Walk{w0, w1, sm.i0, W, G, sm.slot, sm.seq, sm.h});
+        if (warp == 14 && threadIdx.x % 32 == 0) ok = find_role<DP>(a, sm, Walk{w0, w1, sm.i0, W, G, sm.slot, sm.seq, sm.h, slots});
+        if (warp == 15 && cta == 0) report_batch(a.b, a.c.tokens, a.d_status, threadIdx.x % 32, 32, false);
     }
     if (!ok) report(a.d_status, ZC_ETIMEOUT);
     asm volatile("cp.async.wait_all;" ::: "memory");

@@ -87,22 +87,15 @@ __device__ __forceinline__ float two_to(int field) {  // 2^(field - 127), fields
     return __uint_as_float(uint32_t(min(max(field, 1), 254)) << 23);
 }
 
-template <int DT, int kThreads> __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ MoveArgs a) {
-    __shared__ uint32_t s_max;
+template <int DT, int kThreads> __device__ __forceinline__ void write_block(const MoveArgs &a, uint32_t &s_max) {
     uint32_t at;
     const uint32_t s = find_seq(a.b, blockIdx.x, 1, a.c.tokens, 2, at);
-    const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, threadIdx.x == 0 && at == 0);
-    if (!q.ok || q.n == 0) return;
+    const Seq q = read_seq(a.b, s, a.d_status, a.c.tokens, false);
+    if (at == kNoSlot || !q.ok || q.n == 0 || uint32_t(q.len) < q.n) return;
     const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y, kvi = blockIdx.z;
-    if (uint32_t(q.len) < q.n) {  // more new tokens than the sequence has
-        if (threadIdx.x == 0 && at == 0) report(a.d_status, ZC_EFORMAT);
-        return;
-    }
-    const uint32_t start = uint32_t(q.len) - q.n;
-    const uint32_t blk = start / B + at;
-    if (uint64_t(blk) * B >= uint64_t(q.len)) return;
-    const uint32_t lo = max(start, blk * B), hi = min(uint32_t(q.len), (blk + 1) * B);
-    const uint32_t n0 = lo - blk * B, rows = hi - lo;
+    Span span;
+    if (!block_span(uint32_t(q.len), q.n, B, at, span)) return;
+    const uint32_t start = uint32_t(q.len) - q.n, blk = span.blk, lo = span.lo, n0 = lo - blk * B, rows = span.hi - lo;
     const int elt = DT == ZC_FP32 ? 4 : 2;
     const uint8_t *x = static_cast<const uint8_t *>(a.x[kvi].p) +
                        ((int64_t(q.first) + (lo - start)) * a.x[kvi].token + int64_t(h) * a.x[kvi].head) * elt;
@@ -170,6 +163,12 @@ template <int DT, int kThreads> __global__ void __launch_bounds__(kThreads) writ
         e.load(piece_of(i));
         to[i] = e.codes(inv);
     }
+}
+
+template <int DT, int kThreads> __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ MoveArgs a) {
+    __shared__ uint32_t s_max;
+    write_block<DT, kThreads>(a, s_max);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) report_batch(a.b, a.c.tokens, a.d_status, threadIdx.x, kThreads, true);
 }
 
 // Threads by the pieces of a block that a call may write: as few as hold them. (Blocks of 160 pieces take 8 us with 64

@@ -399,7 +399,8 @@ typedef struct {
  * A call skips a sequence whose entries are out of these ranges (ZC_EFORMAT;
  * a length beyond the table: ZC_ECAPACITY), and takes a table entry that
  * names no block as a block that is not there (ZC_EFORMAT): it is not read or
- * written, and outputs that need it are unspecified. */
+ * written, and outputs that need it are unspecified. Where cu falls, a call may
+ * skip other sequences too. */
 typedef struct {
     const int32_t *d_table;
     int64_t table_stride;

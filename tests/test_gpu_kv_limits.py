@@ -44,3 +44,73 @@ def test_an_expanded_block_table_is_refused():
     one = zc.KVBatch(row.expand(1, 6), cu[:2], lens[:1], 1, 1)  # a single row is no overlap
     assert torch.allclose(zc.kv_attend(cache, one, q[:1])[0], out[:1], atol=2 ** -8)
     cache.check()
+
+
+FALLING = [  # cu, lens: every pair but one or a few may be a sequence's
+    ([0, 100, 110, 3, 200], [100, 210, 50, 197]),
+    ([0, 100, 101, 102, 103, 5, 6, 7, 8], [300, 301, 302, 303, 100, 150, 151, 152]),
+    ([0, 40, 90, 20, 25, 30, 35, 10, 15, 200], [200] * 9),
+    ([60, 10, 70, 20, 80, 30, 90], [100] * 6),
+]
+
+
+@pytest.mark.parametrize("cu,lens", FALLING)
+def test_counts_that_fall_are_reported_and_nothing_else_is_touched(cu, lens):
+    """Blocks and scales that belong to no sequence keep their bytes, numbers around the outputs theirs."""
+    n, width, total = len(lens), 20, 200
+    g = torch.Generator(device=DEV).manual_seed(1)
+    cache = _cache(n * width + 40, 2, 64, 16)
+    table = torch.arange(20, 20 + n * width, dtype=torch.int32, device=DEV).view(n, width)
+    batch = zc.KVBatch(table, _i32(cu), _i32(lens), total, total)
+    before = [t.view(torch.uint8).clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    x = torch.randn(total, 2, 64, generator=g, device=DEV).half()
+    q = torch.randn(total, 8, 64, generator=g, device=DEV).half()
+
+    def attend():
+        out = torch.full((total + 200, 8, 64), 3.0, dtype=torch.float16, device=DEV)
+        lse = torch.full((total + 200, 8), 3.0, device=DEV)
+        zc.kv_attend_into(cache, batch, q, out[100:-100], lse[100:-100])
+        assert all((t[:100] == 3.0).all() and (t[-100:] == 3.0).all() for t in (out, lse))
+
+    def read():
+        k = torch.full((2, total + 200, 2, 64), 3.0, dtype=torch.float16, device=DEV)
+        zc.kv_read_into(cache, batch, k[0, 100:-100], k[1, 100:-100])
+        assert (k[:, :100] == 3.0).all() and (k[:, -100:] == 3.0).all()
+
+    def write():
+        zc.kv_write(cache, batch, x, x)
+        for was, t in zip(before, (cache.k, cache.v, cache.k_scale, cache.v_scale)):
+            now = t.view(torch.uint8)
+            assert torch.equal(was[:20], now[:20]) and torch.equal(was[20 + n * width:], now[20 + n * width:])
+
+    for call in (attend, read, write):
+        call()
+        with pytest.raises(zc.ZcError) as e:
+            cache.check()
+        assert e.value.status == zc.EFORMAT, call.__name__
+
+
+def test_a_batch_whose_tokens_begin_inside_the_tensors():
+    """cu that does not begin at 0: the rows before it are nobody's, and are left alone."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    lens, news, past = [1000, 37, 64], [3, 37, 1], 200
+    table = torch.arange(3 * 63, dtype=torch.int32, device=DEV).view(3, 63)
+    total = past + sum(news)
+    x = torch.randn(total, 2, 64, generator=g, device=DEV).half()
+    q = torch.randn(total, 4, 64, generator=g, device=DEV).half()
+    caches = [_cache(3 * 63, 2, 64, 16) for _ in range(2)]
+    got = []
+    for c, off in zip(caches, (0, past)):
+        cu = [off, off + 3, off + 40, off + 41]
+        b = zc.KVBatch(table, _i32(cu), _i32(lens), off + sum(news), max(max(news), (off + sum(news) + 2) // 3))
+        rows = slice(past - off, None)
+        zc.kv_write(c, b, x[rows], x[rows])
+        k = torch.full((2, off + 41, 2, 64), 3.0, dtype=torch.float16, device=DEV)
+        zc.kv_read_into(c, b, k[0], k[1])
+        out = torch.full((off + 41, 4, 64), 3.0, dtype=torch.float16, device=DEV)
+        zc.kv_attend_into(c, b, q[rows], out)
+        c.check()
+        assert (k[:, :off] == 3.0).all() and (out[:off] == 3.0).all()
+        got.append((k[:, off:], out[off:]))
+    assert torch.equal(caches[0].k.view(torch.uint8), caches[1].k.view(torch.uint8)) and torch.equal(caches[0].k_scale, caches[1].k_scale)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
