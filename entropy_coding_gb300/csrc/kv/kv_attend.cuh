@@ -8,7 +8,16 @@ namespace zc {
 namespace kv {
 
 constexpr float kNone = -INFINITY;
-constexpr float kSlack = 8.0f;  // how far (log2) the running maxima may lag behind
+// How far (log2) the running maxima may lag behind: of the scores, and of the contributions.
+constexpr float kSlack = 8.0f, kSlackW = 6.0f;
+// The unit of the largest contribution stands for 2^kRaise in half: a weight of up to 2^(kRaise + kSlackW) = 2^15 is
+// finite there, one above 2^-23 of the unit keeps half's 11 bits, and what a smaller one loses is below 2^-34 of the unit.
+// That matters where one key has nearly all of a row's weight and a small value: the others' weights are the output then,
+// and over 2^17 keys each of them is 2^-24 of the unit if they share a hundredth of the weight. (Following contributions
+// more closely leaves room for a higher unit and costs rescalings: 16 sequences of 2 to 5 tokens take 24.8, 25.5 and 26.4
+// us at 2^8 and 2^7, 2^6 and 2^9, 2^4 and 2^11, an 8192-token prompt 452, 454 and 456.)
+constexpr float kRaise = 9.0f;
+static_assert(kRaise + kSlackW <= 15.0f, "weights that half does not hold");
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -75,9 +84,14 @@ __device__ __forceinline__ uint32_t pack_out(const AttendArgs &a, float x, float
     return a.dtype == ZC_BF16 ? pack2<ZC_BF16>(x, y) : pack2<ZC_FP16>(x, y);
 }
 
-// A finished row is its sum (in units of 2^W) by this factor: out = x / L in the units of M. A row that sees no key
-// is 0, whatever x holds. (L is NaN where a score was.)
-__device__ __forceinline__ float row_factor(float M, float W, float L) { return (W == kNone ? 0.0f : ex2(W - M)) / L; }
+// A finished row is its sum (in units of 2^(W - kRaise)) by this factor: out = x / L in the units of M. A row that sees no
+// key is 0, whatever x holds. (L is NaN where a score was. The power in two halves: neither leaves float's range where
+// value scales are near its ends.)
+__device__ __forceinline__ float row_factor(float M, float W, float L) {
+    if (W == kNone) return 0.0f / L;
+    const float half = 0.5f * (W - M - kRaise), x = ex2(half);
+    return x * (x / L);
+}
 __device__ __forceinline__ float row_lse(float M, float L) { return L == 0.0f ? kNone : (M + log2f(L)) * 0.6931471805599453f; }
 
 // n columns (a multiple of 4) of a finished row from `col` on.

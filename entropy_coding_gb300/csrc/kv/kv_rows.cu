@@ -23,10 +23,11 @@
 // query row is exact in half too after it is multiplied by a power of two that
 // brings its largest element to [2^14, 2^15) (what falls below 2^-24 then is
 // 2^-38 of it). A row's weights w are rounded to half; they are kept in units
-// of the row's running maximum of s + log2 vs (to a factor of 2^8), not of s
-// alone, so that the largest contribution to the output is never below 1 and
-// blocks whose scales differ by any factor keep their precision. The sum of the weights is taken
-// before that rounding, in units of the running maximum of s.
+// of the row's running maximum of s + log2 vs (to a factor of 2^6), not of s
+// alone, so that blocks whose scales differ by any factor keep their precision,
+// and 2^9 above that unit: half keeps its 11 bits down to 2^-23 of the largest
+// w vs. The sum of the weights is taken before that rounding, in units of the
+// running maximum of s.
 //
 // Each warp streams its own keys and values through a ring of slices of 16
 // rows in shared memory: one lane asks for two boxes a slice, and the warps
@@ -342,8 +343,8 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
                         if (key0 + g + 8 * j < lo || key0 + g + 8 * j >= hi) sc[n][2 * j + e] = kNone;
                 }
         }
-        // m and mw follow the maxima only once these are 2^kSlack above them: weights stay below 2^kSlack, which
-        // half holds as precisely, and after the first step a rescaling is rare.
+        // m and mw follow the maxima only once these are 2^kSlack and 2^kSlackW above them: after the first step a
+        // rescaling is rare.
         const float lvs = __log2f(vs);
         bool grows = false;
 #pragma unroll
@@ -351,7 +352,7 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const float top = fmaxf(sc[n][e], sc[n][2 + e]);
-                grows |= top > m[n][e] + kSlack || top + lvs > mw[n][e] + kSlack;
+                grows |= top > m[n][e] + kSlack || top + lvs > mw[n][e] + kSlackW;
             }
         if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
@@ -373,14 +374,15 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
                     o[n][c][0] *= down[0], o[n][c][1] *= down[1], o[n][c][2] *= down[0], o[n][c][3] *= down[1];
             }
         }
-        // Weights p = 2^(s - m), and in the output's units p * 2^(m + log2 vs - mw).
+        // Weights p = 2^(s - m), and in the output's units p * 2^(m + log2 vs - mw + kRaise).
+        constexpr float kUp = float(1 << int(kRaise));
         uint32_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
             float w[4];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const float base = m[n][e] == kNone ? 0.0f : m[n][e], f = vs * unit[n][e];
+                const float base = m[n][e] == kNone ? 0.0f : m[n][e], f = vs * unit[n][e] * kUp;
                 const float p0 = ex2(sc[n][e] - base), p1 = ex2(sc[n][2 + e] - base);
                 l[n][e] += p0 + p1;
                 w[e] = p0 * f, w[2 + e] = p1 * f;

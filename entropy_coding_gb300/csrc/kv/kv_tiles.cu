@@ -6,14 +6,15 @@
 // tiles of 128 keys, with codes kc, vc and block scales ks, vs:
 //   S = Q Kc^T            128 x 128 x dim, half operands, float32 in tensor memory
 //   s_ij = S_ij ks_b c_i  (c_i: the row's power of two and the softmax scale, log2)
-//   w_ij = 2^(s_ij + log2 vs_b - mw_i), rounded to half, back into tensor memory
+//   w_ij = 2^(s_ij + log2 vs_b - mw_i + 9), rounded to half, back into tensor memory
 //   O += W Vc             128 x dim x 128
-//   l_i += sum_b (sum_{j in b} w_ij before rounding) 2^(mw_i - m_i - log2 vs_b)
+//   l_i += sum_b (sum_{j in b} w_ij before rounding) 2^(mw_i - 9 - m_i - log2 vs_b)
 // m_i and mw_i follow the row's maxima of s and of s + log2 vs (and may lag by
-// 2^8), so O is in units of the largest contribution and l in units of the
-// largest weight: block scales cost an exponent's bias for 16 columns, and no
-// spread between them loses precision. A block whose scale is 2^60 below the
-// unit adds less than 2^-51 of it and counts as 2^-60. out = O 2^(mw - m) / l.
+// 2^8 and 2^6), so O is in units of the largest contribution and l in units of
+// the largest weight: block scales cost an exponent's bias for 16 columns, and no
+// spread between them loses precision; half keeps its 11 bits down to 2^-23 of
+// the largest w vs. A block whose scale is 2^69 below the unit adds less than
+// 2^-60 of it and counts as 2^-69. out = O 2^(mw - 9 - m) / l.
 //
 // Work: as in kv_rows.cu, one line of key tiles over all items (an item's
 // beginning and end count as 4 tiles), an equal piece for each of one CTA an SM; items cut by a piece's end leave partial
@@ -712,8 +713,8 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                             topw = fmaxf(topw, g + lvs[4 * part + b]);
                         }
                     }
-                    // As in kv_rows.cu: the maxima are followed once they have grown by 2^kSlack.
-                    const bool grows = top > m + kSlack || topw > mw + kSlack;
+                    // As in kv_rows.cu: the maxima are followed once they have grown by 2^kSlack or 2^kSlackW.
+                    const bool grows = top > m + kSlack || topw > mw + kSlackW;
                     if (__any_sync(0xFFFFFFFFu, grows)) {
                         float down = 1.0f;
                         if (grows) {
@@ -744,7 +745,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<DP> &sm) {
                         if (part) scores64(1, x);
 #pragma unroll
                         for (int b = 0; b < 4; b++) {
-                            const float lf = fminf(fmaxf(lvs[4 * part + b] + (base - mw), -60.0f), 120.0f);  // (mw = -infinity: every vs is 0)
+                            const float lf = fminf(fmaxf(lvs[4 * part + b] + (base - mw + kRaise), -60.0f), 126.0f);  // (mw = -infinity: every vs is 0)
                             const float bias = lf - base;
                             float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll

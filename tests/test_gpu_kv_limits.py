@@ -2,6 +2,7 @@
 the ordinary tests do not reach."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -11,6 +12,8 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import entropy_coding_gb300 as zc  # noqa: E402
+
+from kv_reference import attend, to_codes  # noqa: E402
 
 DEV = torch.device("cuda:0")
 
@@ -114,3 +117,59 @@ def test_a_batch_whose_tokens_begin_inside_the_tensors():
         got.append((k[:, off:], out[off:]))
     assert torch.equal(caches[0].k.view(torch.uint8), caches[1].k.view(torch.uint8)) and torch.equal(caches[0].k_scale, caches[1].k_scale)
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("seqs,new,dim,at", [(1, 1, 128, 0), (600, 1, 128, 0), (600, 1, 64, 40000), (1, 40, 128, 0), (160, 40, 128, 0),
+                                             (160, 40, 64, 70000)])
+@pytest.mark.parametrize("keys,share", [(8192, 0.99), (131072, 0.99), (131072, 0.999)])
+def test_one_key_takes_nearly_all_of_the_weight_and_has_no_value(keys, share, seqs, new, dim, at, dtype):
+    """The other keys' weights are the output then, each of them down to 2^-27 of the largest. Their numbers differ at
+    random, as their roundings to half do: the output errs by no more than one such rounding, 2^-11 of what its values
+    sum to in magnitude, and twice that is allowed, with the scores' own errors (2^-17 of their products' magnitudes)
+    and the output's rounding to its type. Nothing in this grows with the keys. (The same tokens for many sequences: few of
+    them share the key that takes the weight out with a short piece of the others.)"""
+    rng = np.random.default_rng(keys + new + dim)
+    block, heads, at = 64, 4, min(at, keys // 2)
+    k, v = rng.standard_normal((keys, dim)) * dim ** -0.5, np.abs(rng.standard_normal((keys, dim)))
+    k[:, -1], k[at], v[at] = 0.0, 0.0, 0.0
+    k[at, -1] = 1.0
+    q = rng.standard_normal((new, heads, dim))
+    q[:, :, -1] = np.log(share / (1 - share) * keys * np.exp(0.5))
+    kc, vc = (to_codes(x).reshape(keys // block, 1, block, dim) for x in (k, v))
+    ones = np.ones((keys // block, 1), np.float32)
+    table = rng.permutation(keys // block).astype(np.int32).reshape(1, -1)
+    pool = [np.empty_like(c) for c in (kc, vc)]
+    for p, c in zip(pool, (kc, vc)):
+        p[table[0]] = c
+    cache = zc.KVCache(*(torch.from_numpy(p).to(DEV) for p in pool), torch.from_numpy(ones).to(DEV), torch.from_numpy(ones).to(DEV))
+    batch = zc.KVBatch(torch.from_numpy(table).to(DEV).repeat(seqs, 1), _i32(range(0, seqs * new + 1, new)), _i32([keys] * seqs),
+                       seqs * new, new)
+    qt = torch.from_numpy(q).to(DEV).to(dtype)
+    out, lse = zc.kv_attend(cache, batch, qt.repeat(seqs, 1, 1), scale=1.0)
+    cache.check()
+    want, z, mass, size, _, _ = attend(qt.double().cpu().numpy(), pool[0], ones, pool[1], ones, table, [0, new], [keys], 1.0, True, 0)
+    tol = mass * (2.0 ** -10 + 2.0 ** -16 * size)[..., None]
+    low, high = (torch.from_numpy(want + d).to(dtype).double().numpy() for d in (-tol, tol))
+    got = out.double().cpu().numpy().reshape(seqs, *want.shape)
+    assert ((got >= low) & (got <= high)).all(), np.abs(got / want - 1).max()
+    assert np.abs(lse.double().cpu().numpy().reshape(seqs, *z.shape) - z).max() < 2.0 ** -17 * size.max() + 2.0 ** -20 * np.abs(z).max()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("exponent", [-118, 119])
+def test_value_scales_near_the_ends_of_floats_range(exponent, new):
+    """Outputs of 2^-118 and of 2^119 are bfloat16 numbers; 2^(mw - m) alone need not be a float. Weights are rounded to 11
+    bits and the output to 8: 2^-8 of the values' magnitudes is allowed."""
+    rng = np.random.default_rng(3)
+    keys, dim, block = 512, 64, 16
+    kc, vc = (to_codes(x).reshape(keys // block, 1, block, dim) for x in (rng.standard_normal((keys, dim)) * 0.5, np.abs(rng.standard_normal((keys, dim)))))
+    ks, vs = np.ones((keys // block, 1), np.float32), np.full((keys // block, 1), 2.0 ** exponent, np.float32)
+    table = np.arange(keys // block, dtype=np.int32).reshape(1, -1)
+    cache = zc.KVCache(*(torch.from_numpy(np.array(a)).to(DEV) for a in (kc, vc, ks, vs)))
+    batch = zc.KVBatch(torch.from_numpy(table).to(DEV), _i32([0, new]), _i32([keys]), new, new)
+    q = torch.from_numpy(rng.standard_normal((new, 4, dim))).to(DEV).bfloat16()
+    out, _ = zc.kv_attend(cache, batch, q, scale=1.0)
+    cache.check()
+    want, _, mass, _, _, _ = attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, [0, new], [keys], 1.0, True, 0)
+    assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * mass).all()
