@@ -41,6 +41,7 @@ class _Rows(ctypes.Structure):
 
 _entry = None  # (zc_kv_write, zc_kv_read, zc_kv_attend) once the library is loaded
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _fail(what: str):
@@ -110,6 +111,7 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_blocks, self.kv_heads, self.block_tokens, self.head_dim = n, h, b, d
         self.device, self._index = k.device, k.device.index
+        self._many = torch.cuda.device_count() > 1
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                          block_stride, scale_stride, n, h, b, d)
@@ -149,8 +151,8 @@ class KVBatch:
     def __init__(self, block_table: torch.Tensor, cu_tokens: torch.Tensor, lens: torch.Tensor, total_tokens: int,
                  max_tokens: int):
         n = lens.numel()
-        if any(t.dtype != torch.int32 or not t.is_cuda for t in (block_table, cu_tokens, lens)):
-            _fail("KVBatch expects int32 CUDA tensors")
+        if any(t.dtype != torch.int32 or not t.is_cuda or t.device != lens.device for t in (block_table, cu_tokens, lens)):
+            _fail("KVBatch expects int32 CUDA tensors of one device")
         if block_table.dim() != 2 or block_table.shape[0] != n or cu_tokens.shape != (n + 1,) or lens.dim() != 1:
             _fail("KVBatch: block_table is [n_seqs, width], cu_tokens [n_seqs + 1], lens [n_seqs]")
         if (n and block_table.stride(1) != 1) or not cu_tokens.is_contiguous() or not lens.is_contiguous():
@@ -159,6 +161,7 @@ class KVBatch:
             _fail("KVBatch: max_tokens <= total_tokens <= max_tokens * n_seqs")
         self.block_table, self.cu_tokens, self.lens = block_table, cu_tokens, lens
         self.n_seqs, self.total_tokens, self.max_tokens = n, total_tokens, max_tokens
+        self.device, self._index = lens.device, lens.device.index
         self._c = _Batch(block_table.data_ptr(), _outer(block_table, block_table.shape[1], "KVBatch: rows of the table"),
                          cu_tokens.data_ptr(), lens.data_ptr(), n, total_tokens, max_tokens, block_table.shape[1])
         self._ref = ctypes.addressof(self._c)
@@ -201,6 +204,13 @@ def _on(stream, device):
     return torch.cuda.stream(s)
 
 
+def _elsewhere(cache: KVCache, batch: KVBatch, what: str) -> bool:
+    """Whether the cache's device is not the current one, on which an entry point launches."""
+    if batch._index != cache._index:
+        _fail(f"{what}: the batch is on another device than the cache")
+    return _current_device() != cache._index
+
+
 def _check(st: int, what: str) -> None:
     if st:
         from . import ZcError
@@ -208,6 +218,9 @@ def _check(st: int, what: str) -> None:
 
 
 def _move(fn, what, cache, batch, k, v, stream):
+    if cache._many and _elsewhere(cache, batch, what):
+        with torch.cuda.device(cache._index):
+            return _move(fn, what, cache, batch, k, v, stream)
     code = _CODE.get(k.dtype)
     if code is None or v.dtype != k.dtype:
         _fail(f"{what}: k and v are bfloat16, float16 or float32")
@@ -231,6 +244,9 @@ def kv_read_into(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tenso
 
 def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16, stream=None):
     """The batch's tokens as (k, v), [total_tokens, kv_heads, head_dim]."""
+    if cache._many and _elsewhere(cache, batch, "zc_kv_read"):
+        with torch.cuda.device(cache._index):
+            return kv_read(cache, batch, dtype, stream)
     code = _CODE.get(dtype)
     if code is None:
         _fail("zc_kv_read: bfloat16, float16 or float32")
@@ -249,6 +265,9 @@ def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16,
 
 
 def _attend(cache, batch, code, heads, q, out, lse, scale, causal, window, stream):
+    if cache._many and _elsewhere(cache, batch, "zc_kv_attend"):
+        with torch.cuda.device(cache._index):
+            return _attend(cache, batch, code, heads, q, out, lse, scale, causal, window, stream)
     if not 0 <= window <= 0x7FFFFFFF:
         _fail("zc_kv_attend: window >= 0")
     address, size, _ = batch.workspace(cache, heads, stream)

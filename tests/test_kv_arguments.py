@@ -1,6 +1,8 @@
 """Arguments of the 8-bit cache's Python layer that are checked before any pointer is taken; no GPU."""
 from __future__ import annotations
 
+import types
+
 import pytest
 import torch
 
@@ -33,3 +35,72 @@ def test_the_distance_of_slices():
     assert kv._outer(table[:1].expand(1, 6), 6, "rows") == 6 and kv._outer(table[:0], 6, "rows") == 6
     _refused("rows overlap", lambda: kv._outer(table[0].expand(64, 6), 6, "rows"))
     _refused("rows overlap", lambda: kv._outer(table.view(-1).as_strided((4, 6), (4, 1)), 6, "rows"))
+
+
+class _Device:
+    """torch.cuda.device, without a GPU."""
+    now = 0
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.was, _Device.now = _Device.now, self.index
+
+    def __exit__(self, *_):
+        _Device.now = self.was
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """The layer with fakes of the entry points and of two devices, the first of them current; the calls' devices."""
+    seen = []
+
+    def entry(*args):
+        seen.append(_Device.now)
+        return 0
+
+    monkeypatch.setattr(kv, "_entries", lambda: (entry, entry, entry))
+    monkeypatch.setattr(kv, "_current_device", lambda: _Device.now, raising=False)
+    monkeypatch.setattr(kv, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "device", _Device)
+    return seen
+
+
+def _on_device(index):
+    """A cache and a batch that say they are on that device (their tensors are the host's)."""
+    cache, batch = object.__new__(kv.KVCache), object.__new__(kv.KVBatch)
+    cache.__dict__.update(_many=True, kv_heads=2, head_dim=32, device=torch.device("cpu"), _index=index, _ref=0, _status=0)
+    batch.__dict__.update(total_tokens=3, _index=index, _ref=0)
+    batch.workspace = lambda cache, heads, stream=None: (0, 0, None)
+    return cache, batch
+
+
+def _calls(cache, batch):
+    x, q = torch.zeros(3, 2, 32).half(), torch.zeros(3, 4, 32).half()
+    yield lambda: zc.kv_write(cache, batch, x, x)
+    yield lambda: zc.kv_read_into(cache, batch, x, x)
+    yield lambda: zc.kv_read(cache, batch)
+    yield lambda: zc.kv_attend_into(cache, batch, q, q.clone())
+    yield lambda: zc.kv_attend(cache, batch, q)
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_a_call_runs_on_the_caches_device(two_devices, index):
+    for call in _calls(*_on_device(index)):
+        call()
+    assert two_devices == [index] * 5 and _Device.now == 0
+
+
+def test_a_batch_of_another_device_is_refused(two_devices):
+    for call in _calls(_on_device(1)[0], _on_device(0)[1]):
+        _refused("another device", call)
+    assert not two_devices
+
+
+def test_a_batch_on_two_devices_is_refused():
+    def t(index):  # as much of a tensor as is looked at before the refusal
+        return types.SimpleNamespace(dtype=torch.int32, is_cuda=True, device=torch.device("cuda", index), numel=lambda: 2)
+
+    for where in ((1, 0, 0), (0, 1, 0), (0, 0, 1)):
+        _refused("one device", lambda: zc.KVBatch(*map(t, where), 2, 1))
