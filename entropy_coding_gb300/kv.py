@@ -128,11 +128,13 @@ class KVCache:
 
     def check(self) -> None:
         """Raise ZcError if a call on this cache reported an error (and forget
-        it); synchronises."""
+        it). Waits for the device: for calls on every stream."""
         from . import ZcError
+        torch.cuda.synchronize(self.device)
         st = int(self.status.item())
         if st:
             self.status.zero_()
+            torch.cuda.synchronize(self.device)  # forgotten before any later call reports
             raise ZcError(st, "zc_kv (device)")
 
 

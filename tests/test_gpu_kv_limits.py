@@ -173,3 +173,26 @@ def test_value_scales_near_the_ends_of_floats_range(exponent, new):
     cache.check()
     want, _, mass, _, _, _ = attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, [0, new], [keys], 1.0, True, 0)
     assert (np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * mass).all()
+
+
+MS = 2_000_000  # clocks: a millisecond and more
+
+
+def _wrong(cache):
+    """A batch that names a block which the pool does not have."""
+    return zc.KVBatch(_i32([[cache.n_blocks]]), _i32([0, 1]), _i32([1]), 1, 1)
+
+
+def test_check_waits_for_calls_on_other_streams():
+    cache = _cache(4, 2, 64, 16)
+    bad, side = _wrong(cache), torch.cuda.Stream()
+    x = torch.zeros(1, 2, 64, device=DEV).half()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100 * MS)
+        zc.kv_write(cache, bad, x, x, stream=side)
+        with pytest.raises(zc.ZcError) as e:
+            cache.check()
+        assert e.value.status == zc.EFORMAT
+        cache.check()  # and has forgotten it
