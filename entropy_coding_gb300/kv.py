@@ -4,9 +4,11 @@ The cache is a pool of blocks of tokens; each block and key/value head has
 E4M3 codes and one float32 scale, for K and for V. A batch names sequences of
 uneven length by a block table and their lengths, all on the device. The
 operators run in the CUDA kernels of ``libzc.so`` (include/zc.h, zc_kv_*),
-launch on the current stream (or ``stream``) and do not synchronise; errors
-that only the device can see are OR-ed into the cache's status, which
-``KVCache.check`` reads.
+launch on the current stream (or ``stream``, a torch stream or a handle) and
+do not synchronise; errors that only the device can see are OR-ed into the
+cache's status, which ``KVCache.check`` reads. Tensors that the caller gives,
+a cache's and a batch's among them, are ready on the stream of a call and
+outlive it there (``Tensor.record_stream``).
 """
 from __future__ import annotations
 
@@ -148,7 +150,8 @@ class KVBatch:
     ``total_tokens`` and ``max_tokens`` (of one sequence) are the host's
     numbers. The tensors may change between calls (a captured graph is
     replayed with new lengths) as long as the totals hold. The batch keeps
-    attention's workspace: calls that may overlap use batches of their own."""
+    attention's workspaces, one for each stream: a captured graph that may
+    overlap with other calls uses a batch of its own."""
 
     def __init__(self, block_table: torch.Tensor, cu_tokens: torch.Tensor, lens: torch.Tensor, total_tokens: int,
                  max_tokens: int):
@@ -170,9 +173,10 @@ class KVBatch:
         self._ws: dict = {}
 
     def workspace(self, cache: KVCache, heads: int, stream=None) -> tuple:
-        """(address, bytes) of the zeroed workspace for attention of this batch
-        over such a cache, made on the first call and kept."""
-        key = (cache.kv_heads, cache.head_dim, heads)
+        """(address, bytes, tensor) of the zeroed workspace for attention of this
+        batch over such a cache, made on a stream's first call and kept for its
+        calls: zeroed before them, and not handed on before they have run."""
+        key = (cache.kv_heads, cache.head_dim, heads, _handle(stream, cache))
         ws = self._ws.get(key)
         if ws is None:
             from . import lib
@@ -272,10 +276,11 @@ def _attend(cache, batch, code, heads, q, out, lse, scale, causal, window, strea
             return _attend(cache, batch, code, heads, q, out, lse, scale, causal, window, stream)
     if not 0 <= window <= 0x7FFFFFFF:
         _fail("zc_kv_attend: window >= 0")
-    address, size, _ = batch.workspace(cache, heads, stream)
+    handle = _handle(stream, cache)
+    address, size, _ = batch._ws.get((cache.kv_heads, cache.head_dim, heads, handle)) or batch.workspace(cache, heads, stream)
     _check(_entries()[2](cache._ref, batch._ref, code, heads, ctypes.addressof(q), ctypes.addressof(out), lse,
                          cache.head_dim ** -0.5 if scale is None else scale, _CAUSAL if causal else 0, window, address,
-                         size, cache._status, _handle(stream, cache)), "zc_kv_attend")
+                         size, cache._status, handle), "zc_kv_attend")
 
 
 def _query(cache, batch, q):

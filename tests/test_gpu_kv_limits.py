@@ -196,3 +196,61 @@ def test_check_waits_for_calls_on_other_streams():
             cache.check()
         assert e.value.status == zc.EFORMAT
         cache.check()  # and has forgotten it
+
+
+def _decoding(seqs=64, keys=4000, block=32):
+    """A cache, and a maker of batches of one token for each sequence, whose items are cut and joined (by the counters of
+    the workspace); queries, and what attention gives."""
+    per = keys // block
+    cache = _cache(per * 2, 2, 64, block)
+    table = torch.stack([torch.randperm(per * 2, device=DEV)[:per].to(torch.int32) for _ in range(seqs)])
+    cu, lens = torch.arange(seqs + 1, dtype=torch.int32, device=DEV), _i32([keys] * seqs)
+
+    def batch():
+        return zc.KVBatch(table, cu, lens, seqs, 1)
+
+    q = torch.randn(seqs, 8, 64, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV).half()
+    want, _ = zc.kv_attend(cache, batch(), q)
+    cache.check()
+    return cache, batch, q, want
+
+
+def _leave_garbage(size):
+    """Freed memory of this size, on the current stream, holds numbers that are not 0."""
+    t = torch.full((size,), 0x55, dtype=torch.uint8, device=DEV)
+    address = t.data_ptr()
+    del t
+    return address
+
+
+def _size(cache, batch, heads):
+    return max(16, zc.lib().zc_kv_attend_workspace_size(cache._ref, batch._ref, heads))
+
+
+def test_one_batch_on_two_streams():
+    """Its first stream is far behind: what that is to zero is not what the other one counts in."""
+    cache, make, q, want = _decoding()
+    batch, side = make(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _leave_garbage(_size(cache, batch, 8))
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100 * MS)
+    first, _ = zc.kv_attend(cache, batch, q)
+    other, _ = zc.kv_attend(cache, batch, q, stream=side)
+    cache.check()
+    assert torch.equal(first, want) and torch.equal(other, want)
+
+
+def test_a_batch_that_is_dropped_while_another_stream_works_for_it():
+    cache, make, q, want = _decoding()
+    batch, side = make(), torch.cuda.Stream()
+    assert torch.equal(zc.kv_attend(cache, batch, q)[0], want)
+    size = _size(cache, batch, 8)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100 * MS)
+    other, _ = zc.kv_attend(cache, batch, q, stream=side)
+    del batch
+    _leave_garbage(size)
+    cache.check()
+    assert torch.equal(other, want)
