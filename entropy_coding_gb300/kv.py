@@ -8,7 +8,8 @@ launch on the current stream (or ``stream``, a torch stream or a handle) and
 do not synchronise; errors that only the device can see are OR-ed into the
 cache's status, which ``KVCache.check`` reads. Tensors that the caller gives,
 a cache's and a batch's among them, are ready on the stream of a call and
-outlive it there (``Tensor.record_stream``).
+outlive it there (``Tensor.record_stream``), and so does a stream that is
+given by its handle outlive the cache; what a call makes for itself is seen to.
 """
 from __future__ import annotations
 
@@ -114,11 +115,26 @@ class KVCache:
         self.n_blocks, self.kv_heads, self.block_tokens, self.head_dim = n, h, b, d
         self.device, self._index = k.device, k.device.index
         self._many = torch.cuda.device_count() > 1
-        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        with torch.cuda.device(self.device):
+            self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+            self._ready = torch.cuda.Event()
+            self._ready.record()
+        self._streams = {_raw_stream(self._index)}  # that know of the status
         self._c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                          block_stride, scale_stride, n, h, b, d)
         self._ref = ctypes.addressof(self._c)
         self._status = self.status.data_ptr()
+
+    def _meet(self, handle: int) -> None:
+        """A stream's first call: it comes after the status was made, and the status outlives its calls. (A graph is
+        captured with the device at rest, and its owner keeps the cache.)"""
+        stream = torch.cuda.ExternalStream(handle, device=self.device)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+            stream.wait_event(self._ready)
+            self.status.record_stream(stream)
+        self._streams.add(handle)
 
     @classmethod
     def empty(cls, n_blocks: int, kv_heads: int, head_dim: int, block_tokens: int = 64, device="cuda") -> "KVCache":
@@ -198,8 +214,12 @@ def _rows(t: torch.Tensor, shape, device, what: str) -> _Rows:
 
 def _handle(stream, cache: KVCache) -> int:
     if stream is None:
-        return _raw_stream(cache._index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        handle = _raw_stream(cache._index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle not in cache._streams:
+        cache._meet(handle)
+    return handle
 
 
 def _on(stream, device):

@@ -254,3 +254,17 @@ def test_a_batch_that_is_dropped_while_another_stream_works_for_it():
     _leave_garbage(size)
     cache.check()
     assert torch.equal(other, want)
+
+
+def test_an_error_before_the_status_is_zero_is_not_lost():
+    """The stream on which the cache was made is far behind."""
+    tensors, side = _cache(4, 2, 64, 16), torch.cuda.Stream()
+    bad, x = _wrong(tensors), torch.zeros(1, 2, 64, device=DEV).half()
+    zc.kv_write(tensors, bad, x, x, stream=side)  # (a kernel's first launch waits for the device)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100 * MS)
+    cache = zc.KVCache(tensors.k, tensors.v, tensors.k_scale, tensors.v_scale)
+    zc.kv_write(cache, bad, x, x, stream=side)
+    with pytest.raises(zc.ZcError) as e:
+        cache.check()
+    assert e.value.status == zc.EFORMAT

@@ -70,7 +70,7 @@ def two_devices(monkeypatch):
 def _on_device(index):
     """A cache and a batch that say they are on that device (their tensors are the host's)."""
     cache, batch = object.__new__(kv.KVCache), object.__new__(kv.KVBatch)
-    cache.__dict__.update(_many=True, kv_heads=2, head_dim=32, device=torch.device("cpu"), _index=index, _ref=0, _status=0)
+    cache.__dict__.update(_many=True, _streams={0}, kv_heads=2, head_dim=32, device=torch.device("cpu"), _index=index, _ref=0, _status=0)
     batch.__dict__.update(total_tokens=3, _index=index, _ref=0, _ws={})
     batch.workspace = lambda cache, heads, stream=None: (0, 0, None)
     return cache, batch
