@@ -42,6 +42,9 @@ class _Rows(ctypes.Structure):
     _fields_ = [("d_data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+# Calls that a check found to have reported an error: CTAs that gave up never came to their counters, so that a workspace
+# that was in use before then is zeroed before it is used again.
+_failures = 0
 _entry = None  # (zc_kv_write, zc_kv_read, zc_kv_attend) once the library is loaded
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
@@ -146,13 +149,17 @@ class KVCache:
 
     def check(self) -> None:
         """Raise ZcError if a call on this cache reported an error (and forget
-        it). Waits for the device: for calls on every stream."""
+        it). Waits for the device: for calls on every stream. Batches are as
+        good as new after it; one that is used by a captured graph wants
+        ``KVBatch.reset`` before the next replay."""
+        global _failures
         from . import ZcError
         torch.cuda.synchronize(self.device)
         st = int(self.status.item())
         if st:
             self.status.zero_()
             torch.cuda.synchronize(self.device)  # forgotten before any later call reports
+            _failures += 1
             raise ZcError(st, "zc_kv (device)")
 
 
@@ -192,15 +199,32 @@ class KVBatch:
         """(address, bytes, tensor) of the zeroed workspace for attention of this
         batch over such a cache, made on a stream's first call and kept for its
         calls: zeroed before them, and not handed on before they have run."""
-        key = (cache.kv_heads, cache.head_dim, heads, _handle(stream, cache))
+        return self._workspace(cache, heads, stream, _handle(stream, cache))[:3]
+
+    def _workspace(self, cache: KVCache, heads: int, stream, handle: int) -> list:
+        key = (cache.kv_heads, cache.head_dim, heads, handle)
         ws = self._ws.get(key)
-        if ws is None:
-            from . import lib
-            n = int(lib().zc_kv_attend_workspace_size(cache._ref, self._ref, heads))
-            with _on(stream, cache.device):
-                t = torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.device)
-            ws = self._ws[key] = (t.data_ptr(), n, t)
+        if ws is not None and ws[3] == _failures:
+            return ws
+        with _on(stream, cache.device):
+            if ws is None:
+                from . import lib
+                n = int(lib().zc_kv_attend_workspace_size(cache._ref, self._ref, heads))
+                t = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
+                ws = self._ws[key] = [t.data_ptr(), n, t, _failures]
+            ws[2].zero_()
+            # (in a capture the zeroing is part of the graph: a call outside it sees to its own)
+            ws[3] = -1 if torch.cuda.is_current_stream_capturing() else _failures
         return ws
+
+    def reset(self) -> None:
+        """Zero the workspaces again, for the replays of a graph that was captured
+        with this batch, after a call that reported an error. Waits for the
+        device."""
+        torch.cuda.synchronize(self.device)
+        for ws in self._ws.values():
+            ws[2].zero_()
+        torch.cuda.synchronize(self.device)
 
 
 def _rows(t: torch.Tensor, shape, device, what: str) -> _Rows:
@@ -297,10 +321,12 @@ def _attend(cache, batch, code, heads, q, out, lse, scale, causal, window, strea
     if not 0 <= window <= 0x7FFFFFFF:
         _fail("zc_kv_attend: window >= 0")
     handle = _handle(stream, cache)
-    address, size, _ = batch._ws.get((cache.kv_heads, cache.head_dim, heads, handle)) or batch.workspace(cache, heads, stream)
+    ws = batch._ws.get((cache.kv_heads, cache.head_dim, heads, handle))
+    if ws is None or ws[3] != _failures:
+        ws = batch._workspace(cache, heads, stream, handle)
     _check(_entries()[2](cache._ref, batch._ref, code, heads, ctypes.addressof(q), ctypes.addressof(out), lse,
-                         cache.head_dim ** -0.5 if scale is None else scale, _CAUSAL if causal else 0, window, address,
-                         size, cache._status, handle), "zc_kv_attend")
+                         cache.head_dim ** -0.5 if scale is None else scale, _CAUSAL if causal else 0, window, ws[0],
+                         ws[1], cache._status, handle), "zc_kv_attend")
 
 
 def _query(cache, batch, q):

@@ -12,6 +12,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import entropy_coding_gb300 as zc  # noqa: E402
+from entropy_coding_gb300 import kv  # noqa: E402
 
 from kv_reference import attend, to_codes  # noqa: E402
 
@@ -268,3 +269,47 @@ def test_an_error_before_the_status_is_zero_is_not_lost():
     with pytest.raises(zc.ZcError) as e:
         cache.check()
     assert e.value.status == zc.EFORMAT
+
+
+def _give_up(cache, batch, q):
+    """A call whose waits run out, and workspaces as CTAs that gave up at the worst moment leave them."""
+    zc.lib().zc_kv_set_test_hooks(kv.HOOK_COPY_STALL)
+    try:
+        zc.kv_attend(cache, batch, q)
+        torch.cuda.synchronize()
+    finally:
+        zc.lib().zc_kv_set_test_hooks(0)
+    for ws in batch._ws.values():
+        ws[2].fill_(1)
+    with pytest.raises(zc.ZcError) as e:
+        cache.check()
+    assert e.value.status == zc.ETIMEOUT
+
+
+def test_a_batch_is_used_again_after_a_call_that_gave_up():
+    cache, make, q, want = _decoding()
+    batch, other, side = make(), make(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        for b in (batch, other):
+            assert torch.equal(zc.kv_attend(cache, b, q)[0], want)
+        out, _ = zc.kv_attend(cache, batch, q, stream=side)
+        cache.check()
+        assert torch.equal(out, want)
+        _give_up(cache, batch, q)
+
+
+def test_a_captured_call_after_one_that_gave_up():
+    cache, make, q, want = _decoding()
+    batch, out = make(), torch.empty_like(want)
+    zc.kv_attend_into(cache, batch, q, out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        zc.kv_attend_into(cache, batch, q, out)
+    _give_up(cache, batch, q)
+    batch.reset()
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        cache.check()
+        assert torch.equal(out, want)

@@ -72,7 +72,7 @@ def _on_device(index):
     cache, batch = object.__new__(kv.KVCache), object.__new__(kv.KVBatch)
     cache.__dict__.update(_many=True, _streams={0}, kv_heads=2, head_dim=32, device=torch.device("cpu"), _index=index, _ref=0, _status=0)
     batch.__dict__.update(total_tokens=3, _index=index, _ref=0, _ws={})
-    batch.workspace = lambda cache, heads, stream=None: (0, 0, None)
+    batch._workspace = lambda *_: [0, 0, None, 0]
     return cache, batch
 
 
