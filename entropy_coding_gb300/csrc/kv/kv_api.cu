@@ -175,17 +175,27 @@ struct Plan {
         const uint64_t r = rows ? rows_part_bytes(c) : 0, t = tiles ? tiles_part_bytes(c) : 0;
         part_bytes = r > t ? r : t;
     }
-    uint64_t bytes() const { return rows_counters + tiles_counters + part_bytes; }
+    uint64_t counters() const { return rows_counters + tiles_counters; }
+    uint64_t bytes() const { return counters() + part_bytes; }
 };
 
-} // namespace
-
-extern "C" uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads) {
+// counters() or bytes() of a call's plan, 0 for invalid arguments
+uint64_t planned(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads, uint64_t (Plan::*bytes)() const) {
     Cache c{};
     Batch b{};
     if (make_cache(cache, c) != ZC_OK || make_batch(batch, b) != ZC_OK) return 0;
     if (heads == 0 || heads % c.heads || heads > 65535 || uint64_t(b.total) * heads > 0x7FFFFFFFu) return 0;
-    return Plan(b, c, heads / c.heads).bytes();
+    return (Plan(b, c, heads / c.heads).*bytes)();
+}
+
+} // namespace
+
+extern "C" uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads) {
+    return planned(cache, batch, heads, &Plan::bytes);
+}
+
+extern "C" uint64_t zc_kv_attend_counter_bytes(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads) {
+    return planned(cache, batch, heads, &Plan::counters);
 }
 
 extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
@@ -208,7 +218,7 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
     if (!d_ws || !aligned(d_ws, 16)) return ZC_EINVAL;
     if (ws_bytes < plan.bytes()) return ZC_ECAPACITY;
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
-    a.parts = ws + plan.rows_counters + plan.tiles_counters;
+    a.parts = ws + plan.counters();
     a.rows_most = plan.rows_most;
     a.scale_log2 = float(scale * 1.4426950408889634);
     a.causal = flags & ZC_KV_CAUSAL;

@@ -65,8 +65,9 @@ def declare(L: ctypes.CDLL) -> None:
     L.zc_kv_attend.argtypes = [vp, vp, i32, u32, vp, vp, vp, ctypes.c_double, u32, u32, vp, u64, vp, vp]
     L.zc_kv_set_test_hooks.restype = None
     L.zc_kv_set_test_hooks.argtypes = [u32]
-    L.zc_kv_attend_workspace_size.restype = u64
-    L.zc_kv_attend_workspace_size.argtypes = [vp, vp, u32]
+    for f in (L.zc_kv_attend_workspace_size, L.zc_kv_attend_counter_bytes):
+        f.restype = u64
+        f.argtypes = [vp, vp, u32]
 
 
 def _entries():
@@ -174,7 +175,8 @@ class KVBatch:
     numbers. The tensors may change between calls (a captured graph is
     replayed with new lengths) as long as the totals hold. The batch keeps
     attention's workspaces, one for each stream: a captured graph that may
-    overlap with other calls uses a batch of its own."""
+    overlap with other calls uses a batch of its own, and the batch is kept as
+    long as its graphs."""
 
     def __init__(self, block_table: torch.Tensor, cu_tokens: torch.Tensor, lens: torch.Tensor, total_tokens: int,
                  max_tokens: int):
@@ -196,9 +198,11 @@ class KVBatch:
         self._ws: dict = {}
 
     def workspace(self, cache: KVCache, heads: int, stream=None) -> tuple:
-        """(address, bytes, tensor) of the zeroed workspace for attention of this
-        batch over such a cache, made on a stream's first call and kept for its
-        calls: zeroed before them, and not handed on before they have run."""
+        """(address, bytes, tensor) of the workspace for attention of this batch
+        over such a cache, made on a stream's first call and kept for its calls:
+        its counters are zeroed before them, and it is not handed on before they
+        have run. A captured call takes one that another stream's calls use, or
+        memory of its graph, zeroed by each replay."""
         return self._workspace(cache, heads, stream, _handle(stream, cache))[:3]
 
     def _workspace(self, cache: KVCache, heads: int, stream, handle: int) -> list:
@@ -207,23 +211,30 @@ class KVBatch:
         if ws is not None and ws[3] == _failures:
             return ws
         with _on(stream, cache.device):
+            capturing = torch.cuda.is_current_stream_capturing()
             if ws is None:
+                if capturing:
+                    for k, other in self._ws.items():
+                        if k[:3] == key[:3] and other[3] == _failures:
+                            return other
                 from . import lib
-                n = int(lib().zc_kv_attend_workspace_size(cache._ref, self._ref, heads))
-                t = torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
-                ws = self._ws[key] = [t.data_ptr(), n, t, _failures]
-            ws[2].zero_()
-            # (in a capture the zeroing is part of the graph: a call outside it sees to its own)
-            ws[3] = -1 if torch.cuda.is_current_stream_capturing() else _failures
+                size, counters = (int(f(cache._ref, self._ref, heads))
+                                  for f in (lib().zc_kv_attend_workspace_size, lib().zc_kv_attend_counter_bytes))
+                t = torch.empty(max(size, 16), dtype=torch.uint8, device=cache.device)
+                ws = [t.data_ptr(), size, t, -1, t[:counters]]
+            ws[4].zero_()
+            if not capturing:  # (else it is the graph that zeroes)
+                ws[3] = _failures
+                self._ws[key] = ws
         return ws
 
     def reset(self) -> None:
-        """Zero the workspaces again, for the replays of a graph that was captured
-        with this batch, after a call that reported an error. Waits for the
-        device."""
+        """Zero the workspaces' counters again, for the replays of a graph that was
+        captured with this batch, after a call that reported an error. Waits for
+        the device."""
         torch.cuda.synchronize(self.device)
         for ws in self._ws.values():
-            ws[2].zero_()
+            ws[4].zero_()
         torch.cuda.synchronize(self.device)
 
 

@@ -448,10 +448,11 @@ ZC_API int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, int dt
  *   heads   query heads, a multiple of kv_heads; total_tokens * heads < 2^31
  *   q, out  [total_tokens][heads][head_dim]
  *   d_lse   NULL or float [total_tokens][heads]
- *   d_ws    workspace of ws_bytes >= zc_kv_attend_workspace_size(...), zeroed
- *           before its first use; every call leaves it ready for the next with
- *           a batch of these sizes (zero it again after a call that reported an
- *           error). Calls that may overlap need their own.
+ *   d_ws    workspace of ws_bytes >= zc_kv_attend_workspace_size(...), whose
+ *           first zc_kv_attend_counter_bytes(...) are zeroed before its first
+ *           use; every call leaves it ready for the next with a batch of these
+ *           sizes (zero them again after a call that reported an error). Calls
+ *           that may overlap need their own.
  * Every wait inside the kernels gives up after about a second and reports
  * ZC_ETIMEOUT; the outputs are unspecified then.
  * Scores, weights' sums and outputs are accumulated in float32; weights are
@@ -470,6 +471,10 @@ ZC_API void zc_kv_set_test_hooks(uint32_t hooks);
 /* Workspace bytes of zc_kv_attend for this cache, batch and number of query
  * heads (0 for invalid ones). Queries the device's SM count; host only. */
 ZC_API uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads);
+
+/* The part of it, from its beginning, that is zeroed before its first use: the
+ * counters. The rest may hold anything. */
+ZC_API uint64_t zc_kv_attend_counter_bytes(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads);
 
 #ifdef __cplusplus
 }

@@ -313,3 +313,46 @@ def test_a_captured_call_after_one_that_gave_up():
         graph.replay()
         cache.check()
         assert torch.equal(out, want)
+
+
+def test_a_first_call_in_a_capture_and_one_outside_it_before_the_replay():
+    """The captured call's counters are zeroed when the graph runs: another call on the stream must not take them for zero
+    before that (the graphs' memory held other numbers), and the graph keeps its memory when the batch is gone."""
+    cache, make, q, want = _decoding()
+    batch, side, pool = make(), torch.cuda.Stream(), torch.cuda.graph_pool_handle()
+    size, out = _size(cache, batch, 8), torch.empty_like(want)
+    garbage, graph = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(garbage, pool=pool, stream=side):
+        _leave_garbage(size)
+    garbage.replay()
+    with torch.cuda.graph(graph, pool=pool, stream=side):
+        zc.kv_attend_into(cache, batch, q, out)
+    other, _ = zc.kv_attend(cache, batch, q, stream=side)
+    cache.check()
+    assert torch.equal(other, want)
+    del batch
+    _leave_garbage(size)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        cache.check()
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_only_the_counters_of_a_workspace_are_zeroed(new):
+    """The rest held other numbers, NaN as floats, before the batch's first call."""
+    cache = _cache(200, 2, 64, 32)
+    table = torch.randperm(200, device=DEV)[:190].to(torch.int32).view(2, 95)
+    q = torch.randn(2 * new, 8, 64, device=DEV).half()
+    outs = []
+    for fill in (0x00, 0xFF):
+        batch = zc.KVBatch(table, _i32([0, new, 2 * new]), _i32([3000, 2500]), 2 * new, new)
+        t = torch.full((_size(cache, batch, 8),), fill, dtype=torch.uint8, device=DEV)
+        address = t.data_ptr()
+        del t
+        outs.append(zc.kv_attend(cache, batch, q))
+        assert batch.workspace(cache, 8)[0] == address  # (the allocator hands the freed memory on)
+        del batch
+    cache.check()
+    assert not outs[0][0].isnan().any() and all(torch.equal(a, b) for a, b in zip(*outs))

@@ -1,6 +1,7 @@
 """Arguments of the 8-bit cache's Python layer that are checked before any pointer is taken; no GPU."""
 from __future__ import annotations
 
+import ctypes
 import types
 
 import pytest
@@ -104,3 +105,18 @@ def test_a_batch_on_two_devices_is_refused():
 
     for where in ((1, 0, 0), (0, 1, 0), (0, 0, 1)):
         _refused("one device", lambda: zc.KVBatch(*map(t, where), 2, 1))
+
+
+def test_counter_bytes_are_part_of_the_workspace():
+    def sizes(heads=4, tokens=6, most=3, **kw):
+        c = kv._Cache(**{**dict(d_k=1 << 16, d_v=1 << 16, d_k_scale=1 << 16, d_v_scale=1 << 16, block_stride=1024, scale_stride=2,
+                                n_blocks=4, kv_heads=2, block_tokens=16, head_dim=32), **kw})
+        b = kv._Batch(d_table=1 << 16, table_stride=3, d_cu=1 << 16, d_lens=1 << 16, n_seqs=2, total_tokens=tokens, max_tokens=most,
+                      table_width=3)
+        return [f(ctypes.byref(c), ctypes.byref(b), heads)
+                for f in (zc.lib().zc_kv_attend_counter_bytes, zc.lib().zc_kv_attend_workspace_size)]
+
+    for args in (dict(), dict(tokens=600, most=300), dict(heads=64), dict(heads=2, tokens=2, most=1)):
+        counters, size = sizes(**args)
+        assert 0 < counters < size and counters % 256 == 0
+    assert sizes(heads=3) == [0, 0] and sizes(head_dim=24) == [0, 0] and sizes(most=7) == [0, 0]
