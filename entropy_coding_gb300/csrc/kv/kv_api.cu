@@ -222,7 +222,7 @@ extern "C" int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, 
     a.rows_most = plan.rows_most;
     a.scale_log2 = float(scale * 1.4426950408889634);
     a.causal = flags & ZC_KV_CAUSAL;
-    a.window = window;
+    a.window = window < 1u << 30 ? window : 0;  // (lengths are below that: nothing is outside)
     a.d_status = d_status;
     a.stall = g_hooks.load(std::memory_order_relaxed) & ZC_HOOK_KV_COPY_STALL;
     a.limit = a.stall ? kWaitClocksTest : kWaitClocks;

@@ -2,6 +2,8 @@
 the ordinary tests do not reach."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -356,3 +358,21 @@ def test_only_the_counters_of_a_workspace_are_zeroed(new):
         del batch
     cache.check()
     assert not outs[0][0].isnan().any() and all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_windows_of_any_size(new):
+    """From the sequence's length on, a window hides nothing, up to the largest that the C entry takes."""
+    cache = _cache(10, 2, 64, 16)
+    batch = zc.KVBatch(_i32([list(range(10))]), _i32([0, new]), _i32([150]), new, new)
+    q = torch.randn(new, 8, 64, device=DEV).half()
+    want, lse = zc.kv_attend(cache, batch, q)
+    rows = kv._Rows(q.data_ptr(), 8 * 64, 64)
+    address, size, _ = batch.workspace(cache, 8)
+    for window in (150, 2 ** 20, 2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1, 2 ** 31, 2 ** 32 - 1):
+        out = torch.zeros_like(want)
+        st = zc.lib().zc_kv_attend(cache._ref, batch._ref, zc.FP16, 8, ctypes.byref(rows),
+                                   ctypes.byref(kv._Rows(out.data_ptr(), 8 * 64, 64)), None, 64 ** -0.5, 1, window, address, size,
+                                   cache._status, torch.cuda.current_stream().cuda_stream)
+        cache.check()
+        assert st == zc.OK and torch.equal(out, want), window
