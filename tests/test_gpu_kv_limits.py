@@ -376,3 +376,58 @@ def test_windows_of_any_size(new):
                                    cache._status, torch.cuda.current_stream().cuda_stream)
         cache.check()
         assert st == zc.OK and torch.equal(out, want), window
+
+
+def _against_reference(dtype, hkv, group, dim, block, lens, news, window=0):
+    """Attention of a ragged batch against its definition. A weight is rounded to 11 bits, scores err by 2^-17 of their
+    products' magnitudes, and the output is rounded to its type."""
+    rng = np.random.default_rng(len(lens))
+    per = [max(1, -(-n // block)) for n in lens]
+    ids, table, at = rng.permutation(sum(per)), np.zeros((len(lens), max(per)), np.int32), 0
+    for s, p in enumerate(per):
+        table[s, :p] = ids[at: at + p]
+        at += p
+    kc, vc = (to_codes(rng.standard_normal((sum(per), hkv, block, dim)) * m) for m in (dim ** -0.5, 1.0))
+    ks, vs = np.ones((sum(per), hkv), np.float32), np.exp2(rng.integers(-3, 4, (sum(per), hkv))).astype(np.float32)
+    cache = zc.KVCache(*(torch.from_numpy(np.array(a)).to(DEV) for a in (kc, vc, ks, vs)))
+    cu = np.concatenate([[0], np.cumsum(news)])
+    batch = zc.KVBatch(torch.from_numpy(table).to(DEV), _i32(cu.tolist()), _i32(lens), int(cu[-1]), max(news))
+    q = torch.from_numpy(rng.standard_normal((int(cu[-1]), hkv * group, dim))).to(DEV).to(dtype)
+    out, lse = zc.kv_attend(cache, batch, q, scale=1.0, window=window)
+    cache.check()
+    want, z, mass, size, _, _ = attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, cu, lens, 1.0, True, window)
+    tol = mass * (2.0 ** -10 + 2.0 ** -16 * size)[..., None]
+    low, high = (torch.from_numpy(want + d).to(dtype).double().numpy() for d in (-tol, tol))
+    got = out.double().cpu().numpy()
+    assert ((got >= low) & (got <= high)).all()
+    seen = np.isfinite(z)
+    got = lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(got), ~seen) and (np.abs(got - z)[seen] < (2.0 ** -16 * size + 2.0 ** -19)[seen]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("seqs", [129, 256, 400])
+def test_single_tokens_of_more_sequences_than_a_cta_has_threads(seqs, dtype):
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(1, 300, seqs).tolist()
+    news = [0 if i % 17 == 5 else 1 for i in range(seqs)]
+    _against_reference(dtype, 1, 4, 64, 16, lens, news)
+
+
+@pytest.mark.parametrize("dim,window", [(64, 0), (128, 30)])
+def test_prompts_of_more_slots_than_a_cta_has_threads(dim, window):
+    """600 sequences of 17 to 40 tokens of 8 heads: more slots of 256 rows than 512."""
+    rng = np.random.default_rng(dim)
+    news = rng.integers(17, 41, 600).tolist()
+    news[7] = news[599] = 0
+    lens = [n + int(k) for n, k in zip(news, rng.integers(0, 30, 600))]
+    _against_reference(torch.bfloat16, 1, 8, dim, 16, lens, news, window)
+
+
+@pytest.mark.parametrize("at", [0, 130, 259])
+def test_a_prompt_among_more_single_tokens_than_a_cta_has_threads(at):
+    """Both kernels, each on its own sequences."""
+    rng = np.random.default_rng(at)
+    lens, news = rng.integers(1, 200, 260).tolist(), [1] * 260
+    lens[at], news[at] = 700, 300
+    _against_reference(torch.float16, 1, 4, 64, 32, lens, news)
