@@ -45,7 +45,7 @@ class _Rows(ctypes.Structure):
 # Calls that a check found to have reported an error: CTAs that gave up never came to their counters, so that a workspace
 # that was in use before then is zeroed before it is used again.
 _failures = 0
-_entry = None  # (zc_kv_write, zc_kv_read, zc_kv_attend) once the library is loaded
+_entry = None  # zc_kv_write, zc_kv_read, zc_kv_attend and its two sizes, once the library is loaded
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -76,7 +76,7 @@ def _entries():
     if _entry is None:
         from . import lib
         L = lib()
-        _entry = (L.zc_kv_write, L.zc_kv_read, L.zc_kv_attend)
+        _entry = (L.zc_kv_write, L.zc_kv_read, L.zc_kv_attend, L.zc_kv_attend_workspace_size, L.zc_kv_attend_counter_bytes)
     return _entry
 
 
@@ -203,29 +203,31 @@ class KVBatch:
         its counters are zeroed before them, and it is not handed on before they
         have run. A captured call takes one that another stream's calls use, or
         memory of its graph, zeroed by each replay."""
-        return self._workspace(cache, heads, stream, _handle(stream, cache))[:3]
+        with torch.cuda.device(cache.device):
+            return tuple(self._workspace(cache, heads, stream, _handle(stream, cache))[:3])
 
     def _workspace(self, cache: KVCache, heads: int, stream, handle: int) -> list:
+        """The workspace as [address, bytes, tensor, errors found before it was zeroed, its counters]."""
+        if stream is not None:
+            with _on(stream, cache.device):
+                return self._workspace(cache, heads, None, handle)
         key = (cache.kv_heads, cache.head_dim, heads, handle)
         ws = self._ws.get(key)
         if ws is not None and ws[3] == _failures:
             return ws
-        with _on(stream, cache.device):
-            capturing = torch.cuda.is_current_stream_capturing()
-            if ws is None:
-                if capturing:
-                    for k, other in self._ws.items():
-                        if k[:3] == key[:3] and other[3] == _failures:
-                            return other
-                from . import lib
-                size, counters = (int(f(cache._ref, self._ref, heads))
-                                  for f in (lib().zc_kv_attend_workspace_size, lib().zc_kv_attend_counter_bytes))
-                t = torch.empty(max(size, 16), dtype=torch.uint8, device=cache.device)
-                ws = [t.data_ptr(), size, t, -1, t[:counters]]
-            ws[4].zero_()
-            if not capturing:  # (else it is the graph that zeroes)
-                ws[3] = _failures
-                self._ws[key] = ws
+        capturing = torch.cuda.is_current_stream_capturing()
+        if ws is None:
+            if capturing:
+                for k, other in self._ws.items():
+                    if k[:3] == key[:3] and other[3] == _failures:
+                        return other
+            size, counters = (int(f(cache._ref, self._ref, heads)) for f in _entries()[3:])
+            t = torch.empty(max(size, 16), dtype=torch.uint8, device=cache.device)
+            ws = [t.data_ptr(), size, t, -1, t[:counters]]
+        ws[4].zero_()
+        if not capturing:  # (else it is the graph that zeroes)
+            ws[3] = _failures
+            self._ws[key] = ws
         return ws
 
     def reset(self) -> None:
