@@ -46,6 +46,7 @@
 // us); fetching the next piece before the last is finished, 113 to 99.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 
 #include "kv_attend.cuh"
 
@@ -214,7 +215,7 @@ template <int S> __device__ __forceinline__ void drain(const AttendArgs &a, Warp
 template <int DP, int NT> struct Sums {
     float o[NT][DP / 16][4];
     // Of rows 2t, 2t + 1 of each tile: running maxima (the scores', and with the value scales),
-    // 2^(m - mw), and the weights' sums over this thread's keys.
+    // 2^(m - mw), and the weights' sums over this thread's keys (in units of 2^(m - kRaise)).
     float m[NT][2], mw[NT][2], unit[NT][2], l[NT][2];
     uint32_t poison[NT][2];  // of this thread's columns: where a value that the row sees is NaN, and was taken out
 };
@@ -374,15 +375,15 @@ __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMap
                     o[n][c][0] *= down[0], o[n][c][1] *= down[1], o[n][c][2] *= down[0], o[n][c][3] *= down[1];
             }
         }
-        // Weights p = 2^(s - m), and in the output's units p * 2^(m + log2 vs - mw + kRaise).
-        constexpr float kUp = float(1 << int(kRaise));
+        // Weights p = 2^(s - m + kRaise), and in the output's units p * 2^(m + log2 vs - mw). (A block that is louder than
+        // the unit by more than a float holds is hardly attended to: an infinite factor would make its weights of 0 NaN.)
         uint32_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; n++) {
             float w[4];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const float base = m[n][e] == kNone ? 0.0f : m[n][e], f = vs * unit[n][e] * kUp;
+                const float base = (m[n][e] == kNone ? 0.0f : m[n][e]) - kRaise, f = fminf(vs * unit[n][e], FLT_MAX);
                 const float p0 = ex2(sc[n][e] - base), p1 = ex2(sc[n][2 + e] - base);
                 l[n][e] += p0 + p1;
                 w[e] = p0 * f, w[2 + e] = p1 * f;
@@ -465,6 +466,7 @@ __device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const 
             float l = acc.l[n][e];
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+            l *= 1.0f / (1 << int(kRaise));
             if (acc.poison[n][e]) {
 #pragma unroll
                 for (int c = 0; c < kCols; c++)

@@ -431,3 +431,27 @@ def test_a_prompt_among_more_single_tokens_than_a_cta_has_threads(at):
     lens, news = rng.integers(1, 200, 260).tolist(), [1] * 260
     lens[at], news[at] = 700, 300
     _against_reference(torch.float16, 1, 4, 64, 32, lens, news)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_block_louder_by_more_than_a_float_holds(new):
+    """The last block's value scale is 2^130 times the others', its keys' weights 2^-140 of theirs: 2^-10 of the output.
+    (The same tokens for many sequences, so that whole sequences are one piece of work.)"""
+    keys, dim, block, seqs = 256, 64, 16, 600
+    rng = np.random.default_rng(4)
+    k, v = np.zeros((keys, dim)), np.abs(rng.standard_normal((keys, dim)))
+    k[-block:, -1] = -1.0
+    kc, vc = (to_codes(x).reshape(keys // block, 1, block, dim) for x in (k, v))
+    ks, vs = np.ones((keys // block, 1), np.float32), np.full((keys // block, 1), 2.0 ** -100, np.float32)
+    vs[-1] = 2.0 ** 30
+    table = np.arange(keys // block, dtype=np.int32).reshape(1, -1)
+    cache = zc.KVCache(*(torch.from_numpy(np.array(a)).to(DEV) for a in (kc, vc, ks, vs)))
+    batch = zc.KVBatch(torch.from_numpy(table).to(DEV).repeat(seqs, 1), _i32(range(0, seqs * new + 1, new)), _i32([keys] * seqs),
+                       seqs * new, new)
+    q = torch.zeros(new, 4, dim, device=DEV).bfloat16()
+    q[..., -1] = 97.0  # 2^-140
+    out, lse = zc.kv_attend(cache, batch, q.repeat(seqs, 1, 1), scale=1.0, causal=False)
+    cache.check()
+    want, z, mass, _, _, _ = attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, [0, new], [keys], 1.0, False, 0)
+    assert (np.abs(out.double().cpu().numpy().reshape(seqs, *want.shape) - want) <= 2.0 ** -7 * mass).all()
+    assert np.abs(lse.double().cpu().numpy().reshape(seqs, *z.shape) - z).max() < 1e-5
