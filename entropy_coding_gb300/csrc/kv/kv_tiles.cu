@@ -34,15 +34,17 @@
 // cores.
 //
 // Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads
-// of 128, causal) in 452 us, 1.21 PFLOP/s, 0.65 of the measured bfloat16 rate;
-// 912 tokens of two sequences over 28384 keys in 186 us (1.14 PFLOP/s). The
+// of 128, causal) in 454 us, 1.21 PFLOP/s, 0.65 of the measured bfloat16 rate;
+// 912 tokens of two sequences over 28384 keys in 185 us (1.15 PFLOP/s). The
 // tensor cores are busy half of the time. A key tile takes 1.7 us where its
 // products take 1.05: a row tile's chain of scores, weights (about 1.1 us: two
 // passes over the scores, 128 exponentials a thread on a unit shared by two
 // warps, and the conversions' instructions beside them) and its own products is
 // longer than the other tile's products cover. The weights stand where the
-// scores were, so that the next scores wait for these sums: columns for both do
-// not fit. Shared memory is the next limit: by its rate the products take 1536
+// scores were, so that the next scores wait for these sums: with 128 columns of
+// output, columns for both do not fit; with 64 they would (2 x 128 of scores, 2 x
+// 64 of weights, 2 x 64 of sums), which this layout does not use. An item of one
+// row tile leaves half of the row threads without work. Shared memory is the next limit: by its rate the products take 1536
 // clocks of it a key tile, the conversion 768, the copies 256. An item's
 // beginning and end take about 7 us (queries 1.6, output 3, the first scores and
 // the last sums with nothing beside them), joining a cut item 10: 32 columns and

@@ -18,9 +18,10 @@
 // more CTAs on an SM hide.
 //
 // Measured on a GB300: 104 MB of bfloat16 prompts (17138 tokens of 8 heads of
-// 128, blocks of 64) in 20 us, 5.1 TB/s, 0.76 of the copy rate; the arithmetic
-// units are at 48 %, and what is left is the latency of a CTA's start (its
-// place in the batch, its block, its rows: three dependent reads). Divisions
+// 128, blocks of 64) in 19.7 us, 5.3 TB/s, 0.78 of the copy rate; the arithmetic
+// units are at 49 % and 44 % of the warps are there: no unit's rate is the
+// limit, a CTA's start is (its place in the batch, the sequence's length, then
+// its rows: dependent reads, of which the first two need not be). Divisions
 // by the row's pieces, four a piece at first, were 4 us of it; units of several
 // heads in turn in one CTA, with the next rows on their way, were slower (27 us):
 // they leave fewer CTAs. A decoding step of 32 tokens takes 5 us, a launch.

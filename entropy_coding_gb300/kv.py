@@ -10,6 +10,11 @@ cache's status, which ``KVCache.check`` reads. Tensors that the caller gives,
 a cache's and a batch's among them, are ready on the stream of a call and
 outlive it there (``Tensor.record_stream``), and so does a stream that is
 given by its handle outlive the cache; what a call makes for itself is seen to.
+
+The cache serves: nothing here is differentiable, and outputs never require
+gradients, whatever the inputs do. Queries are 16-bit, as the tensor cores take
+them; heads go up to 128 columns, which is what a tile's queries, operands and
+sums fill of shared and of tensor memory.
 """
 from __future__ import annotations
 
