@@ -455,3 +455,21 @@ def test_a_block_louder_by_more_than_a_float_holds(new):
     want, z, mass, _, _, _ = attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, [0, new], [keys], 1.0, False, 0)
     assert (np.abs(out.double().cpu().numpy().reshape(seqs, *want.shape) - want) <= 2.0 ** -7 * mass).all()
     assert np.abs(lse.double().cpu().numpy().reshape(seqs, *z.shape) - z).max() < 1e-5
+
+
+def test_a_stream_in_every_form():
+    """Current, as a torch stream, as a handle, the default one for a cache that was made on another, an external one."""
+    cache, make, q, want = _decoding(seqs=20)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        there = zc.KVCache(cache.k, cache.v, cache.k_scale, cache.v_scale)
+        outs = [zc.kv_attend(there, make(), q)[0]]
+    batch = make()
+    for stream in (None, side, side.cuda_stream, 0, torch.cuda.default_stream(), torch.cuda.ExternalStream(side.cuda_stream)):
+        torch.cuda.synchronize()
+        outs.append(zc.kv_attend(there, batch, q, stream=stream)[0])
+        k, v = zc.kv_read(there, batch, dtype=torch.float16, stream=stream)
+        zc.kv_write(there, batch, k, v, stream=stream)  # what is there already
+    there.check()
+    assert len(batch._ws) == 2 and all(torch.equal(o, want) for o in outs)
