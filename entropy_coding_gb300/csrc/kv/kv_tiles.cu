@@ -34,7 +34,7 @@
 // cores.
 //
 // Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads
-// of 128, causal) in 454 us, 1.21 PFLOP/s, 0.65 of the measured bfloat16 rate;
+// of 128, causal) in 454 to 461 us, 1.2 PFLOP/s, 0.64 of the measured bfloat16 rate;
 // 912 tokens of two sequences over 28384 keys in 185 us (1.15 PFLOP/s). The
 // tensor cores are busy half of the time. A key tile takes 1.7 us where its
 // products take 1.05: a row tile's chain of scores, weights (about 1.1 us: two
