@@ -21,7 +21,8 @@ import torch
 
 from . import build as _build
 from . import kv as _kv
-from .kv import KVBatch, KVCache, kv_attend, kv_attend_into, kv_read, kv_read_into, kv_write
+from .kv import (KV4Cache, KVBatch, KVCache, KVRotation, kv_attend, kv_attend_into, kv_read, kv_read_into, kv_rotate,
+                 kv_rotate_into, kv_write)
 from .workloads import BF16, FP16, FP32, U8, U16, U32
 
 __all__ = ["compress", "decompress", "crc32", "verify", "verify_into", "blob_info", "blob_size", "workspace_size",
@@ -29,7 +30,8 @@ __all__ = ["compress", "decompress", "crc32", "verify", "verify_into", "blob_inf
            "decompress_delta_into", "compress_batch", "compress_batch_into", "decompress_batch",
            "decompress_batch_into", "workspace_size_batch", "decompress_workspace_size_batch", "ZcError", "lib", "SHARED_TABLES", "LANE_WORDS", "OK", "EINVAL", "EFORMAT",
            "ECRC", "ECORRUPT", "ETIMEOUT", "ECAPACITY", "ECUDA", "NO_VERIFY", "PACKED",
-           "KVCache", "KVBatch", "kv_write", "kv_read", "kv_read_into", "kv_attend", "kv_attend_into"]
+           "KVCache", "KV4Cache", "KVBatch", "KVRotation", "kv_write", "kv_read", "kv_read_into", "kv_attend", "kv_attend_into",
+           "kv_rotate", "kv_rotate_into"]
 
 OK, EINVAL, EFORMAT, ECRC, ECORRUPT, ETIMEOUT, ECAPACITY, ECUDA = 0, 1, 2, 4, 8, 16, 32, 64
 NO_VERIFY = 1

@@ -1,8 +1,8 @@
-// kv_common.cuh — argument blocks and device helpers of the 8-bit key/value
-// cache kernels (kv_write.cu, kv_read.cu, kv_rows.cu; the C ABI of the
-// operators is in kv_api.cu and include/zc.h).
+// kv_common.cuh — argument blocks and device helpers of the key/value cache
+// kernels (the C ABI of the operators is in kv_api.cu and include/zc.h; what
+// only the 4-bit cache needs is in kv4_common.cuh).
 //
-// The cache. For block b, head h, row r (a token of the block) and column d,
+// The 8-bit cache. For block b, head h, row r (a token of the block) and column d,
 // the number is value(code) * scale[b][h], with E4M3 codes in
 // [block][head][row][column] order and one float32 scale for each block and
 // head, for K and for V apart.
@@ -34,6 +34,9 @@ struct Cache {
     int64_t scale_stride;  // floats
     uint32_t n_blocks, heads, tokens, dim;
     uint32_t sixteenths;   // 2^32 / (tokens / 16), rounded up; 0 for 16 tokens
+    // The 4-bit cache has, instead of scale[], a byte for every 16 columns of a row; scale_stride is bytes then.
+    uint8_t *group[2];
+    uint32_t row;          // bytes of a row's codes
 };
 
 struct Batch {
@@ -57,6 +60,17 @@ struct MoveArgs {  // write and read
     int32_t *d_status;
 };
 
+struct RotateArgs {
+    Batch b;
+    Rows in[2], out[2];      // q, k
+    const void *weight[2];   // or null
+    const uint64_t *turns;
+    uint32_t dim, rot, heads[2];
+    int weight_dtype;
+    float eps;
+    int32_t *d_status;
+};
+
 struct AttendArgs {
     Cache c;
     Batch b;
@@ -76,8 +90,8 @@ struct AttendArgs {
 };
 
 // The codes as tensor maps, K and V: columns, rows of all heads, blocks; a box
-// is `rows` rows of `columns` bytes, swizzled over that width (64 or 128
-// bytes). Columns past head_dim are read as zeros.
+// is `rows` rows of `columns` bytes, swizzled over that width (32, 64 or 128
+// bytes). Columns past a row's bytes are read as zeros.
 struct CodeMaps {
     CUtensorMap code[2];
 };
@@ -85,17 +99,24 @@ int make_maps(const Cache &c, uint32_t columns, uint32_t rows, CodeMaps &m);
 
 int launch_write(int dtype, const MoveArgs &a, cudaStream_t s);
 int launch_read(int dtype, const MoveArgs &a, cudaStream_t s);
+int launch_write4(int dtype, const MoveArgs &a, cudaStream_t s);
+int launch_read4(int dtype, const MoveArgs &a, cudaStream_t s);
+int launch_rotate(int dtype, bool interleaved, const RotateArgs &a, cudaStream_t s);
 int sm_count();
-// Attention of sequences with at most rows_most rows of a head (kv_rows.cu) and
+// Attention over the 8-bit cache and (…4) the 4-bit one, of sequences with at most rows_most rows of a head (kv_rows.cu) and
 // of those with more (kv_tiles.cu), and what their workspaces hold.
 constexpr uint32_t kRowsMost = 16;
 uint64_t rows_counters(const Batch &b, const Cache &c, uint32_t group);
 uint64_t rows_group_counters();
 uint64_t rows_part_bytes(const Cache &c);
 int launch_rows(const AttendArgs &a, cudaStream_t s);
+uint64_t rows4_group_counters();
+uint64_t rows4_part_bytes(const Cache &c);
+int launch_rows4(const AttendArgs &a, cudaStream_t s);
 uint64_t tiles_counters(const Batch &b, const Cache &c, uint32_t group);
 uint64_t tiles_part_bytes(const Cache &c);
 int launch_tiles(const AttendArgs &a, cudaStream_t s);
+int launch_tiles4(const AttendArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
 
@@ -206,6 +227,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, long lo
 __device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int row, int block, uint64_t *bar) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
                      smem_of(dst)), "l"(map), "r"(0), "r"(row), "r"(block), "r"(smem_of(bar)) : "memory");
+}
+// n bytes (a multiple of 16) from 16-byte aligned memory to such shared memory.
+__device__ __forceinline__ void copy_run(void *dst, const void *src, uint32_t n, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_of(dst)), "l"(src),
+                 "r"(n), "r"(smem_of(bar)) : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

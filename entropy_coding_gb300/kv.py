@@ -1,7 +1,11 @@
-"""An 8-bit key/value cache: writing tokens, reading them back, and attention.
+"""A key/value cache in 8 or 4 bits: writing tokens, reading them back, and
+attention; and what queries and keys go through first, their heads' norms and
+the rotation by their positions.
 
-The cache is a pool of blocks of tokens; each block and key/value head has
-E4M3 codes and one float32 scale, for K and for V. A batch names sequences of
+The cache is a pool of blocks of tokens. In the 8-bit one (``KVCache``) each
+block and key/value head has E4M3 codes and one float32 scale, for K and for V;
+in the 4-bit one (``KV4Cache``) each token and head has E2M1 codes and a scale
+byte for every 16 columns. The calls take either. A batch names sequences of
 uneven length by a block table and their lengths, all on the device. The
 operators run in the CUDA kernels of ``libzc.so`` (include/zc.h, zc_kv_*),
 launch on the current stream (or ``stream``, a torch stream or a handle) and
@@ -19,14 +23,16 @@ sums fill of shared and of tensor memory.
 from __future__ import annotations
 
 import ctypes
+import decimal
 
 import torch
 
-__all__ = ["KVCache", "KVBatch", "kv_write", "kv_read", "kv_read_into", "kv_attend", "kv_attend_into"]
+__all__ = ["KVCache", "KV4Cache", "KVBatch", "KVRotation", "kv_write", "kv_read", "kv_read_into", "kv_attend", "kv_attend_into",
+           "kv_rotate", "kv_rotate_into"]
 
 _BF16, _FP16, _FP32 = 4, 5, 6
 _CODE = {torch.bfloat16: _BF16, torch.float16: _FP16, torch.float32: _FP32}
-_CAUSAL = 1
+_CAUSAL, _INTERLEAVED = 1, 2
 HOOK_COPY_STALL = 1  # test hook (zc_kv_set_test_hooks)
 
 
@@ -35,6 +41,12 @@ class _Cache(ctypes.Structure):
                 ("d_v_scale", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
                 ("n_blocks", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32), ("block_tokens", ctypes.c_uint32),
                 ("head_dim", ctypes.c_uint32)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("d_turns", ctypes.c_void_p), ("rot_dim", ctypes.c_uint32), ("flags", ctypes.c_uint32),
+                ("d_q_weight", ctypes.c_void_p), ("d_k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
 
 
 class _Batch(ctypes.Structure):
@@ -50,7 +62,9 @@ class _Rows(ctypes.Structure):
 # Calls that a check found to have reported an error: CTAs that gave up never came to their counters, so that a workspace
 # that was in use before then is zeroed before it is used again.
 _failures = 0
-_entry = None  # zc_kv_write, zc_kv_read, zc_kv_attend and its two sizes, once the library is loaded
+# zc_kv_write, zc_kv_read, zc_kv_attend and its two sizes, the same of the 4-bit cache, and zc_kv_rotate, once the library is
+# loaded; a cache's are those from its _calls on
+_entry = None
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -63,14 +77,18 @@ def _fail(what: str):
 def declare(L: ctypes.CDLL) -> None:
     """Argument types of the zc_kv_* entry points."""
     vp, u32, u64, i32 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int
-    for f in (L.zc_kv_write, L.zc_kv_read):
+    for f in (L.zc_kv_write, L.zc_kv_read, L.zc_kv4_write, L.zc_kv4_read):
         f.restype = i32
         f.argtypes = [vp, vp, i32, vp, vp, vp, vp]
-    L.zc_kv_attend.restype = i32
-    L.zc_kv_attend.argtypes = [vp, vp, i32, u32, vp, vp, vp, ctypes.c_double, u32, u32, vp, u64, vp, vp]
+    for f in (L.zc_kv_attend, L.zc_kv4_attend):
+        f.restype = i32
+        f.argtypes = [vp, vp, i32, u32, vp, vp, vp, ctypes.c_double, u32, u32, vp, u64, vp, vp]
+    L.zc_kv_rotate.restype = i32
+    L.zc_kv_rotate.argtypes = [vp, vp, i32, u32, u32, u32, vp, vp, vp, vp, vp, vp]
     L.zc_kv_set_test_hooks.restype = None
     L.zc_kv_set_test_hooks.argtypes = [u32]
-    for f in (L.zc_kv_attend_workspace_size, L.zc_kv_attend_counter_bytes):
+    for f in (L.zc_kv_attend_workspace_size, L.zc_kv_attend_counter_bytes, L.zc_kv4_attend_workspace_size,
+              L.zc_kv4_attend_counter_bytes):
         f.restype = u64
         f.argtypes = [vp, vp, u32]
 
@@ -81,7 +99,9 @@ def _entries():
     if _entry is None:
         from . import lib
         L = lib()
-        _entry = (L.zc_kv_write, L.zc_kv_read, L.zc_kv_attend, L.zc_kv_attend_workspace_size, L.zc_kv_attend_counter_bytes)
+        _entry = (L.zc_kv_write, L.zc_kv_read, L.zc_kv_attend, L.zc_kv_attend_workspace_size, L.zc_kv_attend_counter_bytes,
+                  L.zc_kv4_write, L.zc_kv4_read, L.zc_kv4_attend, L.zc_kv4_attend_workspace_size, L.zc_kv4_attend_counter_bytes,
+                  L.zc_kv_rotate)
     return _entry
 
 
@@ -104,6 +124,8 @@ class KVCache:
     the block dimension (one layer of several) are fine as long as K and V
     have the same strides. ``KVCache.empty`` allocates one."""
 
+    _calls = 0  # of _entries()
+
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
             _fail("KVCache: k and v are [n_blocks, kv_heads, block_tokens, head_dim] with the same strides")
@@ -120,6 +142,10 @@ class KVCache:
         block_stride, scale_stride = _outer(k, h * b * d, "KVCache: blocks"), _outer(k_scale, h, "KVCache: scales of blocks")
         if not all(t.is_cuda and t.device == k.device for t in (k, v, k_scale, v_scale)):
             _fail("KVCache expects CUDA tensors of one device")
+        self._set(k, v, k_scale, v_scale, block_stride, scale_stride, h, b, d)
+
+    def _set(self, k, v, k_scale, v_scale, block_stride, scale_stride, h, b, d) -> None:
+        n = k.shape[0]
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_blocks, self.kv_heads, self.block_tokens, self.head_dim = n, h, b, d
         self.device, self._index = k.device, k.device.index
@@ -169,6 +195,45 @@ class KVCache:
             raise ZcError(st, "zc_kv (device)")
 
 
+class KV4Cache(KVCache):
+    """A pool of cache blocks in 4 bits, over tensors that the caller owns.
+
+    ``k``, ``v``: uint8 CUDA tensors [n_blocks, kv_heads, block_tokens, row] of
+    E2M1 codes, two columns to a byte (the even one in the low half) and row =
+    (head_dim + 31) // 32 * 16 bytes; ``k_scale``, ``v_scale``: uint8 [n_blocks,
+    kv_heads, block_tokens, head_dim / 16], the bits 14 to 7 of a float16: a
+    number is code * scale. All are contiguous within a block; slices of a
+    larger pool along the block dimension are fine as long as K and V have the
+    same strides and blocks begin on 16 bytes. ``KV4Cache.empty`` allocates
+    one. Every call that takes a ``KVCache`` takes it."""
+
+    _calls = 5
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if any(t.dim() != 4 or t.dtype != torch.uint8 for t in (k, v, k_scale, v_scale)):
+            _fail("KV4Cache: codes and scales are uint8 [n_blocks, kv_heads, block_tokens, ...]")
+        n, h, b, row = k.shape
+        groups = k_scale.shape[3]
+        if k.shape != v.shape or k.stride() != v.stride() or k_scale.shape != v_scale.shape or k_scale.stride() != v_scale.stride():
+            _fail("KV4Cache: K and V have the same sizes and strides")
+        if k_scale.shape[:3] != k.shape[:3] or row != (groups + 1) // 2 * 16:
+            _fail("KV4Cache: scales are [n_blocks, kv_heads, block_tokens, head_dim / 16], rows of codes (head_dim + 31) // 32 * 16 bytes")
+        if k.stride()[1:] != (b * row, row, 1) or k_scale.stride()[1:] != (b * groups, groups, 1):
+            _fail("KV4Cache: a block's codes, and its scales, are contiguous")
+        strides = _outer(k, h * b * row, "KV4Cache: blocks"), _outer(k_scale, h * b * groups, "KV4Cache: scales of blocks")
+        if not all(t.is_cuda and t.device == k.device for t in (k, v, k_scale, v_scale)):
+            _fail("KV4Cache expects CUDA tensors of one device")
+        self._set(k, v, k_scale, v_scale, *strides, h, b, 16 * groups)
+
+    @classmethod
+    def empty(cls, n_blocks: int, kv_heads: int, head_dim: int, block_tokens: int = 64, device="cuda") -> "KV4Cache":
+        """A cache of zeros."""
+        shape = (n_blocks, kv_heads, block_tokens)
+        k, v, ks, vs = (torch.zeros(*shape, m, dtype=torch.uint8, device=device)
+                        for m in ((head_dim + 31) // 32 * 16,) * 2 + (head_dim // 16,) * 2)
+        return cls(k, v, ks, vs)
+
+
 class KVBatch:
     """The sequences of a call: their block table, their new tokens and their
     lengths with them, made once for all layers of a step.
@@ -216,7 +281,7 @@ class KVBatch:
         if stream is not None:
             with _on(stream, cache.device):
                 return self._workspace(cache, heads, None, handle)
-        key = (cache.kv_heads, cache.head_dim, heads, handle)
+        key = (cache.kv_heads, cache.head_dim, heads, handle, cache._calls)
         ws = self._ws.get(key)
         if ws is not None and ws[3] == _failures:
             return ws
@@ -224,9 +289,9 @@ class KVBatch:
         if ws is None:
             if capturing:
                 for k, other in self._ws.items():
-                    if k[:3] == key[:3] and other[3] == _failures:
+                    if k[:3] == key[:3] and k[4] == key[4] and other[3] == _failures:
                         return other
-            size, counters = (int(f(cache._ref, self._ref, heads)) for f in _entries()[3:])
+            size, counters = (int(f(cache._ref, self._ref, heads)) for f in _entries()[cache._calls + 3:cache._calls + 5])
             t = torch.empty(max(size, 16), dtype=torch.uint8, device=cache.device)
             ws = [t.data_ptr(), size, t, -1, t[:counters]]
         ws[4].zero_()
@@ -299,15 +364,15 @@ def _move(fn, what, cache, batch, k, v, stream):
 
 
 def kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
-    """Quantise the batch's tokens into the cache (zc_kv_write). ``k``, ``v``:
+    """Quantise the batch's tokens into the cache (zc_kv_write, zc_kv4_write). ``k``, ``v``:
     [total_tokens, kv_heads, head_dim] in bfloat16, float16 or float32, any
     strides that are multiples of 16 bytes (views of a fused projection)."""
-    _move(_entries()[0], "zc_kv_write", cache, batch, k, v, stream)
+    _move(_entries()[cache._calls], "zc_kv_write", cache, batch, k, v, stream)
 
 
 def kv_read_into(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """Read the batch's tokens back into ``k`` and ``v`` (zc_kv_read)."""
-    _move(_entries()[1], "zc_kv_read", cache, batch, k, v, stream)
+    _move(_entries()[cache._calls + 1], "zc_kv_read", cache, batch, k, v, stream)
 
 
 def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16, stream=None):
@@ -327,7 +392,7 @@ def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16,
         with _on(stream, device):
             k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
     rk, rv = _Rows(k.data_ptr(), heads * dim, dim), _Rows(v.data_ptr(), heads * dim, dim)
-    _check(_entries()[1](cache._ref, batch._ref, code, ctypes.addressof(rk), ctypes.addressof(rv), cache._status,
+    _check(_entries()[cache._calls + 1](cache._ref, batch._ref, code, ctypes.addressof(rk), ctypes.addressof(rv), cache._status,
                          _handle(stream, cache)), "zc_kv_read")
     return k, v
 
@@ -339,10 +404,10 @@ def _attend(cache, batch, code, heads, q, out, lse, scale, causal, window, strea
     if not 0 <= window <= 0x7FFFFFFF:
         _fail("zc_kv_attend: window >= 0")
     handle = _handle(stream, cache)
-    ws = batch._ws.get((cache.kv_heads, cache.head_dim, heads, handle))
+    ws = batch._ws.get((cache.kv_heads, cache.head_dim, heads, handle, cache._calls))
     if ws is None or ws[3] != _failures:
         ws = batch._workspace(cache, heads, stream, handle)
-    _check(_entries()[2](cache._ref, batch._ref, code, heads, ctypes.addressof(q), ctypes.addressof(out), lse,
+    _check(_entries()[cache._calls + 2](cache._ref, batch._ref, code, heads, ctypes.addressof(q), ctypes.addressof(out), lse,
                          cache.head_dim ** -0.5 if scale is None else scale, _CAUSAL if causal else 0, window, ws[0],
                          ws[1], cache._status, handle), "zc_kv_attend")
 
@@ -392,3 +457,122 @@ def kv_attend(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | No
     _attend(cache, batch, code, heads, rq, _Rows(out.data_ptr(), heads * dim, dim), lse.data_ptr(), scale, causal, window,
             stream)
     return out, lse
+
+
+class KVRotation:
+    """The angles of a position rotation, made once for a model.
+
+    ``frequencies``: radians that each pair of columns turns by for one
+    position, numbers or a float tensor, a multiple of 8 of them (usually
+    base ** (-2 i / rot_dim), or scaled as a model's long-context recipe wants);
+    they are kept as 64-bit fractions of a turn, so that an angle is as good at
+    position 10^9 as at 1. Pair i is the columns i and i + rot_dim / 2, or 2 i and
+    2 i + 1 (``interleaved``); columns from rot_dim = 2 * len(frequencies) on
+    are not turned."""
+
+    def __init__(self, frequencies, interleaved: bool = False, device="cuda"):
+        numbers = frequencies.double().flatten().tolist() if isinstance(frequencies, torch.Tensor) else [float(f) for f in frequencies]
+        if len(numbers) % 8 or len(numbers) > 64 or not all(abs(f) < 2.0 ** 20 for f in numbers):
+            _fail("KVRotation: a multiple of 8 frequencies, up to 64, finite and below 2^20")
+        turns = [fraction_of_turn(f) for f in numbers]
+        self.rot_dim, self.interleaved = 2 * len(turns), bool(interleaved)
+        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.device, self._index = self.turns.device, self.turns.device.index
+        self._ready = None
+        if self.turns.is_cuda:
+            with torch.cuda.device(self.device):
+                self._ready = torch.cuda.Event()
+                self._ready.record()
+                self._streams = {_raw_stream(self._index)}  # that come after the table was made
+
+    def _meet(self, handle: int) -> None:
+        """As KVCache._meet, for the table."""
+        stream = torch.cuda.ExternalStream(handle, device=self.device)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+            stream.wait_event(self._ready)
+            self.turns.record_stream(stream)
+        self._streams.add(handle)
+
+
+_TAU = decimal.Decimal("6.28318530717958647692528676655900576839433879875021")
+
+
+def fraction_of_turn(frequency: float) -> int:
+    """A frequency in radians as a fraction of a turn in units of 2^-64, modulo a turn."""
+    with decimal.localcontext(decimal.Context(prec=60)):
+        return int((decimal.Decimal(frequency) / _TAU * (1 << 64)).to_integral_value()) % (1 << 64)
+
+
+def _rotate(cache, batch, rotation, code, rows, heads, q_weight, k_weight, eps, stream):
+    if cache._many and _elsewhere(cache, batch, "zc_kv_rotate"):
+        with torch.cuda.device(cache._index):
+            return _rotate(cache, batch, rotation, code, rows, heads, q_weight, k_weight, eps, stream)
+    if rotation._index != cache._index:
+        _fail("zc_kv_rotate: the rotation is on another device than the cache")
+    kind = 0
+    for w in (q_weight, k_weight):
+        if w is None:
+            continue
+        if w.shape != (cache.head_dim,) or w.device != cache.device or w.dtype not in _CODE or not w.is_contiguous():
+            _fail("zc_kv_rotate: weights are [head_dim], contiguous, on the cache's device")
+        if kind not in (0, _CODE[w.dtype]) or _CODE[w.dtype] not in (code, _FP32):
+            _fail("zc_kv_rotate: both weights are float32, or of q's type")
+        kind = _CODE[w.dtype]
+    handle = _handle(stream, cache)
+    if handle not in rotation._streams:
+        rotation._meet(handle)
+    r = _Rotation(rotation.turns.data_ptr() if rotation.rot_dim else None, rotation.rot_dim,
+                  _INTERLEAVED if rotation.interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
+                  None if k_weight is None else k_weight.data_ptr(), kind, eps)
+    _check(_entries()[10](batch._ref, ctypes.addressof(r), code, cache.head_dim, heads, cache.kv_heads,
+                          *map(ctypes.addressof, rows), cache._status, handle), "zc_kv_rotate")
+
+
+def _pair(cache, batch, q, k, what=""):
+    """Type code, query heads and rows of queries and keys."""
+    code = _CODE.get(q.dtype)
+    if code is None or k.dtype != q.dtype:
+        _fail("zc_kv_rotate: q and k are bfloat16, float16 or float32")
+    heads = q.shape[1] if q.dim() == 3 else 0
+    return code, heads, [_rows(q, (batch.total_tokens, heads, cache.head_dim), cache.device, "q" + what),
+                         _rows(k, (batch.total_tokens, cache.kv_heads, cache.head_dim), cache.device, "k" + what)]
+
+
+def kv_rotate_into(cache: KVCache, batch: KVBatch, rotation: KVRotation, q: torch.Tensor, k: torch.Tensor, q_out: torch.Tensor,
+                   k_out: torch.Tensor, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                   eps: float = 1e-6, stream=None) -> None:
+    """``kv_rotate`` into ``q_out`` and ``k_out``, which may be ``q`` and ``k``
+    themselves but may not overlap with them otherwise."""
+    code, heads, rows = _pair(cache, batch, q, k)
+    out, heads_out, rows_out = _pair(cache, batch, q_out, k_out, "_out")
+    if out != code or heads_out != heads:
+        _fail("zc_kv_rotate: the outputs have q's type and heads")
+    for x, y in ((q, q_out), (k, k_out)):
+        if x.data_ptr() == y.data_ptr() and x.stride() != y.stride():
+            _fail("zc_kv_rotate: outputs in place have the inputs' strides")
+    _rotate(cache, batch, rotation, code, rows + rows_out, heads, q_weight, k_weight, eps, stream)
+
+
+def kv_rotate(cache: KVCache, batch: KVBatch, rotation: KVRotation, q: torch.Tensor, k: torch.Tensor,
+              q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6, stream=None):
+    """Queries and keys as they are attended with and written: (q, k), each
+    head's columns divided by their root mean square (with ``eps``) and
+    multiplied by the weights, where these are given (float32 or q's type,
+    [head_dim]), and turned by the token's position in its sequence
+    (zc_kv_rotate). ``q`` [total_tokens, heads, head_dim], ``k``
+    [total_tokens, kv_heads, head_dim] in bfloat16, float16 or float32, any
+    strides that are multiples of 16 bytes (views of a fused projection).
+    Sums are float32, and a number is rounded once."""
+    code, heads, rows = _pair(cache, batch, q, k)
+    if stream is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=cache.device)
+    else:
+        with _on(stream, cache.device):
+            q_out, k_out = (torch.empty(x.shape, dtype=q.dtype, device=cache.device) for x in (q, k))
+    dim = cache.head_dim
+    rows += [_Rows(q_out.data_ptr(), heads * dim, dim), _Rows(k_out.data_ptr(), cache.kv_heads * dim, dim)]
+    _rotate(cache, batch, rotation, code, rows, heads, q_weight, k_weight, eps, stream)
+    return q_out, k_out

@@ -476,6 +476,93 @@ ZC_API uint64_t zc_kv_attend_workspace_size(const zc_kv_cache *cache, const zc_k
  * counters. The rest may hold anything. */
 ZC_API uint64_t zc_kv_attend_counter_bytes(const zc_kv_cache *cache, const zc_kv_batch *batch, uint32_t heads);
 
+/* ---------------------------------------------------------------------------
+ * The same cache in 4 bits. A row of a block (one token of one head) is
+ * head_dim E2M1 codes (sign, 2 exponent bits, 1 fraction bit: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6), two columns to a byte with the even one in the low half, and
+ * one scale byte for every 16 columns: bits 14 to 7 of an IEEE half without its
+ * sign (5 exponent bits, 3 fraction bits: 2^-17 to 10240 are 0x01 to 0xE2). A
+ * number is code * scale, at most 6 significant bits: exact in every type
+ * here. A scale byte of 0xFF makes its 16 numbers NaN; what numbers stand
+ * under 0xE3 to 0xFE is unspecified.
+ *   d_k, d_v        codes [n_blocks][kv_heads][block_tokens][row], rows of
+ *                   (head_dim + 31) / 32 * 16 bytes (what is behind the last
+ *                   column is neither used nor written), blocks block_stride
+ *                   bytes apart
+ *   d_k_scale, ...  bytes [n_blocks][kv_heads][block_tokens][head_dim / 16],
+ *                   blocks scale_stride bytes apart
+ *   All four are 16-byte aligned, the strides multiples of 16 and no less than
+ *   a block's bytes; the other fields are zc_kv_cache's. */
+typedef struct {
+    void *d_k, *d_v;
+    uint8_t *d_k_scale, *d_v_scale;
+    int64_t block_stride, scale_stride;
+    uint32_t n_blocks, kv_heads, block_tokens, head_dim;
+} zc_kv4_cache;
+
+/* zc_kv_write for it. For each 16 columns of a row let a be the largest finite
+ * magnitude: the scale is the one nearest to a / 6 (ties to the even byte) of
+ * 0x01 to 0xE2, the codes those nearest to x / scale (ties to the even code,
+ * magnitudes beyond 6 become 6, infinities too). If one of the 16 is NaN, the
+ * scale byte is 0xFF and the codes are 0. Rows do not depend on one another:
+ * only the new tokens' are written. No two tokens of a call may have one
+ * place in a block. */
+ZC_API int zc_kv4_write(const zc_kv4_cache *cache, const zc_kv_batch *batch, int dtype, const zc_kv_rows *k,
+                        const zc_kv_rows *v, int32_t *d_status, void *stream);
+
+/* zc_kv_read for it: the numbers, exact in every type. */
+ZC_API int zc_kv4_read(const zc_kv4_cache *cache, const zc_kv_batch *batch, int dtype, const zc_kv_rows *k,
+                       const zc_kv_rows *v, int32_t *d_status, void *stream);
+
+/* zc_kv_attend for it, with the workspace sizes of its own two functions. The
+ * weights are rounded to half in units of the row's largest (a weight below
+ * 2^-23 of it loses up to 2^-34 of it); keys and values are exact. */
+ZC_API int zc_kv4_attend(const zc_kv4_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
+                         const zc_kv_rows *q, const zc_kv_rows *out, float *d_lse, double scale, uint32_t flags,
+                         uint32_t window, void *d_ws, uint64_t ws_bytes, int32_t *d_status, void *stream);
+ZC_API uint64_t zc_kv4_attend_workspace_size(const zc_kv4_cache *cache, const zc_kv_batch *batch, uint32_t heads);
+ZC_API uint64_t zc_kv4_attend_counter_bytes(const zc_kv4_cache *cache, const zc_kv_batch *batch, uint32_t heads);
+
+/* ---------------------------------------------------------------------------
+ * What a batch's queries and keys go through before they are written and
+ * attended with: a norm over each head's columns, and the rotation of pairs of
+ * columns by an angle that grows with the token's position. For each row x
+ * (one token of one head) of q and of k:
+ *   y = x * w / sqrt(mean(x^2) + eps)    where q's (k's) weights w are given,
+ *   y = x                                else;
+ *   (y_a, y_b) becomes (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+ * for the pairs i < rot_dim / 2, with t = 2 pi p turns[i] / 2^64 at position
+ * p = lens[s] - n + i of the batch; columns from rot_dim on are not turned.
+ * Everything is float32 (angles: 2^-34 of a turn before their sine and
+ * cosine), rounded once.
+ *   d_turns       NULL with rot_dim = 0, else uint64 [rot_dim / 2]: the fraction of a turn
+ *                 that a pair turns by for each position, in units of 2^-64
+ *   rot_dim       0 or a multiple of 16 up to head_dim
+ *   flags         ZC_KV_INTERLEAVED: pair i is columns 2 i and 2 i + 1; else i
+ *                 and i + rot_dim / 2
+ *   d_q_weight, d_k_weight  NULL or [head_dim] of weight_dtype
+ *   weight_dtype  ZC_FP32 or the dtype of q and k; not looked at without weights
+ *   eps           positive and finite; not looked at without weights */
+#define ZC_KV_INTERLEAVED 2u
+typedef struct {
+    const uint64_t *d_turns;
+    uint32_t rot_dim, flags;
+    const void *d_q_weight, *d_k_weight;
+    int weight_dtype;
+    float eps;
+} zc_kv_rotation;
+
+/*   dtype             ZC_BF16, ZC_FP16 or ZC_FP32: of q, k and the outputs
+ *   head_dim          a multiple of 16 up to 128
+ *   heads, kv_heads   of q and of k, 1 to 65535
+ *   q_out, k_out      may be q and k themselves (the same address and strides),
+ *                     or tensors that do not overlap with them
+ * Of the batch only the counts and lengths are looked at; rows of tokens that
+ * belong to no sequence are left as they were. */
+ZC_API int zc_kv_rotate(const zc_kv_batch *batch, const zc_kv_rotation *rotation, int dtype, uint32_t head_dim,
+                        uint32_t heads, uint32_t kv_heads, const zc_kv_rows *q, const zc_kv_rows *k,
+                        const zc_kv_rows *q_out, const zc_kv_rows *k_out, int32_t *d_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
