@@ -15,10 +15,12 @@
 // together by key before that, in nibbles, since a product's inner index runs
 // along the keys.
 //
-// A step's codes come as boxes of 16 rows, its scales as 16 rows in one run of
-// memory. The order of keys in a score tile is free as long as their weights
+// A step's codes come as a box of 32 rows (or two of 16), its scales as one of
+// lines, a line for 16 rows. The order of keys in a score tile is free as long as their weights
 // meet their values: it is chosen (`key_of`) so that reading a fragment of keys
 // and one of values both meet all banks.
+#include <cstddef>
+
 #include "kv4_common.cuh"
 #include "kv_rows.cuh"
 
@@ -26,71 +28,96 @@ namespace zc {
 namespace kv {
 namespace {
 
+constexpr int kResidentMost = 3;
+
 template <int DP> struct Codes4 {
-    static constexpr int kDim = DP, kSlice = 32, kRow = DP / 2;
-    static constexpr int kResident = 3, kStages = 3 * (128 / DP);
+    static constexpr int kDim = DP, kWarps = 4, kSlice = 32, kRow = DP / 2;
+    static constexpr int kStages = 3 * (128 / DP);
+    // CTAs of an SM: 3 hold the registers of one tile of rows (4 of fewer registers, with two steps of a ring each, take as
+    // long), 2 those of two tiles (16 sequences of 16 rows: 23.7 us, with 3 and spilled registers 26.7).
+    template <int NT> static constexpr int resident() { return NT == 1 ? 3 : 2; }
+    static constexpr bool kMergeInRing = true;
+    // (64 sequences of up to 8192 keys: 0 units 83.5 us, with the CTAs that have many short items last, 2 units 74.4, 3 units
+    // 73.8, 4 units 73.2, 6 units 73.9)
+    static constexpr uint32_t kFixed = 4;
     struct Stage {
         uint8_t k[kSlice * kRow];
         uint8_t v[kSlice * kRow];
-        uint8_t ks[2][DP], vs[2][DP];  // of each half's 16 rows, dim / 16 bytes a row
+        uint8_t ks[2][kScaleLine], vs[2][kScaleLine];  // a line for each half's 16 rows, dim / 16 bytes a row
     };
-    static_assert(sizeof(Stage) % (4 * DP) == 0, "boxes begin where their swizzle does");
-    // What a warp keeps in shared memory besides its ring: the ring's barriers, and the blocks of both halves of 64 of its
-    // steps, read 32 at a time.
+    static_assert(sizeof(Stage) % 128 == 0 && offsetof(Stage, ks) % 128 == 0 && 16 * kRow % 128 == 0, "boxes begin on multiples of 128 bytes");
+    static_assert(kStages - 1 <= 16 && sizeof(Stage) % (4 * DP) == 0, "boxes begin where their swizzle does");
+    using Maps = CodeMaps4;
+    // What a warp keeps in shared memory besides its ring: the ring's barriers, and where 32 of its steps are, looked up 16
+    // at a time: a step's block and row in it, or those of its halves.
+    static constexpr int kLook = 16;
     struct Warp {
         uint64_t full[kStages];
-        int32_t block[2 * kAhead][2];
+        int2 place[2 * kLook][2];
     };
     // Row 0 to 7 of a score tile's half: a key of 8. With rows of 64 bytes, swizzled over 64, the 8 lanes that read together
     // have two keys of different parity (of keys) or four whose 16-byte chunks lie apart (of values); with rows of 32 bytes
     // four keys that differ modulo 4 both times.
     static __device__ __forceinline__ int key_of(int r) { return int((DP == 128 ? 0x65742130u : 0x57463120u) >> 4 * r & 7); }
     static __device__ __forceinline__ void look_up(const AttendArgs &a, Warp &wp, const Job &job, int k0);
-    static __device__ __forceinline__ void fetch(const AttendArgs &a, const CodeMaps &maps, Warp &wp, Stage *ring, const Job &job, int k, uint32_t st);
+    static __device__ __forceinline__ void fetch(const AttendArgs &a, const CodeMaps4 &maps, Warp &wp, Stage *ring, const Job &job, int k, uint32_t st);
     template <int NT>
-    static __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMaps &maps, Warp &wp, Stage *ring, const Job &job,
+    static __device__ __forceinline__ bool attend_slices(const AttendArgs &a, const CodeMaps4 &maps, Warp &wp, Stage *ring, const Job &job,
                                                          uint32_t turn, Sums<DP, NT> &acc);
 };
 
-// Which 16 keys (of the sequence) a half of step k holds: its own, or, where the rows see none of them, the nearest that
-// they do see, again.
-__device__ __forceinline__ uint32_t sixteen_of(const Job &job, int k, int half) {
-    return uint32_t(min(max(2 * (job.first + k * kWarps) + half, job.all_lo / 16), (job.all_hi - 1) / 16));
-}
+// Blocks of a multiple of 32 tokens hold a step's keys in one run of 32 rows; of others a step is two boxes of 16.
+__device__ __forceinline__ bool in_halves(const AttendArgs &a) { return a.c.tokens % 32; }
 
-// The blocks of steps k0 .. k0 + 31, a step a lane. A block that is not there is read as block 0.
+// Where steps k0 .. k0 + 15 are, a half of a step a lane. A block that is not there is read as block 0, a half of which the
+// rows see nothing as the nearest 16 keys that they do see.
 template <int DP> __device__ __forceinline__ void Codes4<DP>::look_up(const AttendArgs &a, Warp &wp, const Job &job, int k0) {
-    const int k = k0 + (threadIdx.x & 31);
-    if (k >= job.steps) return;
-#pragma unroll
-    for (int half = 0; half < 2; half++)
-        wp.block[k & (2 * kAhead - 1)][half] =
-            int32_t(max(read_block(a.b, a.c, job.seq.s, block_of_16(a.c, sixteen_of(job, k, half)), a.d_status), int64_t(0)));
+    const int half = threadIdx.x & 1, k = k0 + (threadIdx.x & 31) / 2;
+    if (k >= job.steps || (half && !in_halves(a))) return;
+    uint32_t i = uint32_t(2 * (job.first + k * kWarps) + half);
+    if (in_halves(a)) i = min(max(i, uint32_t(job.all_lo / 16)), uint32_t((job.all_hi - 1) / 16));
+    const uint32_t blk = block_of_16(a.c, i);
+    wp.place[k & (2 * kLook - 1)][half] = make_int2(int(max(read_block(a.b, a.c, job.seq.s, blk, a.d_status), int64_t(0))),
+                                                    int(job.h * a.c.tokens + i * 16 - blk * a.c.tokens));
 }
 
-// Asks for step k's keys and values, a half a lane. Rows that nobody sees come along as they are.
+// Asks for step k's keys and values (one lane). Rows that nobody sees come along as they are.
 template <int DP>
-__device__ __forceinline__ void Codes4<DP>::fetch(const AttendArgs &a, const CodeMaps &maps, Warp &wp, Stage *ring, const Job &job, int k, uint32_t st) {
-    const int half = threadIdx.x & 31;
-    if (half < 2 && k < job.steps && !a.stall) {
+__device__ __forceinline__ void Codes4<DP>::fetch(const AttendArgs &a, const CodeMaps4 &maps, Warp &wp, Stage *ring, const Job &job, int k, uint32_t st) {
+    if ((threadIdx.x & 31) == 0 && k < job.steps && !a.stall) {
         Stage &sl = ring[st];
         uint64_t *bar = &wp.full[st];
-        // (the phase waits for this one arrival; bytes that come before it is made are counted all the same)
-        if (half == 0) bar_expect(bar, 2 * kSlice * kRow + 4 * a.c.dim);
-        const uint32_t i = sixteen_of(job, k, half);
-        const uint32_t row = job.h * a.c.tokens + i * 16 - block_of_16(a.c, i) * a.c.tokens;
-        const int32_t id = wp.block[k & (2 * kAhead - 1)][half];
-        const int64_t at = id * a.c.scale_stride + int64_t(row) * (a.c.dim / 16);
-        copy_box(sl.k + half * 16 * kRow, &maps.code[0], int(row), id, bar);
-        copy_box(sl.v + half * 16 * kRow, &maps.code[1], int(row), id, bar);
-        copy_run(sl.ks[half], a.c.group[0] + at, a.c.dim, bar);
-        copy_run(sl.vs[half], a.c.group[1] + at, a.c.dim, bar);
+        bar_expect(bar, sizeof(Stage));
+#pragma unroll 1
+        for (int half = 0;; half++) {
+            const int2 at = wp.place[k & (2 * kLook - 1)][half];
+            copy_box(sl.k + half * 16 * kRow, &maps.code[0], at.y, at.x, bar);
+            copy_box(sl.v + half * 16 * kRow, &maps.code[1], at.y, at.x, bar);
+            copy_box(sl.ks[half], &maps.scale[0], at.y / 16, at.x, bar);
+            copy_box(sl.vs[half], &maps.scale[1], at.y / 16, at.x, bar);
+            if (half || !in_halves(a)) break;
+        }
     }
+}
+
+// The low half of each byte of x, the high half of each of y.
+__device__ __forceinline__ uint32_t low_halves(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(x), "r"(y), "r"(0x0F0F0F0Fu));  // (x & m) | (y & ~m)
+    return r;
+}
+// x, y = a0 b0 + c0, a1 b1 + c1; x + a, y + b
+__device__ __forceinline__ void fma_pair(float &x, float &y, float a0, float a1, const float (&b)[2], const float (&c)[2]) {
+    asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}"
+        : "=f"(x), "=f"(y) : "f"(a0), "f"(a1), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
+__device__ __forceinline__ void add_pair(float (&x)[2], float a, float b) {
+    asm("{.reg .b64 c, d; mov.b64 c, {%0, %1}; mov.b64 d, {%2, %3}; add.rn.f32x2 c, c, d; mov.b64 {%0, %1}, c;}" : "+f"(x[0]), "+f"(x[1]) : "f"(a), "f"(b));
 }
 
 template <int DP>
 template <int NT>
-__device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, const CodeMaps &maps, Warp &wp, Stage *ring, const Job &job,
+__device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, const CodeMaps4 &maps, Warp &wp, Stage *ring, const Job &job,
                                                           uint32_t turn, Sums<DP, NT> &acc) {
     constexpr int kRows = 8 * NT, S = kStages;
     constexpr int kSteps = DP / 16;      // inner steps of k q, and column tiles of the output
@@ -106,7 +133,24 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
     uint32_t qf[NT][kSteps][2];
     float row_scale[NT][2];  // of rows 2t, 2t + 1 of each tile
     load_queries<DP, NT>(a, job, qf, row_scale);
+    // Scores stay products until their exponentials: a row's scale is positive for that, with its sign in the queries. (And
+    // not 0, since a score that is left out is -infinity: 1e-37 of any product of half numbers is none.)
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+#pragma unroll
+        for (int i = 0; i < kSteps; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) qf[n][i][j] ^= a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int e = 0; e < 2; e++) row_scale[n][e] = fmaxf(fabsf(row_scale[n][e]), 1e-37f);
+    }
     acc.clear();
+    // What a weight's exponent is raised by, and the product of a row and a key from which on its maximum is followed.
+    float raised[NT][2], most[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) raised[n][e] = kRaise, most[n][e] = kNone;
 
     // This thread's keys of a half: key_of(g) and 8 more for scores, four for values; its groups of columns.
     const int key_g = key_of(g), key_v0 = key_of(2 * t), key_v1 = key_of(2 * t + 1);
@@ -118,9 +162,9 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
 
     uint32_t st = turn % S, parity = turn / S & 1;  // of step k
     for (int k = 0; k < job.steps; k++) {
-        if ((k & (kAhead - 1)) == 0) {
+        if ((k & (kLook - 1)) == 0) {
             __syncwarp();
-            look_up(a, wp, job, k + kAhead);
+            look_up(a, wp, job, k + kLook);
         }
         if (!__all_sync(0xFFFFFFFFu, bar_wait(&wp.full[st], parity, a.limit))) {
             drain<Codes4>(a, wp, turn + k, job.steps - k);
@@ -132,16 +176,10 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
         Stage &sl = ring[st];
         if (++st == S) st = 0, parity ^= 1;
         const int key0 = (job.first + k * kWarps) * kSlice;
-
         // Scores of 2 x 16 keys and the rows: c0, c1 are key key_of(g) and rows 2t, 2t + 1, c2, c3 the key 8 on.
-        // (two sums for a single tile: half the chain of dependent products)
-        constexpr int kSums = NT == 1 ? 2 : 1;
         float sc[2][NT][4];
 #pragma unroll
         for (int half = 0; half < 2; half++) {
-            float part[kSums][NT][4];
-#pragma unroll
-            for (int n = 0; n < kSums * NT; n++) part[n / NT][n % NT][0] = part[n / NT][n % NT][1] = part[n / NT][n % NT][2] = part[n / NT][n % NT][3] = 0.0f;
             uint32_t w[2][kRun / 8], s[2][kGroups];
 #pragma unroll
             for (int j = 0; j < 2; j++) {
@@ -170,13 +208,11 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
 #pragma unroll
                 for (int x = 0; x < 2; x++)
 #pragma unroll
-                    for (int n = 0; n < NT; n++) mma(part[x % kSums][n], kf[x], qf[n][2 * i + x][0], qf[n][2 * i + x][1]);
+                    for (int n = 0; n < NT; n++) {
+                        if (i == 0 && x == 0) mma_first(sc[half][n], kf[x], qf[n][0][0], qf[n][0][1]);
+                        else mma(sc[half][n], kf[x], qf[n][2 * i + x][0], qf[n][2 * i + x][1]);
+                    }
             }
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    sc[half][n][j] = (kSums == 1 ? part[0][n][j] : part[0][n][j] + part[kSums - 1][n][j]) * row_scale[n][j & 1];
         }
         const bool edge = key0 < job.x_lo || key0 + kSlice > job.x_hi;  // some row does not see all of it
         if (edge) {
@@ -201,7 +237,7 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 top[n][e] = fmaxf(fmaxf(sc[0][n][e], sc[0][n][2 + e]), fmaxf(sc[1][n][e], sc[1][n][2 + e]));
-                grows |= top[n][e] > m[n][e] + kSlackW;
+                grows |= top[n][e] > most[n][e];
             }
         if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
@@ -211,10 +247,12 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
                 for (int e = 0; e < 2; e++) {
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(0xFFFFFFFFu, top[n][e], d));
-                    const float m1 = fmaxf(m[n][e], top[n][e]);
+                    const float m1 = fmaxf(m[n][e], top[n][e] * row_scale[n][e]);
                     down[e] = ratio2(m[n][e], m1);
                     l[n][e] *= down[e];
                     m[n][e] = m1;
+                    raised[n][e] = kRaise - (m1 == kNone ? 0.0f : m1);
+                    most[n][e] = (m1 + kSlackW) / row_scale[n][e];
                 }
 #pragma unroll
                 for (int c = 0; c < kSteps; c++)
@@ -224,20 +262,17 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
         // Weights 2^(s - m + kRaise).
         uint32_t pf[2][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-            float base[2];
+        for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int e = 0; e < 2; e++) base[e] = (m[n][e] == kNone ? 0.0f : m[n][e]) - kRaise;
+            for (int half = 0; half < 2; half++)
 #pragma unroll
-            for (int half = 0; half < 2; half++) {
-                float p[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) p[j] = ex2(sc[half][n][j] - base[j & 1]);
-                l[n][0] += p[0] + p[2], l[n][1] += p[1] + p[3];
-                pf[half][n][0] = transpose8(half2_of(p[0], p[1]));
-                pf[half][n][1] = transpose8(half2_of(p[2], p[3]));
-            }
-        }
+                for (int j = 0; j < 2; j++) {
+                    float p0, p1;
+                    fma_pair(p0, p1, sc[half][n][2 * j], sc[half][n][2 * j + 1], row_scale[n], raised[n]);
+                    p0 = ex2(p0), p1 = ex2(p1);
+                    add_pair(l[n], p0, p1);
+                    pf[half][n][j] = transpose8(half2_of(p0, p1));
+                }
         if (edge) {
             // A row that does not see a key has weight 0 for it, but 0 times NaN (or an infinity) is NaN: scales that make
             // these are taken out here and given to the rows that do see them.
@@ -288,7 +323,7 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
                     const uint32_t x = w[2 * j][i], y = w[2 * j + 1][i];
-                    const uint32_t even = (x & 0x0F0F0F0Fu) | (y << 4 & 0xF0F0F0F0u), odd = (x >> 4 & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+                    const uint32_t even = low_halves(x, y << 4), odd = low_halves(x >> 4, y);
                     uint32_t h[4];
                     e2m1x8_to_half2x4(even, h[0], h[1], h[2], h[3]);
 #pragma unroll
@@ -312,15 +347,16 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
 }
 
 template <int NT> int launch_tiles_of(const AttendArgs &a, cudaStream_t s) {
-    return a.c.dim <= 64 ? launch<Codes4<64>, NT>(a, 32, s) : launch<Codes4<128>, NT>(a, 64, s);
+    const uint32_t rows = a.c.tokens % 32 ? 16 : 32;
+    return a.c.dim <= 64 ? launch<Codes4<64>, NT>(a, rows, s) : launch<Codes4<128>, NT>(a, rows, s);
 }
 
 } // namespace
 
-uint64_t rows4_group_counters() { return uint64_t(sm_count()) * Codes4<128>::kResident * 2; }
+uint64_t rows4_group_counters() { return uint64_t(sm_count()) * kResidentMost * 2; }
 
 uint64_t rows4_part_bytes(const Cache &c) {
-    return uint64_t(sm_count()) * Codes4<128>::kResident * 2 * (c.dim <= 64 ? sizeof(Part<64, 2>) : sizeof(Part<128, 2>));
+    return uint64_t(sm_count()) * kResidentMost * 2 * (c.dim <= 64 ? sizeof(Part<64, 2>) : sizeof(Part<128, 2>));
 }
 
 // One tile of 8 rows or two.

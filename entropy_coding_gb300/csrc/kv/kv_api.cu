@@ -20,7 +20,11 @@ int sm_count() {
     return sms;
 }
 
-int make_maps(const Cache &c, uint32_t columns, uint32_t rows, CodeMaps &m) {
+namespace {
+
+// A map of bytes [blocks][lines][line], blocks `stride` apart, whose boxes are some lines of `columns` bytes.
+int make_map(CUtensorMap &m, void *base, const Cache &c, uint32_t line, uint64_t lines, int64_t stride, uint32_t columns, uint32_t box_lines,
+             CUtensorMapSwizzle swizzle) {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -35,15 +39,37 @@ int make_maps(const Cache &c, uint32_t columns, uint32_t rows, CodeMaps &m) {
         encode = reinterpret_cast<Encode>(f);
         known.store(encode, std::memory_order_relaxed);
     }
-    const cuuint64_t size[3] = {c.row, cuuint64_t(c.heads) * c.tokens, c.n_blocks};
-    const cuuint64_t stride[2] = {c.row, cuuint64_t(c.block_stride)};
-    const cuuint32_t box[3] = {columns, rows, 1}, step[3] = {1, 1, 1};
-    const CUtensorMapSwizzle swizzle = columns == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : columns == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-    for (int i = 0; i < 2; i++)
-        if (encode(&m.code[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.code[i], size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return ZC_EINVAL;
+    const cuuint64_t size[3] = {line, lines, c.n_blocks};
+    const cuuint64_t strides[2] = {line, cuuint64_t(stride)};
+    const cuuint32_t box[3] = {columns, box_lines, 1}, step[3] = {1, 1, 1};
+    if (encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, size, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return ZC_EINVAL;
+    return ZC_OK;
+}
+
+int make_code_map(CUtensorMap &m, int kv, const Cache &c, uint32_t columns, uint32_t rows) {
+    return make_map(m, c.code[kv], c, c.row, uint64_t(c.heads) * c.tokens, c.block_stride, columns, rows,
+                    columns == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : columns == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+}
+
+} // namespace
+
+int make_maps(const Cache &c, uint32_t columns, uint32_t rows, CodeMaps &m) {
+    for (int i = 0; i < 2; i++) {
+        const int st = make_code_map(m.code[i], i, c, columns, rows);
+        if (st != ZC_OK) return st;
+    }
+    return ZC_OK;
+}
+
+int make_maps(const Cache &c, uint32_t dp, uint32_t rows, CodeMaps4 &m) {
+    for (int i = 0; i < 2; i++) {
+        int st = make_code_map(m.code[i], i, c, dp / 2, rows);
+        if (st == ZC_OK)
+            st = make_map(m.scale[i], c.group[i], c, c.dim, uint64_t(c.heads) * (c.tokens / 16), c.scale_stride, kScaleLine, rows / 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (st != ZC_OK) return st;
+    }
     return ZC_OK;
 }
 

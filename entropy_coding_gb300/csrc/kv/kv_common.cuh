@@ -97,6 +97,15 @@ struct CodeMaps {
 };
 int make_maps(const Cache &c, uint32_t columns, uint32_t rows, CodeMaps &m);
 
+// The same of the 4-bit cache (of dp / 2 bytes), with its scale bytes: 16 rows'
+// are a line of head_dim bytes; a box is `rows` / 16 lines of kScaleLine bytes,
+// not swizzled: a box begins on a multiple of 128 bytes, wherever it is.
+constexpr uint32_t kScaleLine = 128;
+struct CodeMaps4 {
+    CUtensorMap code[2], scale[2];
+};
+int make_maps(const Cache &c, uint32_t dp, uint32_t rows, CodeMaps4 &m);
+
 int launch_write(int dtype, const MoveArgs &a, cudaStream_t s);
 int launch_read(int dtype, const MoveArgs &a, cudaStream_t s);
 int launch_write4(int dtype, const MoveArgs &a, cudaStream_t s);
@@ -228,13 +237,18 @@ __device__ __forceinline__ void copy_box(void *dst, const CUtensorMap *map, int 
     asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
                      smem_of(dst)), "l"(map), "r"(0), "r"(row), "r"(block), "r"(smem_of(bar)) : "memory");
 }
-// n bytes (a multiple of 16) from 16-byte aligned memory to such shared memory.
-__device__ __forceinline__ void copy_run(void *dst, const void *src, uint32_t n, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_of(dst)), "l"(src),
-                 "r"(n), "r"(smem_of(bar)) : "memory");
-}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ void prefetch_maps(const CodeMaps &m) {
+    prefetch_map(&m.code[0]);
+    prefetch_map(&m.code[1]);
+}
+__device__ __forceinline__ void prefetch_maps(const CodeMaps4 &m) {
+    prefetch_map(&m.code[0]);
+    prefetch_map(&m.code[1]);
+    prefetch_map(&m.scale[0]);
+    prefetch_map(&m.scale[1]);
 }
 
 // ---------------------------------------------------------------------------

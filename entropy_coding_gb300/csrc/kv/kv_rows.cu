@@ -42,10 +42,16 @@ namespace zc {
 namespace kv {
 namespace {
 
+constexpr int kAhead = 32;  // steps that are looked up at a time
+
 template <int DP> struct Codes8 {
-    static constexpr int kDim = DP, kSlice = 16;
+    static constexpr int kDim = DP, kWarps = 4, kSlice = 16;
     // CTAs of an SM, as many as their registers allow, and slices of a ring, as many as fit the SM's shared memory then.
     static constexpr int kResident = 3, kStages = 3 * (128 / DP);
+    template <int NT> static constexpr int resident() { return kResident; }
+    static constexpr bool kMergeInRing = false;
+    static constexpr uint32_t kFixed = 0;
+    using Maps = CodeMaps;
     struct Stage {
         uint8_t k[kSlice * DP];
         uint8_t v[kSlice * DP];
@@ -284,7 +290,7 @@ __device__ __forceinline__ bool Codes8<DP>::attend_slices(const AttendArgs &a, c
 }
 
 template <int NT> int launch_tiles_of(const AttendArgs &a, cudaStream_t s) {
-    return a.c.dim <= 64 ? launch<Codes8<64>, NT>(a, 64, s) : launch<Codes8<128>, NT>(a, 128, s);
+    return a.c.dim <= 64 ? launch<Codes8<64>, NT>(a, 16, s) : launch<Codes8<128>, NT>(a, 16, s);
 }
 
 template <int NT> uint64_t part_bytes(uint32_t dim) {

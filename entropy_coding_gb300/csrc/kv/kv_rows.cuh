@@ -13,8 +13,12 @@
 // is left at zero for the next call.
 //
 // The format, `F`, is a class of the cache's numbers for heads of up to F::kDim columns:
-//   kSlice, kStages, kResident   keys of a warp's step, steps of its ring, CTAs of an SM
-//   Stage, Warp                  a step's memory, and what a warp keeps besides
+//   kWarps                       of a CTA
+//   kSlice, kStages              keys of a warp's step, steps of its ring
+//   kFixed                       units that an item's beginning and end count as, besides its keys
+//   resident<NT>()               CTAs of an SM
+//   kMergeInRing                 warps' rows meet in their rings
+//   Maps, Stage, Warp            its tensor maps, a step's memory, and what a warp keeps besides
 //   look_up, fetch               where steps are, and asking for one
 //   attend_slices                a warp's steps of a piece of work
 #pragma once
@@ -29,15 +33,13 @@ namespace zc {
 namespace kv {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 // Parts that are joined at a time, where there are more than twice as many: 57 parts of a long sequence at once made its
 // call 58 us, in two steps 52; for 16 parts the second step costs what it saves.
 constexpr int kGroup = 8;
-constexpr int kAhead = 32;  // steps that are looked up at a time
 
-template <int DP> struct Merge {  // 8 rows of each warp
-    float o[kWarps][8][DP + 4];
-    float m[kWarps][8], mw[kWarps][8], l[kWarps][8];
+template <int DP> struct Merge {  // 8 rows of a warp
+    float o[8][DP + 4];
+    float m[8], mw[8], l[8];
 };
 
 // A part of an item: rows in units of 2^mw (o) and 2^m (l).
@@ -47,18 +49,22 @@ template <int DP, int NT> struct Part {
 };
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // The 8x8 matrix of halves whose rows the quads hold, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 // Units of work of a sequence's items (the same for all of them).
-template <class F> constexpr int kUnit = kWarps * F::kSlice;  // keys of a unit of work
+template <class F> constexpr int kUnit = F::kWarps * F::kSlice;  // keys of a unit of work
 template <class F> __device__ __forceinline__ uint32_t first_unit(const AttendArgs &a, const Seq &q) {
     const int pos = q.len - int(q.n);
     return a.window && pos >= int(a.window) ? uint32_t(pos - int(a.window) + 1) / kUnit<F> : 0;
@@ -67,7 +73,7 @@ template <class F> __device__ __forceinline__ uint32_t units_of(const AttendArgs
     return max((uint32_t(q.len) + kUnit<F> - 1) / kUnit<F>, first_unit<F>(a, q) + 1) - first_unit<F>(a, q);
 }
 template <class F, int NT> __device__ __forceinline__ uint64_t work_of(const AttendArgs &a, const Seq &q) {
-    return q.ok && q.n * a.group <= a.rows_most ? uint64_t((q.n * a.group + 8 * NT - 1) / (8 * NT)) * a.c.heads * units_of<F>(a, q) : 0;
+    return q.ok && q.n * a.group <= a.rows_most ? uint64_t((q.n * a.group + 8 * NT - 1) / (8 * NT)) * a.c.heads * (F::kFixed + units_of<F>(a, q)) : 0;
 }
 
 // A piece of work: units of item (seq, tile, h) on the line of work, and what
@@ -75,7 +81,7 @@ template <class F, int NT> __device__ __forceinline__ uint64_t work_of(const Att
 struct Job {
     Seq seq;
     uint32_t tile, h;
-    uint64_t w, upto, i0, i1;          // the piece [w, upto) of the item's [i0, i1)
+    uint64_t w, upto, i0, i1;          // the piece [w, upto) of the item's keys [i0, i1)
     int all_lo, all_hi, x_lo, x_hi;    // keys seen by some row; by every row
     int first, steps;                  // this warp's slices: first, first + kWarps, ...
     __device__ __forceinline__ bool whole() const { return w == i0 && upto == i1; }
@@ -84,6 +90,7 @@ struct Job {
 // The piece of work at w, whose sequence's work begins at `at` (both moved on).
 template <class F, int NT>
 __device__ __forceinline__ bool next_job(const AttendArgs &a, uint64_t &w, uint64_t w1, uint32_t &s, uint64_t &at, Job &job) {
+    constexpr int kWarps = F::kWarps;
     while (w < w1) {
         const Seq seq = read_seq(a.b, s, a.d_status, a.c.tokens, false);
         const uint64_t work = work_of<F, NT>(a, seq);
@@ -92,26 +99,27 @@ __device__ __forceinline__ bool next_job(const AttendArgs &a, uint64_t &w, uint6
             s++;
             continue;
         }
-        const uint32_t units = units_of<F>(a, seq);
+        const uint32_t units = F::kFixed + units_of<F>(a, seq);
         const uint64_t past = w - at;
         const uint32_t item = past >> 32 ? uint32_t(past / units) : uint32_t(past) / units;
         job.seq = seq;
-        job.i0 = at + item * units;
-        job.i1 = job.i0 + units;
-        job.w = w;
+        job.i1 = at + uint64_t(item + 1) * units;
+        job.i0 = job.i1 - units + F::kFixed;
+        job.w = max(w, job.i0);
         job.upto = min(w1, job.i1);
+        w = job.upto;
+        if (w <= job.i0) continue;  // (the CTA's work ends within the item's beginning, which belongs to the first keys' piece)
         job.tile = item / a.c.heads;
         job.h = item - job.tile * a.c.heads;
         const uint32_t row0 = job.tile * 8 * NT, n_rows = seq.n * a.group;
         bounds(a, seq, row0, job.all_lo, job.x_hi);
         bounds(a, seq, min(row0 + 8 * NT, n_rows) - 1, job.x_lo, job.all_hi);
-        const int unit0 = int(first_unit<F>(a, seq) + uint32_t(w - job.i0)), warp = threadIdx.x >> 5;
+        const int unit0 = int(first_unit<F>(a, seq) + uint32_t(job.w - job.i0)), warp = threadIdx.x >> 5;
         constexpr int kSlice = F::kSlice;
-        const int end = min((job.all_hi + kSlice - 1) / kSlice, (unit0 + int(job.upto - w)) * kWarps);
+        const int end = min((job.all_hi + kSlice - 1) / kSlice, (unit0 + int(job.upto - job.w)) * kWarps);
         job.first = unit0 * kWarps + warp;
         if (job.first < job.all_lo / kSlice) job.first += (job.all_lo / kSlice - job.first + kWarps - 1) / kWarps * kWarps;
         job.steps = job.first < end ? (end - job.first + kWarps - 1) / kWarps : 0;
-        w = job.upto;
         return true;
     }
     return false;
@@ -120,7 +128,7 @@ __device__ __forceinline__ bool next_job(const AttendArgs &a, uint64_t &w, uint6
 // Looks up a piece's first steps and asks for the first of them. turn: the
 // warp's slices before the piece.
 template <class F>
-__device__ __forceinline__ void begin(const AttendArgs &a, const CodeMaps &maps, typename F::Warp &wp, typename F::Stage *ring, const Job &job, uint32_t turn) {
+__device__ __forceinline__ void begin(const AttendArgs &a, const typename F::Maps &maps, typename F::Warp &wp, typename F::Stage *ring, const Job &job, uint32_t turn) {
     constexpr int S = F::kStages;
     F::look_up(a, wp, job, 0);
     __syncwarp();
@@ -200,10 +208,11 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Job &job
 }
 
 // The warps' rows together, 8 at a time: into `part`, or finished.
-template <int DP, int NT>
-__device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const Job &job, Sums<DP, NT> &acc, Part<DP, NT> *part) {
+template <int DP, int NT, int kWarps, class At>
+__device__ __forceinline__ void merge(const AttendArgs &a, const At &mg, const Job &job, Sums<DP, NT> &acc, Part<DP, NT> *part) {
     constexpr int kCols = DP / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    Merge<DP> &mine = mg(warp);
     const uint32_t n_rows = job.seq.n * a.group;
 #pragma unroll
     for (int n = 0; n < NT; n++) {
@@ -222,25 +231,25 @@ __device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const 
                 for (int c = 0; c < kCols; c++)
                     if (acc.poison[n][e] >> c & 1) acc.o[n][c / 2][2 * (c & 1) + e] = NAN;
             }
-            if (g == 0) mg.m[warp][r] = acc.m[n][e], mg.mw[warp][r] = acc.mw[n][e], mg.l[warp][r] = l;
+            if (g == 0) mine.m[r] = acc.m[n][e], mine.mw[r] = acc.mw[n][e], mine.l[r] = l;
 #pragma unroll
             for (int c = 0; c < DP / 16; c += 2)
-                *reinterpret_cast<float4 *>(&mg.o[warp][r][kCols * g + 2 * c]) =
+                *reinterpret_cast<float4 *>(&mine.o[r][kCols * g + 2 * c]) =
                     make_float4(acc.o[n][c][e], acc.o[n][c][2 + e], acc.o[n][c + 1][e], acc.o[n][c + 1][2 + e]);
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < DP; i += kThreads) {
+        for (int i = threadIdx.x; i < DP; i += 32 * kWarps) {
             const int r = i / (DP / 8), col = i % (DP / 8) * 8;
             if (row0 + r >= n_rows || col >= int(a.c.dim)) continue;
             float M = kNone, W = kNone, L = 0.0f, x[8] = {};
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) M = fmaxf(M, mg.m[w][r]), W = fmaxf(W, mg.mw[w][r]);
+            for (int w = 0; w < kWarps; w++) M = fmaxf(M, mg(w).m[r]), W = fmaxf(W, mg(w).mw[r]);
 #pragma unroll
             for (int w = 0; w < kWarps; w++) {
-                L += mg.l[w][r] * ratio2(mg.m[w][r], M);
-                const float f = ratio2(mg.mw[w][r], W);
+                L += mg(w).l[r] * ratio2(mg(w).m[r], M);
+                const float f = ratio2(mg(w).mw[r], W);
 #pragma unroll
-                for (int k = 0; k < 8; k++) x[k] += mg.o[w][r][col + k] * f;
+                for (int k = 0; k < 8; k++) x[k] += mg(w).o[r][col + k] * f;
             }
             if (part) {
                 float4 *p = reinterpret_cast<float4 *>(&part->o[8 * n + r][col]);
@@ -260,7 +269,7 @@ __device__ __forceinline__ void merge(const AttendArgs &a, Merge<DP> &mg, const 
 // `on`, into the finished rows.
 // A thread takes 4 columns of a row and every ways-th part, kRun parts in
 // flight together; the ways meet in shared memory.
-template <int DP, int NT>
+template <int DP, int NT, int kThreads>
 __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Job &item, uint32_t first, uint32_t i0, uint32_t step,
                                      uint32_t n, bool on) {
     constexpr int kCols = DP / 4, kRun = 8;
@@ -354,21 +363,32 @@ __device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t n, int &s_la
     return s_last;
 }
 
-template <class F, int NT> constexpr size_t ring_bytes() { return sizeof(typename F::Stage) * F::kStages * kWarps; }
-template <class F, int NT> constexpr size_t smem_bytes() { return ring_bytes<F, NT>() + sizeof(Merge<F::kDim>); }
+template <class F, int NT> constexpr size_t ring_bytes() { return sizeof(typename F::Stage) * F::kStages * F::kWarps; }
+template <class F> constexpr size_t kJoinBytes = 32 * F::kWarps * 32;  // what join() takes
+template <class F, int NT> constexpr size_t smem_bytes() {
+    return ring_bytes<F, NT>() + (F::kMergeInRing ? sizeof(typename F::Stage) < kJoinBytes<F> ? kJoinBytes<F> : 0 : F::kWarps * sizeof(Merge<F::kDim>));
+}
 
 template <class F, int NT>
-__global__ void __launch_bounds__(kThreads, F::kResident) rows_kernel(const __grid_constant__ AttendArgs a,
-                                                                     const __grid_constant__ CodeMaps maps) {
+__global__ void __launch_bounds__(32 * F::kWarps, F::template resident<NT>()) rows_kernel(const __grid_constant__ AttendArgs a,
+                                                                     const __grid_constant__ typename F::Maps maps) {
     using Warp = typename F::Warp;
     using Stage = typename F::Stage;
-    constexpr int S = F::kStages, DP = F::kDim;
+    constexpr int S = F::kStages, DP = F::kDim, kWarps = F::kWarps, kThreads = 32 * kWarps;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Warp s_warps[kWarps];
     __shared__ uint64_t s_warp[kWarps], s_at;
     __shared__ uint32_t s_seq;
     __shared__ int s_last;
-    Merge<DP> &mg = *reinterpret_cast<Merge<DP> *>(smem + ring_bytes<F, NT>());
+    // Where warps' rows meet: behind the rings, or in the stage of each warp's ring that it has read last, which nothing is
+    // asked for while its next piece begins.
+    static_assert(!F::kMergeInRing || sizeof(Merge<DP>) <= sizeof(Stage), "a warp's rows do not fit a stage");
+    static_assert(F::kMergeInRing || kWarps * sizeof(Merge<DP>) >= kJoinBytes<F>, "no room for joining");
+    __shared__ uint32_t s_free[kWarps];
+    auto mg = [&](int w) -> Merge<DP> & {
+        if (F::kMergeInRing) return *reinterpret_cast<Merge<DP> *>(reinterpret_cast<Stage *>(smem) + w * S + s_free[w]);
+        return reinterpret_cast<Merge<DP> *>(smem + ring_bytes<F, NT>())[w];
+    };
     Part<DP, NT> *parts = reinterpret_cast<Part<DP, NT> *>(a.parts);
     const uint32_t B = a.c.tokens, cta = blockIdx.x;
 
@@ -377,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, F::kResident) rows_kernel(const __gr
     if (threadIdx.x % 32 == 0) {
         for (int i = 0; i < S; i++) bar_init(&wp.full[i], 1);
         bar_init_done();
-        prefetch_map(&maps.code[0]);
-        prefetch_map(&maps.code[1]);
+        prefetch_maps(maps);
     }
 
     // The line of work, and this CTA's piece [w0, w1) of it.
@@ -410,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, F::kResident) rows_kernel(const __gr
     uint32_t turn = 0;  // slices that this warp has asked for
     Job job, next;
     bool more = next_job<F, NT>(a, w, w1, s, at, job);
-    begin<F>(a, maps, wp, ring, job, turn);
+    if (more) begin<F>(a, maps, wp, ring, job, turn);  // (a CTA's work may be an item's beginning alone, which is another's)
     while (more) {
         Sums<DP, NT> acc;
         const bool ok = F::template attend_slices<NT>(a, maps, wp, ring, job, turn, acc);
@@ -418,19 +437,20 @@ __global__ void __launch_bounds__(kThreads, F::kResident) rows_kernel(const __gr
         // The next piece's first slices are on their way while this one is finished.
         more = next_job<F, NT>(a, w, w1, s, at, next);
         if (more && ok) begin<F>(a, maps, wp, ring, next, turn);
+        if (F::kMergeInRing && threadIdx.x % 32 == 0) s_free[threadIdx.x / 32] = (turn + S - 1) % S;
         if (__syncthreads_or(!ok)) {
             if (more && ok) drain<F>(a, wp, turn, next.steps);
             return;
         }
         const bool whole = job.whole();
-        merge<DP, NT>(a, mg, job, acc, whole ? nullptr : parts + 2 * cta + (job.w == job.i0 ? 1 : 0));
+        merge<DP, NT, kWarps>(a, mg, job, acc, whole ? nullptr : parts + 2 * cta + (job.w == job.i0 ? 1 : 0));
         if (!whole) {
             // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
             // W c / G <= u < W (c + 1) / G, rounded down, so c = (u G + G - 1) / W
             const uint32_t c0 = uint32_t((job.i0 * G + G - 1) / W), c1 = uint32_t(((job.i1 - 1) * G + G - 1) / W);
             const uint32_t n = c1 - c0 + 1, mine = cta - c0;
             uint32_t *counter = a.counters + uint64_t(slot_of(job.seq.first, job.seq.s, a.group, 8 * NT, 1) + job.tile) * a.c.heads + job.h;
-            uint8_t *space = reinterpret_cast<uint8_t *>(&mg);
+            uint8_t *space = F::kMergeInRing && sizeof(Stage) < kJoinBytes<F> ? smem + ring_bytes<F, NT>() : reinterpret_cast<uint8_t *>(&mg(0));
             // many parts: each kGroup of them first, by the last CTA of those, then what they make
             const uint32_t groups = n <= 2 * kGroup ? 1 : (n + kGroup - 1) / kGroup, g = groups == 1 ? 0 : mine / kGroup;
             uint32_t i0 = g * kGroup, step = 1, parts_of = groups == 1 ? n : min(uint32_t(kGroup), n - i0);
@@ -438,16 +458,20 @@ __global__ void __launch_bounds__(kThreads, F::kResident) rows_kernel(const __gr
             bool on = groups > 1, go = last_of(first, parts_of, s_last);
 #pragma unroll 1
             while (go) {
-                join<DP, NT>(a, space, job, c0, i0, step, parts_of, on);
+                join<DP, NT, kThreads>(a, space, job, c0, i0, step, parts_of, on);
                 go = on && last_of(counter, groups, s_last);
                 i0 = 0, step = kGroup, parts_of = groups, on = false;
             }
+        }
+        if (F::kMergeInRing) {  // before a stage is asked for again
+            fence_async();
+            __syncthreads();
         }
         job = next;
     }
 }
 
-template <class F, int NT> int launch(const AttendArgs &a, uint32_t columns, cudaStream_t s) {
+template <class F, int NT> int launch(const AttendArgs &a, uint32_t rows, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose kernel may use this much shared memory
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
@@ -457,10 +481,10 @@ template <class F, int NT> int launch(const AttendArgs &a, uint32_t columns, cud
             return ZC_ECUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    CodeMaps maps;
-    const int st = make_maps(a.c, columns, 16, maps);
+    typename F::Maps maps;
+    const int st = make_maps(a.c, F::kDim, rows, maps);
     if (st != ZC_OK) return st;
-    rows_kernel<F, NT><<<uint32_t(sm_count() * F::kResident), kThreads, smem_bytes<F, NT>(), s>>>(a, maps);
+    rows_kernel<F, NT><<<uint32_t(sm_count() * F::template resident<NT>()), 32 * F::kWarps, smem_bytes<F, NT>(), s>>>(a, maps);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }
 

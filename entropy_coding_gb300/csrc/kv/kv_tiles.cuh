@@ -21,6 +21,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "kv4_common.cuh"
 #include "kv_attend.cuh"
@@ -69,11 +70,13 @@ struct Job {
     __device__ __forceinline__ bool edge(int j) const { return j * kTile < x_lo || (j + 1) * kTile > x_hi; }
 };
 
+template <int kBits> using Maps = std::conditional_t<kBits == 8, CodeMaps, CodeMaps4>;
+
 template <int kBits, int DP> struct Smem {
     uint8_t q[2][kTile * DP * 2];       // panels of 64 columns: 128-byte rows, swizzled
     uint8_t op[kOps][kTile * DP * 2];
     static constexpr int kCodes = kTile * DP * kBits / 8;                    // bytes of a code tile
-    uint8_t raw[kRaw][kCodes + (kBits == 4 ? kBoxes * DP : 0)];              // and of its scales, a box's dim bytes DP apart
+    uint8_t raw[kRaw][kCodes + (kBits == 4 ? kBoxes * kScaleLine : 0)];      // and of its scales, a line for 16 rows
     uint8_t out[8][32 * 64];            // a warp's rows, 32 columns at a time
     float ks[kSlots][kBoxes], lvs[kSlots][kBoxes];                           // (8 bits)
     Bars bars;
@@ -261,7 +264,7 @@ template <int kBits, int DP> __device__ __forceinline__ bool job_ready(Smem<kBit
 template <int kBits, int DP> __device__ __forceinline__ void job_done(Smem<kBits, DP> &sm, uint32_t k) { bar_arrive(&sm.bars.job_empty[k % kJobs]); }
 
 template <int kBits, int DP>
-__device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &maps, Smem<kBits, DP> &sm) {
+__device__ __forceinline__ bool copy_role(const AttendArgs &a, const Maps<kBits> &maps, Smem<kBits, DP> &sm) {
     const int lane = threadIdx.x & 31;
     uint32_t item = 0, tile = 0;
     bool ok = true;
@@ -293,13 +296,11 @@ __device__ __forceinline__ bool copy_role(const AttendArgs &a, const CodeMaps &m
                 const int r = item % kRaw;
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(&sm.bars.raw_empty[r], (item / kRaw & 1) ^ 1, a.limit));
                 if (!ok) break;
-                if (lane == 0) bar_expect(&sm.bars.raw_full[r], sm.kCodes + (kBits == 4 ? kBoxes * a.c.dim : 0));
+                if (lane == 0) bar_expect(&sm.bars.raw_full[r], sizeof(sm.raw[r]));
                 __syncwarp();
                 if (lane < kBoxes) {
                     copy_box(sm.raw[r] + lane * (sm.kCodes / kBoxes), &maps.code[kv], row, id, &sm.bars.raw_full[r]);
-                    if constexpr (kBits == 4)
-                        copy_run(sm.raw[r] + sm.kCodes + lane * DP, a.c.group[kv] + id * a.c.scale_stride + int64_t(row) * (a.c.dim / 16), a.c.dim,
-                                 &sm.bars.raw_full[r]);
+                    if constexpr (kBits == 4) copy_box(sm.raw[r] + sm.kCodes + lane * kScaleLine, &maps.scale[kv], row / 16, id, &sm.bars.raw_full[r]);
                 }
             }
         }
@@ -372,7 +373,7 @@ __device__ __forceinline__ void convert4(const uint8_t *raw, const uint8_t *scal
         place(i, row, ch);
         in[i] = *reinterpret_cast<const uint4 *>(raw + row * (DP / 2) + 16 * (ch ^ (DP == 128 ? row >> 1 & 3 : row >> 2 & 1)));
 #pragma unroll
-        for (int k = 0; k < 2; k++) s[i][k] = 2 * ch + k < int(groups) ? scales[row / 16 * DP + row % 16 * groups + 2 * ch + k] : 0;
+        for (int k = 0; k < 2; k++) s[i][k] = 2 * ch + k < int(groups) ? scales[row / 16 * kScaleLine + row % 16 * groups + 2 * ch + k] : 0;
     }
     if (edge) {
         // As in convert8, of scales that make NaN or infinities.
@@ -904,7 +905,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<kBits, DP> &
 }
 
 template <int kBits, int DP>
-__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CodeMaps maps) {
+__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ Maps<kBits> maps) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Smem<kBits, DP> &sm = *reinterpret_cast<Smem<kBits, DP> *>(smem);
     const uint32_t cta = blockIdx.x;
@@ -953,8 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         bar_init(&b.rows, 8);
         bar_init(&b.drained, 1);
         bar_init_done();
-        prefetch_map(&maps.code[0]);
-        prefetch_map(&maps.code[1]);
+        prefetch_maps(maps);
         sm.poison = 0;
     }
     if (warp == 12) {
@@ -998,8 +998,8 @@ template <int kBits, int DP> int launch(const AttendArgs &a, cudaStream_t s) {
             return ZC_ECUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    CodeMaps maps;
-    const int st = make_maps(a.c, DP * kBits / 8, 16, maps);
+    Maps<kBits> maps;
+    const int st = make_maps(a.c, DP, 16, maps);
     if (st != ZC_OK) return st;
     tiles_kernel<kBits, DP><<<uint32_t(sm_count()), kThreads, sizeof(Smem<kBits, DP>), s>>>(a, maps);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
