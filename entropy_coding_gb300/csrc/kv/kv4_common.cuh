@@ -14,6 +14,17 @@ namespace kv {
 
 constexpr uint32_t kScaleMost = 0xE2, kScaleNaN = 0xFF;  // 10240: 6 times that is still finite in half
 
+// Heads that a CTA of a run of tokens does one after another: the run's places are looked up once for them, and the next
+// head's numbers are on their way meanwhile; as many as leave 3 CTAs for 2 SMs. (133678 tokens of 8 heads read: 1 head 148
+// us, 2 heads 119, 4 and 8 heads 113; 17138 tokens 22.3, 18.5, 18.2 and 16.4; 777 tokens 6.2, 6.2, 6.9 and 9.2; 32 tokens 4.1,
+// 5.1, 6.2 and 7.5.)
+inline uint32_t heads_of_a_cta(uint32_t runs, uint32_t heads) {
+    const uint64_t most = uint64_t(runs) * heads * 2 / (3 * uint64_t(sm_count()));
+    if (most <= 1) return 1;
+    const uint32_t groups = most >= heads ? 1 : uint32_t((heads + most - 1) / most);
+    return (heads + groups - 1) / groups;
+}
+
 #ifdef __CUDACC__
 
 // Eight codes (columns in order from the low half of the low byte on) to eight halves.
@@ -23,11 +34,11 @@ __device__ __forceinline__ void e2m1x8_to_half2x4(uint32_t v, uint32_t &h0, uint
         : "=r"(h0), "=r"(h1), "=r"(h2), "=r"(h3) : "r"(v));
 }
 // Eight floats to eight codes, to nearest even, saturating at +-6.
-__device__ __forceinline__ uint32_t floatx8_to_e2m1(const float (&x)[8]) {
+__device__ __forceinline__ uint32_t floatx8_to_e2m1(const float2 *x) {
     uint32_t r;
     asm("{.reg .b8 a, b, c, d; cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3; "
         "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7; mov.b32 %0, {a, b, c, d};}"
-        : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+        : "=r"(r) : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y));
     return r;
 }
 // A scale byte as a half, in both halves of a word.
@@ -54,20 +65,33 @@ template <int DT> struct Piece {
 #pragma unroll
         for (int i = 0; i < kWords; i++) v[i] = make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void get(float *x) const {
+    __device__ __forceinline__ void get(float2 *x) const {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float2 f = DT == ZC_FP32 ? make_float2(__uint_as_float(w[2 * i % (4 * kWords)]), __uint_as_float(w[(2 * i + 1) % (4 * kWords)])) : unpack2<DT>(w[i]);
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
-        }
+        for (int i = 0; i < 4; i++)
+            x[i] = DT == ZC_FP32 ? make_float2(__uint_as_float(w[2 * i % (4 * kWords)]), __uint_as_float(w[(2 * i + 1) % (4 * kWords)])) : unpack2<DT>(w[i]);
     }
-    __device__ __forceinline__ void put(const float *x) {  // rounded once
+    __device__ __forceinline__ void put(const float2 *x) {  // rounded once
         uint32_t *w = reinterpret_cast<uint32_t *>(v);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            if (DT == ZC_FP32) w[2 * i % (4 * kWords)] = __float_as_uint(x[2 * i]), w[(2 * i + 1) % (4 * kWords)] = __float_as_uint(x[2 * i + 1]);
-            else w[i] = pack2<DT>(x[2 * i], x[2 * i + 1]);
+            if (DT == ZC_FP32) w[2 * i % (4 * kWords)] = __float_as_uint(x[i].x), w[(2 * i + 1) % (4 * kWords)] = __float_as_uint(x[i].y);
+            else w[i] = pack2<DT>(x[i].x, x[i].y);
+        }
+    }
+    // Bits of the largest magnitude, as a float: an infinity's or above where there is one or a NaN.
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(v);
+        uint32_t t = 0;
+        if constexpr (DT == ZC_FP32) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) t = max(t, w[i] & 0x7FFFFFFFu);
+            return t;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) t = __vmaxu2(t, w[i] & 0x7FFF7FFFu);
+            t = max(t >> 16, t & 0xFFFFu);
+            return DT == ZC_BF16 ? t << 16 : __float_as_uint(unpack2<DT>(t).x);
         }
     }
 };

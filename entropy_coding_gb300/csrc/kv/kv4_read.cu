@@ -3,8 +3,8 @@
 //
 // A thread has 8 columns: a word of codes, a scale byte, and one 16-byte store
 // (two for float32), so that a warp's stores are whole runs of memory. A CTA
-// has 64 packed tokens of one head, K and V; all of a thread's reads are in
-// flight before the first is used.
+// has 64 packed tokens, K and V, head after head; all of a thread's reads of a
+// head are in flight before the first is used.
 #include "kv4_common.cuh"
 
 namespace zc {
@@ -18,28 +18,24 @@ template <int DT> __device__ __forceinline__ void number(uint32_t codes, uint32_
     uint32_t h[4];
     e2m1x8_to_half2x4(codes, h[0], h[1], h[2], h[3]);
     const uint32_t s = scale_half2(byte);
-    float x[8];
+    float2 x[4];
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        h[k] = mul_half2(h[k], s);
-        const float2 f = unpack2<ZC_FP16>(h[k]);
-        x[2 * k] = f.x, x[2 * k + 1] = f.y;
-    }
+    for (int k = 0; k < 4; k++) h[k] = mul_half2(h[k], s), x[k] = unpack2<ZC_FP16>(h[k]);
     if (DT == ZC_FP16) out.v[0] = make_uint4(h[0], h[1], h[2], h[3]);
     else out.put(x);
 }
 
-template <int DT> __global__ void __launch_bounds__(kThreads) read4_kernel(const __grid_constant__ MoveArgs a) {
+template <int DT> __global__ void __launch_bounds__(kThreads) read4_kernel(const __grid_constant__ MoveArgs a, uint32_t heads) {
     __shared__ int32_t s_pos[kTokens], s_block[kTokens];
     __shared__ uint32_t s_seq[kTokens];
-    const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y, per_row = D / 8;
+    const uint32_t B = a.c.tokens, D = a.c.dim, per_row = D / 8, h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.c.heads);
     const uint32_t t0 = blockIdx.x * kTokens, n = min(uint32_t(kTokens), a.b.total - t0), units = n * per_row;
     const uint32_t inverse = 0xFFFFFFFFu / per_row + 1;  // i / per_row = i * inverse / 2^32
     locate(a.b, B, t0, n, s_pos, s_seq, a.d_status);
     for (uint32_t i = threadIdx.x; i < n; i += kThreads)
         s_block[i] = s_pos[i] < 0 ? -1 : int32_t(read_block(a.b, a.c, s_seq[i], block_of_16(a.c, uint32_t(s_pos[i]) / 16), a.d_status));
     __syncthreads();
-    uint32_t codes[2][kPieces], byte[2][kPieces];
+    int64_t code_at[kPieces], scale_at[kPieces];  // of the next head to be asked for
     bool there[kPieces];
 #pragma unroll
     for (int p = 0; p < kPieces; p++) {
@@ -47,37 +43,60 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read4_kernel(const
         there[p] = i < units && s_block[row] >= 0;
         if (!there[p]) continue;
         const int64_t id = s_block[row];
-        const uint32_t c = i - row * per_row, at = h * B + uint32_t(s_pos[row]) - block_of_16(a.c, uint32_t(s_pos[row]) / 16) * B;
-#pragma unroll
-        for (int kv = 0; kv < 2; kv++) {
-            codes[kv][p] = __ldcs(reinterpret_cast<const uint32_t *>(a.c.code[kv] + id * a.c.block_stride + int64_t(at) * a.c.row + c * 4));
-            byte[kv][p] = __ldg(a.c.group[kv] + id * a.c.scale_stride + int64_t(at) * (D / 16) + c / 2);
-        }
+        const uint32_t c = i - row * per_row, at = h0 * B + uint32_t(s_pos[row]) - block_of_16(a.c, uint32_t(s_pos[row]) / 16) * B;
+        code_at[p] = id * a.c.block_stride + int64_t(at) * a.c.row + c * 4;
+        scale_at[p] = id * a.c.scale_stride + int64_t(at) * (D / 16) + c / 2;
     }
+    uint32_t codes[2][kPieces], byte[2][kPieces];
+    auto ask = [&]() {
+#pragma unroll
+        for (int p = 0; p < kPieces; p++) {
+            if (!there[p]) continue;
+#pragma unroll
+            for (int kv = 0; kv < 2; kv++) {
+                codes[kv][p] = __ldcs(reinterpret_cast<const uint32_t *>(a.c.code[kv] + code_at[p]));
+                byte[kv][p] = __ldg(a.c.group[kv] + scale_at[p]);
+            }
+            code_at[p] += int64_t(B) * a.c.row;
+            scale_at[p] += int64_t(B) * (D / 16);
+        }
+    };
     constexpr int elt = DT == ZC_FP32 ? 4 : 2;
+    ask();
+    for (uint32_t h = h0; h < h1; h++) {
+        uint32_t now[2][kPieces], by[2][kPieces];
 #pragma unroll
-    for (int p = 0; p < kPieces; p++) {
-        if (!there[p]) continue;
-        const uint32_t i = threadIdx.x + p * kThreads, row = __umulhi(i, inverse);
+        for (int p = 0; p < kPieces; p++) now[0][p] = codes[0][p], now[1][p] = codes[1][p], by[0][p] = byte[0][p], by[1][p] = byte[1][p];
+        if (h + 1 < h1) ask();  // the next head's are on their way while this one's are written
 #pragma unroll
-        for (int kv = 0; kv < 2; kv++) {
-            Piece<DT> x;
-            number<DT>(codes[kv][p], byte[kv][p], x);
-            x.store(static_cast<uint8_t *>(a.x[kv].p) +
-                    (int64_t(t0 + row) * a.x[kv].token + int64_t(h) * a.x[kv].head + (i - row * per_row) * 8) * elt);
+        for (int p = 0; p < kPieces; p++) {
+            if (!there[p]) continue;
+            const uint32_t i = threadIdx.x + p * kThreads, row = __umulhi(i, inverse);
+#pragma unroll
+            for (int kv = 0; kv < 2; kv++) {
+                Piece<DT> x;
+                number<DT>(now[kv][p], by[kv][p], x);
+                x.store(static_cast<uint8_t *>(a.x[kv].p) +
+                        (int64_t(t0 + row) * a.x[kv].token + int64_t(h) * a.x[kv].head + (i - row * per_row) * 8) * elt);
+            }
         }
     }
     if (blockIdx.x == 0 && blockIdx.y == 0) report_batch(a.b, B, a.d_status, threadIdx.x, kThreads, true);
 }
 
+template <int DT> void launch(const MoveArgs &a, cudaStream_t s) {
+    const uint32_t runs = (a.b.total + kTokens - 1) / kTokens;
+    const uint32_t heads = heads_of_a_cta(runs, a.c.heads);
+    read4_kernel<DT><<<dim3(runs, (a.c.heads + heads - 1) / heads), kThreads, 0, s>>>(a, heads);
+}
+
 } // namespace
 
 int launch_read4(int dtype, const MoveArgs &a, cudaStream_t s) {
-    const dim3 grid((a.b.total + kTokens - 1) / kTokens, a.c.heads);
     switch (dtype) {
-    case ZC_BF16: read4_kernel<ZC_BF16><<<grid, kThreads, 0, s>>>(a); break;
-    case ZC_FP16: read4_kernel<ZC_FP16><<<grid, kThreads, 0, s>>>(a); break;
-    default: read4_kernel<ZC_FP32><<<grid, kThreads, 0, s>>>(a); break;
+    case ZC_BF16: launch<ZC_BF16>(a, s); break;
+    case ZC_FP16: launch<ZC_FP16>(a, s); break;
+    default: launch<ZC_FP32>(a, s); break;
     }
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }

@@ -106,15 +106,6 @@ __device__ __forceinline__ uint32_t low_halves(uint32_t x, uint32_t y) {
     asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(x), "r"(y), "r"(0x0F0F0F0Fu));  // (x & m) | (y & ~m)
     return r;
 }
-// x, y = a0 b0 + c0, a1 b1 + c1; x + a, y + b
-__device__ __forceinline__ void fma_pair(float &x, float &y, float a0, float a1, const float (&b)[2], const float (&c)[2]) {
-    asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}"
-        : "=f"(x), "=f"(y) : "f"(a0), "f"(a1), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
-}
-__device__ __forceinline__ void add_pair(float (&x)[2], float a, float b) {
-    asm("{.reg .b64 c, d; mov.b64 c, {%0, %1}; mov.b64 d, {%2, %3}; add.rn.f32x2 c, c, d; mov.b64 {%0, %1}, c;}" : "+f"(x[0]), "+f"(x[1]) : "f"(a), "f"(b));
-}
-
 template <int DP>
 template <int NT>
 __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, const CodeMaps4 &maps, Warp &wp, Stage *ring, const Job &job,
@@ -267,11 +258,12 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
             for (int half = 0; half < 2; half++)
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
-                    float p0, p1;
-                    fma_pair(p0, p1, sc[half][n][2 * j], sc[half][n][2 * j + 1], row_scale[n], raised[n]);
-                    p0 = ex2(p0), p1 = ex2(p1);
-                    add_pair(l[n], p0, p1);
-                    pf[half][n][j] = transpose8(half2_of(p0, p1));
+                    float2 p = fma2(make_float2(sc[half][n][2 * j], sc[half][n][2 * j + 1]), make_float2(row_scale[n][0], row_scale[n][1]),
+                                    make_float2(raised[n][0], raised[n][1]));
+                    p.x = ex2(p.x), p.y = ex2(p.y);
+                    const float2 sum = add2(make_float2(l[n][0], l[n][1]), p);
+                    l[n][0] = sum.x, l[n][1] = sum.y;
+                    pf[half][n][j] = transpose8(half2_of(p.x, p.y));
                 }
         if (edge) {
             // A row that does not see a key has weight 0 for it, but 0 times NaN (or an infinity) is NaN: scales that make

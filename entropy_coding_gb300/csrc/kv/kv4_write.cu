@@ -5,22 +5,23 @@
 //   code  = the E2M1 number nearest to x / scale (ties to the even code)
 // as if a / 6 and x / scale were exact: the scale is found by comparing a with
 // 6 times the midpoint of two scales, which float32 holds, and a quotient is
-// rounded correctly (one division for 16 columns, two steps of refinement for
-// each), which is enough for 16-bit x, whose quotients are either a midpoint of
-// two codes or 2^-11 away from it; of float32's, those that round to a midpoint
-// are moved off it by the sign of what remains.
+// taken with the reciprocal in two floats, so that it is within 2^-46 before
+// its rounding: that is enough for 16-bit x, whose quotients are either a
+// midpoint of two codes, and then come out as it, or 2^-11 away from it; of
+// float32's, those that round to a midpoint are moved off it by the sign of what
+// remains. (With the reciprocal in one float x = 3.5 s, s = 1.75, misses its
+// midpoint.)
 //
-// A thread has 16 columns; a CTA up to 64 packed tokens of one head, K and V,
-// so that it writes runs of rows. Its reads do not wait for where the tokens
-// belong: that is looked up meanwhile.
+// A thread has 16 columns of a packed token, K and V, head after head; a CTA up
+// to kTokens of them, so that it writes runs of rows. Its first reads do not wait
+// for where the tokens belong: that is looked up meanwhile.
 #include "kv4_common.cuh"
 
 namespace zc {
 namespace kv {
 namespace {
 
-constexpr int kThreads = 256, kTokens = 64;
-constexpr int kPieces = kTokens * (kMaxHeadDim / 16) / kThreads;  // of K and of V, at most
+constexpr int kThreads = 128, kTokens = kThreads / (kMaxHeadDim / 16);
 
 // Scale byte for 16 columns whose largest magnitude is a (finite).
 __device__ __forceinline__ uint32_t scale_byte(float a) {
@@ -34,96 +35,110 @@ __device__ __forceinline__ uint32_t scale_byte(float a) {
 
 // Codes of 16 columns, and their scale byte.
 template <int DT> __device__ __forceinline__ uint2 quantise(const Piece<DT> (&in)[2], uint32_t &byte) {
-    float x[16];
+    float2 x[8];
     in[0].get(x);
-    in[1].get(x + 8);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 16; i++) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    if (top >= 0x7F800000u) {
-        bool nan = top > 0x7F800000u;
-        if (nan) {
-            byte = kScaleNaN;
-            return make_uint2(0, 0);
-        }
+    in[1].get(x + 4);
+    uint32_t top = max(in[0].top(), in[1].top());
+    if (top > 0x7F800000u) {
+        byte = kScaleNaN;
+        return make_uint2(0, 0);
+    }
+    const bool infinite = top == 0x7F800000u;
+    if (infinite) {
         top = 0;
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-            if (u < 0x7F800000u) top = max(top, u);
+        for (int i = 0; i < 8; i++) {
+            const uint32_t u = __float_as_uint(x[i].x) & 0x7FFFFFFFu, v = __float_as_uint(x[i].y) & 0x7FFFFFFFu;
+            top = max(top, max(u < 0x7F800000u ? u : 0u, v < 0x7F800000u ? v : 0u));
         }
     }
     byte = scale_byte(__uint_as_float(top));
-    const float s = scale_float(byte), inv = 1.0f / s, most = 6.0f * s;
-    uint32_t w[2];
+    const float s = scale_float(byte);
+    if (infinite) {
+        const float most = 6.0f * s;
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float y = fminf(fmaxf(x[8 * h + i], -most), most), q0 = y * inv;
-            q[i] = copysignf(fmaf(fmaf(-q0, s, y), inv, q0), y);  // (a zero keeps its sign)
-            if (DT == ZC_FP32) {
-                const float rest = fmaf(-q[i], s, y);
-                const uint32_t u = __float_as_uint(q[i]);
-                if (rest != 0.0f && (u & 0x1FFFFFu) == 0 && (u & 0x7FFFFFFFu)) q[i] = __uint_as_float((__float_as_int(rest) ^ int(u)) < 0 ? u - 1 : u + 1);
-            }
-        }
-        w[h] = floatx8_to_e2m1(q);
+        for (int i = 0; i < 8; i++) x[i].x = fminf(fmaxf(x[i].x, -most), most), x[i].y = fminf(fmaxf(x[i].y, -most), most);
     }
-    return make_uint2(w[0], w[1]);
+    // 1 / s in two parts, neither negative: a zero keeps its sign
+    const float inv = __frcp_rd(s), rest = fmaf(-s, inv, 1.0f) * inv;
+    float2 q[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        q[i] = fma2(x[i], both(inv), mul2(x[i], both(rest)));
+        if (DT == ZC_FP32) {
+            const float2 left = fma2(q[i], both(-s), x[i]);
+            auto off = [](float q, float left) {
+                const uint32_t u = __float_as_uint(q);
+                return left != 0.0f && (u & 0x1FFFFFu) == 0 && (u & 0x7FFFFFFFu) ? __uint_as_float((__float_as_int(left) ^ int(u)) < 0 ? u - 1 : u + 1) : q;
+            };
+            q[i] = make_float2(off(q[i].x, left.x), off(q[i].y, left.y));
+        }
+    }
+    return make_uint2(floatx8_to_e2m1(q), floatx8_to_e2m1(q + 4));
 }
 
-template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(const __grid_constant__ MoveArgs a) {
+template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(const __grid_constant__ MoveArgs a, uint32_t heads) {
     __shared__ int32_t s_pos[kTokens], s_block[kTokens];
     __shared__ uint32_t s_seq[kTokens];
-    const uint32_t B = a.c.tokens, D = a.c.dim, h = blockIdx.y, per_row = D / 16;
-    const uint32_t t0 = blockIdx.x * kTokens, n = min(uint32_t(kTokens), a.b.total - t0), units = n * per_row;
-    const uint32_t inverse = 0xFFFFFFFFu / per_row + 1;  // i / per_row = i * inverse / 2^32 (1 piece a row: 0)
-    auto row_of = [&](uint32_t i) { return inverse ? __umulhi(i, inverse) : i; };
+    const uint32_t B = a.c.tokens, per_row = a.c.dim / 16, h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.c.heads);
+    const uint32_t t0 = blockIdx.x * kTokens, n = min(uint32_t(kTokens), a.b.total - t0);
+    const uint32_t row = threadIdx.x / per_row, g = threadIdx.x - row * per_row;
+    const bool mine = row < n;
     constexpr int elt = DT == ZC_FP32 ? 4 : 2;
-    Piece<DT> in[2][kPieces][2];
-#pragma unroll
-    for (int p = 0; p < kPieces; p++) {
-        const uint32_t i = threadIdx.x + p * kThreads, row = row_of(i);
-        if (i >= units) continue;
+    Piece<DT> next[2][2];
+    auto ask = [&](uint32_t h) {
+        if (!mine) return;
 #pragma unroll
         for (int kv = 0; kv < 2; kv++) {
-            const uint8_t *x = static_cast<const uint8_t *>(a.x[kv].p) +
-                               (int64_t(t0 + row) * a.x[kv].token + int64_t(h) * a.x[kv].head + (i - row * per_row) * 16) * elt;
-            in[kv][p][0].load(x);
-            in[kv][p][1].load(x + Piece<DT>::kBytes);
+            const uint8_t *x = static_cast<const uint8_t *>(a.x[kv].p) + (int64_t(t0 + row) * a.x[kv].token + int64_t(h) * a.x[kv].head + g * 16) * elt;
+            next[kv][0].load(x);
+            next[kv][1].load(x + Piece<DT>::kBytes);
         }
-    }
+    };
+    ask(h0);
     locate(a.b, B, t0, n, s_pos, s_seq, a.d_status);
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads)
-        s_block[i] = s_pos[i] < 0 ? -1 : int32_t(read_block(a.b, a.c, s_seq[i], block_of_16(a.c, uint32_t(s_pos[i]) / 16), a.d_status));
+    static_assert(kTokens <= kThreads, "a thread looks up one token's block");
+    if (threadIdx.x < n)
+        s_block[threadIdx.x] = s_pos[threadIdx.x] < 0 ? -1 : int32_t(read_block(a.b, a.c, s_seq[threadIdx.x], block_of_16(a.c, uint32_t(s_pos[threadIdx.x]) / 16), a.d_status));
     __syncthreads();
-#pragma unroll
-    for (int p = 0; p < kPieces; p++) {
-        const uint32_t i = threadIdx.x + p * kThreads, row = row_of(i);
-        if (i >= units || s_block[row] < 0) continue;
+    const bool there = mine && s_block[mine ? row : 0] >= 0;
+    int64_t code_at = 0, scale_at = 0;
+    if (there) {
         const int64_t id = s_block[row];
-        const uint32_t g = i - row * per_row, at = h * B + uint32_t(s_pos[row]) - block_of_16(a.c, uint32_t(s_pos[row]) / 16) * B;
+        const uint32_t at = h0 * B + uint32_t(s_pos[row]) - block_of_16(a.c, uint32_t(s_pos[row]) / 16) * B;
+        code_at = id * a.c.block_stride + int64_t(at) * a.c.row + g * 8;
+        scale_at = id * a.c.scale_stride + int64_t(at) * per_row + g;
+    }
+    for (uint32_t h = h0; h < h1; h++) {
+        Piece<DT> in[2][2] = {{next[0][0], next[0][1]}, {next[1][0], next[1][1]}};
+        if (h + 1 < h1) ask(h + 1);  // the next head's are on their way while this one's are worked on
+        if (!there) continue;
 #pragma unroll
         for (int kv = 0; kv < 2; kv++) {
             uint32_t byte;
-            const uint2 codes = quantise<DT>(in[kv][p], byte);
-            *reinterpret_cast<uint2 *>(a.c.code[kv] + id * a.c.block_stride + int64_t(at) * a.c.row + g * 8) = codes;
-            a.c.group[kv][id * a.c.scale_stride + int64_t(at) * per_row + g] = uint8_t(byte);
+            const uint2 codes = quantise<DT>(in[kv], byte);
+            *reinterpret_cast<uint2 *>(a.c.code[kv] + code_at) = codes;
+            a.c.group[kv][scale_at] = uint8_t(byte);
         }
+        code_at += int64_t(B) * a.c.row;
+        scale_at += int64_t(B) * per_row;
     }
     if (blockIdx.x == 0 && blockIdx.y == 0) report_batch(a.b, B, a.d_status, threadIdx.x, kThreads, true);
+}
+
+template <int DT> void launch(const MoveArgs &a, cudaStream_t s) {
+    const uint32_t runs = (a.b.total + kTokens - 1) / kTokens;
+    const uint32_t heads = heads_of_a_cta(runs, a.c.heads);
+    write4_kernel<DT><<<dim3(runs, (a.c.heads + heads - 1) / heads), kThreads, 0, s>>>(a, heads);
 }
 
 } // namespace
 
 int launch_write4(int dtype, const MoveArgs &a, cudaStream_t s) {
-    const dim3 grid((a.b.total + kTokens - 1) / kTokens, a.c.heads);
     switch (dtype) {
-    case ZC_BF16: write4_kernel<ZC_BF16><<<grid, kThreads, 0, s>>>(a); break;
-    case ZC_FP16: write4_kernel<ZC_FP16><<<grid, kThreads, 0, s>>>(a); break;
-    default: write4_kernel<ZC_FP32><<<grid, kThreads, 0, s>>>(a); break;
+    case ZC_BF16: launch<ZC_BF16>(a, s); break;
+    case ZC_FP16: launch<ZC_FP16>(a, s); break;
+    default: launch<ZC_FP32>(a, s); break;
     }
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }

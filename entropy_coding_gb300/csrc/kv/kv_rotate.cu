@@ -11,24 +11,23 @@
 //
 // A lane has 16 columns of a row, both of each of its 8 pairs, so that the
 // rotation needs no other lane and the norm one sum over D / 16 lanes. A CTA has
-// kTokens packed tokens with all their heads: their angles' sines and cosines
-// are computed once, for 16 columns of every head, while the first rows are on
-// their way.
+// a few packed tokens with all their heads, a warp rows of one of them: the
+// angles' sines and cosines are computed once, while the first rows are on
+// their way, and stay in registers. Arithmetic is on two floats at a time.
 #include "kv4_common.cuh"
 
 namespace zc {
 namespace kv {
 namespace {
 
-constexpr int kThreads = 256, kTokens = 4;
-constexpr int kUnroll = 2;                 // rows of a lane in flight
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLanes = kMaxHeadDim / 16;   // of a row, at most
 
-struct Shared {
+template <int kTokens> struct Shared {
     int32_t pos[kTokens];
     uint32_t seq[kTokens];
     // for lane c of a row, quarter j of its pairs (or columns): conflict-free as they are read
-    float4 turn[kTokens][4][kLanes];  // cos, sin of two pairs
+    float4 turn[kTokens][4][kLanes];  // cosines of two pairs, and sines
     float4 weight[2][4][kLanes];      // of q and k
 };
 
@@ -58,7 +57,7 @@ __device__ __forceinline__ float2 turned(const RotateArgs &a, uint32_t pair, int
 }
 
 // The whole CTA: positions, sines and cosines, and weights.
-template <bool kInterleaved> __device__ __forceinline__ void prepare(const RotateArgs &a, Shared &sm, uint32_t t0, uint32_t n) {
+template <bool kInterleaved, int kTokens> __device__ __forceinline__ void prepare(const RotateArgs &a, Shared<kTokens> &sm, uint32_t t0, uint32_t n) {
     locate(a.b, 0, t0, n, sm.pos, sm.seq, a.d_status);
     const uint32_t pairs = a.rot / 2;
     for (uint32_t i = threadIdx.x; i < n * pairs; i += kThreads) {
@@ -66,7 +65,9 @@ template <bool kInterleaved> __device__ __forceinline__ void prepare(const Rotat
         if (sm.pos[token] < 0) continue;
         uint32_t c = pair / 8, m = pair % 8;
         if (kInterleaved) c = pair % (pairs / 2) / 4, m = pair % 4 + (pair < pairs / 2 ? 0 : 4);
-        reinterpret_cast<float2 *>(&sm.turn[token][m / 2][c])[m % 2] = turned(a, pair, sm.pos[token]);
+        const float2 t = turned(a, pair, sm.pos[token]);
+        float *to = reinterpret_cast<float *>(&sm.turn[token][m / 2][c]) + m % 2;
+        to[0] = t.x, to[2] = t.y;
     }
     for (uint32_t i = threadIdx.x; i < 2 * a.dim; i += kThreads) {
         const int kv = i >= a.dim;
@@ -78,13 +79,17 @@ template <bool kInterleaved> __device__ __forceinline__ void prepare(const Rotat
 }
 
 // 1 / sqrt(sum x^2 / D + eps) of a row whose lanes are `lanes` neighbours; the whole warp calls it.
-__device__ __forceinline__ float row_norm(const float (&x)[16], uint32_t lanes, float inverse_dim, float eps) {
+__device__ __forceinline__ float row_norm(const float2 (&x)[8], uint32_t lanes, float inverse_dim, float eps) {
     auto sum_of = [&](float by) {
-        float s = 0.0f;
+        float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 16; i++) s = fmaf(x[i] * by, x[i] * by, s);
-        for (uint32_t d = 1; d < lanes; d *= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        return s;
+        for (int i = 0; i < 8; i++) {
+            const float2 y = by == 1.0f ? x[i] : mul2(x[i], both(by));
+            s = fma2(y, y, s);
+        }
+        float t = s.x + s.y;
+        for (uint32_t d = 1; d < lanes; d *= 2) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+        return t;
     };
     const float sum = sum_of(1.0f);
     // Squares out of float's range: again with the larger of the row's largest magnitude and the root of eps brought to
@@ -93,7 +98,7 @@ __device__ __forceinline__ float row_norm(const float (&x)[16], uint32_t lanes, 
     if (!__any_sync(0xFFFFFFFFu, out)) return rsqrtf(fmaf(sum, inverse_dim, eps));
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; i++) top = fmaxf(top, fabsf(x[i]));
+    for (int i = 0; i < 8; i++) top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
     for (uint32_t d = 1; d < lanes; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     const bool scale = out && top > 0.0f && top < INFINITY;
     const int e = scale ? min(int(__float_as_uint(fmaxf(top, sqrtf(eps))) >> 23) - 127, 120) : 0;
@@ -102,85 +107,102 @@ __device__ __forceinline__ float row_norm(const float (&x)[16], uint32_t lanes, 
     return rsqrtf(fmaf(again, inverse_dim, eps * by * by)) * by;
 }
 
-template <int DT, bool kInterleaved> __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
-    __shared__ Shared sm;
-    constexpr int elt = DT == ZC_FP32 ? 4 : 2;
+template <int DT, bool kInterleaved, int kTokens> __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_constant__ RotateArgs a) {
+    __shared__ Shared<kTokens> sm;
+    constexpr int elt = DT == ZC_FP32 ? 4 : 2, kShare = kWarps / kTokens;  // warps of a token
     const uint32_t t0 = blockIdx.x * kTokens, n = min(uint32_t(kTokens), a.b.total - t0);
-    // lanes of a row, up to the next power of two, and the rows of the CTA that are done together
-    const uint32_t used = a.dim / 16, lanes = used <= 1 ? 1 : used <= 2 ? 2 : used <= 4 ? 4 : 8;
-    const uint32_t c = threadIdx.x & (lanes - 1), together = kThreads / lanes, all = a.heads[0] + a.heads[1];
-    const bool mine = c < used, turns = 16 * c < a.rot;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, token = warp / kShare;
+    // lanes of a row, up to the next power of two, and rows that a warp does together
+    const uint32_t used = a.dim / 16, lanes = used <= 1 ? 1 : used <= 2 ? 2 : used <= 4 ? 4 : 8, together = 32 / lanes;
+    const uint32_t c = lane & (lanes - 1), all = a.heads[0] + a.heads[1];
+    const bool mine = c < used && token < n, turns = 16 * c < a.rot;
     const uint32_t col0 = first_column(a, c), col1 = second_column(a, c);
-    const float inverse_dim = 1.0f / float(a.dim);
-    uint32_t token = 0, head = threadIdx.x / lanes;  // of the thread's next row
-    for (bool first = true;; first = false) {
-        Piece<DT> in[kUnroll][2];
-        uint32_t at_token[kUnroll], at_head[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; u++) {
-            while (head >= all && token < n) head -= all, token++;
-            at_token[u] = token, at_head[u] = head;
-            head += together;
-            const bool there = mine && at_token[u] < n;
-            const int kv = at_head[u] >= a.heads[0];
-            if (there) {
-                const Rows &r = a.in[kv];
-                const uint8_t *x = static_cast<const uint8_t *>(r.p) + (int64_t(t0 + at_token[u]) * r.token + int64_t(at_head[u] - (kv ? a.heads[0] : 0)) * r.head) * elt;
-                in[u][0].load(x + col0 * elt);
-                in[u][1].load(x + col1 * elt);
-            } else {
-                in[u][0].clear();
-                in[u][1].clear();
-            }
+    // a row's address in q or k, of the inputs or outputs
+    auto at = [&](const Rows (&x)[2], uint32_t row) {
+        const int kv = row >= a.heads[0];
+        return static_cast<uint8_t *>(x[kv].p) + (int64_t(t0 + token) * x[kv].token + int64_t(row - (kv ? a.heads[0] : 0)) * x[kv].head) * elt;
+    };
+    const uint32_t r0 = warp % kShare * together;
+    uint32_t row = r0 + lane / lanes;
+    Piece<DT> next[2];
+    auto ask = [&]() {
+        if (mine && row < all) {
+            const uint8_t *x = at(a.in, row);
+            next[0].load(x + col0 * elt);
+            next[1].load(x + col1 * elt);
+        } else {
+            next[0].clear();
+            next[1].clear();
         }
-        if (first) prepare<kInterleaved>(a, sm, t0, n);
+    };
+    ask();
+    prepare<kInterleaved>(a, sm, t0, n);
+    const bool held = token < n && sm.pos[token < n ? token : 0] >= 0;  // (the token belongs to a sequence)
+    float2 cosine[4], sine[4];
 #pragma unroll
-        for (int u = 0; u < kUnroll; u++) {
-            const bool there = mine && at_token[u] < n;
-            const int kv = at_head[u] >= a.heads[0];
-            float x[16];
-            in[u][0].get(x);
-            in[u][1].get(x + 8);
-            if (a.weight[0] || a.weight[1]) {
-                const float norm = row_norm(x, lanes, inverse_dim, a.eps);
-                if (there && a.weight[kv]) {
+    for (int j = 0; j < 4; j++) {
+        const float4 t = sm.turn[token][j][c];
+        cosine[j] = make_float2(t.x, t.y), sine[j] = make_float2(t.z, t.w);
+    }
+    const float inverse_dim = 1.0f / float(a.dim);
+    const bool norms = a.weight[0] || a.weight[1];
+    // (the whole warp goes on as long as one of its rows is there: its sums are over all of it)
+    for (uint32_t r = r0; held && r < all; r += kShare * together) {
+        const uint32_t now = row;
+        const int kv = now >= a.heads[0];
+        float2 x[8];
+        next[0].get(x);
+        next[1].get(x + 4);
+        row += kShare * together;
+        ask();
+        if (norms) {
+            const float norm = row_norm(x, lanes, inverse_dim, a.eps);
+            if (a.weight[kv]) {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const float4 w = sm.weight[kv][j][c];
-                        x[4 * j] *= norm * w.x, x[4 * j + 1] *= norm * w.y, x[4 * j + 2] *= norm * w.z, x[4 * j + 3] *= norm * w.w;
-                    }
+                for (int j = 0; j < 4; j++) {
+                    const float4 w = sm.weight[kv][j][c];
+                    x[2 * j] = mul2(x[2 * j], mul2(make_float2(w.x, w.y), both(norm)));
+                    x[2 * j + 1] = mul2(x[2 * j + 1], mul2(make_float2(w.z, w.w), both(norm)));
                 }
             }
-            if (!there || sm.pos[at_token[u]] < 0) continue;
-            if (turns) {
+        }
+        if (!mine || now >= all) continue;
+        if (turns) {
+            if (kInterleaved) {
 #pragma unroll
                 for (int m = 0; m < 8; m++) {
-                    const float2 t = reinterpret_cast<const float2 *>(&sm.turn[at_token[u]][m / 2][c])[m % 2];
-                    const int i = kInterleaved ? 2 * m : m, j = kInterleaved ? 2 * m + 1 : m + 8;
-                    const float p = x[i], q = x[j];
-                    x[i] = fmaf(p, t.x, -(q * t.y)), x[j] = fmaf(q, t.x, p * t.y);
+                    const float cs = m % 2 ? cosine[m / 2].y : cosine[m / 2].x, sn = m % 2 ? sine[m / 2].y : sine[m / 2].x;
+                    x[m] = make_float2(fmaf(x[m].x, cs, -(x[m].y * sn)), fmaf(x[m].y, cs, x[m].x * sn));
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < 4; m++) {
+                    const float2 p = x[m], q = x[m + 4], minus = make_float2(-sine[m].x, -sine[m].y);
+                    x[m] = fma2(p, cosine[m], mul2(q, minus)), x[m + 4] = fma2(q, cosine[m], mul2(p, sine[m]));
                 }
             }
-            const Rows &r = a.out[kv];
-            uint8_t *y = static_cast<uint8_t *>(r.p) + (int64_t(t0 + at_token[u]) * r.token + int64_t(at_head[u] - (kv ? a.heads[0] : 0)) * r.head) * elt;
-            Piece<DT> out[2];
-            out[0].put(x);
-            out[1].put(x + 8);
-            out[0].store(y + col0 * elt);
-            out[1].store(y + col1 * elt);
         }
-        // (a warp goes on as long as one of its rows is there: its sums are over all of it)
-        while (head >= all && token < n) head -= all, token++;
-        if (!__any_sync(0xFFFFFFFFu, token < n)) break;
+        uint8_t *y = at(a.out, now);
+        Piece<DT> out[2];
+        out[0].put(x);
+        out[1].put(x + 4);
+        out[0].store(y + col0 * elt);
+        out[1].store(y + col1 * elt);
     }
     if (blockIdx.x == 0) report_batch(a.b, 0xFFFFFFFFu, a.d_status, threadIdx.x, kThreads, true);
 }
 
-template <int DT> void launch(bool interleaved, const RotateArgs &a, cudaStream_t s) {
-    const uint32_t grid = (a.b.total + kTokens - 1) / kTokens;
-    if (interleaved) rotate_kernel<DT, true><<<grid, kThreads, 0, s>>>(a);
-    else rotate_kernel<DT, false><<<grid, kThreads, 0, s>>>(a);
+// Tokens of a CTA: one, which then has all of its warps, while that makes no more than 2 CTAs an SM; 4, and 8 of many. (32
+// tokens of 40 heads of 128: 1 token 6.2 us, 4 tokens 8.2; 608 tokens: 4 tokens 9.5, 8 tokens 12.3; 2432 single tokens 16.4 and
+// 18.3, 3648 26.1 and 22.1; 17138 tokens of prompts 65.5 and 63.6.)
+template <int DT, bool kInterleaved> void launch(const RotateArgs &a, cudaStream_t s) {
+    const uint32_t sms = uint32_t(sm_count());
+    if (a.b.total <= 2 * sms) rotate_kernel<DT, kInterleaved, 1><<<a.b.total, kThreads, 0, s>>>(a);
+    else if (a.b.total <= 16 * sms) rotate_kernel<DT, kInterleaved, 4><<<(a.b.total + 3) / 4, kThreads, 0, s>>>(a);
+    else rotate_kernel<DT, kInterleaved, 8><<<(a.b.total + 7) / 8, kThreads, 0, s>>>(a);
 }
+
+template <int DT> void launch(bool interleaved, const RotateArgs &a, cudaStream_t s) { interleaved ? launch<DT, true>(a, s) : launch<DT, false>(a, s); }
 
 } // namespace
 
