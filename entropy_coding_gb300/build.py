@@ -1,5 +1,6 @@
 """Build libzc.so (the C-ABI library) from csrc/*.cu and csrc/kv/*.cu with nvcc
-for sm_103a.
+for sm_103a, and the Python module of the cache's calls on torch tensors
+(csrc/binding) with g++ against the installed torch.
 
 Each translation unit compiles in parallel; the objects are linked into
 entropy_coding_gb300/_lib/libzc.so. Rebuilds only when a source or header is
@@ -9,9 +10,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.machinery
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -74,7 +78,45 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     return LIB
 
 
+def _module_path() -> str:
+    import torch
+    return os.path.join(OUT_DIR, f"zc_torch.{torch.__version__.replace('+', '_')}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+def build_module(force: bool = False) -> str:
+    """The Python module for this torch (its C++ interface differs between versions)."""
+    import torch
+    src, out = os.path.join(CSRC, "binding", "kv_torch.cpp"), _module_path()
+    deps = [src, os.path.join(INCLUDE, "zc.h")]
+    if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+        return out
+    os.makedirs(OUT_DIR, exist_ok=True)
+    root = os.path.dirname(torch.__file__)
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], INCLUDE]
+    libs = os.path.join(root, "lib")
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in includes), src, "-o", tmp,
+           f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
+def load_module():
+    """The Python module, built on first use if absent."""
+    path = build_module()
+    loader = importlib.machinery.ExtensionFileLoader("zc_torch", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("zc_torch", path, loader=loader))
+    loader.exec_module(module)
+    return module
+
+
 if __name__ == "__main__":
     import sys
+    build_module(force="--force" in sys.argv)
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv,
                 extra_flags=["-Xptxas", "-v"] if "--ptxas" in sys.argv else []))

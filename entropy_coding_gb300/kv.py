@@ -65,6 +65,7 @@ _failures = 0
 # zc_kv_write, zc_kv_read, zc_kv_attend and its two sizes, the same of the 4-bit cache, and zc_kv_rotate, once the library is
 # loaded; a cache's are those from its _calls on
 _entry = None
+_torch = None  # the module of the calls on torch tensors (csrc/binding), once a cache is made
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -105,6 +106,16 @@ def _entries():
     return _entry
 
 
+def _quick(first: int):
+    """Addresses of a kind of cache's entry points and of zc_kv_rotate, for the calls that the module makes in one step."""
+    global _torch
+    if _torch is None:
+        from . import _build
+        _torch = _build.load_module()
+    e = _entries()
+    return tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (*e[first:first + 3], e[10]))
+
+
 def _outer(t: torch.Tensor, least: int, what: str) -> int:
     """Distance between a tensor's outermost slices, each of ``least`` elements. A single slice has none of its own;
     slices that overlap (an expanded tensor) are refused, since the kernels step from one to the next."""
@@ -124,7 +135,8 @@ class KVCache:
     the block dimension (one layer of several) are fine as long as K and V
     have the same strides. ``KVCache.empty`` allocates one."""
 
-    _calls = 0  # of _entries()
+    _calls = 0     # of _entries()
+    _quick = None  # where every call is on the cache's device: write, read, attend and rotate's addresses
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
@@ -159,6 +171,7 @@ class KVCache:
                          block_stride, scale_stride, n, h, b, d)
         self._ref = ctypes.addressof(self._c)
         self._status = self.status.data_ptr()
+        self._quick = None if self._many else _quick(self._calls)
 
     def _meet(self, handle: int) -> None:
         """A stream's first call: it comes after the status was made, and the status outlives its calls. (A graph is
@@ -367,6 +380,12 @@ def kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, s
     """Quantise the batch's tokens into the cache (zc_kv_write, zc_kv4_write). ``k``, ``v``:
     [total_tokens, kv_heads, head_dim] in bfloat16, float16 or float32, any
     strides that are multiples of 16 bytes (views of a fused projection)."""
+    quick = cache._quick
+    if quick is not None and stream is None:
+        st = _torch.move(quick[0], cache._ref, batch._ref, cache._status, _handle(None, cache), cache._index, batch.total_tokens,
+                         cache.kv_heads, cache.head_dim, k, v)
+        if st is not None:
+            return _check(st, "zc_kv_write")
     _move(_entries()[cache._calls], "zc_kv_write", cache, batch, k, v, stream)
 
 
@@ -383,6 +402,13 @@ def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16,
     code = _CODE.get(dtype)
     if code is None:
         _fail("zc_kv_read: bfloat16, float16 or float32")
+    quick = cache._quick
+    if quick is not None and stream is None:
+        r = _torch.read(quick[1], cache._ref, batch._ref, cache._status, _handle(None, cache), cache._index, batch.total_tokens,
+                        cache.kv_heads, cache.head_dim, code)
+        if type(r) is not tuple:
+            _check(r, "zc_kv_read")
+        return r
     heads, dim, device = cache.kv_heads, cache.head_dim, cache.device
     shape = (batch.total_tokens, heads, dim)
     if stream is None:
@@ -444,6 +470,18 @@ def kv_attend(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | No
     with j <= p (``causal``) and j > p - window (``window`` > 0). ``scale``
     defaults to head_dim ** -0.5. The tokens' own keys and values are in the
     cache already (kv_write first)."""
+    quick = cache._quick
+    if quick is not None and stream is None and q.dim() == 3 and 0 <= window <= 0x7FFFFFFF:
+        handle, dim = _handle(None, cache), cache.head_dim
+        ws = batch._ws.get((cache.kv_heads, dim, q.shape[1], handle, cache._calls))
+        if ws is not None and ws[3] == _failures:
+            r = _torch.attend(quick[2], cache._ref, batch._ref, cache._status, handle, cache._index, batch.total_tokens,
+                              cache.kv_heads, dim, q, dim ** -0.5 if scale is None else scale, _CAUSAL if causal else 0, window,
+                              ws[0], ws[1])
+            if r is not None:
+                if type(r) is not tuple:
+                    _check(r, "zc_kv_attend")
+                return r
     code, heads, rq = _query(cache, batch, q)
     shape, device = q.shape, cache.device
     if stream is None:
@@ -478,6 +516,8 @@ class KVRotation:
         self.rot_dim, self.interleaved = 2 * len(turns), bool(interleaved)
         self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
         self.device, self._index = self.turns.device, self.turns.device.index
+        self._address = self.turns.data_ptr() if turns else 0
+        self._flags = _INTERLEAVED if self.interleaved else 0
         self._ready = None
         if self.turns.is_cuda:
             with torch.cuda.device(self.device):
@@ -523,8 +563,7 @@ def _rotate(cache, batch, rotation, code, rows, heads, q_weight, k_weight, eps, 
     handle = _handle(stream, cache)
     if handle not in rotation._streams:
         rotation._meet(handle)
-    r = _Rotation(rotation.turns.data_ptr() if rotation.rot_dim else None, rotation.rot_dim,
-                  _INTERLEAVED if rotation.interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
+    r = _Rotation(rotation._address, rotation.rot_dim, rotation._flags, None if q_weight is None else q_weight.data_ptr(),
                   None if k_weight is None else k_weight.data_ptr(), kind, eps)
     _check(_entries()[10](batch._ref, ctypes.addressof(r), code, cache.head_dim, heads, cache.kv_heads,
                           *map(ctypes.addressof, rows), cache._status, handle), "zc_kv_rotate")
@@ -565,6 +604,17 @@ def kv_rotate(cache: KVCache, batch: KVBatch, rotation: KVRotation, q: torch.Ten
     [total_tokens, kv_heads, head_dim] in bfloat16, float16 or float32, any
     strides that are multiples of 16 bytes (views of a fused projection).
     Sums are float32, and a number is rounded once."""
+    quick = cache._quick
+    if quick is not None and stream is None and rotation._index == cache._index:
+        handle = _handle(None, cache)
+        if handle not in rotation._streams:
+            rotation._meet(handle)
+        r = _torch.rotate(quick[3], batch._ref, cache._status, handle, cache._index, batch.total_tokens, cache.kv_heads,
+                          cache.head_dim, rotation._address, rotation.rot_dim, rotation._flags, q, k, q_weight, k_weight, eps)
+        if r is not None:
+            if type(r) is not tuple:
+                _check(r, "zc_kv_rotate")
+            return r
     code, heads, rows = _pair(cache, batch, q, k)
     if stream is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
