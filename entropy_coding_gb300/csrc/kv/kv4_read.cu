@@ -31,6 +31,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read4_kernel(const
     const uint32_t B = a.c.tokens, D = a.c.dim, per_row = D / 8, h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.c.heads);
     const uint32_t t0 = blockIdx.x * kTokens, n = min(uint32_t(kTokens), a.b.total - t0), units = n * per_row;
     const uint32_t inverse = 0xFFFFFFFFu / per_row + 1;  // i / per_row = i * inverse / 2^32
+    after_the_last();
     locate(a.b, B, t0, n, s_pos, s_seq, a.d_status);
     for (uint32_t i = threadIdx.x; i < n; i += kThreads)
         s_block[i] = s_pos[i] < 0 ? -1 : int32_t(read_block(a.b, a.c, s_seq[i], block_of_16(a.c, uint32_t(s_pos[i]) / 16), a.d_status));
@@ -84,21 +85,16 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read4_kernel(const
     if (blockIdx.x == 0 && blockIdx.y == 0) report_batch(a.b, B, a.d_status, threadIdx.x, kThreads, true);
 }
 
-template <int DT> void launch(const MoveArgs &a, cudaStream_t s) {
+template <int DT> int launch(const MoveArgs &a, cudaStream_t s) {
     const uint32_t runs = (a.b.total + kTokens - 1) / kTokens;
     const uint32_t heads = heads_of_a_cta(runs, a.c.heads);
-    read4_kernel<DT><<<dim3(runs, (a.c.heads + heads - 1) / heads), kThreads, 0, s>>>(a, heads);
+    return launch_early(read4_kernel<DT>, dim3(runs, (a.c.heads + heads - 1) / heads), kThreads, 0, s, a, heads);
 }
 
 } // namespace
 
 int launch_read4(int dtype, const MoveArgs &a, cudaStream_t s) {
-    switch (dtype) {
-    case ZC_BF16: launch<ZC_BF16>(a, s); break;
-    case ZC_FP16: launch<ZC_FP16>(a, s); break;
-    default: launch<ZC_FP32>(a, s); break;
-    }
-    return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
+    return dtype == ZC_BF16 ? launch<ZC_BF16>(a, s) : dtype == ZC_FP16 ? launch<ZC_FP16>(a, s) : launch<ZC_FP32>(a, s);
 }
 
 } // namespace kv

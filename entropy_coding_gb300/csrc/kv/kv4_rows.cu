@@ -36,6 +36,7 @@ template <int DP> struct Codes4 {
     // CTAs of an SM: 3 hold the registers of one tile of rows (4 of fewer registers, with two steps of a ring each, take as
     // long), 2 those of two tiles (16 sequences of 16 rows: 23.7 us, with 3 and spilled registers 26.7).
     template <int NT> static constexpr int resident() { return NT == 1 ? 3 : 2; }
+    static constexpr bool kEarly = true;
     static constexpr bool kMergeInRing = true;
     // (64 sequences of up to 8192 keys: 0 units 83.5 us, with the CTAs that have many short items last, 2 units 74.4, 3 units
     // 73.8, 4 units 73.2, 6 units 73.9)

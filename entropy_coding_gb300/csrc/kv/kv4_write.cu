@@ -95,6 +95,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(cons
             next[kv][1].load(x + Piece<DT>::kBytes);
         }
     };
+    after_the_last();
     ask(h0);
     locate(a.b, B, t0, n, s_pos, s_seq, a.d_status);
     static_assert(kTokens <= kThreads, "a thread looks up one token's block");
@@ -126,21 +127,16 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(cons
     if (blockIdx.x == 0 && blockIdx.y == 0) report_batch(a.b, B, a.d_status, threadIdx.x, kThreads, true);
 }
 
-template <int DT> void launch(const MoveArgs &a, cudaStream_t s) {
+template <int DT> int launch(const MoveArgs &a, cudaStream_t s) {
     const uint32_t runs = (a.b.total + kTokens - 1) / kTokens;
     const uint32_t heads = heads_of_a_cta(runs, a.c.heads);
-    write4_kernel<DT><<<dim3(runs, (a.c.heads + heads - 1) / heads), kThreads, 0, s>>>(a, heads);
+    return launch_early(write4_kernel<DT>, dim3(runs, (a.c.heads + heads - 1) / heads), kThreads, 0, s, a, heads);
 }
 
 } // namespace
 
 int launch_write4(int dtype, const MoveArgs &a, cudaStream_t s) {
-    switch (dtype) {
-    case ZC_BF16: launch<ZC_BF16>(a, s); break;
-    case ZC_FP16: launch<ZC_FP16>(a, s); break;
-    default: launch<ZC_FP32>(a, s); break;
-    }
-    return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
+    return dtype == ZC_BF16 ? launch<ZC_BF16>(a, s) : dtype == ZC_FP16 ? launch<ZC_FP16>(a, s) : launch<ZC_FP32>(a, s);
 }
 
 } // namespace kv

@@ -135,6 +135,7 @@ template <int DT, bool kInterleaved, int kTokens> __global__ void __launch_bound
             next[1].clear();
         }
     };
+    after_the_last();
     ask();
     prepare<kInterleaved>(a, sm, t0, n);
     const bool held = token < n && sm.pos[token < n ? token : 0] >= 0;  // (the token belongs to a sequence)
@@ -195,24 +196,19 @@ template <int DT, bool kInterleaved, int kTokens> __global__ void __launch_bound
 // Tokens of a CTA: one, which then has all of its warps, while that makes no more than 2 CTAs an SM; 4, and 8 of many. (32
 // tokens of 40 heads of 128: 1 token 6.2 us, 4 tokens 8.2; 608 tokens: 4 tokens 9.5, 8 tokens 12.3; 2432 single tokens 16.4 and
 // 18.3, 3648 26.1 and 22.1; 17138 tokens of prompts 65.5 and 63.6.)
-template <int DT, bool kInterleaved> void launch(const RotateArgs &a, cudaStream_t s) {
+template <int DT, bool kInterleaved> int launch(const RotateArgs &a, cudaStream_t s) {
     const uint32_t sms = uint32_t(sm_count());
-    if (a.b.total <= 2 * sms) rotate_kernel<DT, kInterleaved, 1><<<a.b.total, kThreads, 0, s>>>(a);
-    else if (a.b.total <= 16 * sms) rotate_kernel<DT, kInterleaved, 4><<<(a.b.total + 3) / 4, kThreads, 0, s>>>(a);
-    else rotate_kernel<DT, kInterleaved, 8><<<(a.b.total + 7) / 8, kThreads, 0, s>>>(a);
+    if (a.b.total <= 2 * sms) return launch_early(rotate_kernel<DT, kInterleaved, 1>, dim3(a.b.total), kThreads, 0, s, a);
+    if (a.b.total <= 16 * sms) return launch_early(rotate_kernel<DT, kInterleaved, 4>, dim3((a.b.total + 3) / 4), kThreads, 0, s, a);
+    return launch_early(rotate_kernel<DT, kInterleaved, 8>, dim3((a.b.total + 7) / 8), kThreads, 0, s, a);
 }
 
-template <int DT> void launch(bool interleaved, const RotateArgs &a, cudaStream_t s) { interleaved ? launch<DT, true>(a, s) : launch<DT, false>(a, s); }
+template <int DT> int launch(bool interleaved, const RotateArgs &a, cudaStream_t s) { return interleaved ? launch<DT, true>(a, s) : launch<DT, false>(a, s); }
 
 } // namespace
 
 int launch_rotate(int dtype, bool interleaved, const RotateArgs &a, cudaStream_t s) {
-    switch (dtype) {
-    case ZC_BF16: launch<ZC_BF16>(interleaved, a, s); break;
-    case ZC_FP16: launch<ZC_FP16>(interleaved, a, s); break;
-    default: launch<ZC_FP32>(interleaved, a, s); break;
-    }
-    return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
+    return dtype == ZC_BF16 ? launch<ZC_BF16>(interleaved, a, s) : dtype == ZC_FP16 ? launch<ZC_FP16>(interleaved, a, s) : launch<ZC_FP32>(interleaved, a, s);
 }
 
 } // namespace kv

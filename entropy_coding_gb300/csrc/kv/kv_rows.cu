@@ -49,6 +49,7 @@ template <int DP> struct Codes8 {
     // CTAs of an SM, as many as their registers allow, and slices of a ring, as many as fit the SM's shared memory then.
     static constexpr int kResident = 3, kStages = 3 * (128 / DP);
     template <int NT> static constexpr int resident() { return kResident; }
+    static constexpr bool kEarly = false;
     static constexpr bool kMergeInRing = false;
     static constexpr uint32_t kFixed = 0;
     using Maps = CodeMaps;

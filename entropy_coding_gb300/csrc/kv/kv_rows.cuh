@@ -17,6 +17,7 @@
 //   kSlice, kStages              keys of a warp's step, steps of its ring
 //   kFixed                       units that an item's beginning and end count as, besides its keys
 //   resident<NT>()               CTAs of an SM
+//   kEarly                       launched while the kernel before it still runs
 //   kMergeInRing                 warps' rows meet in their rings
 //   Maps, Stage, Warp            its tensor maps, a step's memory, and what a warp keeps besides
 //   look_up, fetch               where steps are, and asking for one
@@ -400,6 +401,8 @@ __global__ void __launch_bounds__(32 * F::kWarps, F::template resident<NT>()) ro
         prefetch_maps(maps);
     }
 
+    if (F::kEarly) after_the_last();
+
     // The line of work, and this CTA's piece [w0, w1) of it.
     uint64_t mine = 0, sum, W;
     for (uint32_t s = threadIdx.x; s < a.b.n_seqs; s += kThreads) {
@@ -484,7 +487,9 @@ template <class F, int NT> int launch(const AttendArgs &a, uint32_t rows, cudaSt
     typename F::Maps maps;
     const int st = make_maps(a.c, F::kDim, rows, maps);
     if (st != ZC_OK) return st;
-    rows_kernel<F, NT><<<uint32_t(sm_count() * F::template resident<NT>()), 32 * F::kWarps, smem_bytes<F, NT>(), s>>>(a, maps);
+    const uint32_t grid = uint32_t(sm_count() * F::template resident<NT>()), threads = 32 * F::kWarps;
+    if (F::kEarly) return launch_early(rows_kernel<F, NT>, dim3(grid), threads, smem_bytes<F, NT>(), s, a, maps);
+    rows_kernel<F, NT><<<grid, threads, smem_bytes<F, NT>(), s>>>(a, maps);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }
 

@@ -911,6 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const uint32_t cta = blockIdx.x;
     const int warp = threadIdx.x / 32;
 
+    if (kBits == 4) after_the_last();
+
     // The line of work, and this CTA's piece of it.
     const uint32_t slots = slot_of(a.b.total, a.b.n_seqs, a.group, kRows, 1);
     auto work_at = [&](uint32_t u, uint32_t &s, uint32_t &units) -> uint64_t {
@@ -1001,6 +1003,7 @@ template <int kBits, int DP> int launch(const AttendArgs &a, cudaStream_t s) {
     Maps<kBits> maps;
     const int st = make_maps(a.c, DP, 16, maps);
     if (st != ZC_OK) return st;
+    if (kBits == 4) return launch_early(tiles_kernel<kBits, DP>, dim3(uint32_t(sm_count())), kThreads, sizeof(Smem<kBits, DP>), s, a, maps);
     tiles_kernel<kBits, DP><<<uint32_t(sm_count()), kThreads, sizeof(Smem<kBits, DP>), s>>>(a, maps);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }

@@ -537,3 +537,72 @@ def test_both_caches_with_one_batch():
             c.check()
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3]) and not torch.equal(outs[0], outs[1])
     assert (outs[0] - outs[1]).abs().max() < 0.5
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_first_call_in_a_capture_among_other_kernels(new):
+    """The graph zeroes the workspace itself; its calls follow kernels and copies of others, and one another."""
+    rng = np.random.default_rng(7)
+    lens = [300, 90]
+    table, n = _table([l + 8 for l in lens], 32, rng)
+    caches = [zc.KV4Cache.empty(n, 2, 64, 32) for _ in range(2)]
+    fill, _ = _batch(table, lens, lens)
+    x = torch.randn(390, 2, 64, device=DEV).bfloat16()
+    for c in caches:
+        zc.kv_write(c, fill, x, x)
+    rotation = zc.KVRotation([0.5 ** i for i in range(32)])
+    batches = [_batch(table, [new, new], lens)[0] for _ in caches]
+    qs = torch.randn(2 * new, 8, 64, device=DEV).bfloat16()
+    ks = torch.randn(2 * new, 2, 64, device=DEV).bfloat16()
+
+    def step(c, b, q, k):
+        b.lens.add_(1)
+        q, k = zc.kv_rotate(c, b, rotation, q * 1.0, k + 0.0)
+        zc.kv_write(c, b, k, k)
+        out, lse = zc.kv_attend(c, b, q)
+        return out * 2.0, lse, zc.kv_read(c, b)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured = step(caches[1], batches[1], qs, ks)
+    for _ in range(6):
+        qs.copy_(torch.randn(2 * new, 8, 64, device=DEV))
+        ks.copy_(torch.randn(2 * new, 2, 64, device=DEV))
+        want = step(caches[0], batches[0], qs, ks)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((want[0], want[1], *want[2]), (captured[0], captured[1], *captured[2])):
+            assert torch.equal(a, b)
+    for c in caches:
+        c.check()
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v_scale, caches[1].v_scale)
+
+
+def test_calls_one_after_another_see_what_the_last_has_written():
+    """Kernels that begin before the one in front of them has ended: each step reads what the last one wrote, many in a row."""
+    rng = np.random.default_rng(8)
+    table, n = _table([4000], 64, rng)
+    cache = zc.KV4Cache.empty(n, 4, 128, 64)
+    rotation = zc.KVRotation([1.0 / (i + 1) for i in range(64)])
+    whole, _ = _batch(table, [4000], [4000])
+    x = torch.randn(4000, 4, 128, device=DEV).half()
+    results = []
+    for _ in range(3):
+        a = x
+        for i in range(30):  # each pass through the cache and the rotation is the next one's input
+            zc.kv_write(cache, whole, a, a)
+            k, v = zc.kv_read(cache, whole, dtype=torch.float16)
+            _, a = zc.kv_rotate(cache, whole, rotation, v, k)
+        results.append(a)
+    # the same with everything waited for
+    a = x
+    for i in range(30):
+        zc.kv_write(cache, whole, a, a)
+        torch.cuda.synchronize()
+        k, v = zc.kv_read(cache, whole, dtype=torch.float16)
+        torch.cuda.synchronize()
+        _, a = zc.kv_rotate(cache, whole, rotation, v, k)
+        torch.cuda.synchronize()
+    cache.check()
+    assert torch.isfinite(a).all() and all(torch.equal(a, r) for r in results)
