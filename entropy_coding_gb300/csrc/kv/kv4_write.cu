@@ -12,8 +12,8 @@
 // remains. (With the reciprocal in one float x = 3.5 s, s = 1.75, misses its
 // midpoint.)
 //
-// A thread has 16 columns of a packed token, K and V, head after head; a CTA up
-// to kTokens of them, so that it writes runs of rows. Its first reads do not wait
+// A thread has 16 columns of a packed token, K and V, head after head; a CTA as
+// many tokens as that makes, so that it writes runs of rows. Its first reads do not wait
 // for where the tokens belong: that is looked up meanwhile.
 #include "kv4_common.cuh"
 
@@ -21,7 +21,7 @@ namespace zc {
 namespace kv {
 namespace {
 
-constexpr int kThreads = 128, kTokens = kThreads / (kMaxHeadDim / 16);
+constexpr int kThreads = 128;
 
 // Scale byte for 16 columns whose largest magnitude is a (finite).
 __device__ __forceinline__ uint32_t scale_byte(float a) {
@@ -78,10 +78,10 @@ template <int DT> __device__ __forceinline__ uint2 quantise(const Piece<DT> (&in
 }
 
 template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(const __grid_constant__ MoveArgs a, uint32_t heads) {
-    __shared__ int32_t s_pos[kTokens], s_block[kTokens];
-    __shared__ uint32_t s_seq[kTokens];
-    const uint32_t B = a.c.tokens, per_row = a.c.dim / 16, h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.c.heads);
-    const uint32_t t0 = blockIdx.x * kTokens, n = min(uint32_t(kTokens), a.b.total - t0);
+    __shared__ int32_t s_pos[kThreads], s_block[kThreads];
+    __shared__ uint32_t s_seq[kThreads];
+    const uint32_t B = a.c.tokens, per_row = a.c.dim / 16, tokens = kThreads / per_row, h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.c.heads);
+    const uint32_t t0 = blockIdx.x * tokens, n = min(tokens, a.b.total - t0);
     const uint32_t row = threadIdx.x / per_row, g = threadIdx.x - row * per_row;
     const bool mine = row < n;
     constexpr int elt = DT == ZC_FP32 ? 4 : 2;
@@ -98,7 +98,6 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(cons
     after_the_last();
     ask(h0);
     locate(a.b, B, t0, n, s_pos, s_seq, a.d_status);
-    static_assert(kTokens <= kThreads, "a thread looks up one token's block");
     if (threadIdx.x < n)
         s_block[threadIdx.x] = s_pos[threadIdx.x] < 0 ? -1 : int32_t(read_block(a.b, a.c, s_seq[threadIdx.x], block_of_16(a.c, uint32_t(s_pos[threadIdx.x]) / 16), a.d_status));
     __syncthreads();
@@ -128,7 +127,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(cons
 }
 
 template <int DT> int launch(const MoveArgs &a, cudaStream_t s) {
-    const uint32_t runs = (a.b.total + kTokens - 1) / kTokens;
+    const uint32_t tokens = kThreads / (a.c.dim / 16), runs = (a.b.total + tokens - 1) / tokens;
     const uint32_t heads = heads_of_a_cta(runs, a.c.heads);
     return launch_early(write4_kernel<DT>, dim3(runs, (a.c.heads + heads - 1) / heads), kThreads, 0, s, a, heads);
 }

@@ -45,9 +45,15 @@ constexpr int kSlots = 8;               // key tiles whose scales are held: the 
 constexpr uint32_t kColumns = 512;      // of tensor memory: S (and W in its place) 0, 128, O 256, 384
 
 // Registers of a thread by warpgroup: two of rows, the conversion, the rest. What the groups take together is what the
-// CTA was launched with, 128 for each of 512 threads; a sum above that would wait for registers for ever.
-constexpr int kRowRegs = 160, kConvertRegs = 96, kOtherRegs = 96;
-static_assert(2 * kRowRegs + kConvertRegs + kOtherRegs <= 4 * 128, "more registers than the CTA has");
+// CTA was launched with, 128 for each of 512 threads; a sum above that would wait for registers for ever, and a group gives
+// some up or takes some as its role does. (4 bits, an 8192-token prompt: rows 160 and the others 96 443 us, 152, 112 and 96
+// 442, 144 and 112 437, 136, 128 and 112 445.)
+template <int kBits> constexpr int kRowRegs = kBits == 8 ? 160 : 144;
+template <int kBits> constexpr int kConvertRegs = kBits == 8 ? 96 : 112;
+template <int kBits> constexpr int kOtherRegs = kBits == 8 ? 96 : 112;
+template <int kBits> constexpr bool fits = 2 * kRowRegs<kBits> + kConvertRegs<kBits> + kOtherRegs<kBits> <= 4 * 128 && kRowRegs<kBits> >= 128 &&
+                                           kConvertRegs<kBits> <= 128 && kOtherRegs<kBits> <= 128;
+static_assert(fits<8> && fits<4>, "more registers than the CTA has, or a group that would take them where it gives some up");
 
 struct Bars {
     uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps], scale_full[kSlots];
@@ -159,17 +165,8 @@ __device__ __forceinline__ bool elected() {
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-__device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {  // x, y = a0 b + c, a1 b + c
-    asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5}; fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}"
-        : "=f"(x), "=f"(y) : "f"(a0), "f"(a1), "f"(b), "f"(c));
-}
-
 // Where an operand tile holds 16-byte chunk c of row r.
 __device__ __forceinline__ int panel_at(int r, int c) { return c / 8 * (kTile * 128) + r * 128 + 16 * (c % 8 ^ (r & 7)); }
-
-__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {  // x + a, y + b
-    asm("{.reg .b64 c, d; mov.b64 c, {%0, %1}; mov.b64 d, {%2, %3}; add.rn.f32x2 c, c, d; mov.b64 {%0, %1}, c;}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
-}
 
 // ---------------------------------------------------------------------------
 // The line of work
@@ -681,6 +678,20 @@ template <int kBits, int DP> __device__ __forceinline__ float ready_query(const 
     return c;
 }
 
+// A row's sums in tensor memory, times `by`.
+template <int DP> __device__ __forceinline__ void rescale(uint32_t at, float by) {
+#pragma unroll 1
+    for (int i = 0; i < DP; i += 32) {
+        float o[32];
+        tm_load32(at + i, o);
+        tm_wait_load();
+        tm_loaded(o);
+#pragma unroll
+        for (int k = 0; k < 32; k++) o[k] *= by;
+        tm_store32(at + i, reinterpret_cast<uint32_t *>(o));
+    }
+}
+
 template <int kBits, int DP>
 __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<kBits, DP> &sm) {
     Part<DP> *parts = reinterpret_cast<Part<DP> *>(a.parts);
@@ -700,14 +711,13 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<kBits, DP> &
         int lo = 0, hi = 0;
         if (mine) bounds(a, job.seq, row, lo, hi);
         float m = kNone, mw = kNone, l = 0.0f;
+        float raised = kRaise, most = kNone;    // (4 bits) what a weight's exponent is raised by; the product beyond which m follows
         if (job.n && half >= job.tiles) tile += job.n;  // no rows in this tile
         if (job.n && half < job.tiles) {
             const float c = ready_query(a, sm);
             {
                 for (int j = job.j0; j < job.j0 + job.n; j++, tile++, scored++) {
-                    float by[kBoxes], lvs[kBoxes];
-#pragma unroll
-                    for (int b = 0; b < kBoxes; b++) by[b] = 1.0f, lvs[b] = 0.0f;
+                    float by[kBoxes] = {}, lvs[kBoxes] = {};
                     if constexpr (kBits == 8) {
                         // A half that had no rows in the pieces before may be ahead of the copies by more than the ring of scales,
                         // where a wait for a phase tells nothing: its first scores come after their scales.
@@ -731,6 +741,66 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<kBits, DP> &
                     }
                     tm_after();
                     const int from = lo - j * kTile, to = hi - j * kTile;
+                    if constexpr (kBits == 4) {
+                        const float by = fmaxf(c, 1e-37f);  // (0 * -infinity would be NaN)
+                        float x[64], top = kNone;
+                        auto scores64 = [&](int part) {
+                            tm_load32(tmS + 64 * part, x);
+                            tm_load32(tmS + 64 * part + 32, x + 32);
+                            tm_wait_load();
+                            tm_loaded(x);
+                            tm_loaded(x + 32);
+                            if (edge) {
+#pragma unroll
+                                for (int q = 0; q < 64; q += 32) {
+                                    const uint32_t seen = below(to - 64 * part - q) & ~below(from - 64 * part - q);
+#pragma unroll
+                                    for (int i = 0; i < 32; i++) x[q + i] = seen >> i & 1 ? x[q + i] : kNone;
+                                }
+                            }
+                        };
+#pragma unroll
+                        for (int part = 1; part >= 0; part--) {
+                            scores64(part);
+                            float t0 = x[0], t1 = x[1];
+#pragma unroll
+                            for (int i = 2; i < 64; i += 4) t0 = fmaxf(fmaxf(x[i], x[i + 1]), t0), t1 = i + 3 < 64 ? fmaxf(fmaxf(x[i + 2], x[i + 3]), t1) : t1;
+                            top = fmaxf(fmaxf(t0, t1), top);
+                        }
+                        if (__any_sync(0xFFFFFFFFu, top > most)) {
+                            float down = 1.0f;
+                            if (top > most) {
+                                const float m1 = fmaxf(m, top * by);
+                                down = ratio2(m, m1);
+                                l *= down;
+                                m = m1;
+                                raised = kRaise - m, most = (m + kSlackW) / by;
+                            }
+                            // the last sums are done: the scores were issued after them
+                            if (j > job.j0) rescale<DP>(tmO, down);
+                        }
+                        float2 sum = both(0.0f);
+                        uint32_t *p = reinterpret_cast<uint32_t *>(x);
+#pragma unroll
+                        for (int part = 0; part < 2; part++) {  // the products start on the first 64 keys' weights
+                            // (the weights take the columns of scores 0 to 63; those from 64 on are there until the next products)
+                            if (part) scores64(1);
+#pragma unroll
+                            for (int i = 0; i < 64; i += 2) {
+                                float2 w = fma2(make_float2(x[i], x[i + 1]), both(by), both(raised));
+                                w.x = ex2(w.x), w.y = ex2(w.y);
+                                sum = add2(sum, w);
+                                p[i / 2] = half2_of(w.x, w.y);
+                            }
+                            tm_store32(tmS + 32 * part, p);
+                            tm_wait_store();
+                            tm_before();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(&sm.bars.p_full[half][part]);
+                        }
+                        l += (sum.x + sum.y) * (1.0f / (1 << int(kRaise)));
+                        continue;
+                    }
                     // 64 scores at a time, for their maxima and then for the weights: with all 128 in registers the loop spilled
                     // (drafts 27 us, with 64 25 us)
                     auto scores64 = [&](int part, float (&x)[64]) {
@@ -774,18 +844,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<kBits, DP> &
                             m = m1, mw = w1;
                         }
                         // the last sums are done: the scores were issued after them
-                        if (j > job.j0) {
-#pragma unroll 1
-                            for (int i = 0; i < DP; i += 32) {
-                                float o[32];
-                                tm_load32(tmO + i, o);
-                                tm_wait_load();
-                                tm_loaded(o);
-#pragma unroll
-                                for (int k = 0; k < 32; k++) o[k] *= down;
-                                tm_store32(tmO + i, reinterpret_cast<uint32_t *>(o));
-                            }
-                        }
+                        if (j > job.j0) rescale<DP>(tmO, down);
                     }
                     const float base = m == kNone ? 0.0f : m;
                     uint32_t *p = reinterpret_cast<uint32_t *>(x);
@@ -797,16 +856,15 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<kBits, DP> &
                         for (int b = 0; b < 4; b++) {
                             const float lf = fminf(fmaxf(lvs[4 * part + b] + (base - mw + kRaise), -60.0f), 126.0f);  // (mw = -infinity: every vs is 0)
                             const float bias = lf - base;
-                            float sum0 = 0.0f, sum1 = 0.0f;
+                            float2 sum = both(0.0f);
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                float y0, y1;
-                                fma2(y0, y1, x[16 * b + i], x[16 * b + i + 1], by[4 * part + b], bias);
-                                y0 = ex2(y0), y1 = ex2(y1);
-                                add2(sum0, sum1, y0, y1);
-                                p[8 * b + i / 2] = half2_of(y0, y1);
+                                float2 y = fma2(make_float2(x[16 * b + i], x[16 * b + i + 1]), both(by[4 * part + b]), both(bias));
+                                y.x = ex2(y.x), y.y = ex2(y.y);
+                                sum = add2(sum, y);
+                                p[8 * b + i / 2] = half2_of(y.x, y.y);
                             }
-                            l += (sum0 + sum1) * ex2(-lf);
+                            l += (sum.x + sum.y) * ex2(-lf);
                         }
                         tm_store32(tmS + 32 * part, p);
                         tm_wait_store();
@@ -824,6 +882,7 @@ __device__ __forceinline__ bool rows_role(const AttendArgs &a, Smem<kBits, DP> &
         if (!__all_sync(0xFFFFFFFFu, job_ready(sm, k + 1, a.limit))) return false;
         fetch_queries(a, sm, next);
 
+        if (kBits == 4) mw = m;
         // The rows' ends: finished, or a part.
         const bool whole = job.whole;
         Part<DP> *part = parts + job.part;
@@ -969,13 +1028,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     
     bool ok = true;
     if (warp < 8) {
-        more_registers<kRowRegs>();
+        more_registers<kRowRegs<kBits>>();
         ok = rows_role<kBits, DP>(a, sm);
     } else if (warp < 12) {
-        fewer_registers<kConvertRegs>();
+        fewer_registers<kConvertRegs<kBits>>();
         ok = convert_role<kBits, DP>(sm, a.c.dim / 16, a.limit);
     } else {
-        fewer_registers<kOtherRegs>();
+        fewer_registers<kOtherRegs<kBits>>();
         if (warp == 12) ok = product_role<kBits, DP>(sm, a.limit);
         if (warp == 13) ok = copy_role<kBits, DP>(a, maps, sm);
         if (warp == 14 && threadIdx.x % 32 == 0) ok = find_role<kBits, DP>(a, sm, Walk{w0, w1, sm.i0, W, G, sm.slot, sm.seq, sm.h, slots});

@@ -241,6 +241,8 @@ class KV4Cache(KVCache):
     @classmethod
     def empty(cls, n_blocks: int, kv_heads: int, head_dim: int, block_tokens: int = 64, device="cuda") -> "KV4Cache":
         """A cache of zeros."""
+        if head_dim % 16 or not 16 <= head_dim <= 128:
+            _fail("KV4Cache: head_dim is a multiple of 16 up to 128")
         shape = (n_blocks, kv_heads, block_tokens)
         k, v, ks, vs = (torch.zeros(*shape, m, dtype=torch.uint8, device=device)
                         for m in ((head_dim + 31) // 32 * 16,) * 2 + (head_dim // 16,) * 2)

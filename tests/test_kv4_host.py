@@ -146,6 +146,8 @@ def test_layouts_that_the_python_layer_refuses():
     _refused("scales are", lambda: zc.KV4Cache(k[..., :40], k[..., :40], s, s))
     _refused("contiguous", lambda: zc.KV4Cache(k.transpose(1, 2), k.transpose(1, 2), *[s.transpose(1, 2)] * 2))
     _refused("contiguous", lambda: zc.KV4Cache(k, k, *[torch.zeros(4, 2, 16, 6, **u8)[..., :5]] * 2))
+    for dim in (0, 24, 144):
+        _refused("head_dim", lambda: zc.KV4Cache.empty(4, 2, dim, 16, "cpu"))
     _refused("blocks overlap", lambda: zc.KV4Cache(*[k[:1].expand(4, 2, 16, 48)] * 2, s, s))
     _refused("scales of blocks overlap", lambda: zc.KV4Cache(k, k, *[s[:1].expand(4, 2, 16, 5)] * 2))
 
