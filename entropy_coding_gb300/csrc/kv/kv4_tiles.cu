@@ -8,7 +8,17 @@
 //   l_i += sum_j w_ij before rounding
 // with k and v = code * scale: their products are exact in half, so that the
 // conversion's warps apply the scales, weights know no unit but that of the
-// largest score, and out = O / l.
+// largest score, and out = O / l. Scores stay products until their exponentials:
+// a row's scale goes into those.
+//
+// Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads of
+// 128, causal) in 437 us, 1.26 PFLOP/s, 0.64 of the measured bfloat16 rate; 16
+// sequences of 2 to 5 tokens, 8 query heads to a head, over up to 4096 keys in 23.
+// As with the 8-bit cache the chain of a row tile is the bound: its scores, their
+// maximum, their exponentials, its products. Exponentials beside the search for
+// the maximum, done again where it has grown, leave the products waiting for
+// longer (518 us for a whole tile, 484 for its first half, 443 with the maximum
+// first); fewer registers for the rows and more for the conversion 443 to 437.
 #include "kv_tiles.cuh"
 
 namespace zc {

@@ -1,5 +1,5 @@
-// kv_api.cu — the C ABI of the 8-bit key/value cache operators: argument
-// checks and launches. As in zc_api.cu, no entry point allocates or
+// kv_api.cu — the C ABI of the key/value cache operators: argument checks and
+// launches. As in zc_api.cu, no entry point allocates or
 // synchronises; what only the device can see is reported through *d_status.
 #include <atomic>
 #include <cmath>
@@ -251,9 +251,10 @@ namespace {
 // Which kernels a batch needs. A sequence's rows of a head are its new tokens times the group. Up to 16 of them the
 // cache's bytes are what counts, and the kernel that streams them does the work; more rows fill the tensor cores'
 // 128-row tiles. (16 sequences of up to 8000 keys: 16 rows 66 us there and 78 us on tiles; 20 or 32 rows, two passes
-// over the bytes, 94 and 95 us there and 78 us on tiles.)
+// over the bytes, 94 and 95 us there and 78 us on tiles. Over the 4-bit cache, 2 heads: 8 rows 16 us and 25 on tiles, 16
+// rows 22 and 25, 20 and 32 rows 25 and 26 either way.)
 // A batch of prompts (more than a tile's rows) among single tokens runs both, each on its own sequences: a prompt of 400
-// tokens among 47 single ones takes 134 us so and 185 us on tiles alone. The host does not know how many sequences are of
+// tokens among 47 single ones takes 134 us so and 185 us on tiles alone (4 bits: 128 and 208). The host does not know how many sequences are of
 // which kind: where they have a tile's rows on average, or are no more than 8, the few single tokens are not worth a
 // second launch (24 sequences, two of them single tokens: 63 us with both, 54 us on tiles), nor are drafts of uneven
 // length (16 sequences of 2 to 5 tokens: 29 and 25 us). The average is moved by one long prompt: with 4 heads to a head

@@ -106,14 +106,19 @@ def _entries():
     return _entry
 
 
+_addresses: dict = {}
+
+
 def _quick(first: int):
     """Addresses of a kind of cache's entry points and of zc_kv_rotate, for the calls that the module makes in one step."""
     global _torch
     if _torch is None:
         from . import _build
         _torch = _build.load_module()
-    e = _entries()
-    return tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (*e[first:first + 3], e[10]))
+    if first not in _addresses:
+        e = _entries()
+        _addresses[first] = tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (*e[first:first + 3], e[10]))
+    return _addresses[first]
 
 
 def _outer(t: torch.Tensor, least: int, what: str) -> int:
@@ -538,13 +543,16 @@ class KVRotation:
         self._streams.add(handle)
 
 
-_TAU = decimal.Decimal("6.28318530717958647692528676655900576839433879875021")
+# 2^256 / (2 pi), which holds any frequency's fraction of a turn to more than 64 bits
+with decimal.localcontext(decimal.Context(prec=100)):
+    _TURN = int(decimal.Decimal(2) ** 256 / decimal.Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563281"))
 
 
 def fraction_of_turn(frequency: float) -> int:
-    """A frequency in radians as a fraction of a turn in units of 2^-64, modulo a turn."""
-    with decimal.localcontext(decimal.Context(prec=60)):
-        return int((decimal.Decimal(frequency) / _TAU * (1 << 64)).to_integral_value()) % (1 << 64)
+    """A frequency in radians as a fraction of a turn in units of 2^-64, modulo a turn, rounded to nearest."""
+    above, below = frequency.as_integer_ratio()
+    below <<= 192
+    return (2 * above * _TURN + below) // (2 * below) % (1 << 64)
 
 
 def _rotate(cache, batch, rotation, code, rows, heads, q_weight, k_weight, eps, stream):
