@@ -47,7 +47,7 @@ def pack(code: np.ndarray) -> np.ndarray:
 
 def numbers(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
     """Numbers of rows of packed codes [..., row] and scale bytes [..., dim / 16]."""
-    c = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], -1)[..., : scales.shape[-1] * 16]
+    c = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], 2 * codes.shape[-1])[..., : scales.shape[-1] * 16]
     v = np.where(c >= 8, -CODES[c & 7], CODES[c & 7])
     return v * np.repeat(scale_of(scales), 16, -1)
 
@@ -73,7 +73,7 @@ def rows_of(codes, scales, table_row, total):
     """[heads, total, dim] numbers of a sequence's first `total` positions."""
     at = [int(i) for i in table_row[: -(-total // codes.shape[2])]]
     x = numbers(codes[at], scales[at])
-    return x.transpose(1, 0, 2, 3).reshape(codes.shape[1], -1, x.shape[-1])[:, :total]
+    return x.transpose(1, 0, 2, 3).reshape(codes.shape[1], len(at) * codes.shape[2], x.shape[-1])[:, :total]
 
 
 def attend(q, kc, ks, vc, vs, table, cu, lens, scale, causal, window):

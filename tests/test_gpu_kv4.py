@@ -324,10 +324,19 @@ def test_one_key_takes_nearly_all_of_the_weight_and_has_no_value(new):
     _attend_case("fp16", 32, 1, 4, dim, [keys], [new], False, 0, edit=edit, scale=z)
 
 
-def test_scale_is_the_callers():
-    _attend_case("bf16", 64, 1, 4, 128, [300], [1], True, 0, scale=0.01)
-    _attend_case("fp16", 64, 1, 4, 128, [300], [200], True, 0, scale=-0.2)
-    _attend_case("fp16", 64, 1, 4, 128, [300], [200], True, 0, scale=0.0)
+@pytest.mark.parametrize("scale", [0.01, -0.2, 0.0, -0.0])
+@pytest.mark.parametrize("dtype,new", [("bf16", 1), ("fp16", 3), ("bf16", 30), ("fp16", 200)])
+def test_scale_is_the_callers(dtype, new, scale):
+    _attend_case(dtype, 64, 1, 4, 128, [300], [new], True, 0, scale=scale)
+
+
+@pytest.mark.parametrize("group,news", [(4, [20, 31, 5]), (8, [3, 16, 9]), (1, [100, 17, 128])])
+@pytest.mark.parametrize("dim,window", [(64, 0), (128, 0), (80, 700), (128, 130)])
+def test_rows_of_one_tile_over_one_to_many_key_tiles(dim, window, group, news):
+    """Items of one row tile over one, two, three and many key tiles, and pieces that begin and end inside items."""
+    for lens in ([128, 129, 256], [257, 300, 384], [385, 513, 1100], [3000, 2600, 150]):
+        _attend_case("fp16", 32, 3, group, dim, [max(a, b) for a, b in zip(lens, news)], news, True, window)
+        _attend_case("bf16", 16, 1, group, dim, [max(a, b) for a, b in zip(lens, news)], news, False, window)
 
 
 def test_blocks_past_four_gigabytes_and_slices_of_a_pool():
