@@ -14,8 +14,10 @@
 // Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads of
 // 128, causal) in 437 us, 1.26 PFLOP/s, 0.64 of the measured bfloat16 rate; 16
 // sequences of 2 to 5 tokens, 8 query heads to a head, over up to 4096 keys in 23.
-// As with the 8-bit cache the chain of a row tile is the bound: its scores, their
-// maximum, their exponentials, its products. Exponentials beside the search for
+// Of 3480 clocks a key tile the products' warp waits 850; their operations would
+// take 2048, but scores' products read both operands from a shared memory that the
+// conversion and the copies use too. A row tile's chain is 350 clocks for the
+// maximum, 500 and 520 for the halves' weights, and its products. Exponentials beside the search for
 // the maximum, done again where it has grown, leave the products waiting for
 // longer (518 us for a whole tile, 484 for its first half, 443 with the maximum
 // first); fewer registers for the rows and more for the conversion 443 to 437.

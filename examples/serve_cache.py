@@ -1,11 +1,13 @@
-"""One attention layer in service on an 8-bit key/value cache, and a sequence that leaves the device and comes back.
+"""One attention layer in service on an 8-bit (or 4-bit) key/value cache, and a sequence that leaves the device and comes back.
 
 Prompts of uneven length are admitted (their keys and values written, their queries attended to the cache), then every
 sequence is decoded a token at a time. Half way one sequence is parked: its blocks, which are bytes, are compressed
 without loss into page-locked host memory (format v3) and its blocks are taken by others; later it is restored into
 other blocks and goes on. The outputs equal those of a run in which it never left.
 
-    python examples/serve_cache.py [--steps 8] [--heads 32] [--kv-heads 8] [--dim 128]
+With --rotate queries and keys go through each head's norm and the rotation by their positions first.
+
+    python examples/serve_cache.py [--steps 8] [--heads 32] [--kv-heads 8] [--dim 128] [--bits 8] [--rotate]
 """
 from __future__ import annotations
 
@@ -23,8 +25,10 @@ import entropy_coding_gb300 as zc  # noqa: E402
 class Server:
     """Sequences over one cache; blocks are handed out from a free list."""
 
-    def __init__(self, n_blocks, kv_heads, dim, block, device="cuda"):
-        self.cache = zc.KVCache.empty(n_blocks, kv_heads, dim, block, device)
+    def __init__(self, n_blocks, kv_heads, dim, block, device="cuda", bits=8, rotate=False):
+        self.cache = (zc.KVCache if bits == 8 else zc.KV4Cache).empty(n_blocks, kv_heads, dim, block, device)
+        self.rotation = zc.KVRotation([10000.0 ** (-2 * i / dim) for i in range(dim // 2)], device=device) if rotate else None
+        self.norm = torch.ones(dim, device=device)
         self.free = list(range(n_blocks))[::-1]
         self.blocks: dict[int, list[int]] = {}
         self.length: dict[int, int] = {}
@@ -52,9 +56,14 @@ class Server:
         batch = self.batch(news)
         x = torch.cat([qkv[s] for s in news])
         h = self.cache.kv_heads
-        zc.kv_write(self.cache, batch, x[:, heads: heads + h], x[:, heads + h:])
-        out, _ = zc.kv_attend(self.cache, batch, x[:, :heads])
+        q, k = self.before(batch, x[:, :heads], x[:, heads: heads + h])
+        zc.kv_write(self.cache, batch, k, x[:, heads + h:])
+        out, _ = zc.kv_attend(self.cache, batch, q)
         return dict(zip(news, out.split(list(news.values()))))
+
+    def before(self, batch, q, k):
+        """Queries and keys as they are attended with and written."""
+        return zc.kv_rotate(self.cache, batch, self.rotation, q, k, self.norm, self.norm) if self.rotation else (q, k)
 
     def _parts(self, s):
         """The bytes that hold a sequence: codes and scales of its blocks."""
@@ -85,6 +94,8 @@ def main(argv=None) -> dict:
     ap.add_argument("--heads", type=int, default=32)
     ap.add_argument("--kv-heads", type=int, default=8)
     ap.add_argument("--dim", type=int, default=128)
+    ap.add_argument("--bits", type=int, default=8, choices=[8, 4])
+    ap.add_argument("--rotate", action="store_true")
     a = ap.parse_args(argv)
     prompts = {0: 700, 1: 130, 2: 1500, 3: 64}
     g = torch.Generator(device="cuda").manual_seed(0)
@@ -96,7 +107,7 @@ def main(argv=None) -> dict:
     xs = [{s: tokens(1) for s in prompts} for _ in range(a.steps)]
 
     def serve(leaves: bool):
-        srv = Server(64, a.kv_heads, a.dim, 64)
+        srv = Server(64, a.kv_heads, a.dim, 64, bits=a.bits, rotate=a.rotate)
         outs = [srv.step(prompts, x0, a.heads)]
         ratio = None
         for i, x in enumerate(xs):
@@ -121,16 +132,18 @@ def main(argv=None) -> dict:
 
     same = all(alike(i, p[s], m[s]) for i, (p, m) in enumerate(zip(plain, moved)) for s in prompts)
     # against attention in float32 over the numbers that the cache holds
-    q = xs[-1][2][:, :a.heads].float()
-    one = zc.KVBatch(torch.tensor([srv.blocks[2]], dtype=torch.int32, device="cuda"),
-                     torch.tensor([0, srv.length[2]], dtype=torch.int32, device="cuda"),
-                     torch.tensor([srv.length[2]], dtype=torch.int32, device="cuda"), srv.length[2], srv.length[2])
+    def last(n):  # the sequence's last n tokens
+        i32 = dict(dtype=torch.int32, device="cuda")
+        return zc.KVBatch(torch.tensor([srv.blocks[2]], **i32), torch.tensor([0, n], **i32), torch.tensor([srv.length[2]], **i32), n, n)
+
+    q, _ = srv.before(last(1), xs[-1][2][:, :a.heads], xs[-1][2][:, a.heads: a.heads + a.kv_heads])
+    q, one = q.float(), last(srv.length[2])
     k, v = (t.repeat_interleave(a.heads // a.kv_heads, 1).float() for t in zc.kv_read(srv.cache, one))
     p = torch.softmax(torch.einsum("qhd,khd->hqk", q, k) * a.dim ** -0.5, -1)
     want = torch.einsum("hqk,khd->qhd", p, v)
     err = float((moved[-1][2].float() - want).abs().max() / want.abs().max())
     print(f"{sum(prompts.values())} prompt tokens, {a.steps} steps of {len(prompts)} sequences; parked sequence "
-          f"{100 * ratio:.1f} % of its 8-bit blocks; same outputs: {same}; error against float32 {err:.2g}")
+          f"{100 * ratio:.1f} % of its {a.bits}-bit blocks; same outputs: {same}; error against float32 {err:.2g}")
     return dict(same=same, ratio=ratio, error=err)
 
 

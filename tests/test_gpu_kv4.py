@@ -615,3 +615,16 @@ def test_calls_one_after_another_see_what_the_last_has_written():
         torch.cuda.synchronize()
     cache.check()
     assert torch.isfinite(a).all() and all(torch.equal(a, r) for r in results)
+
+
+@pytest.mark.parametrize("args", [["--bits", "4"], ["--bits", "4", "--rotate"], ["--rotate", "--heads", "10", "--kv-heads", "2", "--dim", "80", "--steps", "3"]])
+def test_the_example_of_a_layer_in_service(args):
+    """In 4 bits, and with norms and rotation: the outputs of a run in which the parked sequence never left."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_cache.py")
+    spec = importlib.util.spec_from_file_location("serve_cache", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    r = m.main(args)
+    assert r["same"] and r["ratio"] < 1.05 and r["error"] < 2 ** -6
