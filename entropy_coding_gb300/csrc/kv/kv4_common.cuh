@@ -103,7 +103,15 @@ __device__ __forceinline__ void locate(const Batch &b, uint32_t block_tokens, ui
                                        int32_t *d_status) {
     for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) s_pos[i] = -1;
     __syncthreads();
-    for (uint32_t s0 = 0; s0 < b.n_seqs; s0 += blockDim.x) {
+    // Of many sequences the first that matters is found by halving (9728 single tokens rotated: 43 us, with all of them looked at 60).
+    uint32_t s0 = 0;
+    if (b.n_seqs > 8 * blockDim.x)
+        for (uint32_t above = b.n_seqs; above - s0 > 1;) {
+            const uint32_t mid = (s0 + above) / 2;
+            if (tokens_before(b, mid) <= t0) s0 = mid;
+            else above = mid;
+        }
+    for (; s0 < b.n_seqs && (s0 == 0 || tokens_before(b, s0) < t0 + n); s0 += blockDim.x) {
         const uint32_t s = s0 + threadIdx.x;
         uint32_t lo = 0, hi = 0;
         int32_t from = 0;  // position of token lo

@@ -628,3 +628,33 @@ def test_the_example_of_a_layer_in_service(args):
     spec.loader.exec_module(m)
     r = m.main(args)
     assert r["same"] and r["ratio"] < 1.05 and r["error"] < 2 ** -6
+
+
+@pytest.mark.parametrize("seqs", [1500, 5000])
+def test_tokens_of_thousands_of_sequences(seqs):
+    """More sequences than a CTA looks at one after another, some without new tokens: writing, reading and rotation."""
+    rng = np.random.default_rng(10)
+    news = rng.integers(0, 3, seqs)
+    lens = news + rng.integers(0, 20, seqs)
+    table = rng.permutation(seqs * 2).reshape(seqs, 2).astype(np.int32)
+    kc, ks = _pool(seqs * 2, 1, 16, 32, rng)
+    vc, vs = _pool(seqs * 2, 1, 16, 32, rng)
+    batch, cu = _batch(table, news, lens)
+    cache = _cache(kc, ks, vc, vs)
+    T = int(cu[-1])
+    x = torch.from_numpy(rng.standard_normal((T, 1, 32))).to(DEV).bfloat16()
+    zc.kv_write(cache, batch, x, -x)
+    cache.check()
+    for c, s, y, got_c, got_s in ((kc, ks, x, cache.k, cache.k_scale), (vc, vs, -x, cache.v, cache.v_scale)):
+        write(c, s, y.double().cpu().numpy(), table, cu, lens)
+        assert np.array_equal(got_s.cpu().numpy(), s) and np.array_equal(got_c.cpu().numpy(), c)
+    k, _ = zc.kv_read(cache, batch, dtype=torch.float32)
+    want = np.concatenate([rows_of(kc, ks, table[i], n)[:, n - m:].transpose(1, 0, 2) for i, (n, m) in enumerate(zip(lens, news))])
+    assert np.array_equal(k.double().cpu().numpy(), want)
+    q, _ = zc.kv_rotate(cache, batch, zc.KVRotation([0.3 ** i for i in range(16)]), x.float(), x.float())
+    cache.check()
+    p = torch.tensor([n - m + i for n, m in zip(lens, news) for i in range(m)], device=DEV, dtype=torch.float64)
+    t = p[:, None, None] * torch.tensor([0.3 ** i for i in range(16)], device=DEV, dtype=torch.float64)
+    a, b = x.double().split(16, -1)
+    want = torch.cat([a * t.cos() - b * t.sin(), b * t.cos() + a * t.sin()], -1)
+    assert torch.allclose(q.double(), want, rtol=0, atol=2 ** -18)
