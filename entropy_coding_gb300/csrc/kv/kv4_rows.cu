@@ -173,6 +173,7 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
         if ((k & (kLook - 1)) == 0) {
             __syncwarp();
             look_up(a, wp, job, k + kLook);
+            __syncwarp();
         }
         if (!__all_sync(0xFFFFFFFFu, bar_wait(&wp.full[st], parity, a.limit))) {
             drain<Codes4>(a, wp, turn + k, job.steps - k);

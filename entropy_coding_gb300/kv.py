@@ -141,7 +141,7 @@ class KVCache:
     have the same strides. ``KVCache.empty`` allocates one."""
 
     _calls = 0     # of _entries()
-    _quick = None  # where every call is on the cache's device: write, read, attend and rotate's addresses
+    _quick = None  # write, read, attend and rotate's addresses, for the calls that the module makes
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride():
@@ -176,7 +176,7 @@ class KVCache:
                          block_stride, scale_stride, n, h, b, d)
         self._ref = ctypes.addressof(self._c)
         self._status = self.status.data_ptr()
-        self._quick = None if self._many else _quick(self._calls)
+        self._quick = _quick(self._calls)
 
     def _meet(self, handle: int) -> None:
         """A stream's first call: it comes after the status was made, and the status outlives its calls. (A graph is
@@ -364,6 +364,14 @@ def _elsewhere(cache: KVCache, batch: KVBatch, what: str) -> bool:
     return _current_device() != cache._index
 
 
+def _at_once(cache: KVCache, batch: KVBatch, stream):
+    """The addresses for a call that the module makes in one step, or None: on the current stream, with the cache's device
+    the current one and the batch on it."""
+    if stream is None and (not cache._many or batch._index == cache._index == _current_device()):
+        return cache._quick
+    return None
+
+
 def _check(st: int, what: str) -> None:
     if st:
         from . import ZcError
@@ -387,8 +395,8 @@ def kv_write(cache: KVCache, batch: KVBatch, k: torch.Tensor, v: torch.Tensor, s
     """Quantise the batch's tokens into the cache (zc_kv_write, zc_kv4_write). ``k``, ``v``:
     [total_tokens, kv_heads, head_dim] in bfloat16, float16 or float32, any
     strides that are multiples of 16 bytes (views of a fused projection)."""
-    quick = cache._quick
-    if quick is not None and stream is None:
+    quick = _at_once(cache, batch, stream)
+    if quick is not None:
         st = _torch.move(quick[0], cache._ref, batch._ref, cache._status, _handle(None, cache), cache._index, batch.total_tokens,
                          cache.kv_heads, cache.head_dim, k, v)
         if st is not None:
@@ -409,8 +417,8 @@ def kv_read(cache: KVCache, batch: KVBatch, dtype: torch.dtype = torch.bfloat16,
     code = _CODE.get(dtype)
     if code is None:
         _fail("zc_kv_read: bfloat16, float16 or float32")
-    quick = cache._quick
-    if quick is not None and stream is None:
+    quick = _at_once(cache, batch, stream)
+    if quick is not None:
         r = _torch.read(quick[1], cache._ref, batch._ref, cache._status, _handle(None, cache), cache._index, batch.total_tokens,
                         cache.kv_heads, cache.head_dim, code)
         if type(r) is not tuple:
@@ -477,8 +485,8 @@ def kv_attend(cache: KVCache, batch: KVBatch, q: torch.Tensor, scale: float | No
     with j <= p (``causal``) and j > p - window (``window`` > 0). ``scale``
     defaults to head_dim ** -0.5. The tokens' own keys and values are in the
     cache already (kv_write first)."""
-    quick = cache._quick
-    if quick is not None and stream is None and q.dim() == 3 and 0 <= window <= 0x7FFFFFFF:
+    quick = _at_once(cache, batch, stream)
+    if quick is not None and q.dim() == 3 and 0 <= window <= 0x7FFFFFFF:
         handle, dim = _handle(None, cache), cache.head_dim
         ws = batch._ws.get((cache.kv_heads, dim, q.shape[1], handle, cache._calls))
         if ws is not None and ws[3] == _failures:
@@ -513,7 +521,8 @@ class KVRotation:
     they are kept as 64-bit fractions of a turn, so that an angle is as good at
     position 10^9 as at 1. Pair i is the columns i and i + rot_dim / 2, or 2 i and
     2 i + 1 (``interleaved``); columns from rot_dim = 2 * len(frequencies) on
-    are not turned."""
+    are not turned. A rotation is kept as long as the graphs that it is used
+    by."""
 
     def __init__(self, frequencies, interleaved: bool = False, device="cuda"):
         numbers = frequencies.double().flatten().tolist() if isinstance(frequencies, torch.Tensor) else [float(f) for f in frequencies]
@@ -614,8 +623,8 @@ def kv_rotate(cache: KVCache, batch: KVBatch, rotation: KVRotation, q: torch.Ten
     [total_tokens, kv_heads, head_dim] in bfloat16, float16 or float32, any
     strides that are multiples of 16 bytes (views of a fused projection).
     Sums are float32, and a number is rounded once."""
-    quick = cache._quick
-    if quick is not None and stream is None and rotation._index == cache._index:
+    quick = _at_once(cache, batch, stream)
+    if quick is not None and rotation._index == cache._index:
         handle = _handle(None, cache)
         if handle not in rotation._streams:
             rotation._meet(handle)

@@ -554,7 +554,8 @@ typedef struct {
 
 /*   dtype             ZC_BF16, ZC_FP16 or ZC_FP32: of q, k and the outputs
  *   head_dim          a multiple of 16 up to 128
- *   heads, kv_heads   of q and of k, 1 to 65535
+ *   heads, kv_heads   of q and of k, 1 to 65535; total_tokens times their sum
+ *                     is below 2^31
  *   q_out, k_out      may be q and k themselves (the same address and strides),
  *                     or tensors that do not overlap with them
  * Of the batch only the counts and lengths are looked at; rows of tokens that

@@ -7,7 +7,7 @@ import ctypes
 import pytest
 import torch
 
-from entropy_coding_gb300 import build
+from entropy_coding_gb300 import build, kv
 
 
 @pytest.fixture(scope="module")
@@ -48,3 +48,19 @@ def test_wrong_numbers_of_arguments_and_no_numbers_are_errors(module):
 
 def test_a_module_is_kept_for_each_torch(module):
     assert torch.__version__.replace("+", "_") in build._module_path() and build.build_module() == build._module_path()
+
+
+def test_calls_are_made_at_once_only_on_the_caches_device(monkeypatch):
+    """Fakes of two devices and of the module: a call on another stream, with another device current or with a batch of
+    another device goes through the layer that sees to these."""
+    cache, batch = object.__new__(kv.KVCache), object.__new__(kv.KVBatch)
+    now = [0]
+    monkeypatch.setattr(kv, "_current_device", lambda: now[0], raising=False)
+    for many, mine, batchs, current, stream, at_once in ((False, 0, 0, 0, None, True), (False, 0, 0, 0, 7, False), (True, 1, 1, 1, None, True),
+                                                         (True, 1, 1, 0, None, False), (True, 1, 0, 1, None, False), (True, 0, 0, 0, 7, False)):
+        cache.__dict__.update(_many=many, _index=mine, _quick=(1, 2, 3, 4))
+        batch.__dict__.update(_index=batchs)
+        now[0] = current
+        assert (kv._at_once(cache, batch, stream) is not None) == at_once
+    del cache.__dict__["_quick"]
+    assert kv._at_once(cache, batch, None) is None
