@@ -129,10 +129,10 @@ int launch_tiles4(const AttendArgs &a, cudaStream_t s);
 
 #ifdef __CUDACC__
 
-// A kernel that may be launched while the one before it on the stream still runs: it does nothing to global memory, not
-// even read it, before after_the_last() returns, which is when that one is done and its writes are there. Its own
-// successor may come as soon as all of its CTAs have begun. (A step's rotation, one after another: 6.2 us, early 3.8; its
-// writing and reading back 10.3 and 6.2.)
+// A kernel that may be launched while the one before it on the stream ends: it does nothing to global memory, not even read
+// it, before after_the_last() returns, which is when that one is done and its writes are there. (A step's rotation, one after
+// another: 6.2 us, early 3.6; its writing and reading back 10.3 and 6.0. A kernel that lets its successor come as soon as its
+// own CTAs have begun has that one's beside them, waiting: 3.8 and 6.5, and 17138 tokens written and read back 34.2 for 30.5.)
 template <class... P, class... A> int launch_early(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t s, const A &...a) {
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -147,7 +147,6 @@ template <class... P, class... A> int launch_early(void (*kernel)(P...), dim3 gr
     return cudaLaunchKernelEx(&c, kernel, a...) == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }
 __device__ __forceinline__ void after_the_last() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
