@@ -22,9 +22,9 @@
 // piece's end, in the steps of their rings that they have read last.
 //
 // Measured on a GB300: the next tokens of 64 sequences of up to 8192 keys (8
-// heads of 128, 4 query heads each), 314 MB of cache, in 71 us: 4.4 TB/s, 0.65
+// heads of 128, 4 query heads each), 314 MB of cache, in 70 us: 4.5 TB/s, 0.66
 // of the copy rate, where the 8-bit cache's 558 MB take 98; one token over 131072
-// keys in 39. Bytes are not the bound here: with the steps' arithmetic left out
+// keys in 38. Bytes are not the bound here: with the steps' arithmetic left out
 // the same copies take 58 us, of which 12 are the start, the pieces' ends and the
 // joining. A step of 32 keys is 660 instructions of a warp, 128 conversions and
 // 128 products with scales among them, 190 of them for copies, waits and pieces'
@@ -34,7 +34,7 @@
 // flight are faster. What was: an item's beginning and end counted as work (83.5
 // to 73.2 us), boxes of 32 rows and scale lines by the tensor memory accelerator
 // (90 to 84), beginning before the kernel in front of this one has ended (73.2 to
-// 71.3).
+// 70.4).
 #include <cstddef>
 
 #include "kv4_common.cuh"

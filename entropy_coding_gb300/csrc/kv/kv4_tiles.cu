@@ -12,8 +12,8 @@
 // a row's scale goes into those.
 //
 // Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads of
-// 128, causal) in 437 us, 1.26 PFLOP/s, 0.64 of the measured bfloat16 rate; 16
-// sequences of 2 to 5 tokens, 8 query heads to a head, over up to 4096 keys in 23.
+// 128, causal) in 435 us, 1.26 PFLOP/s, 0.64 of the measured bfloat16 rate; 16
+// sequences of 2 to 5 tokens, 8 query heads to a head, over up to 4096 keys in 22.
 // Of 3480 clocks a key tile the products' warp waits 850; their operations would
 // take 2048, but scores' products read both operands from a shared memory that the
 // conversion and the copies use too. A row tile's chain is 350 clocks for the

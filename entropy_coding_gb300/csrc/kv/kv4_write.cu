@@ -17,7 +17,7 @@
 // for where the tokens belong: that is looked up meanwhile.
 //
 // Measured on a GB300: 17138 tokens of 8 heads of 128, bfloat16, 70 MB read and 20
-// written, in about 17 us (5.3 TB/s); 32 tokens in 3.1. The arithmetic units are
+// written, in about 14.5 us (6.2 TB/s); 32 tokens in 3. The arithmetic units are
 // half busy: what counted was two numbers to an instruction, the type's own
 // comparisons for the largest magnitude and a head's rows on their way while the
 // one before them is worked on (27 us without); CTAs of 128 threads are faster
