@@ -53,7 +53,7 @@ template <int DP> struct Codes4 {
     // long), 2 those of two tiles (16 sequences of 16 rows: 23.7 us, with 3 and spilled registers 26.7).
     template <int NT> static constexpr int resident() { return NT == 1 ? 3 : 2; }
     static constexpr bool kEarly = true;
-    static constexpr bool kMergeInRing = true;
+    static constexpr bool kMergeInRing = true, kUnits = false;
     // (64 sequences of up to 8192 keys: 0 units 83.5 us, with the CTAs that have many short items last, 2 units 74.4, 3 units
     // 73.8, 4 units 73.2, 6 units 73.9)
     static constexpr uint32_t kFixed = 4;
@@ -135,7 +135,6 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
     const Seq &seq = job.seq;
     const uint32_t row0 = job.tile * kRows, n_rows = seq.n * a.group, groups = a.c.dim / 16;
     auto &o = acc.o;
-    auto &m = acc.m;
     auto &l = acc.l;
 
     uint32_t qf[NT][kSteps][2];
@@ -153,12 +152,15 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
         for (int e = 0; e < 2; e++) row_scale[n][e] = fmaxf(fabsf(row_scale[n][e]), 1e-37f);
     }
     acc.clear();
-    // What a weight's exponent is raised by, and the product of a row and a key from which on its maximum is followed.
-    float raised[NT][2], most[NT][2];
+    // The largest product of a row and a key, as far as it was followed (or 0), and that from which on it is followed again.
+    // A weight's exponent is a difference of products by the row's scale: of products close to one another that is exact,
+    // however large they are. (One multiply-add of the product, its scale and the score's maximum is off by hundreds next to
+    // a score of 10^9, and no faster.)
+    float base[NT][2], most[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int e = 0; e < 2; e++) raised[n][e] = kRaise, most[n][e] = kNone;
+        for (int e = 0; e < 2; e++) base[n][e] = 0.0f, most[n][e] = kNone;
 
     // This thread's keys of a half: key_of(g) and 8 more for scores, four for values; its groups of columns.
     const int key_g = key_of(g), key_v0 = key_of(2 * t), key_v1 = key_of(2 * t + 1);
@@ -238,7 +240,7 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
                     }
                 }
         }
-        // m follows the maximum only once that is 2^kSlackW above it: after the first step a rescaling is rare.
+        // The base follows the maximum only once that is 2^kSlackW above it: after the first step a rescaling is rare.
         bool grows = false;
         float top[NT][2];
 #pragma unroll
@@ -256,19 +258,18 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
                 for (int e = 0; e < 2; e++) {
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(0xFFFFFFFFu, top[n][e], d));
-                    const float m1 = fmaxf(m[n][e], top[n][e] * row_scale[n][e]);
-                    down[e] = ratio2(m[n][e], m1);
+                    const float was = most[n][e] == kNone ? kNone : base[n][e], now = fmaxf(was, top[n][e]);
+                    down[e] = was == kNone ? 0.0f : ex2((was - now) * row_scale[n][e]);
                     l[n][e] *= down[e];
-                    m[n][e] = m1;
-                    raised[n][e] = kRaise - (m1 == kNone ? 0.0f : m1);
-                    most[n][e] = (m1 + kSlackW) / row_scale[n][e];
+                    base[n][e] = now == kNone ? 0.0f : now;
+                    most[n][e] = followed(now, row_scale[n][e]);
                 }
 #pragma unroll
                 for (int c = 0; c < kSteps; c++)
                     o[n][c][0] *= down[0], o[n][c][1] *= down[1], o[n][c][2] *= down[0], o[n][c][3] *= down[1];
             }
         }
-        // Weights 2^(s - m + kRaise).
+        // Weights 2^((product - base) scale + kRaise).
         uint32_t pf[2][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -276,8 +277,8 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
             for (int half = 0; half < 2; half++)
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
-                    float2 p = fma2(make_float2(sc[half][n][2 * j], sc[half][n][2 * j + 1]), make_float2(row_scale[n][0], row_scale[n][1]),
-                                    make_float2(raised[n][0], raised[n][1]));
+                    const float2 past = add2(make_float2(sc[half][n][2 * j], sc[half][n][2 * j + 1]), make_float2(-base[n][0], -base[n][1]));
+                    float2 p = fma2(past, make_float2(row_scale[n][0], row_scale[n][1]), both(kRaise));
                     p.x = ex2(p.x), p.y = ex2(p.y);
                     const float2 sum = add2(make_float2(l[n][0], l[n][1]), p);
                     l[n][0] = sum.x, l[n][1] = sum.y;
@@ -352,7 +353,8 @@ __device__ __forceinline__ bool Codes4<DP>::attend_slices(const AttendArgs &a, c
 #pragma unroll
     for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int e = 0; e < 2; e++) acc.mw[n][e] = m[n][e];
+        for (int e = 0; e < 2; e++)
+            if (most[n][e] != kNone) acc.m[n][e] = base[n][e] * row_scale[n][e];
     return true;
 }
 

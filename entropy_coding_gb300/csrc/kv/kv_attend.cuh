@@ -30,6 +30,13 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
 }
 // 2^(a - b) with 2^(-inf - anything) = 0
 __device__ __forceinline__ float ratio2(float a, float b) { return a == kNone ? 0.0f : ex2(a - b); }
+// A row's running maximum of its scores is m (log2). The unit of its contributions, weights times value scales, stands
+// at m + d: d is kept apart, since next to a large m there is no room for it (m = 10^9 has neighbours 64 away). This is
+// m + d above another maximum, whose unit may be anywhere.
+__device__ __forceinline__ float above(float d, float m, float other) { return m == kNone ? kNone : d + (m - other); }
+// (4 bits) The product from which on a row's largest, `top`, is followed: kSlackW above it as a score. Rounded down, so that
+// no weight is beyond what half holds where that is less than a product's last place.
+__device__ __forceinline__ float followed(float top, float row_scale) { return __fadd_rd(top, __fdiv_rd(kSlackW, row_scale)); }
 // Whether one of the four codes is NaN (0x7F or 0xFF).
 __device__ __forceinline__ bool any_nan(uint32_t v) { return __vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0; }
 
@@ -84,12 +91,12 @@ __device__ __forceinline__ uint32_t pack_out(const AttendArgs &a, float x, float
     return a.dtype == ZC_BF16 ? pack2<ZC_BF16>(x, y) : pack2<ZC_FP16>(x, y);
 }
 
-// A finished row is its sum (in units of 2^(W - kRaise)) by this factor: out = x / L in the units of M. A row that sees no
-// key is 0, whatever x holds. (L is NaN where a score was. The power in two halves: neither leaves float's range where
+// A finished row is its sum (in units of 2^(d - kRaise)) by this factor: out = x / L, both in units of 2^M. A row that sees
+// no key is 0, whatever x holds. (L is NaN where a score was. The power in two halves: neither leaves float's range where
 // value scales are near its ends.)
-__device__ __forceinline__ float row_factor(float M, float W, float L) {
-    if (W == kNone) return 0.0f / L;
-    const float half = 0.5f * (W - M - kRaise), x = ex2(half);
+__device__ __forceinline__ float row_factor(float d, float L) {
+    if (d == kNone) return 0.0f / L;
+    const float half = 0.5f * (d - kRaise), x = ex2(half);
     return x * (x / L);
 }
 __device__ __forceinline__ float row_lse(float M, float L) { return L == 0.0f ? kNone : (M + log2f(L)) * 0.6931471805599453f; }
@@ -97,8 +104,8 @@ __device__ __forceinline__ float row_lse(float M, float L) { return L == 0.0f ? 
 // n columns (a multiple of 4) of a finished row from `col` on.
 template <int n>
 __device__ __forceinline__ void emit(const AttendArgs &a, const Seq &seq, uint32_t h, uint32_t row, int col,
-                                     const float (&x)[n], float M, float W, float L) {
-    const float by = row_factor(M, W, L);
+                                     const float (&x)[n], float M, float d, float L) {
+    const float by = row_factor(d, L);
     uint16_t *o = static_cast<uint16_t *>(a.out.p) + row_at(a, a.out, seq, h, row) + col;
 #pragma unroll
     for (int k = 0; k < n; k += 4)

@@ -50,7 +50,7 @@ template <int DP> struct Codes8 {
     static constexpr int kResident = 3, kStages = 3 * (128 / DP);
     template <int NT> static constexpr int resident() { return kResident; }
     static constexpr bool kEarly = false;
-    static constexpr bool kMergeInRing = false;
+    static constexpr bool kMergeInRing = false, kUnits = true;
     static constexpr uint32_t kFixed = 0;
     using Maps = CodeMaps;
     struct Stage {
@@ -117,7 +117,7 @@ __device__ __forceinline__ bool Codes8<DP>::attend_slices(const AttendArgs &a, c
     const uint32_t row0 = job.tile * kRows, n_rows = seq.n * a.group;
     auto &o = acc.o;
     auto &m = acc.m;
-    auto &mw = acc.mw;
+    auto &d = acc.d;
     auto &unit = acc.unit;
     auto &l = acc.l;
 
@@ -172,7 +172,8 @@ __device__ __forceinline__ bool Codes8<DP>::attend_slices(const AttendArgs &a, c
         for (int n = 0; n < NT; n++)
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                sc[n][j] = (kSums == 1 ? part_sc[0][n][j] : part_sc[0][n][j] + part_sc[kSums - 1][n][j]) * (row_scale[n][j & 1] * ks);
+                // (rounded here: what is subtracted below is the same number)
+                sc[n][j] = __fmul_rn(kSums == 1 ? part_sc[0][n][j] : part_sc[0][n][j] + part_sc[kSums - 1][n][j], row_scale[n][j & 1] * ks);
         if (edge) {
 #pragma unroll
             for (int n = 0; n < NT; n++)
@@ -185,8 +186,8 @@ __device__ __forceinline__ bool Codes8<DP>::attend_slices(const AttendArgs &a, c
                         if (key0 + g + 8 * j < lo || key0 + g + 8 * j >= hi) sc[n][2 * j + e] = kNone;
                 }
         }
-        // m and mw follow the maxima only once these are 2^kSlack and 2^kSlackW above them: after the first step a
-        // rescaling is rare.
+        // m and m + d follow the maxima only once these are 2^kSlack and 2^kSlackW above them: after the first step a
+        // rescaling is rare. (Scores are compared by their differences, which float32 holds however large they are.)
         const float lvs = __log2f(vs);
         bool grows = false;
 #pragma unroll
@@ -194,7 +195,7 @@ __device__ __forceinline__ bool Codes8<DP>::attend_slices(const AttendArgs &a, c
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const float top = fmaxf(sc[n][e], sc[n][2 + e]);
-                grows |= top > m[n][e] + kSlack || top + lvs > mw[n][e] + kSlackW;
+                grows |= top - m[n][e] > kSlack || (top - m[n][e]) + lvs > d[n][e] + kSlackW;
             }
         if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
@@ -205,18 +206,19 @@ __device__ __forceinline__ bool Codes8<DP>::attend_slices(const AttendArgs &a, c
                     float top = fmaxf(sc[n][e], sc[n][2 + e]);
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    const float m1 = fmaxf(m[n][e], top), w1 = fmaxf(mw[n][e], top + lvs);
+                    const float m1 = fmaxf(m[n][e], top), was = above(d[n][e], m[n][e], m1);
+                    const float d1 = fmaxf(was, above(lvs, top, m1));
                     l[n][e] *= ratio2(m[n][e], m1);
-                    down[e] = ratio2(mw[n][e], w1);
-                    m[n][e] = m1, mw[n][e] = w1;
-                    unit[n][e] = w1 == kNone || m1 == kNone ? 0.0f : ex2(fminf(m1 - w1, 126.0f));
+                    down[e] = ratio2(was, d1);
+                    m[n][e] = m1, d[n][e] = d1;
+                    unit[n][e] = d1 == kNone ? 0.0f : ex2(fminf(-d1, 126.0f));
                 }
 #pragma unroll
                 for (int c = 0; c < kSteps; c++)
                     o[n][c][0] *= down[0], o[n][c][1] *= down[1], o[n][c][2] *= down[0], o[n][c][3] *= down[1];
             }
         }
-        // Weights p = 2^(s - m + kRaise), and in the output's units p * 2^(m + log2 vs - mw). (A block that is louder than
+        // Weights p = 2^(s - m + kRaise), and in the output's units p * 2^(log2 vs - d). (A block that is louder than
         // the unit by more than a float holds is hardly attended to: an infinite factor would make its weights of 0 NaN.)
         uint32_t pf[NT][2];
 #pragma unroll
@@ -224,8 +226,8 @@ __device__ __forceinline__ bool Codes8<DP>::attend_slices(const AttendArgs &a, c
             float w[4];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const float base = (m[n][e] == kNone ? 0.0f : m[n][e]) - kRaise, f = fminf(vs * unit[n][e], FLT_MAX);
-                const float p0 = ex2(sc[n][e] - base), p1 = ex2(sc[n][2 + e] - base);
+                const float base = m[n][e] == kNone ? 0.0f : m[n][e], f = fminf(vs * unit[n][e], FLT_MAX);
+                const float p0 = ex2((sc[n][e] - base) + kRaise), p1 = ex2((sc[n][2 + e] - base) + kRaise);
                 l[n][e] += p0 + p1;
                 w[e] = p0 * f, w[2 + e] = p1 * f;
             }

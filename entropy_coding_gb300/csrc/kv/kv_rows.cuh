@@ -19,6 +19,7 @@
 //   resident<NT>()               CTAs of an SM
 //   kEarly                       launched while the kernel before it still runs
 //   kMergeInRing                 warps' rows meet in their rings
+//   kUnits                       contributions have a unit of their own (else d is 0, and looked at nowhere)
 //   Maps, Stage, Warp            its tensor maps, a step's memory, and what a warp keeps besides
 //   look_up, fetch               where steps are, and asking for one
 //   attend_slices                a warp's steps of a piece of work
@@ -40,13 +41,13 @@ constexpr int kGroup = 8;
 
 template <int DP> struct Merge {  // 8 rows of a warp
     float o[8][DP + 4];
-    float m[8], mw[8], l[8];
+    float m[8], d[8], l[8];
 };
 
-// A part of an item: rows in units of 2^mw (o) and 2^m (l).
+// A part of an item: rows in units of 2^(m + d) (o) and 2^m (l).
 template <int DP, int NT> struct Part {
     float o[8 * NT][DP];
-    float m[8 * NT], mw[8 * NT], l[8 * NT];
+    float m[8 * NT], d[8 * NT], l[8 * NT];
 };
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -146,9 +147,9 @@ template <class F> __device__ __forceinline__ void drain(const AttendArgs &a, ty
 // All of the rows' work, as far as this warp's slices go.
 template <int DP, int NT> struct Sums {
     float o[NT][DP / 16][4];
-    // Of rows 2t, 2t + 1 of each tile: running maxima (the scores', and with the value scales),
-    // 2^(m - mw), and the weights' sums over this thread's keys (in units of 2^(m - kRaise)).
-    float m[NT][2], mw[NT][2], unit[NT][2], l[NT][2];
+    // Of rows 2t, 2t + 1 of each tile: the scores' running maximum, how far above it the contributions' is,
+    // 2^-d, and the weights' sums over this thread's keys (in units of 2^(m - kRaise)).
+    float m[NT][2], d[NT][2], unit[NT][2], l[NT][2];
     uint32_t poison[NT][2];  // of this thread's columns: where a value that the row sees is NaN, and was taken out
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -160,7 +161,7 @@ template <int DP, int NT> struct Sums {
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int e = 0; e < 2; e++) m[n][e] = mw[n][e] = kNone, unit[n][e] = l[n][e] = 0.0f, poison[n][e] = 0;
+            for (int e = 0; e < 2; e++) m[n][e] = d[n][e] = kNone, unit[n][e] = l[n][e] = 0.0f, poison[n][e] = 0;
     }
 };
 
@@ -209,7 +210,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Job &job
 }
 
 // The warps' rows together, 8 at a time: into `part`, or finished.
-template <int DP, int NT, int kWarps, class At>
+template <int DP, int NT, int kWarps, bool kUnits, class At>
 __device__ __forceinline__ void merge(const AttendArgs &a, const At &mg, const Job &job, Sums<DP, NT> &acc, Part<DP, NT> *part) {
     constexpr int kCols = DP / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -232,7 +233,8 @@ __device__ __forceinline__ void merge(const AttendArgs &a, const At &mg, const J
                 for (int c = 0; c < kCols; c++)
                     if (acc.poison[n][e] >> c & 1) acc.o[n][c / 2][2 * (c & 1) + e] = NAN;
             }
-            if (g == 0) mine.m[r] = acc.m[n][e], mine.mw[r] = acc.mw[n][e], mine.l[r] = l;
+            if (g == 0) mine.m[r] = acc.m[n][e], mine.l[r] = l;
+            if (g == 0 && kUnits) mine.d[r] = acc.d[n][e];
 #pragma unroll
             for (int c = 0; c < DP / 16; c += 2)
                 *reinterpret_cast<float4 *>(&mine.o[r][kCols * g + 2 * c]) =
@@ -244,11 +246,13 @@ __device__ __forceinline__ void merge(const AttendArgs &a, const At &mg, const J
             if (row0 + r >= n_rows || col >= int(a.c.dim)) continue;
             float M = kNone, W = kNone, L = 0.0f, x[8] = {};
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) M = fmaxf(M, mg(w).m[r]), W = fmaxf(W, mg(w).mw[r]);
+            for (int w = 0; w < kWarps; w++) M = fmaxf(M, mg(w).m[r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) W = kUnits ? fmaxf(W, above(mg(w).d[r], mg(w).m[r], M)) : M == kNone ? kNone : 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; w++) {
-                L += mg(w).l[r] * ratio2(mg(w).m[r], M);
-                const float f = ratio2(mg(w).mw[r], W);
+                const float by = ratio2(mg(w).m[r], M), f = kUnits ? ratio2(above(mg(w).d[r], mg(w).m[r], M), W) : by;
+                L += mg(w).l[r] * by;
 #pragma unroll
                 for (int k = 0; k < 8; k++) x[k] += mg(w).o[r][col + k] * f;
             }
@@ -256,7 +260,8 @@ __device__ __forceinline__ void merge(const AttendArgs &a, const At &mg, const J
                 float4 *p = reinterpret_cast<float4 *>(&part->o[8 * n + r][col]);
                 __stcg(p, make_float4(x[0], x[1], x[2], x[3]));
                 __stcg(p + 1, make_float4(x[4], x[5], x[6], x[7]));
-                if (col == 0) __stcg(&part->m[8 * n + r], M), __stcg(&part->mw[8 * n + r], W), __stcg(&part->l[8 * n + r], L);
+                if (col == 0) __stcg(&part->m[8 * n + r], M), __stcg(&part->l[8 * n + r], L);
+                if (col == 0 && kUnits) __stcg(&part->d[8 * n + r], W);
             } else {
                 emit(a, job.seq, job.h, row0 + r, col, x, M, W, L);
             }
@@ -270,13 +275,13 @@ __device__ __forceinline__ void merge(const AttendArgs &a, const At &mg, const J
 // `on`, into the finished rows.
 // A thread takes 4 columns of a row and every ways-th part, kRun parts in
 // flight together; the ways meet in shared memory.
-template <int DP, int NT, int kThreads>
+template <int DP, int NT, int kThreads, bool kUnits>
 __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const Job &item, uint32_t first, uint32_t i0, uint32_t step,
                                      uint32_t n, bool on) {
     constexpr int kCols = DP / 4, kRun = 8;
     struct Way {
         float4 x;
-        float m, mw, l;
+        float m, d, l;
     };
     Way *met = reinterpret_cast<Way *>(smem);
     Part<DP, NT> *parts = static_cast<Part<DP, NT> *>(a.parts);
@@ -291,37 +296,40 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const J
         const int r = job / kCols, col = job % kCols * 4;
         const bool mine = job < jobs && way < ways && col < D;
         Way w = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), kNone, kNone, 0.0f};
-        // brings w to the units (m, mw)
-        auto to_units = [&](float m, float mw) {
-            const float f = ratio2(w.mw, mw);
-            w.l *= ratio2(w.m, m);
+        // brings w to the units (m, d)
+        auto to_units = [&](float m, float d) {
+            const float by = ratio2(w.m, m), f = kUnits ? ratio2(above(w.d, w.m, m), d) : by;
+            w.l *= by;
             w.x.x *= f, w.x.y *= f, w.x.z *= f, w.x.w *= f;
-            w.m = m, w.mw = mw;
+            w.m = m, w.d = d;
         };
-        auto add = [&](float4 x, float m, float mw, float l) {
-            const float f = ratio2(mw, w.mw);
-            w.l += l * ratio2(m, w.m);
+        auto add = [&](float4 x, float m, float d, float l) {
+            const float by = ratio2(m, w.m), f = kUnits ? ratio2(above(d, m, w.m), w.d) : by;
+            w.l += l * by;
             w.x.x += x.x * f, w.x.y += x.y * f, w.x.z += x.z * f, w.x.w += x.w * f;
         };
         if (mine) {
 #pragma unroll 1
             for (uint32_t i = way; i < n; i += kRun * ways) {
                 float4 x[kRun];
-                float m[kRun], mw[kRun], l[kRun];
+                float m[kRun], d[kRun], l[kRun];
 #pragma unroll
                 for (int k = 0; k < kRun; k++) {
                     const uint32_t of = i + k * ways;
                     const bool there = of < n;
                     const Part<DP, NT> &p = part(there ? i0 + of * step : i0);
                     x[k] = there ? __ldcg(reinterpret_cast<const float4 *>(&p.o[r][col])) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    m[k] = there ? __ldcg(&p.m[r]) : kNone, mw[k] = there ? __ldcg(&p.mw[r]) : kNone, l[k] = there ? __ldcg(&p.l[r]) : 0.0f;
+                    m[k] = there ? __ldcg(&p.m[r]) : kNone, d[k] = there && kUnits ? __ldcg(&p.d[r]) : kNone, l[k] = there ? __ldcg(&p.l[r]) : 0.0f;
                 }
-                float m1 = w.m, w1 = w.mw;
+                float m1 = w.m;
 #pragma unroll
-                for (int k = 0; k < kRun; k++) m1 = fmaxf(m1, m[k]), w1 = fmaxf(w1, mw[k]);
-                to_units(m1, w1);
+                for (int k = 0; k < kRun; k++) m1 = fmaxf(m1, m[k]);
+                float d1 = kUnits ? above(w.d, w.m, m1) : m1 == kNone ? kNone : 0.0f;
 #pragma unroll
-                for (int k = 0; k < kRun; k++) add(x[k], m[k], mw[k], l[k]);
+                for (int k = 0; k < kRun; k++) d1 = kUnits ? fmaxf(d1, above(d[k], m[k], m1)) : d1;
+                to_units(m1, d1);
+#pragma unroll
+                for (int k = 0; k < kRun; k++) add(x[k], m[k], d[k], l[k]);
             }
         }
         if (ways > 1) {
@@ -331,8 +339,9 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const J
 #pragma unroll 1
                 for (int k = 1; k < ways; k++) {
                     const Way v = met[threadIdx.x + k * jobs];
-                    to_units(fmaxf(w.m, v.m), fmaxf(w.mw, v.mw));
-                    add(v.x, v.m, v.mw, v.l);
+                    const float m1 = fmaxf(w.m, v.m);
+                    to_units(m1, kUnits ? fmaxf(above(w.d, w.m, m1), above(v.d, v.m, m1)) : m1 == kNone ? kNone : 0.0f);
+                    add(v.x, v.m, v.d, v.l);
                 }
         }
         if (on) {
@@ -340,11 +349,12 @@ __device__ __forceinline__ void join(const AttendArgs &a, uint8_t *smem, const J
             if (mine && way == 0) {
                 Part<DP, NT> &p = part(i0);
                 __stcg(reinterpret_cast<float4 *>(&p.o[r][col]), w.x);
-                if (col == 0) __stcg(&p.m[r], w.m), __stcg(&p.mw[r], w.mw), __stcg(&p.l[r], w.l);
+                if (col == 0) __stcg(&p.m[r], w.m), __stcg(&p.l[r], w.l);
+                if (col == 0 && kUnits) __stcg(&p.d[r], w.d);
             }
         } else if (mine && way == 0) {
             const float y[4] = {w.x.x, w.x.y, w.x.z, w.x.w};
-            emit(a, item.seq, item.h, row0 + r, col, y, w.m, w.mw, w.l);
+            emit(a, item.seq, item.h, row0 + r, col, y, w.m, w.d, w.l);
         }
     }
 }
@@ -446,7 +456,7 @@ __global__ void __launch_bounds__(32 * F::kWarps, F::template resident<NT>()) ro
             return;
         }
         const bool whole = job.whole();
-        merge<DP, NT, kWarps>(a, mg, job, acc, whole ? nullptr : parts + 2 * cta + (job.w == job.i0 ? 1 : 0));
+        merge<DP, NT, kWarps, F::kUnits>(a, mg, job, acc, whole ? nullptr : parts + 2 * cta + (job.w == job.i0 ? 1 : 0));
         if (!whole) {
             // CTAs from that of the item's first unit to that of its last: unit u is CTA c's where
             // W c / G <= u < W (c + 1) / G, rounded down, so c = (u G + G - 1) / W
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(32 * F::kWarps, F::template resident<NT>()) ro
             bool on = groups > 1, go = last_of(first, parts_of, s_last);
 #pragma unroll 1
             while (go) {
-                join<DP, NT, kThreads>(a, space, job, c0, i0, step, parts_of, on);
+                join<DP, NT, kThreads, F::kUnits>(a, space, job, c0, i0, step, parts_of, on);
                 go = on && last_of(counter, groups, s_last);
                 i0 = 0, step = kGroup, parts_of = groups, on = false;
             }

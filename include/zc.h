@@ -456,7 +456,9 @@ ZC_API int zc_kv_read(const zc_kv_cache *cache, const zc_kv_batch *batch, int dt
  * Every wait inside the kernels gives up after about a second and reports
  * ZC_ETIMEOUT; the outputs are unspecified then.
  * Scores, weights' sums and outputs are accumulated in float32; weights are
- * rounded to half, in units of the row's largest contribution. */
+ * rounded to half, in units of the row's largest contribution. Scores may be
+ * as large as float32 holds: a weight is taken from a score's difference to
+ * the row's largest, and what is lost of a large score is its own last place. */
 #define ZC_KV_CAUSAL 1u
 ZC_API int zc_kv_attend(const zc_kv_cache *cache, const zc_kv_batch *batch, int dtype, uint32_t heads,
                         const zc_kv_rows *q, const zc_kv_rows *out, float *d_lse, double scale, uint32_t flags,
