@@ -7,7 +7,8 @@
 //   y_a' = y_a cos t - y_b sin t,  y_b' = y_b cos t + y_a sin t,  t = 2 pi f p
 // f is a 64-bit fixed-point fraction of a turn: f p modulo 1 is the low 64 bits
 // of an integer product, exact whatever the position; its quarter turn is split
-// off, and what is left is within an eighth of a turn, where 32 bits are plenty.
+// off, and what is left, within an eighth of a turn, is rounded once to float:
+// a sine is right relative to itself, of a slow pair near the beginning too.
 //
 // A lane has 16 columns of a row, both of each of its 8 pairs, so that the
 // rotation needs no other lane and the norm one sum over D / 16 lanes. A CTA has
@@ -53,10 +54,10 @@ __device__ __forceinline__ float weight_at(const RotateArgs &a, int kv, uint32_t
 
 // cos and sin of `position` times the pair's turns.
 __device__ __forceinline__ float2 turned(const RotateArgs &a, uint32_t pair, int32_t position) {
-    const uint32_t at = uint32_t(__ldg(reinterpret_cast<const unsigned long long *>(a.turns) + pair) * uint64_t(uint32_t(position)) >> 32);
-    const uint32_t quarter = (at + 0x20000000u) >> 30;
+    const uint64_t at = __ldg(reinterpret_cast<const unsigned long long *>(a.turns) + pair) * uint64_t(uint32_t(position));
+    const uint32_t quarter = uint32_t((at + (uint64_t(1) << 61)) >> 62);
     float s, c;
-    sincospif(float(int32_t(at - (quarter << 30))) * 0x1p-31f, &s, &c);
+    sincospif(__ll2float_rn(static_cast<long long>(at - (uint64_t(quarter) << 62))) * 0x1p-63f, &s, &c);
     if (quarter & 1) {
         const float t = s;
         s = c, c = -t;

@@ -535,8 +535,8 @@ ZC_API uint64_t zc_kv4_attend_counter_bytes(const zc_kv4_cache *cache, const zc_
  *   (y_a, y_b) becomes (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
  * for the pairs i < rot_dim / 2, with t = 2 pi p turns[i] / 2^64 at position
  * p = lens[s] - n + i of the batch; columns from rot_dim on are not turned.
- * Everything is float32 (angles: 2^-34 of a turn before their sine and
- * cosine), rounded once.
+ * Everything is float32, rounded once. (p turns[i] / 2^64 is exact modulo 1;
+ * what it is beside the nearest quarter of a turn is rounded to float32.)
  *   d_turns       NULL with rot_dim = 0, else uint64 [rot_dim / 2]: the fraction of a turn
  *                 that a pair turns by for each position, in units of 2^-64
  *   rot_dim       0 or a multiple of 16 up to head_dim
