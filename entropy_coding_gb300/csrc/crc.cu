@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(VerifyArgs a)
 
 int launch_verify(const VerifyArgs &a, cudaStream_t s) {
     int dev = 0, sms = 1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return ZC_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cuda_failed();
     const uint64_t units = uint64_t(a.n_chunks) + 1;
     const uint64_t cap = uint64_t(sms) * 4;
     verify_kernel<<<int(units < cap ? units : cap), kVerifyWarps * 32, 0, s>>>(a);
@@ -104,8 +104,8 @@ int launch_verify(const VerifyArgs &a, cudaStream_t s) {
 int launch_crc(const CrcArgs &a, cudaStream_t s) {
     if (a.n_units == 0) return ZC_OK;
     int dev = 0, sms = 1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return ZC_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cuda_failed();
     uint64_t blocks = (a.n_units + kWarps - 1) / kWarps;
     uint64_t cap = uint64_t(sms) * 8;
     crc_kernel<<<int(blocks < cap ? blocks : cap), kWarps * 32, 0, s>>>(a);

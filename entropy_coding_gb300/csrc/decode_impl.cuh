@@ -1174,7 +1174,7 @@ int launch_decode_mode(const DecodeArgs &a, uint32_t pc, cudaStream_t s) {
     const size_t smem_max = crc_smem<C>() + most * sizeof(PairSmem<kBig>);
     if (cudaFuncSetAttribute(decode_kernel<DT, kBig, kDelta, kLanes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(std::min<size_t>(smem_max, 227 * 1024))) != cudaSuccess)
-        return ZC_ECUDA;
+        return cuda_failed();
     const int grid = int((a.total_chunks + pc - 1) / pc);
     decode_kernel<DT, kBig, kDelta, kLanes><<<grid, 32 * warps_per_chunk<kBig>() * pc, smem, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
@@ -1183,8 +1183,8 @@ int launch_decode_mode(const DecodeArgs &a, uint32_t pc, cudaStream_t s) {
 template <int DT, bool kDelta, bool kLanes>
 int launch_decode_lt(const DecodeArgs &a, cudaStream_t s) {
     int dev = 0, sms = 1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return ZC_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return cuda_failed();
     // One CTA per SM holding the SM's share of the chunks. Few chunks per SM
     // (the rANS chains are then the critical path): one-level tables. Many:
     // the smaller two-level tables, up to kPairs chunks per CTA. Either way
@@ -1214,7 +1214,7 @@ int launch_decode_v2_t(const DecodeArgs &a, cudaStream_t s) {
     const size_t smem_max = fixed + size_t(kV2Pairs) * sizeof(PairSmemV2);
     if (cudaFuncSetAttribute(decode_v2_kernel<DT, kDelta>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(smem_max)) != cudaSuccess)
-        return ZC_ECUDA;
+        return cuda_failed();
     decode_v2_kernel<DT, kDelta><<<a.n_ctas, 64 * a.pairs, smem, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? ZC_OK : ZC_ECUDA;
 }

@@ -1500,12 +1500,12 @@ int launch_wave_t(const EncodeArgs &a, cudaStream_t s) {
     const size_t ssm = sizeof(StatsSmem<W>);
     const size_t csm = kCodeCrcBytes + size_t(kCodeWarps) * kCodeWarpSmem;
     if (cudaFuncSetAttribute(stats_kernel<DT, kDelta>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ssm)) != cudaSuccess)
-        return ZC_ECUDA;
+        return cuda_failed();
     if (cudaFuncSetAttribute(code_kernel<DT, kDelta>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(csm)) != cudaSuccess)
-        return ZC_ECUDA;
+        return cuda_failed();
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stats_kernel<DT, kDelta>, kStatThreads, ssm) != cudaSuccess)
-        return ZC_ECUDA;
+        return cuda_failed();
     const uint64_t most = uint64_t(per_sm < 1 ? 1 : per_sm) * uint64_t(sms_of_device() < 1 ? 1 : sms_of_device());
     const int sgrid = int(a.wave_n < most ? a.wave_n : most);
     stats_kernel<DT, kDelta><<<sgrid, kStatThreads, ssm, s>>>(a);

@@ -13,9 +13,9 @@ namespace kv {
 int sm_count() {
     static std::atomic<int> known[64];
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed(), 1;
     if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 1;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return cuda_failed(), 1;
     if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
@@ -35,7 +35,7 @@ int make_map(CUtensorMap &m, void *base, const Cache &c, uint32_t line, uint64_t
         cudaDriverEntryPointQueryResult found{};
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
             found != cudaDriverEntryPointSuccess || !f)
-            return ZC_ECUDA;
+            return cuda_failed();
         encode = reinterpret_cast<Encode>(f);
         known.store(encode, std::memory_order_relaxed);
     }

@@ -14,6 +14,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "../zc_error.cuh"
 #include "kv_slots.h"
 #include "zc.h"  // from include/ (on the -I path)
 
@@ -144,7 +145,7 @@ template <class... P, class... A> int launch_early(void (*kernel)(P...), dim3 gr
     c.stream = s;
     c.attrs = &early;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, a...) == cudaSuccess ? ZC_OK : ZC_ECUDA;
+    return cudaLaunchKernelEx(&c, kernel, a...) == cudaSuccess ? ZC_OK : cuda_failed();
 }
 __device__ __forceinline__ void after_the_last() {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -487,11 +487,11 @@ __global__ void __launch_bounds__(32 * F::kWarps, F::template resident<NT>()) ro
 template <class F, int NT> int launch(const AttendArgs &a, uint32_t rows, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose kernel may use this much shared memory
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
         if (cudaFuncSetAttribute(rows_kernel<F, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_bytes<F, NT>())) != cudaSuccess)
-            return ZC_ECUDA;
+            return cuda_failed();
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     typename F::Maps maps;

@@ -1108,11 +1108,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 template <int kBits, int DP> int launch(const AttendArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose kernel may use this much shared memory
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ZC_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
         if (cudaFuncSetAttribute(tiles_kernel<kBits, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Smem<kBits, DP>))) != cudaSuccess)
-            return ZC_ECUDA;
+            return cuda_failed();
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     Maps<kBits> maps;

@@ -390,7 +390,7 @@ int run_compress(EncodeArgs &a, const TensorDesc *table, uint32_t n, bool delta,
     a.ws_hist = version == 2 ? reinterpret_cast<unsigned long long *>(a.ws_ctrl + head) : nullptr;
     a.ws_ptab = version == 2 ? a.ws_ctrl + head + hist_bytes(n, W, version) : nullptr;
     a.ws_status = reinterpret_cast<unsigned long long *>(a.ws_ctrl + head + planes);
-    if (cudaMemsetAsync(d_ws, 0, fixed, s) != cudaSuccess) return ZC_ECUDA;
+    if (cudaMemsetAsync(d_ws, 0, fixed, s) != cudaSuccess) return cuda_failed();
     if (n > 1) {
         const int st = upload_table(table, sizeof(TensorDesc) * n, const_cast<TensorDesc *>(a.tensors), s);
         if (st != ZC_OK) return st;
@@ -767,7 +767,7 @@ extern "C" int zc_crc32(const void *d_data, uint64_t nbytes, uint64_t piece_byte
     const uint64_t pieces = piece_bytes ? (nbytes + piece - 1) / piece : 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (pieces == 0) return ZC_OK;
-    if (cudaMemsetAsync(d_out, 0, pieces * 4, s) != cudaSuccess) return ZC_ECUDA;
+    if (cudaMemsetAsync(d_out, 0, pieces * 4, s) != cudaSuccess) return cuda_failed();
     if (nbytes == 0) return ZC_OK;
     CrcArgs a{};
     a.data = static_cast<const uint8_t *>(d_data);

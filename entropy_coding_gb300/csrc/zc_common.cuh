@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "zc.h"  // from include/ (on the -I path)
+#include "zc_error.cuh"
 
 namespace zc {
 

@@ -47,11 +47,11 @@ void *g_scratch[kMaxDevices] = {};
 // Device address of the array on the current device (looked up once).
 int scratch_address(void **out) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ZC_ECUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return zc::cuda_failed();
     std::lock_guard<std::mutex> guard(g_lock);
     if (!g_scratch[dev]) {
         void *p = nullptr;
-        if (cudaGetSymbolAddress(&p, zc_static_scratch) != cudaSuccess || !p) return ZC_ECUDA;
+        if (cudaGetSymbolAddress(&p, zc_static_scratch) != cudaSuccess || !p) return zc::cuda_failed();
         g_scratch[dev] = p;
     }
     *out = g_scratch[dev];
