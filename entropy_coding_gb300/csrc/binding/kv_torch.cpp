@@ -8,7 +8,10 @@
 // something is not as it is most of the time (a layout or a type that the
 // Python layer refuses, or words differently), without having done anything; or
 // the entry point's status where that is not 0. It checks what the Python layer
-// checks: nothing else may come between a tensor and its address.
+// checks: nothing else may come between a tensor and its address. Outputs are
+// made and the kernels launched without the interpreter's lock: memory that has
+// to be freed first, or a full queue, holds up no other thread of Python, whose
+// work the device may be waiting for.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
@@ -82,6 +85,17 @@ bool wrong(Py_ssize_t n, Py_ssize_t want) {
     return n != want;
 }
 
+// The interpreter's lock is someone else's while this lives.
+class Unlocked {
+    PyThreadState *state_ = PyEval_SaveThread();
+
+public:
+    Unlocked() = default;
+    ~Unlocked() { PyEval_RestoreThread(state_); }
+    Unlocked(const Unlocked &) = delete;
+    Unlocked &operator=(const Unlocked &) = delete;
+};
+
 using Move = int (*)(const void *, const zc_kv_batch *, int, const zc_kv_rows *, const zc_kv_rows *, int32_t *, void *);
 using Attend = int (*)(const void *, const zc_kv_batch *, int, uint32_t, const zc_kv_rows *, const zc_kv_rows *, float *, double, uint32_t, uint32_t,
                        void *, uint64_t, int32_t *, void *);
@@ -96,10 +110,20 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const at::Tensor *q = rows_of(a[0], c, 0, rq);
     if (!q || q->scalar_type() == at::kFloat) return none();
     const int64_t heads = q->size(1);
-    at::Tensor out = made(c, heads, q->scalar_type(), ro), lse = at::empty({c.tokens, heads}, out.options().dtype(at::kFloat));
-    const int st = address<Attend>(args[0])(address<const void *>(args[1]), c.batch, code_of(q->scalar_type()), uint32_t(heads), &rq, &ro,
-                                            lse.data_ptr<float>(), real(a[1]), uint32_t(number(a[2])), uint32_t(number(a[3])),
-                                            address<void *>(a[4]), number(a[5]), c.status, c.stream);
+    const at::ScalarType type = q->scalar_type();
+    const auto entry = address<Attend>(args[0]);
+    const auto cache = address<const void *>(args[1]);
+    const double scale = real(a[1]);
+    const uint32_t flags = uint32_t(number(a[2])), window = uint32_t(number(a[3]));
+    void *const workspace = address<void *>(a[4]);
+    const uint64_t bytes = number(a[5]);
+    at::Tensor out, lse;
+    int st;
+    {
+        Unlocked unlocked;
+        out = made(c, heads, type, ro), lse = at::empty({c.tokens, heads}, out.options().dtype(at::kFloat));
+        st = entry(cache, c.batch, code_of(type), uint32_t(heads), &rq, &ro, lse.data_ptr<float>(), scale, flags, window, workspace, bytes, c.status, c.stream);
+    }
     return st ? PyLong_FromLong(st) : both(std::move(out), std::move(lse));
     END_HANDLE_TH_ERRORS
 }
@@ -111,9 +135,16 @@ PyObject *read(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const Call c(args + 2);
     const int code = int(number(args[2 + Call::kArgs]));
     const at::ScalarType type = code == ZC_BF16 ? at::kBFloat16 : code == ZC_FP16 ? at::kHalf : at::kFloat;
+    const auto entry = address<Move>(args[0]);
+    const auto cache = address<const void *>(args[1]);
     zc_kv_rows rk, rv;
-    at::Tensor k = made(c, c.kv_heads, type, rk), v = made(c, c.kv_heads, type, rv);
-    const int st = address<Move>(args[0])(address<const void *>(args[1]), c.batch, code, &rk, &rv, c.status, c.stream);
+    at::Tensor k, v;
+    int st;
+    {
+        Unlocked unlocked;
+        k = made(c, c.kv_heads, type, rk), v = made(c, c.kv_heads, type, rv);
+        st = entry(cache, c.batch, code, &rk, &rv, c.status, c.stream);
+    }
     return st ? PyLong_FromLong(st) : both(std::move(k), std::move(v));
     END_HANDLE_TH_ERRORS
 }
@@ -126,7 +157,15 @@ PyObject *move(PyObject *, PyObject *const *args, Py_ssize_t n) {
     zc_kv_rows rk, rv;
     const at::Tensor *k = rows_of(args[2 + Call::kArgs], c, c.kv_heads, rk), *v = rows_of(args[3 + Call::kArgs], c, c.kv_heads, rv);
     if (!k || !v || k->scalar_type() != v->scalar_type()) return none();
-    return PyLong_FromLong(address<Move>(args[0])(address<const void *>(args[1]), c.batch, code_of(k->scalar_type()), &rk, &rv, c.status, c.stream));
+    const int code = code_of(k->scalar_type());
+    const auto entry = address<Move>(args[0]);
+    const auto cache = address<const void *>(args[1]);
+    int st;
+    {
+        Unlocked unlocked;
+        st = entry(cache, c.batch, code, &rk, &rv, c.status, c.stream);
+    }
+    return PyLong_FromLong(st);
     END_HANDLE_TH_ERRORS
 }
 
@@ -155,11 +194,18 @@ PyObject *rotate(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const at::Tensor *q = rows_of(a[3], c, 0, rq), *k = rows_of(a[4], c, c.kv_heads, rk);
     if (!q || !k || q->scalar_type() != k->scalar_type()) return none();
     if (!weights(a[5], c, q->scalar_type(), r.d_q_weight, r.weight_dtype) || !weights(a[6], c, q->scalar_type(), r.d_k_weight, r.weight_dtype)) return none();
-    at::Tensor q2 = made(c, q->size(1), q->scalar_type(), oq), k2 = made(c, c.kv_heads, q->scalar_type(), ok);
     using Rotate = int (*)(const zc_kv_batch *, const zc_kv_rotation *, int, uint32_t, uint32_t, uint32_t, const zc_kv_rows *, const zc_kv_rows *,
                            const zc_kv_rows *, const zc_kv_rows *, int32_t *, void *);
-    const int st = address<Rotate>(args[0])(c.batch, &r, code_of(q->scalar_type()), uint32_t(c.dim), uint32_t(q->size(1)), uint32_t(c.kv_heads), &rq, &rk,
-                                            &oq, &ok, c.status, c.stream);
+    const int64_t heads = q->size(1);
+    const at::ScalarType type = q->scalar_type();
+    const auto entry = address<Rotate>(args[0]);
+    at::Tensor q2, k2;
+    int st;
+    {
+        Unlocked unlocked;
+        q2 = made(c, heads, type, oq), k2 = made(c, c.kv_heads, type, ok);
+        st = entry(c.batch, &r, code_of(type), uint32_t(c.dim), uint32_t(heads), uint32_t(c.kv_heads), &rq, &rk, &oq, &ok, c.status, c.stream);
+    }
     return st ? PyLong_FromLong(st) : both(std::move(q2), std::move(k2));
     END_HANDLE_TH_ERRORS
 }
