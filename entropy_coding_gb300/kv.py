@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import decimal
+import warnings
 
 import torch
 
@@ -65,7 +66,9 @@ _failures = 0
 # zc_kv_write, zc_kv_read, zc_kv_attend and its two sizes, the same of the 4-bit cache, and zc_kv_rotate, once the library is
 # loaded; a cache's are those from its _calls on
 _entry = None
-_torch = None  # the module of the calls on torch tensors (csrc/binding), once a cache is made
+# the module of the calls on torch tensors (csrc/binding), once a cache is made; False where there is none (no compiler, a
+# folder that cannot be written): every call goes through ctypes then
+_torch = None
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -110,11 +113,18 @@ _addresses: dict = {}
 
 
 def _quick(first: int):
-    """Addresses of a kind of cache's entry points and of zc_kv_rotate, for the calls that the module makes in one step."""
+    """Addresses of a kind of cache's entry points and of zc_kv_rotate, for the calls that the module makes in one step, or
+    None without the module."""
     global _torch
     if _torch is None:
         from . import _build
-        _torch = _build.load_module()
+        try:
+            _torch = _build.load_module()
+        except (OSError, RuntimeError, ImportError) as e:
+            _torch = False
+            warnings.warn(f"the key/value cache's calls go through ctypes, which takes longer on the host: {e}", RuntimeWarning, stacklevel=4)
+    if not _torch:
+        return None
     if first not in _addresses:
         e = _entries()
         _addresses[first] = tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (*e[first:first + 3], e[10]))
