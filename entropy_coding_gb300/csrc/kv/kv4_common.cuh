@@ -96,12 +96,12 @@ template <int DT> struct Piece {
     }
 };
 
-// Positions of the packed tokens [t0, t0 + n) and their sequences, by the whole CTA: each sequence's thread writes its own
-// tokens, or, if they are many, its warp does. Tokens of no sequence (or of one whose counts are wrong) get -1.
+// Positions (x) of the packed tokens [t0, t0 + n) and their sequences (y), by the whole CTA: each sequence's thread writes its
+// own tokens, or, if they are many, its warp does. Tokens of no sequence (or of one whose counts are wrong) get position -1.
+// Where counts fall, two sequences may claim a token: one store for both numbers, so that the position is its sequence's.
 // block_tokens: a sequence must not be longer than its table; 0 for calls that do not use the table.
-__device__ __forceinline__ void locate(const Batch &b, uint32_t block_tokens, uint32_t t0, uint32_t n, int32_t *s_pos, uint32_t *s_seq,
-                                       int32_t *d_status) {
-    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) s_pos[i] = -1;
+__device__ __forceinline__ void locate(const Batch &b, uint32_t block_tokens, uint32_t t0, uint32_t n, int2 *s_at, int32_t *d_status) {
+    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) s_at[i] = make_int2(-1, 0);
     __syncthreads();
     // Of many sequences the first that matters is found by halving (9728 single tokens rotated: 43 us, with all of them looked at 60).
     uint32_t s0 = 0;
@@ -124,7 +124,7 @@ __device__ __forceinline__ void locate(const Batch &b, uint32_t block_tokens, ui
         }
         const bool many = int32_t(hi - lo) > 4;
         if (!many)
-            for (uint32_t t = lo; t < hi; t++) s_pos[t - t0] = from + int32_t(t - lo), s_seq[t - t0] = s;
+            for (uint32_t t = lo; t < hi; t++) s_at[t - t0] = make_int2(from + int32_t(t - lo), int32_t(s));
         uint32_t left = __ballot_sync(0xFFFFFFFFu, many);
         while (left) {
             const int of = __ffs(int(left)) - 1;
@@ -132,7 +132,7 @@ __device__ __forceinline__ void locate(const Batch &b, uint32_t block_tokens, ui
             const uint32_t l = __shfl_sync(0xFFFFFFFFu, lo, of), e = __shfl_sync(0xFFFFFFFFu, hi, of);
             const int32_t p = __shfl_sync(0xFFFFFFFFu, from, of);
             const uint32_t q = s - (threadIdx.x & 31) + of;
-            for (uint32_t t = l + (threadIdx.x & 31); t < e; t += 32) s_pos[t - t0] = p + int32_t(t - l), s_seq[t - t0] = q;
+            for (uint32_t t = l + (threadIdx.x & 31); t < e; t += 32) s_at[t - t0] = make_int2(p + int32_t(t - l), int32_t(q));
         }
     }
     __syncthreads();

@@ -45,15 +45,15 @@ __device__ __forceinline__ void store_paired(uint8_t *to, const Piece<ZC_FP32> &
 }
 
 template <int DT> __global__ void __launch_bounds__(kThreads) read4_kernel(const __grid_constant__ MoveArgs a, uint32_t heads) {
-    __shared__ int32_t s_pos[kTokens], s_block[kTokens];
-    __shared__ uint32_t s_seq[kTokens];
+    __shared__ int2 s_at[kTokens];  // position, sequence
+    __shared__ int32_t s_block[kTokens];
     const uint32_t B = a.c.tokens, D = a.c.dim, per_row = D / 8, h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.c.heads);
     const uint32_t t0 = blockIdx.x * kTokens, n = min(uint32_t(kTokens), a.b.total - t0), units = n * per_row;
     const uint32_t inverse = 0xFFFFFFFFu / per_row + 1;  // i / per_row = i * inverse / 2^32
     after_the_last();
-    locate(a.b, B, t0, n, s_pos, s_seq, a.d_status);
+    locate(a.b, B, t0, n, s_at, a.d_status);
     for (uint32_t i = threadIdx.x; i < n; i += kThreads)
-        s_block[i] = s_pos[i] < 0 ? -1 : int32_t(read_block(a.b, a.c, s_seq[i], block_of_16(a.c, uint32_t(s_pos[i]) / 16), a.d_status));
+        s_block[i] = s_at[i].x < 0 ? -1 : int32_t(read_block(a.b, a.c, uint32_t(s_at[i].y), block_of_16(a.c, uint32_t(s_at[i].x) / 16), a.d_status));
     __syncthreads();
     int64_t code_at[kPieces], scale_at[kPieces];  // of the next head to be asked for
     bool there[kPieces];
@@ -63,7 +63,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads) read4_kernel(const
         there[p] = i < units && s_block[row] >= 0;
         if (!there[p]) continue;
         const int64_t id = s_block[row];
-        const uint32_t c = i - row * per_row, at = h0 * B + uint32_t(s_pos[row]) - block_of_16(a.c, uint32_t(s_pos[row]) / 16) * B;
+        const uint32_t c = i - row * per_row, at = h0 * B + uint32_t(s_at[row].x) - block_of_16(a.c, uint32_t(s_at[row].x) / 16) * B;
         code_at[p] = id * a.c.block_stride + int64_t(at) * a.c.row + c * 4;
         scale_at[p] = id * a.c.scale_stride + int64_t(at) * (D / 16) + c / 2;
     }

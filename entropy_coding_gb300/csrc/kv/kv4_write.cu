@@ -85,8 +85,8 @@ template <int DT> __device__ __forceinline__ uint2 quantise(const Piece<DT> (&in
 }
 
 template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(const __grid_constant__ MoveArgs a, uint32_t heads) {
-    __shared__ int32_t s_pos[kThreads], s_block[kThreads];
-    __shared__ uint32_t s_seq[kThreads];
+    __shared__ int2 s_at[kThreads];  // position, sequence
+    __shared__ int32_t s_block[kThreads];
     const uint32_t B = a.c.tokens, per_row = a.c.dim / 16, tokens = kThreads / per_row, h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.c.heads);
     const uint32_t t0 = blockIdx.x * tokens, n = min(tokens, a.b.total - t0);
     const uint32_t row = threadIdx.x / per_row, g = threadIdx.x - row * per_row;
@@ -104,15 +104,17 @@ template <int DT> __global__ void __launch_bounds__(kThreads) write4_kernel(cons
     };
     after_the_last();
     ask(h0);
-    locate(a.b, B, t0, n, s_pos, s_seq, a.d_status);
-    if (threadIdx.x < n)
-        s_block[threadIdx.x] = s_pos[threadIdx.x] < 0 ? -1 : int32_t(read_block(a.b, a.c, s_seq[threadIdx.x], block_of_16(a.c, uint32_t(s_pos[threadIdx.x]) / 16), a.d_status));
+    locate(a.b, B, t0, n, s_at, a.d_status);
+    if (threadIdx.x < n) {
+        const int2 at = s_at[threadIdx.x];
+        s_block[threadIdx.x] = at.x < 0 ? -1 : int32_t(read_block(a.b, a.c, uint32_t(at.y), block_of_16(a.c, uint32_t(at.x) / 16), a.d_status));
+    }
     __syncthreads();
     const bool there = mine && s_block[mine ? row : 0] >= 0;
     int64_t code_at = 0, scale_at = 0;
     if (there) {
         const int64_t id = s_block[row];
-        const uint32_t at = h0 * B + uint32_t(s_pos[row]) - block_of_16(a.c, uint32_t(s_pos[row]) / 16) * B;
+        const uint32_t at = h0 * B + uint32_t(s_at[row].x) - block_of_16(a.c, uint32_t(s_at[row].x) / 16) * B;
         code_at = id * a.c.block_stride + int64_t(at) * a.c.row + g * 8;
         scale_at = id * a.c.scale_stride + int64_t(at) * per_row + g;
     }

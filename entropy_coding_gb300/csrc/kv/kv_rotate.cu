@@ -33,8 +33,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLanes = kMaxHeadDim / 16;   // of a row, at most
 
 template <int kTokens> struct Shared {
-    int32_t pos[kTokens];
-    uint32_t seq[kTokens];
+    int2 at[kTokens];  // position, sequence
     // for lane c of a row, quarter j of its pairs (or columns): conflict-free as they are read
     float4 turn[kTokens][4][kLanes];  // cosines of two pairs, and sines
     float4 weight[2][4][kLanes];      // of q and k
@@ -67,14 +66,14 @@ __device__ __forceinline__ float2 turned(const RotateArgs &a, uint32_t pair, int
 
 // The whole CTA: positions, sines and cosines, and weights.
 template <bool kInterleaved, int kTokens> __device__ __forceinline__ void prepare(const RotateArgs &a, Shared<kTokens> &sm, uint32_t t0, uint32_t n) {
-    locate(a.b, 0, t0, n, sm.pos, sm.seq, a.d_status);
+    locate(a.b, 0, t0, n, sm.at, a.d_status);
     const uint32_t pairs = a.rot / 2;
     for (uint32_t i = threadIdx.x; i < n * pairs; i += kThreads) {
         const uint32_t token = i / pairs, pair = i - token * pairs;
-        if (sm.pos[token] < 0) continue;
+        if (sm.at[token].x < 0) continue;
         uint32_t c = pair / 8, m = pair % 8;
         if (kInterleaved) c = pair % (pairs / 2) / 4, m = pair % 4 + (pair < pairs / 2 ? 0 : 4);
-        const float2 t = turned(a, pair, sm.pos[token]);
+        const float2 t = turned(a, pair, sm.at[token].x);
         float *to = reinterpret_cast<float *>(&sm.turn[token][m / 2][c]) + m % 2;
         to[0] = t.x, to[2] = t.y;
     }
@@ -147,7 +146,7 @@ template <int DT, bool kInterleaved, int kTokens> __global__ void __launch_bound
     after_the_last();
     ask();
     prepare<kInterleaved>(a, sm, t0, n);
-    const bool held = token < n && sm.pos[token < n ? token : 0] >= 0;  // (the token belongs to a sequence)
+    const bool held = token < n && sm.at[token < n ? token : 0].x >= 0;  // (the token belongs to a sequence)
     float2 cosine[4], sine[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
