@@ -1,7 +1,7 @@
 // kv_torch.cpp — the cache's calls on torch tensors, as one step from Python: a
 // decoding step is a handful of kernels of a few microseconds, and making the
 // outputs, the descriptors and the call one by one from Python takes longer than
-// they run (a step's attention: 13.7 us so and 7.5 us here).
+// they run (a step's attention: 13.7 us so and 7.9 us here).
 //
 // Each function takes the C entry point's address, the addresses that a cache
 // and a batch keep, and the tensors. It returns the outputs; or None where

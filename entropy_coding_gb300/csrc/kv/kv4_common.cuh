@@ -16,7 +16,7 @@ constexpr uint32_t kScaleMost = 0xE2, kScaleNaN = 0xFF;  // 10240: 6 times that 
 
 // Heads that a CTA of a run of tokens does one after another: the run's places are looked up once for them, and the next
 // head's numbers are on their way meanwhile; as many as leave 3 CTAs for 2 SMs. (133678 tokens of 8 heads read: 1 head 148
-// us, 2 heads 118, 4 and 8 heads 111; 17138 tokens 20.1, 16.2, 15.9 and 14.9; 777 tokens 3.3, 3.9, 5.0 and 7.1; 32 tokens
+// us, 2 heads 118, 4 and 8 heads 111; 16978 tokens 20.1, 16.2, 15.9 and 14.9; 777 tokens 3.3, 3.9, 5.0 and 7.1; 32 tokens
 // written and read back 5.6, 6.4, 8.3 and 12.2.)
 inline uint32_t heads_of_a_cta(uint32_t runs, uint32_t heads) {
     const uint64_t most = uint64_t(runs) * heads * 2 / (3 * uint64_t(sm_count()));

@@ -9,7 +9,7 @@
 // Measured on a GB300: 133678 tokens of 8 heads of 128 to bfloat16, 702 MB, four
 // fifths of them written, in 111 us: 6.3 TB/s, 0.94 of the copy rate (one head a
 // CTA, with its lookups before its reads, 148); 777 tokens of float16 in 3.3;
-// 17138 tokens to float32, 160 MB, in 29.1 (5.5 TB/s).
+// 16978 tokens to float32, 159 MB, in 29.1 (5.5 TB/s).
 #include "kv4_common.cuh"
 
 namespace zc {
@@ -32,7 +32,7 @@ template <int DT> __device__ __forceinline__ void number(uint32_t codes, uint32_
 
 // The 32 bytes of each of two neighbours, each of whose stores of 16 bytes is then beside the other's: the first store is of
 // the even thread's 32 bytes, the second of the odd one's, whole sectors. Both are here, in one row and as far: a row has an
-// even number of pieces (head_dim is a multiple of 16). (17138 tokens: 40.4 us without, 29.1 with.)
+// even number of pieces (head_dim is a multiple of 16). (16978 tokens: 40.4 us without, 29.1 with.)
 __device__ __forceinline__ void store_paired(uint8_t *to, const Piece<ZC_FP32> &x) {
     const bool odd = threadIdx.x & 1;
     const uint32_t both = 3u << (threadIdx.x & 30);

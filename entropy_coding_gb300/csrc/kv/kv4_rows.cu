@@ -26,14 +26,14 @@
 // of the copy rate, where the 8-bit cache's 558 MB take 98; one token over 131072
 // keys in 38. Bytes are not the bound here: with the steps' arithmetic left out
 // the same copies take 58 us, of which 12 are the start, the pieces' ends and the
-// joining. A step of 32 keys is 660 instructions of a warp, 128 conversions and
+// joining. A step of 32 keys is about 660 instructions of a warp, 128 conversions and
 // 128 products with scales among them, 190 of them for copies, waits and pieces'
 // ends; conversions, half products and tensor-core products contend for issue
 // (together at 0.5 instructions a clock, each alone at its unit's rate), so that
 // neither more warps (4 CTAs an SM, or CTAs of 8, 12 or 16 warps) nor more steps in
 // flight are faster. What was: an item's beginning and end counted as work (83.5
 // to 73.2 us), boxes of 32 rows and scale lines by the tensor memory accelerator
-// (90 to 84), beginning before the kernel in front of this one has ended (73.2 to
+// (90 to 84), beginning as the kernel in front of this one ends (73.2 to
 // 70.4).
 #include <cstddef>
 

@@ -12,8 +12,12 @@
 // a row's scale goes into those.
 //
 // Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads of
-// 128, causal) in 435 us, 1.26 PFLOP/s, 0.64 of the measured bfloat16 rate; 16
-// sequences of 2 to 5 tokens, 8 query heads to a head, over up to 4096 keys in 22.
+// 128, causal) in 434 us, 1.27 PFLOP/s, 0.64 of the measured bfloat16 rate; 912
+// tokens of two sequences over 28384 keys in 178 (1.19 PFLOP/s); 16 sequences of 2
+// to 5 tokens, 8 query heads to a head, over up to 4096 keys in 22. A 4096-token
+// prompt of heads of 64 in 121 us, 0.57 PFLOP/s: products are half as long there,
+// the rows' work is not, and with this split of registers the kernel of 64 columns
+// spills (132 bytes of stores, that of 128 columns 20).
 // Of 3480 clocks a key tile the products' warp waits 850; their operations would
 // take 2048, but scores' products read both operands from a shared memory that the
 // conversion and the copies use too. A row tile's chain is 350 clocks for the

@@ -16,8 +16,8 @@
 // many tokens as that makes, so that it writes runs of rows. Its first reads do not wait
 // for where the tokens belong: that is looked up meanwhile.
 //
-// Measured on a GB300: 17138 tokens of 8 heads of 128, bfloat16, 70 MB read and 20
-// written, in about 14.5 us (6.2 TB/s); 32 tokens in 3. The arithmetic units are
+// Measured on a GB300: 16978 tokens of 8 heads of 128, bfloat16, 70 MB read and 20
+// written, in about 14.5 us (6.1 TB/s); 32 tokens in 3. The arithmetic units are
 // half busy: what counted was two numbers to an instruction, the type's own
 // comparisons for the largest magnitude and a head's rows on their way while the
 // one before them is worked on (27 us without); CTAs of 128 threads are faster

@@ -133,7 +133,7 @@ int launch_tiles4(const AttendArgs &a, cudaStream_t s);
 // A kernel that may be launched while the one before it on the stream ends: it does nothing to global memory, not even read
 // it, before after_the_last() returns, which is when that one is done and its writes are there. (A step's rotation, one after
 // another: 6.2 us, early 3.6; its writing and reading back 10.3 and 6.0. A kernel that lets its successor come as soon as its
-// own CTAs have begun has that one's beside them, waiting: 3.8 and 6.5, and 17138 tokens written and read back 34.2 for 30.5.)
+// own CTAs have begun has that one's beside them, waiting: 3.8 and 6.5, and 16978 tokens written and read back 34.2 for 30.5.)
 template <class... P, class... A> int launch_early(void (*kernel)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t s, const A &...a) {
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;

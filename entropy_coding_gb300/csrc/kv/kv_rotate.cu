@@ -16,10 +16,10 @@
 // angles' sines and cosines are computed once, while the first rows are on
 // their way, and stay in registers. Arithmetic is on two floats at a time.
 //
-// Measured on a GB300: 17138 tokens of 32 and 8 heads of 128, bfloat16, 351 MB
-// read and written, in 62 us: 5.6 TB/s, 0.83 of the copy rate (float32, 702 MB, in 113: 0.92);
-// 32 tokens in 3.6.
-// Schedulers issue in 0.73 of the clocks, the arithmetic units are busy in 0.56:
+// Measured on a GB300: 16978 tokens of 32 and 8 heads of 128, bfloat16, 348 MB
+// read and written, in 62 us: 5.6 TB/s, 0.82 of the copy rate (neighbouring columns 63;
+// float32, 695 MB, in 112: 0.92); 32 tokens in 3.5.
+// Schedulers issue in 0.74 of the clocks, the arithmetic units are busy in 0.56:
 // both the bytes and the instructions are near. Four CTAs an SM (64 registers) beat
 // three (66 us); sines and cosines in registers and no addresses but sums beat
 // neither (63.5, registers spilled).
@@ -203,7 +203,7 @@ template <int DT, bool kInterleaved, int kTokens> __global__ void __launch_bound
 
 // Tokens of a CTA: one, which then has all of its warps, while that makes no more than 2 CTAs an SM; 4, and 8 of many. (32
 // tokens of 40 heads of 128: 1 token 6.2 us, 4 tokens 8.2; 608 tokens: 4 tokens 9.5, 8 tokens 12.3; 2432 single tokens 16.4 and
-// 18.3, 3648 26.1 and 22.1; 17138 tokens of prompts 65.5 and 63.6.)
+// 18.3, 3648 26.1 and 22.1; 16978 tokens of prompts 65.5 and 63.6.)
 template <int DT, bool kInterleaved> int launch(const RotateArgs &a, cudaStream_t s) {
     const uint32_t sms = uint32_t(sm_count());
     if (a.b.total <= 2 * sms) return launch_early(rotate_kernel<DT, kInterleaved, 1>, dim3(a.b.total), kThreads, 0, s, a);

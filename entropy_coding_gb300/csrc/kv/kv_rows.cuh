@@ -17,7 +17,7 @@
 //   kSlice, kStages              keys of a warp's step, steps of its ring
 //   kFixed                       units that an item's beginning and end count as, besides its keys
 //   resident<NT>()               CTAs of an SM
-//   kEarly                       launched while the kernel before it still runs
+//   kEarly                       launched so that it may begin as the kernel before it ends
 //   kMergeInRing                 warps' rows meet in their rings
 //   kUnits                       contributions have a unit of their own (else d is 0, and looked at nowhere)
 //   Maps, Stage, Warp            its tensor maps, a step's memory, and what a warp keeps besides

@@ -6,21 +6,23 @@
 // tiles of 128 keys, with codes kc, vc and block scales ks, vs:
 //   S = Q Kc^T            128 x 128 x dim, half operands, float32 in tensor memory
 //   s_ij = S_ij ks_b c_i  (c_i: the row's power of two and the softmax scale, log2)
-//   w_ij = 2^(s_ij + log2 vs_b - mw_i + 9), rounded to half, back into tensor memory
+//   w_ij = 2^(s_ij - m_i + log2 vs_b - d_i + 9), rounded to half, back into tensor memory
 //   O += W Vc             128 x dim x 128
-//   l_i += sum_b (sum_{j in b} w_ij before rounding) 2^(mw_i - 9 - m_i - log2 vs_b)
-// m_i and mw_i follow the row's maxima of s and of s + log2 vs (and may lag by
+//   l_i += sum_b (sum_{j in b} w_ij before rounding) 2^(d_i - 9 - log2 vs_b)
+// m_i and m_i + d_i follow the row's maxima of s and of s + log2 vs (and may lag by
 // 2^8 and 2^6), so O is in units of the largest contribution and l in units of
 // the largest weight: block scales cost an exponent's bias for 16 columns, and no
 // spread between them loses precision; half keeps its 11 bits down to 2^-23 of
 // the largest w vs. A block whose scale is 2^69 below the unit adds less than
-// 2^-60 of it and counts as 2^-69. out = O 2^(mw - 9 - m) / l.
+// 2^-60 of it and counts as 2^-69. out = O 2^(d - 9) / l.
 //
 // The work and the roles of a CTA's warps are in kv_tiles.cuh.
 //
 // Measured on a GB300: an 8192-token prompt (32 query heads, 8 key/value heads
-// of 128, causal) in 454 to 461 us, 1.2 PFLOP/s, 0.64 of the measured bfloat16 rate;
-// 912 tokens of two sequences over 28384 keys in 185 us (1.15 PFLOP/s). The
+// of 128, causal) in 462 to 464 us, 1.19 PFLOP/s, 0.60 of the measured bfloat16 rate;
+// 912 tokens of two sequences over 28384 keys in 191 us (1.11 PFLOP/s). (454 and 186
+// without the code for large scores, which these calls do not come to: the schedulers
+// wait for instructions as it is, and a row's loop grows by it.) The
 // tensor cores are busy half of the time. A key tile takes 1.7 us where its
 // products take 1.05: a row tile's chain of scores, weights (about 1.1 us: two
 // passes over the scores, 128 exponentials a thread on a unit shared by two

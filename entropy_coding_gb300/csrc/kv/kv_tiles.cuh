@@ -699,8 +699,8 @@ template <int DP> __device__ __forceinline__ void rescale(uint32_t at, float by)
 // A weight's exponent is one multiply-add of a product, its scale and the row's maximum, off by as much as the maximum's
 // rounding: up to a maximum of kFar by less than a tenth of a weight's own rounding to half, next to 10^9 by hundreds. In a warp with a
 // row beyond kFar the products of a key tile, in tensor memory, become differences from the maximum first, which are exact
-// where they are near it. (Taking the difference of every product: an 8192-token prompt in 456 us for 438 over the 4-bit
-// cache, 524 for 462 over the 8-bit one.)
+// where they are near it. (Taking the difference of every product: an 8192-token prompt in 456 us for 434 over the 4-bit
+// cache, 524 for 462 over the 8-bit one; doing so in the weights' own loop, behind a test, 474 and 552.)
 constexpr float kFar = 1024.0f;
 __device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && fabsf(m) < INFINITY; }
 // `with`: what becomes of score i of 32 columns' chunk q.

@@ -17,7 +17,7 @@
 // allows: what bounds it is the latency of its few dependent reads, which only
 // more CTAs on an SM hide.
 //
-// Measured on a GB300: 104 MB of bfloat16 prompts (17138 tokens of 8 heads of
+// Measured on a GB300: 104 MB of bfloat16 prompts (16978 tokens of 8 heads of
 // 128, blocks of 64) in 19.7 us, 5.3 TB/s, 0.78 of the copy rate; the arithmetic
 // units are at 49 % and 44 % of the warps are there: no unit's rate is the
 // limit, a CTA's start is (its place in the batch, the sequence's length, then

@@ -18,7 +18,8 @@ given by its handle outlive the cache; what a call makes for itself is seen to.
 The cache serves: nothing here is differentiable, and outputs never require
 gradients, whatever the inputs do. Queries are 16-bit, as the tensor cores take
 them; heads go up to 128 columns, which is what a tile's queries, operands and
-sums fill of shared and of tensor memory.
+sums fill of shared and of tensor memory. The rotation takes a cache's heads, in
+float32 too, and positions from the batch.
 """
 from __future__ import annotations
 
