@@ -6,6 +6,7 @@ are 0 whatever the scores' size, and a key whose product is the largest by a las
 * keys that are alike get one weight: the output is the values' mean, to what the 8- and 4-bit tests allow besides the
   scores' own error (2^-11 for a weight, 2^-23 for each addition, and the 8-bit cache's 2^-25 of the loudest block);
 * a key that is above the others by more than a last place is the output, exactly (a value has no more than 6 bits);
+* the same of the keys that a row sees, under a causal limit and a window;
 * of any keys the output is a mean with some weights: between the least and the largest of a column's values, less and plus
   2^-10 of the largest magnitude for weights that are rounded to half and sums of them that are not (2^-11, and 2^-23 for
   each of 3000 keys), and one rounding to the type. The log sum is within the products' error, 2^-17 of the largest sum of
@@ -197,3 +198,47 @@ def test_value_scales_far_apart_under_large_scores(dim, lens, news, size, scale)
         tol = mass * (2.0 ** -11 + len(v) * 2.0 ** -23) + np.abs(v).max() * 2.0 ** -25
         tol += HALF_STEP["bf16"] * (np.abs(want) + tol)
         assert (np.abs(out[row, h] - want) <= tol).all(), (row, h, out[row, h][:4], want[:4])
+
+
+MASKS = [([3000], [1], True, 500), ([700, 90], [3, 1], True, 60), ([700], [260], True, 0), ([700], [260], True, 100), ([130, 300], [130, 150], True, 17),
+         ([500], [200], False, 130)]  # lens, new, causal, window
+
+
+@pytest.mark.parametrize("kind", CACHES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,news,causal,window", MASKS)
+@pytest.mark.parametrize("dtype,size,scale", [s for s in SIZES if s[1] * (s[2] or 1) > 0])
+def test_keys_that_a_row_does_not_see(kind, dim, lens, news, causal, window, dtype, size, scale):
+    """Keys of four loudnesses, far apart as scores: a row's output is the mean of the values at the loudest keys that it sees.
+    Past a sequence's end there is NaN."""
+    rng, table, pool, _, batch, q = _case(kind, dim, lens, news, dtype, 5, 3)
+    kc, ks, vc, vs = pool
+    kind.alike(kc, ks)
+    loud = rng.choice(4, p=[0.7, 0.2, 0.08, 0.02], size=kc.shape[:3])
+    if kind is _Eight:
+        kc[..., 3] = np.array([0x38, 0x3C, 0x40, 0x44], np.uint8)[loud]
+    else:
+        kc[..., 1] = np.array([0x22, 0x32, 0x42, 0x52], np.uint8)[loud]
+    for s, n in enumerate(lens):
+        if n % BLOCK:
+            for codes, scales in ((kc, ks), (vc, vs)):
+                (codes if kind is _Eight else scales)[table[s][n // BLOCK], :, n % BLOCK:] = 0x7F if kind is _Eight else 0xFF
+    q.fill_(size)
+    cache = kind.cache(*pool)
+    out, _ = zc.kv_attend(cache, batch, q, scale=scale, causal=causal, window=window)
+    cache.check()
+    out, row = out.double().cpu().numpy(), 0
+    for s, n in enumerate(lens):
+        v = kind.ref.rows_of(vc, vs, table[s], n)
+        at = loud[table[s]].transpose(1, 0, 2).reshape(HKV, -1)[:, :n]
+        for i in range(0, news[s], 13 if news[s] > 16 else 1):
+            p = n - news[s] + i
+            lo, hi = (max(0, p - window + 1) if window else 0), (p + 1 if causal else n)
+            for h in range(HKV * GROUP):
+                seen = at[h // GROUP, lo:hi]
+                values = v[h // GROUP, lo:hi][seen == seen.max()]
+                want, mass = values.mean(0), np.abs(values).mean(0)
+                tol = mass * (2.0 ** -11 + len(values) * 2.0 ** -23) + (np.abs(v).max() * 2.0 ** -25 if kind is _Eight else 0.0)
+                tol += HALF_STEP[dtype] * (np.abs(want) + tol) + (2.0 ** -25 if dtype == "fp16" else 0.0)
+                assert (np.abs(out[row + i, h] - want) <= tol).all(), (s, i, h, out[row + i, h][:4], want[:4])
+        row += news[s]
